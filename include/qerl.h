@@ -61,7 +61,8 @@ typedef enum {
     QERL_ERR_RANGE = 8              /* a weight the packed layout cannot hold (MXFP4 scale span; status word) */
 } qerl_status;
 
-typedef enum { QERL_F32 = 0, QERL_BF16 = 1 } qerl_dtype;
+/* QERL_E4M3 is a type of the key-value cache only. */
+typedef enum { QERL_F32 = 0, QERL_BF16 = 1, QERL_E4M3 = 2 } qerl_dtype;
 /* Element code of a packed weight (qerl_linear_desc.w_format): E2M1
  * (NVFP4, and MXFP4 after qerl_mxfp4_pack) or the NF4 level table. */
 typedef enum { QERL_W_NVFP4 = 0, QERL_W_NF4 = 1 } qerl_w_format;
@@ -449,6 +450,104 @@ QERL_API qerl_status qerl_lora_linear_noalloc(const void* x, int64_t m, int64_t 
                                               const uint8_t* wpacked, const float* tensor_scale, int64_t n,
                                               const float* z, const void* A, const void* B, int r, float alpha,
                                               void* y, int y_dtype, void* stream);
+
+/* ========================================================================
+ * Attention between the q/k/v linears and the o linear: a paged key-value
+ * cache, the rotation of q and k with the append to it, attention of one new
+ * token per sequence over it, and causal attention of packed whole prompts.
+ * (No counterpart in the paper, which measures rollouts as a whole.)
+ *
+ * Query head h reads key-value head h / (num_heads / num_kv_heads).
+ * num_heads % num_kv_heads == 0; head_dim is 64 or 128.
+ *
+ * The cache: pages of page_size token rows.  All buffers are the caller's.
+ *   k, v     device, [num_pages][num_kv_heads][page_size][head_dim] of dtype
+ *            (QERL_BF16 or QERL_E4M3), 16-byte aligned.
+ *   k_scale, v_scale  device float [num_kv_heads] or NULL (1): a QERL_E4M3
+ *            cache holds value / scale.  NULL for QERL_BF16.
+ *   page_table  device int32, row s (stride ld_table) holds the page numbers
+ *            of sequence s: position p lies in page page_table[s][p /
+ *            page_size], row p % page_size.  Entries past a sequence's last
+ *            page are never read.  Sequences may share pages.
+ *   num_seqs rows of max_pages entries.
+ * Limits: 1 <= page_size <= 65536, max_pages * page_size <= INT32_MAX,
+ * num_pages <= INT32_MAX, num_seqs <= 2^20, num_heads <= 1024.
+ * ======================================================================== */
+typedef struct {
+    void* k;
+    void* v;
+    int dtype;
+    int num_kv_heads;
+    int head_dim;
+    int page_size;
+    int64_t num_pages;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* page_table;
+    int64_t num_seqs;
+    int64_t max_pages;
+    int64_t ld_table;
+} qerl_kv_cache;
+
+/* Rotates q and k to their positions and appends k and v to the cache.
+ * For token t at position p = positions[t], head by head, half = rot_dim / 2:
+ *   theta_i = p * inv_freq[i],
+ *   (x[i], x[i + half]) -> (x[i] cos theta_i - x[i + half] sin theta_i,
+ *                           x[i + half] cos theta_i + x[i] sin theta_i), i < half;
+ * elements from rot_dim on stay.  fp32 arithmetic, angles reduced in 64-bit
+ * fixed point (exact for far positions), one rounding.  v is not rotated.
+ *   q        bf16 rows of num_heads * head_dim, row stride ldq, or NULL.
+ *   k, v     bf16 rows of num_kv_heads * head_dim, row strides ldk, ldv.
+ *   positions  device int32 [tokens]; a negative one marks padding: nothing of
+ *            that token is read or written.
+ *   seq_ids  device int32 [tokens], the token's row of the page table; NULL:
+ *            token t belongs to sequence t.
+ *   inv_freq device double [rot_dim / 2], radians per position, finite.
+ *   q_out    bf16 rows, required with q; may be q itself (same stride).
+ *   k_out    bf16 rows or NULL; may be k itself (same stride).
+ *   cache    NULL: rotation only (v, seq_ids are then not read; k_out required).
+ * The cache gets the fp32 rotated k (and v) rounded once to its type: bf16, or
+ * E4M3(value / scale), nearest even, saturating at +-448, NaN kept.
+ * Pointers of q, k, v, q_out, k_out 16-byte aligned, strides multiples of 8.
+ * rot_dim % 16 == 0, 0 <= rot_dim <= head_dim.  The num_kv_heads and head_dim
+ * arguments equal the cache's.  Two tokens of one call at one place of the
+ * cache give either's row.
+ * A sequence number or position outside the page table, or a page number
+ * outside the cache, records QERL_ERR_RANGE: that token is not appended.
+ * workspace >= qerl_rope_append_workspace_size(), 256-byte aligned, zero-filled
+ * before its first use (status word only). */
+QERL_API size_t qerl_rope_append_workspace_size(void);
+QERL_API qerl_status qerl_rope_append(const qerl_kv_cache* cache, const void* q, int64_t ldq, int num_heads,
+                                      const void* k, int64_t ldk, const void* v, int64_t ldv, int num_kv_heads,
+                                      int head_dim, int64_t tokens, const int32_t* seq_ids,
+                                      const int32_t* positions, const double* inv_freq, int rot_dim, void* q_out,
+                                      int64_t ldqo, void* k_out, int64_t ldko, void* workspace, size_t ws_bytes,
+                                      void* stream);
+
+/* Attention of one new token per sequence over the cache:
+ *   s_j = scale * q . k_j,  j < lengths[s];   lse = ln sum_j exp(s_j);
+ *   out = sum_j exp(s_j - lse) v_j,
+ * for each of num_seqs sequences and num_heads heads.  A sequence of length 0
+ * (or with every s_j = -inf) gives out = 0, lse = -inf.  Cache rows at and past
+ * the length are not used, whatever they hold (NaN included).
+ *   q        bf16 [num_seqs] rows of num_heads * head_dim, row stride ldq.
+ *   lengths  device int32 [num_seqs]: the rows in the cache, the new token's
+ *            included.  Below 0 counts as 0, above max_pages * page_size as
+ *            that; either records QERL_ERR_RANGE.
+ *   out      bf16 rows, stride ldo; lse float [num_seqs][num_heads] or NULL.
+ * q and out 16-byte aligned, strides multiples of 8.  Scores, softmax and sums
+ * are fp32; for a QERL_E4M3 cache the softmax weights are rounded to fp16.  A
+ * non-finite q, k or v in use makes the outputs it reaches non-finite.
+ * A page number outside the cache records QERL_ERR_RANGE and its rows read as
+ * zeros.  The result does not depend on timing (partial sums are joined in a
+ * fixed order), only on the shapes, the lengths and the device.
+ * workspace >= qerl_decode_attention_workspace_size(), 256-byte aligned,
+ * zero-filled before its first use; calls that share one must be ordered. */
+QERL_API size_t qerl_decode_attention_workspace_size(int64_t num_seqs, int num_heads, int num_kv_heads,
+                                                     int head_dim);
+QERL_API qerl_status qerl_decode_attention(const qerl_kv_cache* cache, const void* q, int64_t ldq, int num_heads,
+                                           const int32_t* lengths, float scale, void* out, int64_t ldo, float* lse,
+                                           void* workspace, size_t ws_bytes, void* stream);
 
 /* Synchronizes `stream`, returns the status word recorded in `workspace` by
  * the kernels of earlier calls (QERL_OK if none failed) and resets it to

@@ -19,8 +19,11 @@ The functions named like the C entry points take torch tensors:
     qerl_lora_linear(x, wpacked, tensor_scale, z, A, B, alpha, y, workspace)
     qerl_lora_linear_noalloc(x, wpacked, tensor_scale, z, A, B, alpha, y)
     qerl_lora_linear_group(x, z, [(wpacked, tensor_scale, A, B, alpha, y), ...], workspace)
+    qerl_rope_append(cache, q, k, v, positions, inv_freq, q_out, k_out, workspace, seq_ids)
+    qerl_decode_attention(cache, q, lengths, scale, out, lse, workspace)
     qerl_read_status(workspace)
 
+`kv_cache()` builds the descriptor of a paged key-value cache once, and
 `linear_descs()` builds the descriptor array of a group once; passing it
 instead of the list skips that marshalling on every call.
 
@@ -47,6 +50,8 @@ __all__ = [
     "qerl_lora_linear_workspace_size", "qerl_lora_linear", "qerl_lora_linear_noalloc", "qerl_read_status",
     "qerl_lora_linear_group", "qerl_lora_linear_group_workspace_size", "LinearDesc", "linear_descs",
     "quantize", "lora_linear", "workspace",
+    "QERL_E4M3", "KvCache", "kv_cache", "qerl_rope_append", "qerl_rope_append_workspace_size",
+    "qerl_decode_attention", "qerl_decode_attention_workspace_size", "rope_append", "decode_attention",
 ]
 
 class LinearDesc(ctypes.Structure):
@@ -56,8 +61,17 @@ class LinearDesc(ctypes.Structure):
                 ("y", ctypes.c_void_p), ("y_dtype", ctypes.c_int), ("w_format", ctypes.c_int)]
 
 
+class KvCache(ctypes.Structure):
+    """Mirror of qerl_kv_cache (include/qerl.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("num_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_int64), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("num_seqs", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("ld_table", ctypes.c_int64)]
+
+
 QERL_OK = 0
-QERL_F32, QERL_BF16 = 0, 1
+QERL_F32, QERL_BF16, QERL_E4M3 = 0, 1, 2
 QERL_W_NVFP4, QERL_W_NF4 = 0, 1
 QERL_SCHEDULE_EXPONENTIAL, QERL_SCHEDULE_LINEAR, QERL_SCHEDULE_COSINE, QERL_SCHEDULE_LOGARITHMIC = 0, 1, 2, 3
 STATUS_NAMES = {0: "QERL_OK", 1: "QERL_ERR_INVALID_ARGUMENT", 2: "QERL_ERR_UNSUPPORTED_SHAPE",
@@ -160,6 +174,18 @@ def lib():
             L.qerl_lora_linear_noalloc.restype = ctypes.c_int
             L.qerl_lora_linear_noalloc.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp,
                                                    ctypes.c_int, ctypes.c_float, _vp, ctypes.c_int, _vp]
+            _c = ctypes.POINTER(KvCache)
+            L.qerl_rope_append_workspace_size.restype = ctypes.c_size_t
+            L.qerl_rope_append_workspace_size.argtypes = []
+            L.qerl_rope_append.restype = ctypes.c_int
+            L.qerl_rope_append.argtypes = [_c, _vp, _i64, ctypes.c_int, _vp, _i64, _vp, _i64, ctypes.c_int,
+                                           ctypes.c_int, _i64, _vp, _vp, _vp, ctypes.c_int, _vp, _i64, _vp, _i64,
+                                           _vp, ctypes.c_size_t, _vp]
+            L.qerl_decode_attention_workspace_size.restype = ctypes.c_size_t
+            L.qerl_decode_attention_workspace_size.argtypes = [_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+            L.qerl_decode_attention.restype = ctypes.c_int
+            L.qerl_decode_attention.argtypes = [_c, _vp, _i64, ctypes.c_int, _vp, ctypes.c_float, _vp, _i64, _vp,
+                                                _vp, ctypes.c_size_t, _vp]
             L.qerl_read_status.restype = ctypes.c_int
             L.qerl_read_status.argtypes = [_vp, _vp]
             _lib = L
@@ -417,6 +443,119 @@ def qerl_rmsnorm_noise(h, w_norm, Z, delta, out, stream=None) -> int:
                                     out.stride(0), _stream(stream))
 
 
+# ---- attention ----------------------------------------------------------------
+
+def _expect(name, t, dtype, dims=None):
+    """Raises unless t is a CUDA tensor of this type (and dimension count): a raw pointer of another
+    type would be misread."""
+    if not t.is_cuda or t.dtype != dtype or (dims is not None and t.dim() != dims):
+        raise TypeError(f"{name}: expected a {'' if dims is None else f'{dims}-d '}CUDA tensor of {dtype}, got "
+                        f"{tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _heads(name, t):
+    """Row stride of bf16 rows of heads [rows, heads, head_dim] whose heads lie side by side."""
+    _expect(name, t, torch.bfloat16, 3)
+    rows, heads, dim = t.shape
+    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {t.stride()}")
+    return t.stride(0) if rows > 1 else max(t.stride(0), heads * dim)
+
+
+def kv_cache(k, v, page_table, k_scale=None, v_scale=None):
+    """The qerl_kv_cache descriptor of pages k, v [num_pages, num_kv_heads, page_size, head_dim]
+    (bfloat16 or float8_e4m3fn), page_table [num_seqs, max_pages] int32 and, for float8_e4m3fn,
+    scales [num_kv_heads] float32 (or None).  It keeps the tensors alive."""
+    if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError("k: the cache holds bfloat16 or float8_e4m3fn")
+    _expect("k", k, k.dtype, 4)
+    _expect("v", v, k.dtype, 4)
+    _expect("page_table", page_table, torch.int32, 2)
+    if v.shape != k.shape or not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError("k and v: contiguous pages of one shape")
+    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table: the entries of a row must be contiguous")
+    c = KvCache()
+    c.num_pages, c.num_kv_heads, c.page_size, c.head_dim = k.shape
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is not None:
+            _expect(name, t, torch.float32, 1)
+            if t.numel() != c.num_kv_heads or not t.is_contiguous():
+                raise ValueError(f"{name}: one contiguous float per key-value head")
+    c.k, c.v = _p(k), _p(v)
+    c.dtype = QERL_E4M3 if k.dtype == torch.float8_e4m3fn else QERL_BF16
+    c.k_scale, c.v_scale = _p(k_scale), _p(v_scale)
+    c.page_table = _p(page_table)
+    c.num_seqs, c.max_pages = page_table.shape
+    c.ld_table = max(page_table.stride(0), c.max_pages)
+    c.tensors = (k, v, page_table, k_scale, v_scale)
+    return c
+
+
+def qerl_rope_append_workspace_size() -> int:
+    return lib().qerl_rope_append_workspace_size()
+
+
+def qerl_rope_append(cache, q, k, v, positions, inv_freq, q_out, k_out, workspace, seq_ids=None, stream=None) -> int:
+    """q [tokens, num_heads, head_dim] or None, k, v [tokens, num_kv_heads, head_dim] (bf16, strided rows),
+    positions [tokens] int32 (negative: padding), inv_freq [rot_dim / 2] float64, seq_ids [tokens] int32 or
+    None (token t is sequence t); q_out, k_out like q, k (may be them; k_out may be None with a cache).
+    cache None: rotation only (v may be None)."""
+    tokens, hk, d = k.shape
+    ldk = _heads("k", k)
+    h, ldq, ldqo, ldv, ldko = 0, 0, 0, 0, 0
+    if q is not None:
+        ldq, ldqo, h = _heads("q", q), _heads("q_out", q_out), q.shape[1]
+        if q.shape != q_out.shape or q.shape[0] != tokens or q.shape[2] != d:
+            raise ValueError("q, q_out: [tokens, num_heads, head_dim] of k's tokens and head_dim")
+    if v is not None:
+        ldv = _heads("v", v)
+        if v.shape != k.shape:
+            raise ValueError("v: k's shape")
+    if k_out is not None:
+        ldko = _heads("k_out", k_out)
+        if k_out.shape != k.shape:
+            raise ValueError("k_out: k's shape")
+    _expect("positions", positions, torch.int32, 1)
+    _expect("inv_freq", inv_freq, torch.float64, 1)
+    if seq_ids is not None:
+        _expect("seq_ids", seq_ids, torch.int32, 1)
+    for name, t in (("positions", positions), ("seq_ids", seq_ids)):
+        if t is not None and (t.numel() != tokens or not t.is_contiguous()):
+            raise ValueError(f"{name}: one contiguous entry per token")
+    if not inv_freq.is_contiguous():
+        raise ValueError("inv_freq: contiguous")
+    return lib().qerl_rope_append(cache, _p(q), ldq, h, _p(k), ldk, _p(v), ldv, hk, d, tokens, _p(seq_ids),
+                                  _p(positions), _p(inv_freq), 2 * inv_freq.numel(), _p(q_out), ldqo, _p(k_out), ldko,
+                                  _p(workspace), _nbytes(workspace), _stream(stream))
+
+
+def qerl_decode_attention_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return lib().qerl_decode_attention_workspace_size(int(num_seqs), int(num_heads), int(num_kv_heads), int(head_dim))
+
+
+def _lse(lse, rows, heads):
+    if lse is not None:
+        _expect("lse", lse, torch.float32, 2)
+        if lse.shape[0] != rows or lse.shape[1] != heads or not lse.is_contiguous():
+            raise ValueError("lse: contiguous [rows, num_heads]")
+
+
+def qerl_decode_attention(cache, q, lengths, scale, out, lse, workspace, stream=None) -> int:
+    """q, out [num_seqs, num_heads, head_dim] bf16 (strided rows), lengths [num_seqs] int32, lse [num_seqs,
+    num_heads] float32 or None: one new token per sequence over the cache's first lengths[s] rows."""
+    n, h, d = q.shape
+    ldq, ldo = _heads("q", q), _heads("out", out)
+    _expect("lengths", lengths, torch.int32, 1)
+    if out.shape != q.shape or n != cache.num_seqs or d != cache.head_dim:
+        raise ValueError("q, out: [num_seqs, num_heads, head_dim] of the cache")
+    if lengths.numel() != n or not lengths.is_contiguous():
+        raise ValueError("lengths: one contiguous entry per sequence")
+    _lse(lse, n, h)
+    return lib().qerl_decode_attention(cache, _p(q), ldq, h, _p(lengths), scale, _p(out), ldo, _p(lse), _p(workspace),
+                                       _nbytes(workspace), _stream(stream))
+
+
 def qerl_read_status(workspace, stream=None) -> int:
     return lib().qerl_read_status(_p(workspace), _stream(stream))
 
@@ -496,3 +635,22 @@ def lora_linear(x, wpacked, tensor_scale, n, z=None, A=None, B=None, alpha=0.0, 
     ws = workspace(qerl_lora_linear_workspace_size(m, n, k, r), x.device) if ws is None else ws
     check(qerl_lora_linear(x, wpacked, tensor_scale, z, A, B, alpha, y, ws), "qerl_lora_linear")
     return y
+
+
+def rope_append(cache, q, k, v, positions, inv_freq, seq_ids=None, ws=None):
+    """Rotated copies (q, k) of q and k, with k and v appended to the cache (see qerl_rope_append)."""
+    q_out, k_out = torch.empty_like(q, memory_format=torch.contiguous_format), torch.empty_like(
+        k, memory_format=torch.contiguous_format)
+    ws = workspace(qerl_rope_append_workspace_size(), k.device) if ws is None else ws
+    check(qerl_rope_append(cache, q, k, v, positions, inv_freq, q_out, k_out, ws, seq_ids), "qerl_rope_append")
+    return q_out, k_out
+
+
+def decode_attention(cache, q, lengths, scale, ws=None):
+    """(out, lse) of one new token per sequence over the cache (see qerl_decode_attention)."""
+    n, h, d = q.shape
+    out = torch.empty((n, h, d), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((n, h), dtype=torch.float32, device=q.device)
+    ws = workspace(qerl_decode_attention_workspace_size(n, h, cache.num_kv_heads, d), q.device) if ws is None else ws
+    check(qerl_decode_attention(cache, q, lengths, scale, out, lse, ws), "qerl_decode_attention")
+    return out, lse

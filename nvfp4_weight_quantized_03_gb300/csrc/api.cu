@@ -437,6 +437,131 @@ qerl_status qerl_lora_linear(const void* x, int64_t m, int64_t k, int64_t ldx, c
   return qerl_lora_linear_group(x, m, k, ldx, z, &d, 1, workspace, ws_bytes, stream);
 }
 
+namespace {
+
+// The checks of a cache descriptor and of rows of heads, shared by the attention calls.
+qerl_status check_heads(int num_heads, int num_kv_heads, int head_dim) {
+  if (num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0) return QERL_ERR_INVALID_ARGUMENT;
+  if (num_heads % num_kv_heads != 0) return QERL_ERR_INVALID_ARGUMENT;
+  if (head_dim != 64 && head_dim != 128) return QERL_ERR_UNSUPPORTED_SHAPE;
+  if (num_heads > 1024) return QERL_ERR_UNSUPPORTED_SHAPE;
+  return QERL_OK;
+}
+
+qerl_status check_rows(const void* rows, int64_t ld, int64_t width) {
+  if (ld < width) return QERL_ERR_INVALID_ARGUMENT;
+  if (!aligned(rows, 16) || ld % 8 != 0) return QERL_ERR_MISALIGNED;
+  return QERL_OK;
+}
+
+qerl_status check_cache(const qerl_kv_cache* c) {
+  if (c->dtype != QERL_BF16 && c->dtype != QERL_E4M3) return QERL_ERR_INVALID_ARGUMENT;
+  if (c->dtype == QERL_BF16 && (c->k_scale != nullptr || c->v_scale != nullptr)) return QERL_ERR_INVALID_ARGUMENT;
+  if (c->page_size < 1 || c->num_pages < 0 || c->num_seqs < 0 || c->max_pages < 0 || c->ld_table < c->max_pages)
+    return QERL_ERR_INVALID_ARGUMENT;
+  if (c->page_size > 65536 || c->num_pages > INT32_MAX || c->num_seqs > (1 << 20) ||
+      c->max_pages > INT32_MAX / c->page_size)
+    return QERL_ERR_UNSUPPORTED_SHAPE;
+  if (c->num_pages > 0 && (c->k == nullptr || c->v == nullptr)) return QERL_ERR_INVALID_ARGUMENT;
+  if (c->num_seqs > 0 && c->max_pages > 0 && c->page_table == nullptr) return QERL_ERR_INVALID_ARGUMENT;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return QERL_ERR_MISALIGNED;
+  if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) || !aligned(c->page_table, 4)) return QERL_ERR_MISALIGNED;
+  return QERL_OK;
+}
+
+}  // namespace
+
+size_t qerl_rope_append_workspace_size(void) { return kWsHeaderBytes; }
+
+qerl_status qerl_rope_append(const qerl_kv_cache* cache, const void* q, int64_t ldq, int num_heads, const void* k,
+                             int64_t ldk, const void* v, int64_t ldv, int num_kv_heads, int head_dim, int64_t tokens,
+                             const int32_t* seq_ids, const int32_t* positions, const double* inv_freq, int rot_dim,
+                             void* q_out, int64_t ldqo, void* k_out, int64_t ldko, void* workspace, size_t ws_bytes,
+                             void* stream) {
+  if (tokens < 0 || rot_dim < 0) return QERL_ERR_INVALID_ARGUMENT;
+  qerl_status st = check_heads(q != nullptr ? num_heads : num_kv_heads, num_kv_heads, head_dim);
+  if (st != QERL_OK) return st;
+  if (rot_dim > head_dim) return QERL_ERR_INVALID_ARGUMENT;
+  if (rot_dim % 16 != 0) return QERL_ERR_UNSUPPORTED_SHAPE;
+  if (cache != nullptr) {
+    if ((st = check_cache(cache)) != QERL_OK) return st;
+    if (cache->num_kv_heads != num_kv_heads || cache->head_dim != head_dim) return QERL_ERR_INVALID_ARGUMENT;
+  }
+  if (tokens == 0) return QERL_OK;
+  if (tokens > INT32_MAX) return QERL_ERR_UNSUPPORTED_SHAPE;
+  if (k == nullptr || positions == nullptr || (rot_dim > 0 && inv_freq == nullptr)) return QERL_ERR_INVALID_ARGUMENT;
+  if (cache != nullptr ? v == nullptr : k_out == nullptr) return QERL_ERR_INVALID_ARGUMENT;
+  if ((q == nullptr) != (q_out == nullptr)) return QERL_ERR_INVALID_ARGUMENT;
+  const int64_t q_width = static_cast<int64_t>(num_heads) * head_dim;
+  const int64_t kv_width = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (q != nullptr && (st = check_rows(q, ldq, q_width)) != QERL_OK) return st;
+  if (q != nullptr && (st = check_rows(q_out, ldqo, q_width)) != QERL_OK) return st;
+  if ((st = check_rows(k, ldk, kv_width)) != QERL_OK) return st;
+  if (cache != nullptr && (st = check_rows(v, ldv, kv_width)) != QERL_OK) return st;
+  if (k_out != nullptr && (st = check_rows(k_out, ldko, kv_width)) != QERL_OK) return st;
+  if ((q != nullptr && q == q_out && ldq != ldqo) || (k == k_out && ldk != ldko)) return QERL_ERR_INVALID_ARGUMENT;
+  if (!aligned(positions, 4) || !aligned(seq_ids, 4) || !aligned(inv_freq, 8)) return QERL_ERR_MISALIGNED;
+  if ((st = check_ws(workspace, ws_bytes, kWsHeaderBytes)) != QERL_OK) return st;
+  qerl::RopeAppendArgs a{};
+  a.cache = cache;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.tokens = tokens;
+  a.seq_ids = seq_ids;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.rot_dim = rot_dim;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.ldqo = ldqo;
+  a.ldko = ldko;
+  a.status = &static_cast<qerl::WsHeader*>(workspace)->status;
+  return qerl::launch_rope_append(a, as_stream(stream));
+}
+
+size_t qerl_decode_attention_workspace_size(int64_t num_seqs, int num_heads, int num_kv_heads, int head_dim) {
+  if (num_seqs < 0 || check_heads(num_heads, num_kv_heads, head_dim) != QERL_OK) return 0;
+  return qerl::decode_attention_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim);
+}
+
+qerl_status qerl_decode_attention(const qerl_kv_cache* cache, const void* q, int64_t ldq, int num_heads,
+                                  const int32_t* lengths, float scale, void* out, int64_t ldo, float* lse,
+                                  void* workspace, size_t ws_bytes, void* stream) {
+  if (cache == nullptr) return QERL_ERR_INVALID_ARGUMENT;
+  qerl_status st = check_heads(num_heads, cache->num_kv_heads, cache->head_dim);
+  if (st != QERL_OK) return st;
+  if ((st = check_cache(cache)) != QERL_OK) return st;
+  if (!std::isfinite(scale)) return QERL_ERR_INVALID_ARGUMENT;
+  if (cache->num_seqs == 0) return QERL_OK;
+  if (q == nullptr || lengths == nullptr || out == nullptr) return QERL_ERR_INVALID_ARGUMENT;
+  const int64_t width = static_cast<int64_t>(num_heads) * cache->head_dim;
+  if ((st = check_rows(q, ldq, width)) != QERL_OK || (st = check_rows(out, ldo, width)) != QERL_OK) return st;
+  if (!aligned(lengths, 4) || !aligned(lse, 4)) return QERL_ERR_MISALIGNED;
+  st = check_ws(workspace, ws_bytes,
+                qerl::decode_attention_workspace_bytes(cache->num_seqs, num_heads, cache->num_kv_heads,
+                                                       cache->head_dim));
+  if (st != QERL_OK) return st;
+  qerl::DecodeAttentionArgs a{};
+  a.cache = cache;
+  a.q = q;
+  a.ldq = ldq;
+  a.num_heads = num_heads;
+  a.lengths = lengths;
+  a.scale = scale;
+  a.out = out;
+  a.ldo = ldo;
+  a.lse = lse;
+  a.workspace = workspace;
+  return qerl::launch_decode_attention(a, as_stream(stream));
+}
+
 qerl_status qerl_read_status(void* workspace, void* stream) {
   if (workspace == nullptr) return QERL_ERR_INVALID_ARGUMENT;
   cudaStream_t s = as_stream(stream);

@@ -1,0 +1,704 @@
+// decode_attention.cu -- attention of one new token per sequence over the
+// paged key-value cache.
+//
+//   s_j = scale * q . k_j,  j < len;   o = sum_j exp(s_j - lse) v_j,
+//   lse = log sum_j exp(s_j)
+// for every query head; the G = num_heads / num_kv_heads query heads of a
+// key-value head read its rows together.  One pass: the running reference m
+// (a maximum in base-2 units), the sum l of 2^(s - m) and the unnormalised
+// output stay in registers.
+//
+// Bound: bytes of the cache (G multiply-adds per byte).  The work is cut by
+// bytes, not by sequences: all (sequence, key-value head, key tile) units in
+// order form one line that the resident CTAs share out evenly, computed on the
+// device from the lengths, so ragged batches balance and no host copy of the
+// lengths is needed.  A CTA whose stretch begins or ends inside a (sequence,
+// head) leaves its partial (m, l, o) in the workspace; the last of that
+// head's CTAs to arrive joins the partials in CTA order (the result does not
+// depend on the arrival order).
+//
+// A warp owns kKeys keys of every tile and its own ring of cp.async stages, so
+// the key loop has no CTA barrier.  Products run on mma.sync.m16n8k16 with the
+// keys (then the head's elements) as the 16-row operand and the query heads as
+// the 8 columns: up to 8 heads fill the tile, where heads as rows would leave
+// half of it empty.  A tcgen05 tile needs 64 or 128 rows, which G <= 16 heads
+// do not fill.
+//
+// Roundings: scores, m, l and o are fp32.  bf16 cache: 2^(s - m) enters the
+// value product as bf16 high + bf16 low (16 bits), which costs 8 more MMAs per
+// 16 keys where the memory is the bound anyway.  E4M3 cache: keys and values
+// are exact in fp16, q is scaled by a power of two per head to fp16 (exact
+// unless an element is 2^14 below the head's largest), 2^(s - m) is rounded to
+// fp16 (half a step 2^-11).
+#include "qerl_internal.h"
+#include "qerl_ptx.cuh"
+
+#include <atomic>
+#include <cuda_bf16.h>
+
+namespace qerl {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxCtas = 1024;
+// How far (base 2) a score may pass the reference m before m moves: 2^8 keeps
+// the fp32 sums and the fp16 probabilities in range, and most steps then skip
+// the maximum's reduction and the rescaling.
+constexpr float kSlack = 8.0f;
+
+struct DecodeParams {
+  const __nv_bfloat16* q;
+  int64_t ldq;
+  const uint8_t *kp, *vp;
+  const float *k_scale, *v_scale;
+  const int* table;
+  int64_t ld_table, num_pages;
+  int page_size, page_shift;  // shift < 0: not a power of two
+  int64_t capacity;           // max_pages * page_size
+  int num_seqs, heads, kv_heads, group;
+  int zgroups, zheads;  // a key-value head's query heads in zgroups parts of zheads
+  const int* lengths;
+  float scale_log2;
+  __nv_bfloat16* out;
+  int64_t ldo;
+  float* lse;
+  float* part;         // [CTA][2][NT * 8][D + 2]
+  unsigned* counters;  // [num_seqs * kv_heads * zgroups], zero between calls
+  int* status;
+};
+
+template <int D, bool kFp8, int NT>
+struct Shape {
+  static constexpr int kRow = D * (kFp8 ? 1 : 2);  // bytes of a cache row
+  static constexpr int kChunks = kRow / 16;
+  static constexpr int kKeys = kRow >= 256 ? 16 : 32;  // per warp and stage
+  static constexpr int kTile = kKeys * kWarps;
+  static constexpr int kStage = 2 * kKeys * kRow;  // K then V
+  static constexpr int kStages = NT == 1 ? (kStage > 4096 ? 3 : 5) : (kStage > 4096 ? 2 : 4);
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kOStride = D + 4;  // columns 2c, 2c+1 of 8 rows fall in 32 banks
+  static constexpr int kJoin = kWarps * NT * 8 * kOStride * 4;
+  static constexpr int kSmem = kRing + kJoin;
+  static constexpr int kPartRow = D + 2;
+};
+
+// Physical 16-byte chunk of a row in shared memory: 8 rows of one logical
+// chunk fall into 8 different bank groups.
+template <int kRow>
+__device__ __forceinline__ uint32_t at_chunk(int row, int chunk) {
+  if (kRow == 64) return static_cast<uint32_t>(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+  return static_cast<uint32_t>(row * kRow + ((chunk ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t o;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(o) : "r"(v));
+  return o;
+}
+template <bool kFp8>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (kFp8)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Four E4M3 bytes -> two f16x2 words (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A place on the line of work units: key tile `tile` of `tiles` of (sequence
+// b, part hz of its kv_heads * zgroups).
+struct Cursor {
+  int b, hz, tile, tiles, len;
+};
+
+__device__ __forceinline__ int live_length(const DecodeParams& p, int b) {
+  const int n = p.lengths[b];
+  return n < 0 ? 0 : n > p.capacity ? static_cast<int>(p.capacity) : n;
+}
+
+template <int kTile>
+__device__ __forceinline__ void advance(const DecodeParams& p, Cursor& c) {
+  if (++c.tile < c.tiles) return;
+  c.tile = 0;
+  if (++c.hz < p.kv_heads * p.zgroups) return;
+  c.hz = 0;
+  while (++c.b < p.num_seqs) {
+    c.len = live_length(p, c.b);
+    if (c.len > 0) {
+      c.tiles = (c.len - 1) / kTile + 1;
+      return;
+    }
+  }
+}
+
+template <int D, bool kFp8, int NT>
+__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams p) {
+  using S = Shape<D, kFp8, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long red[kWarps];
+  __shared__ long long found[2];
+  __shared__ float ml[kWarps][NT * 8][2];
+  __shared__ unsigned arrived;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hz_all = p.kv_heads * p.zgroups;
+  const uint32_t ring = smem_u32(smem) + warp * (S::kStages * S::kStage);
+  float* o_join = reinterpret_cast<float*>(smem + S::kRing);
+  const float kInf = __int_as_float(0x7f800000);
+
+  // ---- this CTA's stretch of the line ---------------------------------------
+  auto units = [&](int b) -> long long {
+    const int n = live_length(p, b);
+    return n > 0 ? static_cast<long long>((n - 1) / S::kTile + 1) * hz_all : 0;
+  };
+  long long total = 0;
+  for (int b = tid; b < p.num_seqs; b += kThreads) {
+    const int n = p.lengths[b];
+    if (n < 0 || n > p.capacity) record_error(p.status, QERL_ERR_RANGE);
+    total += units(b);
+  }
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) total += __shfl_xor_sync(~0u, total, i);
+  if (lane == 0) red[warp] = total;
+  // A sequence without keys: zeros and lse = -inf, shared out over the CTAs.
+  for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
+    if (live_length(p, b) > 0) continue;
+    for (int i = tid; i < p.heads * D / 8; i += kThreads)
+      *reinterpret_cast<uint4*>(p.out + b * p.ldo + i * 8) = make_uint4(0, 0, 0, 0);
+    if (p.lse != nullptr)
+      for (int i = tid; i < p.heads; i += kThreads) p.lse[static_cast<int64_t>(b) * p.heads + i] = -kInf;
+  }
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) total += red[i];
+  // No CTA without a unit between two that have one: the join counts the CTAs of a range.
+  const long long ctas = total < gridDim.x ? total : gridDim.x;
+  if (blockIdx.x >= ctas) return;
+  auto stretch = [&](long long c) -> long long { return total * c / ctas; };
+  const long long begin = stretch(blockIdx.x), end = stretch(blockIdx.x + 1);
+  // The sequence that holds unit `begin`.
+  long long base = 0;
+  for (int b0 = 0;; b0 += kThreads) {
+    const int b = b0 + tid;
+    const long long mine = b < p.num_seqs ? units(b) : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const long long up = __shfl_up_sync(~0u, incl, i);
+      if (lane >= i) incl += up;
+    }
+    __syncthreads();
+    if (lane == 31) red[warp] = incl;
+    __syncthreads();
+    long long before = base, all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) before += red[i];
+      all += red[i];
+    }
+    incl += before;
+    if (begin < base + all) {  // uniform: in this block of sequences
+      if (incl - mine <= begin && begin < incl) {
+        found[0] = b;
+        found[1] = begin - (incl - mine);
+      }
+      __syncthreads();
+      break;
+    }
+    base += all;
+  }
+  Cursor cur;
+  cur.b = static_cast<int>(found[0]);
+  cur.len = live_length(p, cur.b);
+  cur.tiles = (cur.len - 1) / S::kTile + 1;
+  cur.hz = static_cast<int>(found[1] / cur.tiles);
+  cur.tile = static_cast<int>(found[1] - static_cast<long long>(cur.hz) * cur.tiles);
+
+  // ---- loads ----------------------------------------------------------------
+  // Byte offset of this lane's key row of the cursor's tile; -1 past the length
+  // or for a page number outside the cache (the row then reads as zeros).
+  auto lookup = [&](const Cursor& c) -> int64_t {
+    const int64_t key = static_cast<int64_t>(c.tile) * S::kTile + warp * S::kKeys + (lane & (S::kKeys - 1));
+    if (key >= c.len) return -1;
+    const int pi = p.page_shift >= 0 ? static_cast<int>(key) >> p.page_shift : static_cast<int>(key) / p.page_size;
+    const int64_t page = p.table[c.b * p.ld_table + pi];
+    if (page < 0 || page >= p.num_pages) {
+      record_error(p.status, QERL_ERR_RANGE);
+      return -1;
+    }
+    return ((page * p.kv_heads + c.hz / p.zgroups) * p.page_size + (key - static_cast<int64_t>(pi) * p.page_size)) *
+           S::kRow;
+  };
+  auto issue = [&](int stage, int64_t off) {
+    const uint32_t base_a = ring + stage * S::kStage;
+    constexpr int kPer = S::kKeys * S::kChunks / 32;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int row = (i * 32 + lane) / S::kChunks, chunk = lane % S::kChunks;
+      const int64_t o = __shfl_sync(~0u, off, row);
+      const uint32_t dst = base_a + at_chunk<S::kRow>(row, chunk);
+      const int64_t from = o < 0 ? 0 : o + chunk * 16;
+      cp_async_16(dst, p.kp + from, o < 0 ? 0 : 16);
+      cp_async_16(dst + S::kKeys * S::kRow, p.vp + from, o < 0 ? 0 : 16);
+    }
+  };
+  Cursor ahead = cur;
+  long long to_load = end - begin;
+  int64_t off = lookup(ahead);
+#pragma unroll
+  for (int s = 0; s < S::kStages - 1; ++s) {
+    if (to_load > 0) {
+      issue(s, off);
+      if (--to_load > 0) {
+        advance<S::kTile>(p, ahead);
+        off = lookup(ahead);
+      }
+    }
+    cp_async_commit();
+  }
+
+  // ---- the key loop ----------------------------------------------------------
+  constexpr int KS = D / 16;  // 16-element steps of a head
+  constexpr int MT = S::kKeys / 16;
+  const int t4 = lane & 3, g8 = lane >> 2;
+  uint32_t qf[NT][KS][2];
+  float mult[NT][2];
+  float o[NT][KS][4];
+  float m[NT][2], l[NT][2];
+  bool fresh = true;
+  int stage = 0;
+  long long seg_begin = begin - cur.tile;  // first unit of the segment
+  for (long long u = begin; u < end; ++u) {
+    const int kvh = cur.hz / p.zgroups, z = cur.hz - kvh * p.zgroups;
+    const int head0 = kvh * p.group + z * p.zheads;
+    const int nheads = min(p.zheads, p.group - z * p.zheads);
+    if (fresh) {
+      fresh = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int h = nt * 8 + g8;
+        const __nv_bfloat16* src = p.q + cur.b * p.ldq + static_cast<int64_t>(head0 + h) * D;
+        if (!kFp8) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            qf[nt][ks][0] = h < nheads ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * t4) : 0;
+            qf[nt][ks][1] = h < nheads ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + 2 * t4) : 0;
+          }
+          mult[nt][0] = mult[nt][1] = p.scale_log2;
+        } else {
+          // elements 4 t4 .. 4 t4 + 3 of every 16 (the order the E4M3 bytes of a key arrive in)
+          float amax = 0.0f;
+          uint2 raw[KS];
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            raw[ks] = h < nheads ? *reinterpret_cast<const uint2*>(src + ks * 16 + 4 * t4) : make_uint2(0, 0);
+            amax = fmaxf(amax, fmaxf(fabsf(bf_lo(raw[ks].x)), fabsf(bf_hi(raw[ks].x))));
+            amax = fmaxf(amax, fmaxf(fabsf(bf_lo(raw[ks].y)), fabsf(bf_hi(raw[ks].y))));
+          }
+          amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
+          // 2^-e for amax in [2^e, 2^(e+1)), kept in the normal range
+          int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+          e = amax == 0.0f || e > 127 ? 0 : e < -126 ? -126 : e > 126 ? 126 : e;
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            qf[nt][ks][0] = pack_f16(bf_lo(raw[ks].x) * down, bf_hi(raw[ks].x) * down);
+            qf[nt][ks][1] = pack_f16(bf_lo(raw[ks].y) * down, bf_hi(raw[ks].y) * down);
+          }
+          const float f = p.scale_log2 * (p.k_scale != nullptr ? p.k_scale[kvh] : 1.0f) * up;
+          mult[nt][0] = __shfl_sync(~0u, f, 8 * t4);      // head 2 t4
+          mult[nt][1] = __shfl_sync(~0u, f, 8 * t4 + 4);  // head 2 t4 + 1
+        }
+        m[nt][0] = m[nt][1] = -kInf;
+        l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[nt][ks][i] = 0.0f;
+      }
+    }
+    // Refill the stage the previous step emptied, then wait for this one.
+    {
+      const int fill = stage == 0 ? S::kStages - 1 : stage - 1;
+      if (to_load > 0) {
+        issue(fill, off);
+        if (--to_load > 0) {
+          advance<S::kTile>(p, ahead);
+          off = lookup(ahead);
+        }
+      }
+      cp_async_commit();
+      cp_async_wait_group<S::kStages - 1>();
+      __syncwarp();
+    }
+    const uint32_t k_a = ring + stage * S::kStage, v_a = k_a + S::kKeys * S::kRow;
+
+    // scores: keys x heads
+    float x[NT][MT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[nt][mt][i] = 0.0f;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int c2 = 0; c2 < S::kChunks / 2; ++c2) {
+        uint32_t r[4];
+        ldsm4(k_a + at_chunk<S::kRow>(mt * 16 + (lane & 15), 2 * c2 + (lane >> 4)), r);
+        if (!kFp8) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816<false>(x[nt][mt], r, qf[nt][c2][0], qf[nt][c2][1]);
+        } else {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t a[4];
+            e4m3x4_to_f16(r[2 * half], a[0], a[2]);
+            e4m3x4_to_f16(r[2 * half + 1], a[1], a[3]);
+            const int ks = (2 * c2 + half) % KS;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<true>(x[nt][mt], a, qf[nt][ks][0], qf[nt][ks][1]);
+          }
+        }
+      }
+    }
+    const int64_t key0 = static_cast<int64_t>(cur.tile) * S::kTile + warp * S::kKeys;
+    const int keys_left = static_cast<int>(cur.len - key0 < S::kKeys ? cur.len - key0 : S::kKeys);  // may be <= 0
+    bool grow = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float top[2] = {-kInf, -kInf};
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v = x[nt][mt][i] * mult[nt][i & 1];
+          if (mt * 16 + g8 + (i >> 1) * 8 >= keys_left) v = -kInf;
+          x[nt][mt][i] = v;
+          top[i & 1] = fmaxf(top[i & 1], v);
+        }
+      grow |= top[0] > m[nt][0] + kSlack || top[1] > m[nt][1] + kSlack;
+    }
+    if (__any_sync(~0u, grow)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float top = m[nt][c];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(x[nt][mt][c], x[nt][mt][c + 2]));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+          const float f = m[nt][c] == -kInf ? 1.0f : ex2(m[nt][c] - top);  // no sum yet (or NaN, kept) at -inf
+          m[nt][c] = top;
+          l[nt][c] *= f;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            o[nt][ks][c] *= f;
+            o[nt][ks][c + 2] *= f;
+          }
+        }
+    }
+    // probabilities as the 8-column operand: heads x keys after the transpose
+    uint32_t ph[NT][MT][2], pl[NT][MT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float m0 = m[nt][0] == -kInf ? 0.0f : m[nt][0], m1 = m[nt][1] == -kInf ? 0.0f : m[nt][1];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float a = ex2(x[nt][mt][2 * r] - m0), b = ex2(x[nt][mt][2 * r + 1] - m1);
+          l[nt][0] += a;
+          l[nt][1] += b;
+          if (kFp8) {
+            ph[nt][mt][r] = transpose8(pack_f16(a, b));
+          } else {
+            const uint32_t hi = pack_bf16(a, b);
+            ph[nt][mt][r] = transpose8(hi);
+            pl[nt][mt][r] = transpose8(pack_bf16(a - bf_lo(hi), b - bf_hi(hi)));
+          }
+        }
+    }
+    // o (elements x heads) += V^T (elements x keys) P^T (keys x heads)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int c2 = 0; c2 < S::kChunks / 2; ++c2) {
+        uint32_t r[4];
+        if (!kFp8) {
+          ldsm4_t(v_a + at_chunk<S::kRow>(mt * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * c2 + ((lane >> 3) & 1)), r);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816<false>(o[nt][c2], r, ph[nt][mt][0], ph[nt][mt][1]);
+            mma16816<false>(o[nt][c2], r, pl[nt][mt][0], pl[nt][mt][1]);
+          }
+        } else {
+          // A 16-bit unit holds elements 2j, 2j+1 of one key: unzip the pair of
+          // keys into one word per element (rows j and j + 8 of the tile).
+          ldsm4_t(v_a + at_chunk<S::kRow>(mt * 16 + (lane & 15), 2 * c2 + (lane >> 4)), r);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t a[4];
+            e4m3x4_to_f16(__byte_perm(r[2 * half], 0, 0x3120), a[0], a[1]);
+            e4m3x4_to_f16(__byte_perm(r[2 * half + 1], 0, 0x3120), a[2], a[3]);
+            const int ks = (2 * c2 + half) % KS;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<true>(o[nt][ks], a, ph[nt][mt][0], ph[nt][mt][1]);
+          }
+        }
+      }
+    }
+    __syncwarp();  // every lane has read the stage before it is refilled
+    stage = stage + 1 == S::kStages ? 0 : stage + 1;
+
+    // ---- end of a (sequence, head) or of the stretch -------------------------
+    if (cur.tile + 1 == cur.tiles || u + 1 == end) {
+      const long long seg_end = seg_begin + cur.tiles;
+      const bool whole = seg_begin >= begin && seg_end <= end;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float s = l[nt][c];
+          s += __shfl_xor_sync(~0u, s, 4);
+          s += __shfl_xor_sync(~0u, s, 8);
+          s += __shfl_xor_sync(~0u, s, 16);
+          const int h = nt * 8 + 2 * t4 + c;
+          if (g8 == 0) {
+            ml[warp][h][0] = m[nt][c];
+            ml[warp][h][1] = s;
+          }
+          float* dst = o_join + (warp * NT * 8 + h) * S::kOStride;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            dst[ks * 16 + (kFp8 ? 2 * g8 : g8)] = o[nt][ks][c];
+            dst[ks * 16 + (kFp8 ? 2 * g8 + 1 : g8 + 8)] = o[nt][ks][c + 2];
+          }
+        }
+      __syncthreads();
+      const float vs = kFp8 && p.v_scale != nullptr ? p.v_scale[kvh] : 1.0f;
+      auto finish = [&](int h, int d, float top, float sum, const float4& v) {
+        const int head = head0 + h;
+        const float f = sum == 0.0f ? 0.0f : vs / sum;
+        uint2 w;
+        w.x = pack_bf16(v.x * f, v.y * f);
+        w.y = pack_bf16(v.z * f, v.w * f);
+        *reinterpret_cast<uint2*>(p.out + cur.b * p.ldo + static_cast<int64_t>(head) * D + d) = w;
+        if (d == 0 && p.lse != nullptr)
+          p.lse[static_cast<int64_t>(cur.b) * p.heads + head] =
+              sum == 0.0f ? -kInf : (top + log2f(sum)) * 0.69314718055994530942f;
+      };
+      constexpr int64_t kSlot = static_cast<int64_t>(NT * 8) * S::kPartRow;
+      float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (seg_begin <= begin ? 0 : 1)) * kSlot;
+      for (int i = tid; i < nheads * (D / 4); i += kThreads) {
+        const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+        float top = -kInf;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][h][0]);
+        float sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          // a warp without a finite score has sums of 0 (or NaN, which stays)
+          const float f = ml[w][h][0] == -kInf ? 1.0f : ex2(ml[w][h][0] - top);
+          const float4 v = *reinterpret_cast<const float4*>(o_join + (w * NT * 8 + h) * S::kOStride + d);
+          sum += f * ml[w][h][1];
+          acc.x += f * v.x;
+          acc.y += f * v.y;
+          acc.z += f * v.z;
+          acc.w += f * v.w;
+        }
+        if (whole) {
+          finish(h, d, top, sum, acc);
+        } else {
+          __stcg(reinterpret_cast<float4*>(slot + h * D + d), acc);
+          if (d == 0) __stcg(reinterpret_cast<float2*>(slot + NT * 8 * D + 2 * h), make_float2(top, sum));
+        }
+      }
+      if (!whole) {
+        // The CTAs that hold units of this segment: those of its first and last unit.
+        auto owner = [&](long long unit) -> int {  // the largest c with stretch(c) <= unit
+          long long c = (unit * ctas) / total;
+          while (stretch(c + 1) <= unit) ++c;
+          while (stretch(c) > unit) --c;
+          return static_cast<int>(c);
+        };
+        const int c0 = owner(seg_begin), c1 = owner(seg_end - 1);
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+          unsigned* counter = p.counters + static_cast<int64_t>(cur.b) * hz_all + cur.hz;
+          const unsigned before = atomicAdd(counter, 1u);
+          arrived = before;
+          if (before == static_cast<unsigned>(c1 - c0)) *counter = 0;  // ready for the next call
+          __threadfence();
+        }
+        __syncthreads();
+        if (arrived == static_cast<unsigned>(c1 - c0)) {
+          for (int i = tid; i < nheads * (D / 4); i += kThreads) {
+            const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+            float top = -kInf, sum = 0.0f;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) {
+              const float* s = p.part + (2 * static_cast<int64_t>(c) + (c == c0 && stretch(c) < seg_begin ? 1 : 0)) * kSlot;
+              const float2 e = __ldcg(reinterpret_cast<const float2*>(s + NT * 8 * D + 2 * h));
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(s + h * D + d));
+              const float up = fmaxf(top, e.x);
+              const float fa = top == -kInf ? 1.0f : ex2(top - up), fb = e.x == -kInf ? 1.0f : ex2(e.x - up);
+              top = up;
+              sum = sum * fa + e.y * fb;
+              acc.x = acc.x * fa + v.x * fb;
+              acc.y = acc.y * fa + v.y * fb;
+              acc.z = acc.z * fa + v.z * fb;
+              acc.w = acc.w * fa + v.w * fb;
+            }
+            finish(h, d, top, sum, acc);
+          }
+        }
+      }
+      __syncthreads();  // the join buffer is free again
+      fresh = true;
+      seg_begin = seg_end;
+    }
+    if (u + 1 < end) advance<S::kTile>(p, cur);
+  }
+  cp_async_wait_group<0>();
+}
+
+template <int D, bool kFp8, int NT>
+qerl_status launch(const DecodeParams& p, int sms, int dev, cudaStream_t s) {
+  using S = Shape<D, kFp8, NT>;
+  static std::atomic<uint64_t> ready{0};  // one bit per device: the attribute belongs to the device's function
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if ((ready.load() & bit) == 0) {
+    if (cudaFuncSetAttribute(decode_kernel<D, kFp8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) !=
+        cudaSuccess)
+      return QERL_ERR_CUDA;
+    ready.fetch_or(bit);
+  }
+  int64_t grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+  const int64_t most =
+      static_cast<int64_t>(p.num_seqs) * p.kv_heads * p.zgroups * ((p.capacity + S::kTile - 1) / S::kTile);
+  if (most < grid) grid = most > 0 ? most : 1;
+  decode_kernel<D, kFp8, NT><<<static_cast<unsigned>(grid), kThreads, S::kSmem, s>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+struct Split {
+  int zgroups, zheads, tiles;
+};
+// A key-value head's query heads: up to 8 in one column tile, up to 16 in two;
+// more are cut into equal parts that read the cache once each.
+Split split_heads(int group) {
+  Split s;
+  s.zgroups = (group + 15) / 16;
+  s.zheads = (group + s.zgroups - 1) / s.zgroups;
+  s.zgroups = (group + s.zheads - 1) / s.zheads;
+  s.tiles = s.zheads > 8 ? 2 : 1;
+  return s;
+}
+
+size_t counter_bytes(int64_t num_seqs, int num_kv_heads, const Split& s) {
+  return align_up(static_cast<size_t>(num_seqs) * num_kv_heads * s.zgroups * sizeof(unsigned), 256);
+}
+
+}  // namespace
+
+size_t decode_attention_workspace_bytes(int64_t num_seqs, int num_heads, int num_kv_heads, int head_dim) {
+  const Split s = split_heads(num_heads / num_kv_heads);
+  return kWsHeaderBytes + counter_bytes(num_seqs, num_kv_heads, s) +
+         static_cast<size_t>(kMaxCtas) * 2 * (s.tiles * 8) * (head_dim + 2) * sizeof(float);
+}
+
+qerl_status launch_decode_attention(const DecodeAttentionArgs& a, cudaStream_t s) {
+  const qerl_kv_cache& c = *a.cache;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return QERL_ERR_CUDA;
+  const Split sp = split_heads(a.num_heads / c.num_kv_heads);
+  DecodeParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.ldq = a.ldq;
+  p.kp = static_cast<const uint8_t*>(c.k);
+  p.vp = static_cast<const uint8_t*>(c.v);
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.table = c.page_table;
+  p.ld_table = c.ld_table;
+  p.num_pages = c.num_pages;
+  p.page_size = c.page_size;
+  p.page_shift = (c.page_size & (c.page_size - 1)) == 0 ? __builtin_ctz(c.page_size) : -1;
+  p.capacity = c.max_pages * c.page_size;
+  p.num_seqs = static_cast<int>(c.num_seqs);
+  p.heads = a.num_heads;
+  p.kv_heads = c.num_kv_heads;
+  p.group = a.num_heads / c.num_kv_heads;
+  p.zgroups = sp.zgroups;
+  p.zheads = sp.zheads;
+  p.lengths = a.lengths;
+  p.scale_log2 = a.scale * 1.44269504088896340736f;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.ldo = a.ldo;
+  p.lse = a.lse;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.status = &reinterpret_cast<WsHeader*>(ws)->status;
+  p.counters = reinterpret_cast<unsigned*>(ws + kWsHeaderBytes);
+  p.part = reinterpret_cast<float*>(ws + kWsHeaderBytes + counter_bytes(c.num_seqs, c.num_kv_heads, sp));
+  const bool f8 = c.dtype == QERL_E4M3;
+  const bool one = sp.tiles == 1;
+  if (c.head_dim == 128) {
+    if (f8) return one ? launch<128, true, 1>(p, sms, dev, s) : launch<128, true, 2>(p, sms, dev, s);
+    return one ? launch<128, false, 1>(p, sms, dev, s) : launch<128, false, 2>(p, sms, dev, s);
+  }
+  if (f8) return one ? launch<64, true, 1>(p, sms, dev, s) : launch<64, true, 2>(p, sms, dev, s);
+  return one ? launch<64, false, 1>(p, sms, dev, s) : launch<64, false, 2>(p, sms, dev, s);
+}
+
+}  // namespace qerl

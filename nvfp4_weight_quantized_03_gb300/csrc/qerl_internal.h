@@ -123,6 +123,56 @@ struct BackwardArgs {
 size_t backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int r);
 qerl_status launch_lora_linear_backward(const BackwardArgs& b, cudaStream_t s);
 
+// kv_cache.cu: rotation of q and k with the append to the paged cache.
+struct RopeAppendArgs {
+  const qerl_kv_cache* cache;  // null: rotation only
+  const void *q, *k, *v;       // bf16 rows
+  int64_t ldq, ldk, ldv;
+  int num_heads, num_kv_heads, head_dim;
+  int64_t tokens;
+  const int *seq_ids, *positions;
+  const double* inv_freq;
+  int rot_dim;
+  void *q_out, *k_out;
+  int64_t ldqo, ldko;
+  int* status;
+};
+qerl_status launch_rope_append(const RopeAppendArgs& a, cudaStream_t s);
+
+// decode_attention.cu: one new token per sequence over the paged cache.
+struct DecodeAttentionArgs {
+  const qerl_kv_cache* cache;
+  const void* q;
+  int64_t ldq;
+  int num_heads;
+  const int* lengths;
+  float scale;
+  void* out;
+  int64_t ldo;
+  float* lse;
+  void* workspace;
+};
+size_t decode_attention_workspace_bytes(int64_t num_seqs, int num_heads, int num_kv_heads, int head_dim);
+qerl_status launch_decode_attention(const DecodeAttentionArgs& a, cudaStream_t s);
+
+// prompt_attention.cu: causal attention of packed whole prompts.
+struct PromptAttentionArgs {
+  const void *q, *k, *v;
+  int64_t ldq, ldk, ldv;
+  int64_t tokens;
+  int num_heads, num_kv_heads, head_dim;
+  const int* cu_seqlens;
+  int64_t num_seqs;
+  float scale;
+  void* out;
+  int64_t ldo;
+  float* lse;
+  void* workspace;
+};
+size_t prompt_attention_workspace_bytes(int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
+                                        int64_t num_seqs);
+qerl_status launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t s);
+
 // api.cu: the argument checks shared by every linear entry point.
 qerl_status prepare_linear_group(const void* x, int64_t m, int64_t k, int64_t ldx, const float* z,
                                  const qerl_linear_desc* linears, int count, LinearArgs* out, bool* empty);
