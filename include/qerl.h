@@ -549,6 +549,35 @@ QERL_API qerl_status qerl_decode_attention(const qerl_kv_cache* cache, const voi
                                            const int32_t* lengths, float scale, void* out, int64_t ldo, float* lse,
                                            void* workspace, size_t ws_bytes, void* stream);
 
+/* Causal attention of packed whole prompts: sequence s holds the rows
+ * cu_seqlens[s] .. cu_seqlens[s + 1] - 1 of q, k, v, and row i attends to rows
+ * j <= i of its sequence:
+ *   s_ij = scale * q_i . k_j;  lse_i = ln sum_j exp(s_ij);
+ *   out_i = sum_j exp(s_ij - lse_i) v_j.
+ *   q, out   bf16 rows of num_heads * head_dim, strides ldq, ldo.
+ *   k, v     bf16 rows of num_kv_heads * head_dim, strides ldk, ldv.
+ *   cu_seqlens  device int32 [num_seqs + 1], not decreasing, within 0 ..
+ *            tokens.  A sequence that breaks this records QERL_ERR_RANGE and
+ *            is skipped; the other sequences' rows may then be skipped too.
+ *            Empty sequences are allowed; rows of no sequence are left as they
+ *            are in out and lse.
+ *   lse      float [tokens][num_heads] or NULL.
+ * q, k, v, out 16-byte aligned, strides multiples of 8 and below 2^36; tokens
+ * <= 2^30, num_seqs <= 2^20, num_heads * (tokens / 256 + min(num_seqs, tokens))
+ * <= INT32_MAX.  out overlaps none of q, k, v.  Rows that a row does not attend
+ * to do not change it, whatever they hold; a row with every s_ij = -inf gives
+ * out = 0, lse = -inf.  Scores, softmax and sums are fp32; the softmax weights
+ * are rounded to bf16 for the product with v.
+ * workspace >= qerl_prompt_attention_workspace_size(), 256-byte aligned,
+ * zero-filled before its first use (status word only). */
+QERL_API size_t qerl_prompt_attention_workspace_size(int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
+                                                     int64_t num_seqs);
+QERL_API qerl_status qerl_prompt_attention(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                                           int64_t ldv, int64_t tokens, int num_heads, int num_kv_heads,
+                                           int head_dim, const int32_t* cu_seqlens, int64_t num_seqs, float scale,
+                                           void* out, int64_t ldo, float* lse, void* workspace, size_t ws_bytes,
+                                           void* stream);
+
 /* Synchronizes `stream`, returns the status word recorded in `workspace` by
  * the kernels of earlier calls (QERL_OK if none failed) and resets it to
  * QERL_OK.  A failing CUDA call returns QERL_ERR_CUDA. */

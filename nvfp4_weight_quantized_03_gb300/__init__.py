@@ -21,6 +21,7 @@ The functions named like the C entry points take torch tensors:
     qerl_lora_linear_group(x, z, [(wpacked, tensor_scale, A, B, alpha, y), ...], workspace)
     qerl_rope_append(cache, q, k, v, positions, inv_freq, q_out, k_out, workspace, seq_ids)
     qerl_decode_attention(cache, q, lengths, scale, out, lse, workspace)
+    qerl_prompt_attention(q, k, v, cu_seqlens, scale, out, lse, workspace)
     qerl_read_status(workspace)
 
 `kv_cache()` builds the descriptor of a paged key-value cache once, and
@@ -52,6 +53,7 @@ __all__ = [
     "quantize", "lora_linear", "workspace",
     "QERL_E4M3", "KvCache", "kv_cache", "qerl_rope_append", "qerl_rope_append_workspace_size",
     "qerl_decode_attention", "qerl_decode_attention_workspace_size", "rope_append", "decode_attention",
+    "qerl_prompt_attention", "qerl_prompt_attention_workspace_size", "prompt_attention",
 ]
 
 class LinearDesc(ctypes.Structure):
@@ -186,6 +188,12 @@ def lib():
             L.qerl_decode_attention.restype = ctypes.c_int
             L.qerl_decode_attention.argtypes = [_c, _vp, _i64, ctypes.c_int, _vp, ctypes.c_float, _vp, _i64, _vp,
                                                 _vp, ctypes.c_size_t, _vp]
+            L.qerl_prompt_attention_workspace_size.restype = ctypes.c_size_t
+            L.qerl_prompt_attention_workspace_size.argtypes = [_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64]
+            L.qerl_prompt_attention.restype = ctypes.c_int
+            L.qerl_prompt_attention.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, ctypes.c_int, ctypes.c_int,
+                                                ctypes.c_int, _vp, _i64, ctypes.c_float, _vp, _i64, _vp, _vp,
+                                                ctypes.c_size_t, _vp]
             L.qerl_read_status.restype = ctypes.c_int
             L.qerl_read_status.argtypes = [_vp, _vp]
             _lib = L
@@ -556,6 +564,30 @@ def qerl_decode_attention(cache, q, lengths, scale, out, lse, workspace, stream=
                                        _nbytes(workspace), _stream(stream))
 
 
+def qerl_prompt_attention_workspace_size(tokens: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                         num_seqs: int) -> int:
+    return lib().qerl_prompt_attention_workspace_size(int(tokens), int(num_heads), int(num_kv_heads), int(head_dim),
+                                                      int(num_seqs))
+
+
+def qerl_prompt_attention(q, k, v, cu_seqlens, scale, out, lse, workspace, stream=None) -> int:
+    """q, out [tokens, num_heads, head_dim], k, v [tokens, num_kv_heads, head_dim] bf16 (strided rows),
+    cu_seqlens [num_seqs + 1] int32, lse [tokens, num_heads] float32 or None: causal attention of the
+    packed sequences."""
+    t, h, d = q.shape
+    hk = k.shape[1]
+    ldq, ldk, ldv, ldo = _heads("q", q), _heads("k", k), _heads("v", v), _heads("out", out)
+    if out.shape != q.shape or v.shape != k.shape or k.shape[0] != t or k.shape[2] != d:
+        raise ValueError("q, out: [tokens, num_heads, head_dim]; k, v: [tokens, num_kv_heads, head_dim]")
+    _expect("cu_seqlens", cu_seqlens, torch.int32, 1)
+    if cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens: contiguous [num_seqs + 1]")
+    _lse(lse, t, h)
+    return lib().qerl_prompt_attention(_p(q), ldq, _p(k), ldk, _p(v), ldv, t, h, hk, d, _p(cu_seqlens),
+                                       cu_seqlens.numel() - 1, scale, _p(out), ldo, _p(lse), _p(workspace),
+                                       _nbytes(workspace), _stream(stream))
+
+
 def qerl_read_status(workspace, stream=None) -> int:
     return lib().qerl_read_status(_p(workspace), _stream(stream))
 
@@ -653,4 +685,16 @@ def decode_attention(cache, q, lengths, scale, ws=None):
     lse = torch.empty((n, h), dtype=torch.float32, device=q.device)
     ws = workspace(qerl_decode_attention_workspace_size(n, h, cache.num_kv_heads, d), q.device) if ws is None else ws
     check(qerl_decode_attention(cache, q, lengths, scale, out, lse, ws), "qerl_decode_attention")
+    return out, lse
+
+
+def prompt_attention(q, k, v, cu_seqlens, scale, ws=None):
+    """(out, lse) of causal attention of packed sequences (see qerl_prompt_attention); rows of no sequence
+    are 0 and -inf."""
+    t, h, d = q.shape
+    out = torch.zeros((t, h, d), dtype=torch.bfloat16, device=q.device)
+    lse = torch.full((t, h), -float("inf"), dtype=torch.float32, device=q.device)
+    n = cu_seqlens.numel() - 1
+    ws = workspace(qerl_prompt_attention_workspace_size(t, h, k.shape[1], d, n), q.device) if ws is None else ws
+    check(qerl_prompt_attention(q, k, v, cu_seqlens, scale, out, lse, ws), "qerl_prompt_attention")
     return out, lse

@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqerl.so")
 SOURCES = ["api.cu", "quantize.cu", "aqn.cu", "linear.cu", "backward.cu", "noalloc.cu", "kv_cache.cu",
-           "decode_attention.cu"]
+           "decode_attention.cu", "prompt_attention.cu"]
 HEADERS = ["qerl_ptx.cuh", "qerl_internal.h", os.path.join("..", "..", "include", "qerl.h")]
 
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]

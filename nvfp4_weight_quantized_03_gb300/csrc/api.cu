@@ -562,6 +562,56 @@ qerl_status qerl_decode_attention(const qerl_kv_cache* cache, const void* q, int
   return qerl::launch_decode_attention(a, as_stream(stream));
 }
 
+size_t qerl_prompt_attention_workspace_size(int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
+                                            int64_t num_seqs) {
+  if (tokens < 0 || num_seqs < 0 || check_heads(num_heads, num_kv_heads, head_dim) != QERL_OK) return 0;
+  return qerl::prompt_attention_workspace_bytes(tokens, num_heads, num_kv_heads, head_dim, num_seqs);
+}
+
+qerl_status qerl_prompt_attention(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                  int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
+                                  const int32_t* cu_seqlens, int64_t num_seqs, float scale, void* out, int64_t ldo,
+                                  float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  if (tokens < 0 || num_seqs < 0) return QERL_ERR_INVALID_ARGUMENT;
+  qerl_status st = check_heads(num_heads, num_kv_heads, head_dim);
+  if (st != QERL_OK) return st;
+  if (!std::isfinite(scale)) return QERL_ERR_INVALID_ARGUMENT;
+  if (tokens > (1 << 30) || num_seqs > (1 << 20)) return QERL_ERR_UNSUPPORTED_SHAPE;
+  if (tokens == 0 || num_seqs == 0) return QERL_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || out == nullptr || cu_seqlens == nullptr)
+    return QERL_ERR_INVALID_ARGUMENT;
+  const int64_t q_width = static_cast<int64_t>(num_heads) * head_dim;
+  const int64_t kv_width = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if ((st = check_rows(q, ldq, q_width)) != QERL_OK || (st = check_rows(k, ldk, kv_width)) != QERL_OK ||
+      (st = check_rows(v, ldv, kv_width)) != QERL_OK || (st = check_rows(out, ldo, q_width)) != QERL_OK)
+    return st;
+  const int64_t most = int64_t{1} << 36;  // a tensor map's stride is below 2^40 bytes
+  if (ldq >= most || ldk >= most || ldv >= most) return QERL_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(cu_seqlens, 4) || !aligned(lse, 4)) return QERL_ERR_MISALIGNED;
+  st = check_ws(workspace, ws_bytes,
+                qerl::prompt_attention_workspace_bytes(tokens, num_heads, num_kv_heads, head_dim, num_seqs));
+  if (st != QERL_OK) return st;
+  qerl::PromptAttentionArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.tokens = tokens;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.cu_seqlens = cu_seqlens;
+  a.num_seqs = num_seqs;
+  a.scale = scale;
+  a.out = out;
+  a.ldo = ldo;
+  a.lse = lse;
+  a.workspace = workspace;
+  return qerl::launch_prompt_attention(a, as_stream(stream));
+}
+
 qerl_status qerl_read_status(void* workspace, void* stream) {
   if (workspace == nullptr) return QERL_ERR_INVALID_ARGUMENT;
   cudaStream_t s = as_stream(stream);

@@ -1,0 +1,580 @@
+// prompt_attention.cu -- causal attention of packed whole prompts on the
+// tensor cores.
+//
+//   s_ij = scale * q_i . k_j,  j <= i within the sequence;
+//   out_i = sum_j exp(s_ij - lse_i) v_j,   lse_i = log sum_j exp(s_ij)
+//
+// Bound: the two products, 4 head_dim multiply-adds... per (i, j, head) pair
+// 4 * head_dim operations, half of the square left out by the mask.
+//
+// A CTA takes 256 query rows of one head as two tiles of 128 rows and walks
+// the keys in tiles of 128, so that one key tile in shared memory serves both
+// and the tensor core always has one query tile's product to run while the
+// other tile's softmax is computed:
+//   warps 0-3, 4-7  softmax of tile 0, tile 1: a thread owns a row, reads its
+//                   128 scores from tensor memory, keeps the reference m and
+//                   the sum l in registers and writes the weights back as bf16
+//                   over the scores, where the second product reads them
+//   warp 8          TMA: q once, then k, v tiles through a ring
+//   warp 9          issues S_i = Q_i K^T and O_i += P_i V
+//   warps 10, 11    idle
+// Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each).
+//
+// The reference m moves only when a score passes it by 2^8 (base-2 units), so
+// rescaling O (a round trip through the registers) is rare; 2^(s - m) and the
+// sums stay far inside fp32's and bf16's range.
+//
+// Roundings: scores, m, l, O are fp32.  The weights 2^(s - m) are rounded to
+// bf16 for the product with v (the tensor core takes both operands in one
+// type, and v is bf16); l sums the unrounded weights.
+//
+// A masked weight is 0, but 0 * NaN is NaN: the value rows of the diagonal
+// tile (the only one with masked keys) are looked through before the product,
+// non-finite elements are replaced by 0 there and added back in the epilogue
+// to the rows that do attend to them.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "qerl_internal.h"
+#include "qerl_ptx.cuh"
+
+namespace qerl {
+namespace {
+
+constexpr int kRows = 128;   // rows of a query tile, keys of a key tile
+constexpr int kBlock = 256;  // query rows of a CTA
+// Two softmax warpgroups and one of which two warps work (the third group
+// exists so that registers can be moved to the softmax: at launch 384 threads
+// have 168 each; 256 * 224 + 128 * 56 = 384 * 168).
+constexpr int kThreads = 384;
+constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
+constexpr uint32_t kPanel = kRows * 128;  // 128 rows of 64 bf16, 128-byte swizzle
+constexpr float kSlack = 8.0f;
+
+struct PromptParams {
+  const __nv_bfloat16* v;  // for the epilogue of a tile with non-finite values
+  int64_t ldv;
+  const int* cu;
+  int num_seqs;
+  int tokens, heads, group;
+  float c;       // |scale| * log2(e)
+  int negative;  // scale < 0: the first product is negated
+  __nv_bfloat16* out;
+  int64_t ldo;
+  float* lse;
+  int* status;
+};
+struct PromptMaps {
+  CUtensorMap q, k, v;
+};
+
+template <int D>
+struct Shape {
+  static constexpr int kPanels = D / 64;
+  static constexpr uint32_t kTile = kPanels * kPanel;
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr uint32_t kRing = 2 * kTile;
+  static constexpr uint32_t kBars = kRing + kSlots * kTile;
+  static constexpr uint32_t kSmem = 1024 + kBars + 256;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// 16 or 32 columns of this thread's lane without waiting for them.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Descriptor of an operand whose rows run along the contraction (v: [key][64
+// elements] panels): 128-byte swizzle, 8-key groups 1024 B apart (stride
+// offset), the next 64 elements one panel on (leading offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(kPanel >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// The work of a CTA: query rows [row0, row0 + 256) of one sequence.
+struct Item {
+  int start, len, t;  // the sequence's first row and length; the block's index in it
+};
+
+__device__ __forceinline__ int blocks_of(const PromptParams& p, int s, int& start, int& len) {
+  start = p.cu[s];
+  const int end = p.cu[s + 1];
+  len = end - start;
+  if (start < 0 || end < start || end > p.tokens) {
+    record_error(p.status, QERL_ERR_RANGE);
+    len = 0;
+  }
+  return (len + kBlock - 1) / kBlock;
+}
+
+// The rank-th block of all sequences' blocks, longest key range first (the
+// blocks with index t in their sequence, t descending): the last blocks to
+// start are then the cheapest.  Every warp works it out for itself.
+__device__ __forceinline__ bool find_item(const PromptParams& p, int64_t rank, Item& it) {
+  const int lane = threadIdx.x & 31;
+  int start, len;
+  int most = 0;
+  for (int s = lane; s < p.num_seqs; s += 32) most = max(most, blocks_of(p, s, start, len));
+  most = __reduce_max_sync(~0u, most);
+  // count(t): blocks of index >= t.  The largest t with count(t) > rank.
+  auto count = [&](int t) -> int64_t {
+    long long n = 0;
+    for (int s = lane; s < p.num_seqs; s += 32) n += max(0, blocks_of(p, s, start, len) - t);
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) n += __shfl_xor_sync(~0u, n, i);
+    return n;
+  };
+  if (p.num_seqs == 1) {
+    it.t = most - 1 - static_cast<int>(rank);
+    if (rank >= most) return false;
+    blocks_of(p, 0, it.start, it.len);
+    return true;
+  }
+  if (count(0) <= rank) return false;
+  int lo = 0, hi = most;  // count(lo) > rank >= count(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (count(mid) > rank)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  int64_t left = rank - count(lo + 1);  // the left-th sequence with more than lo blocks
+  for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+    const int s = s0 + lane;
+    const bool has = s < p.num_seqs && blocks_of(p, s, start, len) > lo;
+    const unsigned mask = __ballot_sync(~0u, has);
+    const int n = __popc(mask);
+    if (left < n) {
+      const int src = __fns(mask, 0, static_cast<int>(left) + 1);
+      it.t = lo;
+      it.start = __shfl_sync(~0u, start, src);
+      it.len = __shfl_sync(~0u, len, src);
+      return true;
+    }
+    left -= n;
+  }
+  return false;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ PromptMaps maps, const PromptParams p) {
+  using S = Shape<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* gen = smem_raw + (sbase - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  Item it;
+  if (!find_item(p, static_cast<int64_t>(blockIdx.x) / p.heads, it)) return;  // the whole CTA
+  const int head = static_cast<int>(blockIdx.x % p.heads), kvh = head / p.group;
+  const int n0 = 2 * it.t + 1;                                         // key tiles of query tile 0
+  const int n1 = it.t * kBlock + kRows < it.len ? 2 * it.t + 2 : 0;    // of query tile 1 (0: no such rows)
+  const int n = max(n0, n1);
+
+  const uint32_t bars = sbase + S::kBars;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (S::kSlots + s); };
+  const uint32_t misc = bars + 16u * S::kSlots;
+  const uint32_t q_full = misc;
+  auto s_full = [&](int i) { return misc + 8u * (1 + i); };
+  auto p_full = [&](int i) { return misc + 8u * (3 + i); };
+  auto o_full = [&](int i) { return misc + 8u * (5 + i); };
+  const uint32_t done = misc + 8u * 7;
+  const uint32_t tmem_holder = misc + 8u * 8;
+  uint8_t* misc_gen = gen + S::kBars + 16 * S::kSlots;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc_gen + 8 * 8 + 4);
+  volatile int* dirty = reinterpret_cast<volatile int*>(misc_gen + 8 * 9);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kSlots; ++s) {
+      mbar_init_a(full(s), 1);
+      mbar_init_a(empty(s), 1);
+    }
+    mbar_init_a(q_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init_a(s_full(i), 1);
+      mbar_init_a(p_full(i), 4);
+      mbar_init_a(o_full(i), 1);
+    }
+    mbar_init_a(done, 1);
+    *abort_flag = 0;
+    *dirty = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc_gen + 8 * 8);
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int i = warp >> 2;  // query tile
+    const int mine = i == 0 ? n0 : n1;
+    const int r = (warp & 3) * 32 + lane;  // row of the tile
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_t = tmem + lanes + i * 128, o_t = tmem + lanes + 256 + i * D;
+    const float kInf = __int_as_float(0x7f800000);
+    float mc = -kInf, l = 0.0f;  // the reference in base-2 units and the sum of 2^(s - m)
+    bool ok = true;
+    for (int j = 0; j < mine; ++j) {
+      if (!mbar_wait_a(s_full(i), j & 1, abort_flag, p.status)) {
+        ok = false;
+        break;
+      }
+      __syncwarp();
+      tc_fence_after();
+      float x[128];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32(s_t + q * 32, x + q * 32);
+      const bool diagonal = j + 1 == mine;
+      if (diagonal) {
+        // Look through this tile's values while the scores arrive.
+        const int u = 2 * j + 1, s = u % S::kSlots;
+        if (!mbar_wait_a(full(s), (u / S::kSlots) & 1, abort_flag, p.status)) ok = false;
+        __syncwarp();
+        if (ok) {
+          const uint32_t row = sbase + S::kRing + s * S::kTile + r * 128;
+          bool bad = false;
+#pragma unroll 4
+          for (int q = 0; q < S::kPanels * 8; ++q) {
+            const uint4 w = lds128(row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4));
+            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              bad |= (a[e] & 0x7F800000u) == 0x7F800000u || (a[e] & 0x7F80u) == 0x7F80u;
+          }
+          if (bad) {
+            *dirty = 1;
+            for (int q = 0; q < S::kPanels * 8; ++q) {
+              const uint32_t at = row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4);
+              uint4 w = lds128(at);
+              uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((a[e] & 0x7F800000u) == 0x7F800000u) a[e] &= 0x0000FFFFu;
+                if ((a[e] & 0x7F80u) == 0x7F80u) a[e] &= 0xFFFF0000u;
+              }
+              sts128(at, make_uint4(a[0], a[1], a[2], a[3]));
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        __syncwarp();
+      }
+      tmem_ld_wait();
+      if (diagonal) {
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+          if (e > r) x[e] = -kInf;
+      }
+      float top = fmaxf(x[0], x[1]);
+#pragma unroll
+      for (int e = 2; e < 128; e += 2) top = fmaxf(top, fmaxf(x[e], x[e + 1]));
+      const float tc = top == -kInf ? -kInf : top * p.c;
+      if (__any_sync(~0u, tc > mc + kSlack)) {
+        const float up = fmaxf(mc, tc);
+        if (j > 0) {
+          const float f = mc == up ? 1.0f : ex2(mc - up);
+          l *= f;
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            float v[32];
+            tmem_ld32(o_t + q * 32, v);
+            tmem_ld_wait();
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(v[e] * f);
+            tmem_st_x32(o_t + q * 32, w);
+          }
+        }
+        mc = up;
+      }
+      const float sub = mc == -kInf ? 0.0f : mc;
+      float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          float a = fmaf(x[q * 64 + 2 * e], p.c, -sub), b = fmaf(x[q * 64 + 2 * e + 1], p.c, -sub);
+          if (diagonal) {  // also where c is 0
+            if (q * 64 + 2 * e > r) a = -kInf;
+            if (q * 64 + 2 * e + 1 > r) b = -kInf;
+          }
+          a = ex2(a);
+          b = ex2(b);
+          sum0 += a;
+          sum1 += b;
+          w[e] = pack_bf16(a, b);
+        }
+        tmem_st_x32(s_t + q * 32, w);
+      }
+      l += sum0 + sum1;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_a(p_full(i));
+      if (!ok) break;
+    }
+    ok = ok && mine > 0 && mbar_wait_a(o_full(i), 0, abort_flag, p.status);
+    __syncwarp();
+    if (mine > 0) {
+      tc_fence_after();
+      const int rs = it.t * kBlock + i * kRows + r;  // row in the sequence
+      const bool live = ok && rs < it.len;
+      const bool fix = *dirty != 0;
+      const float f = l == 0.0f ? 0.0f : 1.0f / l;
+      const uint32_t stage = sbase + i * S::kTile + (warp & 3) * 32 * (D * 2);  // this warp's rows of the q tile
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        float v[32];
+        tmem_ld32(o_t + q * 32, v);
+        tmem_ld_wait();
+        if (fix && live) {
+          for (int j = (n0 - 1) * kRows; j <= rs; ++j) {
+            const __nv_bfloat16* src = p.v + static_cast<int64_t>(it.start + j) * p.ldv + kvh * D + q * 32;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float y = __bfloat162float(src[e]);
+              if (!(fabsf(y) < kInf)) v[e] += y;
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint4 w = make_uint4(pack_bf16(v[8 * e] * f, v[8 * e + 1] * f), pack_bf16(v[8 * e + 2] * f, v[8 * e + 3] * f),
+                                     pack_bf16(v[8 * e + 4] * f, v[8 * e + 5] * f),
+                                     pack_bf16(v[8 * e + 6] * f, v[8 * e + 7] * f));
+          sts128(stage + lane * (D * 2) + (((q * 4 + e) ^ (lane & 7)) << 4), w);
+        }
+      }
+      if (live && p.lse != nullptr)
+        p.lse[static_cast<int64_t>(it.start + rs) * p.heads + head] =
+            l == 0.0f ? -kInf : (mc + log2f(l)) * 0.69314718055994530942f;
+      __syncwarp();
+      // Rows of D * 2 bytes, D / 8 lanes a row.
+      constexpr int kPer = 32 / (D / 8);
+      const int first = it.t * kBlock + i * kRows + (warp & 3) * 32;
+#pragma unroll 4
+      for (int q = 0; q < 32; q += kPer) {
+        const int row = q + lane / (D / 8), ch = lane % (D / 8);
+        const uint4 w = lds128(stage + row * (D * 2) + ((ch ^ (row & 7)) << 4));
+        if (ok && first + row < it.len)
+          *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(it.start + first + row) * p.ldo + head * D + ch * 8) = w;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8) {
+      if (lane == 0) {
+        const int row0 = it.start + it.t * kBlock;
+        const int tiles = n1 > 0 ? 2 : 1;
+        mbar_arrive_expect_tx_a(q_full, tiles * S::kTile);
+        for (int i = 0; i < tiles; ++i)
+  #pragma unroll
+          for (int d = 0; d < S::kPanels; ++d)
+            tma_load_2d(sbase + i * S::kTile + d * kPanel, &maps.q, head * D + d * 64, row0 + i * kRows, q_full);
+        int issued = 0;
+        for (int u = 0; u < 2 * n; ++u) {  // k, v, k, v, ...
+          const int s = u % S::kSlots;
+          if (u >= S::kSlots && !mbar_wait_a(empty(s), ((u / S::kSlots) & 1) ^ 1, abort_flag, p.status)) break;
+          mbar_arrive_expect_tx_a(full(s), S::kTile);
+          const uint32_t dst = sbase + S::kRing + s * S::kTile;
+  #pragma unroll
+          for (int d = 0; d < S::kPanels; ++d)
+            tma_load_2d(dst + d * kPanel, (u & 1) ? &maps.v : &maps.k, kvh * D + d * 64, it.start + (u >> 1) * kRows,
+                        full(s));
+          issued = u + 1;
+        }
+        // Every issued copy lands before the CTA exits (after an expired wait too).
+        volatile int no_abort = 0;
+        mbar_wait_a(q_full, 0, &no_abort, p.status);
+        for (int s = 0; s < min(issued, S::kSlots); ++s) {
+          const int last = issued - 1 - ((issued - 1 - s) % S::kSlots);
+          mbar_wait_a(full(s), (last / S::kSlots) & 1, &no_abort, p.status);
+        }
+      }
+    } else if (warp == 9) {
+      if (lane == 0) {
+        const uint32_t id_s = idesc_bf16_f32(128, 128) | (p.negative ? 1u << 13 : 0u);
+        const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // v: rows along the contraction
+        auto slot = [&](int u) { return sbase + S::kRing + (u % S::kSlots) * S::kTile; };
+        auto wait_slot = [&](int u) {
+          return mbar_wait_a(full(u % S::kSlots), (u / S::kSlots) & 1, abort_flag, p.status);
+        };
+        auto scores = [&](int i, int j) {
+          const uint32_t qa = sbase + i * S::kTile, ka = slot(2 * j);
+  #pragma unroll
+          for (int d = 0; d < S::kPanels; ++d)
+  #pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f16(tmem + i * 128, sw128_kmajor_desc(qa + d * kPanel + kk * 32),
+                         sw128_kmajor_desc(ka + d * kPanel + kk * 32), id_s, d + kk > 0 ? 1u : 0u);
+          tc_commit(s_full(i));
+        };
+        auto values = [&](int i, int j) {
+          const uint32_t va = slot(2 * j + 1);
+  #pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc_mma_f16_ts(tmem + 256 + i * D, tmem + i * 128 + kk * 8, sw128_mnmajor_desc(va + kk * 2048), id_o,
+                          j + kk > 0 ? 1u : 0u);
+        };
+        bool ok = mbar_wait_a(q_full, 0, abort_flag, p.status) && wait_slot(0);
+        if (ok) {
+          tc_fence_after();
+          scores(0, 0);
+          if (n1 > 0) scores(1, 0);
+          tc_commit(empty(0));
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          ok = wait_slot(2 * j + 1) && (j + 1 >= n || wait_slot(2 * j + 2));
+          for (int i = 0; ok && i < 2; ++i) {
+            const int mine = i == 0 ? n0 : n1;
+            if (j >= mine) continue;
+            if (!mbar_wait_a(p_full(i), j & 1, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            values(i, j);
+            if (j + 1 < mine)
+              scores(i, j + 1);
+            else
+              tc_commit(o_full(i));
+          }
+          if (!ok) break;
+          tc_commit(empty((2 * j + 1) % S::kSlots));
+          if (j + 1 < n) tc_commit(empty((2 * j + 2) % S::kSlots));
+        }
+        tc_commit(done);  // also after an expired wait: arrives once the issued MMAs are done
+      }
+    }
+  }
+  __syncwarp();
+  {  // every MMA is done before the tensor memory goes back (bounded)
+    volatile int no_abort = 0;
+    mbar_wait_a(done, 0, &no_abort, p.status);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 f = fn.load();
+  if (f == nullptr) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    fn.store(f);
+  }
+  return f;
+}
+
+// Rows of `width` bf16 (stride ld), read in boxes of 64 columns x 128 rows.
+bool rows_map(CUtensorMap* map, const void* base, int64_t width, int64_t rows, int64_t ld) {
+  const auto enc = encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {64, kRows}, estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+qerl_status launch(const PromptMaps& maps, const PromptParams& p, int64_t grid, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};  // one bit per device: the attribute belongs to the device's function
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return QERL_ERR_CUDA;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if ((ready.load() & bit) == 0) {
+    if (cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem) !=
+        cudaSuccess)
+      return QERL_ERR_CUDA;
+    ready.fetch_or(bit);
+  }
+  prompt_kernel<D><<<static_cast<unsigned>(grid), kThreads, Shape<D>::kSmem, s>>>(maps, p);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+
+size_t prompt_attention_workspace_bytes(int64_t, int, int, int, int64_t) { return kWsHeaderBytes; }
+
+qerl_status launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t s) {
+  PromptMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  const int64_t qw = static_cast<int64_t>(a.num_heads) * a.head_dim, kw = static_cast<int64_t>(a.num_kv_heads) * a.head_dim;
+  if (!rows_map(&maps.q, a.q, qw, a.tokens, a.ldq) || !rows_map(&maps.k, a.k, kw, a.tokens, a.ldk) ||
+      !rows_map(&maps.v, a.v, kw, a.tokens, a.ldv))
+    return QERL_ERR_CUDA;
+  PromptParams p{};
+  p.v = static_cast<const __nv_bfloat16*>(a.v);
+  p.ldv = a.ldv;
+  p.cu = a.cu_seqlens;
+  p.num_seqs = static_cast<int>(a.num_seqs);
+  p.tokens = static_cast<int>(a.tokens);
+  p.heads = a.num_heads;
+  p.group = a.num_heads / a.num_kv_heads;
+  p.negative = a.scale < 0.0f;
+  p.c = (a.scale < 0.0f ? -a.scale : a.scale) * 1.44269504088896340736f;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.ldo = a.ldo;
+  p.lse = a.lse;
+  p.status = &static_cast<WsHeader*>(a.workspace)->status;
+  // Every sequence has at most one block that is not full.
+  const int64_t blocks = a.tokens / kBlock + std::min(a.num_seqs, a.tokens);
+  const int64_t grid = blocks * a.num_heads;
+  if (grid > INT32_MAX) return QERL_ERR_UNSUPPORTED_SHAPE;
+  return a.head_dim == 128 ? launch<128>(maps, p, grid, s) : launch<64>(maps, p, grid, s);
+}
+
+}  // namespace qerl

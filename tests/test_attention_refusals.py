@@ -113,6 +113,30 @@ def test_decode_shapes(L):
     assert L.qerl_decode_attention_workspace_size(3, 28, 4, 100) == 0
 
 
+def _prompt(L, **kw):
+    a = dict(q=0x1000, ldq=3584, k=0x2000, ldk=512, v=0x3000, ldv=512, tokens=300, heads=28, hk=4, dim=128, cu=0x4000,
+             n=2, scale=0.1, out=0x5000, ldo=3584, lse=0x6000, ws=0x8000, wsb=256)
+    a.update(kw)
+    return q.STATUS_NAMES[L.qerl_prompt_attention(a["q"], a["ldq"], a["k"], a["ldk"], a["v"], a["ldv"], a["tokens"],
+                                                  a["heads"], a["hk"], a["dim"], a["cu"], a["n"], a["scale"], a["out"],
+                                                  a["ldo"], a["lse"], a["ws"], a["wsb"], None)]
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(tokens=-1), INVALID), (dict(n=-1), INVALID), (dict(heads=27), INVALID), (dict(hk=0), INVALID),
+    (dict(dim=96), SHAPE), (dict(dim=256), SHAPE), (dict(tokens=2 ** 30 + 1), SHAPE), (dict(n=2 ** 20 + 1), SHAPE),
+    (dict(scale=float("nan")), INVALID), (dict(scale=-float("inf")), INVALID), (dict(q=None), INVALID),
+    (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(out=None), INVALID), (dict(cu=None), INVALID),
+    (dict(ldq=3576), INVALID), (dict(ldk=504), INVALID), (dict(ldv=504), INVALID), (dict(ldo=3576), INVALID),
+    (dict(ldq=3588), ALIGN), (dict(ldv=516), ALIGN), (dict(q=0x1008), ALIGN), (dict(k=0x2002), ALIGN),
+    (dict(v=0x3004), ALIGN), (dict(out=0x5008), ALIGN), (dict(cu=0x4002), ALIGN), (dict(lse=0x6002), ALIGN),
+    (dict(ldq=2 ** 36), SHAPE), (dict(ldk=2 ** 36), SHAPE), (dict(ws=None), WS), (dict(wsb=255), WS),
+    (dict(ws=0x8080), ALIGN), (dict(tokens=0), "QERL_OK"), (dict(n=0), "QERL_OK"),
+])
+def test_prompt_arguments(L, kw, want):
+    assert _prompt(L, **kw) == want
+
+
 def test_descriptor_layout():
     """KvCache mirrors the C struct: 13 fields, 8-byte aligned, no padding but what C has."""
     assert ctypes.sizeof(q.KvCache) == 4 * 4 + 9 * 8
