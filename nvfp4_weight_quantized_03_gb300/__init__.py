@@ -217,8 +217,13 @@ def _p(t):
     return t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream() builds an object: 3 us a call
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -453,21 +458,44 @@ def qerl_rmsnorm_noise(h, w_norm, Z, delta, out, stream=None) -> int:
 
 # ---- attention ----------------------------------------------------------------
 
-def _expect(name, t, dtype, dims=None):
-    """Raises unless t is a CUDA tensor of this type (and dimension count): a raw pointer of another
-    type would be misread."""
-    if not t.is_cuda or t.dtype != dtype or (dims is not None and t.dim() != dims):
-        raise TypeError(f"{name}: expected a {'' if dims is None else f'{dims}-d '}CUDA tensor of {dtype}, got "
-                        f"{tuple(t.shape)} {t.dtype} on {t.device}")
+_BF16, _I32, _F32, _F64 = torch.bfloat16, torch.int32, torch.float32, torch.float64
 
 
-def _heads(name, t):
-    """Row stride of bf16 rows of heads [rows, heads, head_dim] whose heads lie side by side."""
-    _expect(name, t, torch.bfloat16, 3)
-    rows, heads, dim = t.shape
-    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
-        raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {t.stride()}")
-    return t.stride(0) if rows > 1 else max(t.stride(0), heads * dim)
+def _expect(name, t, dtype, dims):
+    """Raises unless t is a CUDA tensor of this type and dimension count: a raw pointer of another type
+    would be misread."""
+    if t.dtype is not dtype or not t.is_cuda or t.dim() != dims:
+        raise TypeError(f"{name}: expected a {dims}-d CUDA tensor of {dtype}, got {tuple(t.shape)} {t.dtype} on "
+                        f"{t.device}")
+
+
+def _heads(name, t, shape):
+    """Row stride of bf16 rows of heads [rows, heads, head_dim], of this shape, whose heads lie side by side."""
+    if t.dtype is not _BF16 or not t.is_cuda:
+        _expect(name, t, _BF16, 3)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    ld, s1, s2 = t.stride()
+    rows, heads, dim = shape
+    if s2 != 1 or s1 != dim or rows < 2:
+        if (dim > 1 and s2 != 1) or (heads > 1 and s1 != dim):
+            raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {t.stride()}")
+        ld = ld if rows > 1 else max(ld, heads * dim)
+    return ld
+
+
+def _vector(name, t, dtype, n):
+    """Raises unless t is a contiguous CUDA vector of n entries of this type."""
+    if t.dtype is not dtype or not t.is_cuda or t.dim() != 1:
+        _expect(name, t, dtype, 1)
+    if t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous entries, got {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _heads_shape(name, t):
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected [rows, heads, head_dim], got {tuple(t.shape)}")
+    return t.shape
 
 
 def kv_cache(k, v, page_table, k_scale=None, v_scale=None):
@@ -509,33 +537,27 @@ def qerl_rope_append(cache, q, k, v, positions, inv_freq, q_out, k_out, workspac
     positions [tokens] int32 (negative: padding), inv_freq [rot_dim / 2] float64, seq_ids [tokens] int32 or
     None (token t is sequence t); q_out, k_out like q, k (may be them; k_out may be None with a cache).
     cache None: rotation only (v may be None)."""
-    tokens, hk, d = k.shape
-    ldk = _heads("k", k)
-    h, ldq, ldqo, ldv, ldko = 0, 0, 0, 0, 0
+    shape = _heads_shape("k", k)
+    tokens, hk, d = shape
+    ldk = _heads("k", k, shape)
+    h = ldq = ldqo = ldv = ldko = 0
     if q is not None:
-        ldq, ldqo, h = _heads("q", q), _heads("q_out", q_out), q.shape[1]
-        if q.shape != q_out.shape or q.shape[0] != tokens or q.shape[2] != d:
-            raise ValueError("q, q_out: [tokens, num_heads, head_dim] of k's tokens and head_dim")
+        h = _heads_shape("q", q)[1]
+        ldq = _heads("q", q, (tokens, h, d))
+        ldqo = _heads("q_out", q_out, (tokens, h, d))
     if v is not None:
-        ldv = _heads("v", v)
-        if v.shape != k.shape:
-            raise ValueError("v: k's shape")
+        ldv = _heads("v", v, shape)
     if k_out is not None:
-        ldko = _heads("k_out", k_out)
-        if k_out.shape != k.shape:
-            raise ValueError("k_out: k's shape")
-    _expect("positions", positions, torch.int32, 1)
-    _expect("inv_freq", inv_freq, torch.float64, 1)
+        ldko = _heads("k_out", k_out, shape)
+    _vector("positions", positions, _I32, tokens)
+    half = inv_freq.numel()
+    _vector("inv_freq", inv_freq, _F64, half)
     if seq_ids is not None:
-        _expect("seq_ids", seq_ids, torch.int32, 1)
-    for name, t in (("positions", positions), ("seq_ids", seq_ids)):
-        if t is not None and (t.numel() != tokens or not t.is_contiguous()):
-            raise ValueError(f"{name}: one contiguous entry per token")
-    if not inv_freq.is_contiguous():
-        raise ValueError("inv_freq: contiguous")
-    return lib().qerl_rope_append(cache, _p(q), ldq, h, _p(k), ldk, _p(v), ldv, hk, d, tokens, _p(seq_ids),
-                                  _p(positions), _p(inv_freq), 2 * inv_freq.numel(), _p(q_out), ldqo, _p(k_out), ldko,
-                                  _p(workspace), _nbytes(workspace), _stream(stream))
+        _vector("seq_ids", seq_ids, _I32, tokens)
+    return (_lib or lib()).qerl_rope_append(cache, _p(q), ldq, h, k.data_ptr(), ldk, _p(v), ldv, hk, d, tokens,
+                                            _p(seq_ids), positions.data_ptr(), inv_freq.data_ptr(), 2 * half,
+                                            _p(q_out), ldqo, _p(k_out), ldko, workspace.data_ptr(),
+                                            _nbytes(workspace), _stream(stream))
 
 
 def qerl_decode_attention_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
@@ -543,25 +565,25 @@ def qerl_decode_attention_workspace_size(num_seqs: int, num_heads: int, num_kv_h
 
 
 def _lse(lse, rows, heads):
-    if lse is not None:
-        _expect("lse", lse, torch.float32, 2)
-        if lse.shape[0] != rows or lse.shape[1] != heads or not lse.is_contiguous():
-            raise ValueError("lse: contiguous [rows, num_heads]")
+    if lse.dtype is not _F32 or not lse.is_cuda or lse.dim() != 2:
+        _expect("lse", lse, _F32, 2)
+    if lse.shape != (rows, heads) or not lse.is_contiguous():
+        raise ValueError("lse: contiguous [rows, num_heads]")
+    return lse.data_ptr()
 
 
 def qerl_decode_attention(cache, q, lengths, scale, out, lse, workspace, stream=None) -> int:
     """q, out [num_seqs, num_heads, head_dim] bf16 (strided rows), lengths [num_seqs] int32, lse [num_seqs,
     num_heads] float32 or None: one new token per sequence over the cache's first lengths[s] rows."""
-    n, h, d = q.shape
-    ldq, ldo = _heads("q", q), _heads("out", out)
-    _expect("lengths", lengths, torch.int32, 1)
-    if out.shape != q.shape or n != cache.num_seqs or d != cache.head_dim:
-        raise ValueError("q, out: [num_seqs, num_heads, head_dim] of the cache")
-    if lengths.numel() != n or not lengths.is_contiguous():
-        raise ValueError("lengths: one contiguous entry per sequence")
-    _lse(lse, n, h)
-    return lib().qerl_decode_attention(cache, _p(q), ldq, h, _p(lengths), scale, _p(out), ldo, _p(lse), _p(workspace),
-                                       _nbytes(workspace), _stream(stream))
+    shape = _heads_shape("q", q)
+    n, h, d = shape
+    if n != cache.num_seqs or d != cache.head_dim:
+        raise ValueError("q: [num_seqs, num_heads, head_dim] of the cache")
+    ldq, ldo = _heads("q", q, shape), _heads("out", out, shape)
+    _vector("lengths", lengths, _I32, n)
+    return (_lib or lib()).qerl_decode_attention(cache, q.data_ptr(), ldq, h, lengths.data_ptr(), scale,
+                                                 out.data_ptr(), ldo, None if lse is None else _lse(lse, n, h),
+                                                 workspace.data_ptr(), _nbytes(workspace), _stream(stream))
 
 
 def qerl_prompt_attention_workspace_size(tokens: int, num_heads: int, num_kv_heads: int, head_dim: int,
@@ -574,18 +596,19 @@ def qerl_prompt_attention(q, k, v, cu_seqlens, scale, out, lse, workspace, strea
     """q, out [tokens, num_heads, head_dim], k, v [tokens, num_kv_heads, head_dim] bf16 (strided rows),
     cu_seqlens [num_seqs + 1] int32, lse [tokens, num_heads] float32 or None: causal attention of the
     packed sequences."""
-    t, h, d = q.shape
-    hk = k.shape[1]
-    ldq, ldk, ldv, ldo = _heads("q", q), _heads("k", k), _heads("v", v), _heads("out", out)
-    if out.shape != q.shape or v.shape != k.shape or k.shape[0] != t or k.shape[2] != d:
-        raise ValueError("q, out: [tokens, num_heads, head_dim]; k, v: [tokens, num_kv_heads, head_dim]")
-    _expect("cu_seqlens", cu_seqlens, torch.int32, 1)
-    if cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens: contiguous [num_seqs + 1]")
-    _lse(lse, t, h)
-    return lib().qerl_prompt_attention(_p(q), ldq, _p(k), ldk, _p(v), ldv, t, h, hk, d, _p(cu_seqlens),
-                                       cu_seqlens.numel() - 1, scale, _p(out), ldo, _p(lse), _p(workspace),
-                                       _nbytes(workspace), _stream(stream))
+    shape = _heads_shape("q", q)
+    t, h, d = shape
+    hk = _heads_shape("k", k)[1]
+    ldq, ldo = _heads("q", q, shape), _heads("out", out, shape)
+    ldk, ldv = _heads("k", k, (t, hk, d)), _heads("v", v, (t, hk, d))
+    n = cu_seqlens.numel()
+    _vector("cu_seqlens", cu_seqlens, _I32, n)
+    if n < 1:
+        raise ValueError("cu_seqlens: [num_seqs + 1]")
+    return (_lib or lib()).qerl_prompt_attention(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, t, h, hk, d,
+                                                 cu_seqlens.data_ptr(), n - 1, scale, out.data_ptr(), ldo,
+                                                 None if lse is None else _lse(lse, t, h), workspace.data_ptr(),
+                                                 _nbytes(workspace), _stream(stream))
 
 
 def qerl_read_status(workspace, stream=None) -> int:

@@ -171,6 +171,12 @@ __device__ __forceinline__ void advance(const DecodeParams& p, Cursor& c) {
   }
 }
 
+// a / b for a >= 0, b > 0; the 64-bit division costs several times the 32-bit one.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
 template <int D, bool kFp8, int NT>
 __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams p) {
   using S = Shape<D, kFp8, NT>;
@@ -187,72 +193,94 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
 
   // ---- this CTA's stretch of the line ---------------------------------------
   auto units = [&](int b) -> long long {
+    if (b >= p.num_seqs) return 0;
     const int n = live_length(p, b);
     return n > 0 ? static_cast<long long>((n - 1) / S::kTile + 1) * hz_all : 0;
   };
-  long long total = 0;
-  for (int b = tid; b < p.num_seqs; b += kThreads) {
-    const int n = p.lengths[b];
-    if (n < 0 || n > p.capacity) record_error(p.status, QERL_ERR_RANGE);
-    total += units(b);
-  }
+  auto scan = [&](long long v) -> long long {  // inclusive over the warp
 #pragma unroll
-  for (int i = 16; i > 0; i >>= 1) total += __shfl_xor_sync(~0u, total, i);
-  if (lane == 0) red[warp] = total;
+    for (int i = 1; i < 32; i <<= 1) {
+      const long long up = __shfl_up_sync(~0u, v, i);
+      if (lane >= i) v += up;
+    }
+    return v;
+  };
   // A sequence without keys: zeros and lse = -inf, shared out over the CTAs.
   for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
-    if (live_length(p, b) > 0) continue;
+    const int n = p.lengths[b];
+    if (tid == 0 && (n < 0 || n > p.capacity)) record_error(p.status, QERL_ERR_RANGE);
+    if (n > 0 && p.capacity > 0) continue;
     for (int i = tid; i < p.heads * D / 8; i += kThreads)
       *reinterpret_cast<uint4*>(p.out + b * p.ldo + i * 8) = make_uint4(0, 0, 0, 0);
     if (p.lse != nullptr)
       for (int i = tid; i < p.heads; i += kThreads) p.lse[static_cast<int64_t>(b) * p.heads + i] = -kInf;
   }
-  __syncthreads();
-  total = 0;
+  long long total = 0, incl = 0, mine = 0;
+  if (p.num_seqs <= 32) {  // every warp for itself, no barrier
+    mine = units(lane);
+    incl = scan(mine);
+    total = __shfl_sync(~0u, incl, 31);
+  } else {
+    for (int b = tid; b < p.num_seqs; b += kThreads) total += units(b);
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) total += red[i];
-  // No CTA without a unit between two that have one: the join counts the CTAs of a range.
+    for (int i = 16; i > 0; i >>= 1) total += __shfl_xor_sync(~0u, total, i);
+    if (lane == 0) red[warp] = total;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) total += red[i];
+  }
+  if (total == 0) return;
+  // Even stretches; no CTA without a unit between two that have one (the join
+  // counts the CTAs of a range).
   const long long ctas = total < gridDim.x ? total : gridDim.x;
   if (blockIdx.x >= ctas) return;
-  auto stretch = [&](long long c) -> long long { return total * c / ctas; };
+  const long long each = quotient(total, ctas), extra = total - each * ctas;  // the first `extra` CTAs get one more
+  auto stretch = [&](long long c) -> long long { return each * c + (c < extra ? c : extra); };
+  auto owner = [&](long long unit) -> int {  // the CTA that holds a unit
+    const long long wide = extra * (each + 1);
+    return static_cast<int>(unit < wide ? quotient(unit, each + 1) : extra + quotient(unit - wide, each));
+  };
   const long long begin = stretch(blockIdx.x), end = stretch(blockIdx.x + 1);
-  // The sequence that holds unit `begin`.
-  long long base = 0;
-  for (int b0 = 0;; b0 += kThreads) {
-    const int b = b0 + tid;
-    const long long mine = b < p.num_seqs ? units(b) : 0;
-    long long incl = mine;
-#pragma unroll
-    for (int i = 1; i < 32; i <<= 1) {
-      const long long up = __shfl_up_sync(~0u, incl, i);
-      if (lane >= i) incl += up;
-    }
-    __syncthreads();
-    if (lane == 31) red[warp] = incl;
-    __syncthreads();
-    long long before = base, all = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) before += red[i];
-      all += red[i];
-    }
-    incl += before;
-    if (begin < base + all) {  // uniform: in this block of sequences
-      if (incl - mine <= begin && begin < incl) {
-        found[0] = b;
-        found[1] = begin - (incl - mine);
-      }
-      __syncthreads();
-      break;
-    }
-    base += all;
-  }
+  // The sequence that holds unit `begin`, and the unit's place in it.
   Cursor cur;
-  cur.b = static_cast<int>(found[0]);
+  long long inside;
+  if (p.num_seqs <= 32) {
+    const unsigned hit = __ballot_sync(~0u, incl - mine <= begin && begin < incl);
+    cur.b = __ffs(hit) - 1;
+    inside = begin - __shfl_sync(~0u, incl - mine, cur.b);
+  } else {
+    long long base = 0;
+    for (int b0 = 0;; b0 += kThreads) {
+      mine = units(b0 + tid);
+      incl = scan(mine);
+      __syncthreads();
+      if (lane == 31) red[warp] = incl;
+      __syncthreads();
+      long long before = base, all = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) before += red[i];
+        all += red[i];
+      }
+      incl += before;
+      if (begin < base + all) {  // uniform: in this block of sequences
+        if (incl - mine <= begin && begin < incl) {
+          found[0] = b0 + tid;
+          found[1] = begin - (incl - mine);
+        }
+        __syncthreads();
+        break;
+      }
+      base += all;
+    }
+    cur.b = static_cast<int>(found[0]);
+    inside = found[1];
+  }
   cur.len = live_length(p, cur.b);
   cur.tiles = (cur.len - 1) / S::kTile + 1;
-  cur.hz = static_cast<int>(found[1] / cur.tiles);
-  cur.tile = static_cast<int>(found[1] - static_cast<long long>(cur.hz) * cur.tiles);
+  cur.hz = static_cast<int>(quotient(inside, cur.tiles));
+  cur.tile = static_cast<int>(inside - static_cast<long long>(cur.hz) * cur.tiles);
 
   // ---- loads ----------------------------------------------------------------
   // Byte offset of this lane's key row of the cursor's tile; -1 past the length
@@ -282,20 +310,25 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
       cp_async_16(dst + S::kKeys * S::kRow, p.vp + from, o < 0 ? 0 : 16);
     }
   };
+  // The page numbers of the first stages are fetched together, later ones a
+  // step before their rows.
   Cursor ahead = cur;
   long long to_load = end - begin;
-  int64_t off = lookup(ahead);
+  int64_t offs[S::kStages];
+#pragma unroll
+  for (int s = 0; s < S::kStages; ++s) {
+    if (s > 0 && s < to_load) advance<S::kTile>(p, ahead);
+    offs[s] = s < to_load ? lookup(ahead) : -1;
+  }
 #pragma unroll
   for (int s = 0; s < S::kStages - 1; ++s) {
-    if (to_load > 0) {
-      issue(s, off);
-      if (--to_load > 0) {
-        advance<S::kTile>(p, ahead);
-        off = lookup(ahead);
-      }
+    if (s < end - begin) {
+      issue(s, offs[s]);
+      --to_load;
     }
     cp_async_commit();
   }
+  int64_t off = offs[S::kStages - 1];
 
   // ---- the key loop ----------------------------------------------------------
   constexpr int KS = D / 16;  // 16-element steps of a head
@@ -305,6 +338,35 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
   float mult[NT][2];
   float o[NT][KS][4];
   float m[NT][2], l[NT][2];
+  // This thread's words of the queries of a (sequence, head): for the bf16
+  // cache elements 2 t4, 2 t4 + 1 and 8 more on of every 16; for the E4M3 cache
+  // 4 t4 .. 4 t4 + 3 (the order the bytes of a key arrive in).
+  auto load_q = [&](const Cursor& c, uint32_t (&w)[NT][KS][2]) {
+    const int kvh = c.hz / p.zgroups, z = c.hz - kvh * p.zgroups;
+    const int nheads = min(p.zheads, p.group - z * p.zheads);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = nt * 8 + g8;
+      const __nv_bfloat16* src =
+          p.q + c.b * p.ldq + static_cast<int64_t>(kvh * p.group + z * p.zheads + (h < nheads ? h : 0)) * D;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        if (kFp8) {
+          const uint2 v = *reinterpret_cast<const uint2*>(src + ks * 16 + 4 * t4);
+          w[nt][ks][0] = v.x;
+          w[nt][ks][1] = v.y;
+        } else {
+          w[nt][ks][0] = *reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * t4);
+          w[nt][ks][1] = *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + 2 * t4);
+        }
+      }
+    }
+  };
+  // With one column tile there are registers to fetch the next segment's
+  // queries during the last tile of this one.
+  constexpr bool kAheadQ = NT == 1;
+  uint32_t qn[NT][KS][2];
+  load_q(cur, qn);
   bool fresh = true;
   int stage = 0;
   long long seg_begin = begin - cur.tile;  // first unit of the segment
@@ -314,26 +376,22 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
     const int nheads = min(p.zheads, p.group - z * p.zheads);
     if (fresh) {
       fresh = false;
+      if (!kAheadQ && u > begin) load_q(cur, qn);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int h = nt * 8 + g8;
-        const __nv_bfloat16* src = p.q + cur.b * p.ldq + static_cast<int64_t>(head0 + h) * D;
         if (!kFp8) {
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
-            qf[nt][ks][0] = h < nheads ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * t4) : 0;
-            qf[nt][ks][1] = h < nheads ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + 2 * t4) : 0;
+            qf[nt][ks][0] = qn[nt][ks][0];
+            qf[nt][ks][1] = qn[nt][ks][1];
           }
           mult[nt][0] = mult[nt][1] = p.scale_log2;
         } else {
-          // elements 4 t4 .. 4 t4 + 3 of every 16 (the order the E4M3 bytes of a key arrive in)
           float amax = 0.0f;
-          uint2 raw[KS];
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
-            raw[ks] = h < nheads ? *reinterpret_cast<const uint2*>(src + ks * 16 + 4 * t4) : make_uint2(0, 0);
-            amax = fmaxf(amax, fmaxf(fabsf(bf_lo(raw[ks].x)), fabsf(bf_hi(raw[ks].x))));
-            amax = fmaxf(amax, fmaxf(fabsf(bf_lo(raw[ks].y)), fabsf(bf_hi(raw[ks].y))));
+            amax = fmaxf(amax, fmaxf(fabsf(bf_lo(qn[nt][ks][0])), fabsf(bf_hi(qn[nt][ks][0]))));
+            amax = fmaxf(amax, fmaxf(fabsf(bf_lo(qn[nt][ks][1])), fabsf(bf_hi(qn[nt][ks][1]))));
           }
           amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
           amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
@@ -344,8 +402,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
           const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
-            qf[nt][ks][0] = pack_f16(bf_lo(raw[ks].x) * down, bf_hi(raw[ks].x) * down);
-            qf[nt][ks][1] = pack_f16(bf_lo(raw[ks].y) * down, bf_hi(raw[ks].y) * down);
+            qf[nt][ks][0] = pack_f16(bf_lo(qn[nt][ks][0]) * down, bf_hi(qn[nt][ks][0]) * down);
+            qf[nt][ks][1] = pack_f16(bf_lo(qn[nt][ks][1]) * down, bf_hi(qn[nt][ks][1]) * down);
           }
           const float f = p.scale_log2 * (p.k_scale != nullptr ? p.k_scale[kvh] : 1.0f) * up;
           mult[nt][0] = __shfl_sync(~0u, f, 8 * t4);      // head 2 t4
@@ -358,6 +416,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[nt][ks][i] = 0.0f;
       }
+    }
+    const bool last_tile = cur.tile + 1 == cur.tiles;
+    Cursor next = cur;
+    if (u + 1 < end) {
+      advance<S::kTile>(p, next);
+      if (kAheadQ && last_tile) load_q(next, qn);
     }
     // Refill the stage the previous step emptied, then wait for this one.
     {
@@ -497,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
 
     // ---- end of a (sequence, head) or of the stretch -------------------------
-    if (cur.tile + 1 == cur.tiles || u + 1 == end) {
+    if (last_tile || u + 1 == end) {
       const long long seg_end = seg_begin + cur.tiles;
       const bool whole = seg_begin >= begin && seg_end <= end;
 #pragma unroll
@@ -534,44 +598,42 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
               sum == 0.0f ? -kInf : (top + log2f(sum)) * 0.69314718055994530942f;
       };
       constexpr int64_t kSlot = static_cast<int64_t>(NT * 8) * S::kPartRow;
-      float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (seg_begin <= begin ? 0 : 1)) * kSlot;
-      for (int i = tid; i < nheads * (D / 4); i += kThreads) {
-        const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
-        float top = -kInf;
+      // The warps' (m, l, o) of a head joined, in warp order, and handed on.
+      auto join = [&](auto&& use) {
+        for (int i = tid; i < nheads * (D / 4); i += kThreads) {
+          const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+          float top = -kInf;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][h][0]);
-        float sum = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][h][0]);
+          float sum = 0.0f;
+          float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          // a warp without a finite score has sums of 0 (or NaN, which stays)
-          const float f = ml[w][h][0] == -kInf ? 1.0f : ex2(ml[w][h][0] - top);
-          const float4 v = *reinterpret_cast<const float4*>(o_join + (w * NT * 8 + h) * S::kOStride + d);
-          sum += f * ml[w][h][1];
-          acc.x += f * v.x;
-          acc.y += f * v.y;
-          acc.z += f * v.z;
-          acc.w += f * v.w;
+          for (int w = 0; w < kWarps; ++w) {
+            // a warp without a finite score has sums of 0 (or NaN, which stays)
+            const float f = ml[w][h][0] == -kInf ? 1.0f : ex2(ml[w][h][0] - top);
+            const float4 v = *reinterpret_cast<const float4*>(o_join + (w * NT * 8 + h) * S::kOStride + d);
+            sum += f * ml[w][h][1];
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+          }
+          use(h, d, top, sum, acc);
         }
-        if (whole) {
-          finish(h, d, top, sum, acc);
-        } else {
-          __stcg(reinterpret_cast<float4*>(slot + h * D + d), acc);
+      };
+      if (whole) {
+        join(finish);
+      } else {
+        float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (seg_begin <= begin ? 0 : 1)) * kSlot;
+        join([&](int h, int d, float top, float sum, const float4& v) {
+          __stcg(reinterpret_cast<float4*>(slot + h * D + d), v);
           if (d == 0) __stcg(reinterpret_cast<float2*>(slot + NT * 8 * D + 2 * h), make_float2(top, sum));
-        }
-      }
-      if (!whole) {
+        });
         // The CTAs that hold units of this segment: those of its first and last unit.
-        auto owner = [&](long long unit) -> int {  // the largest c with stretch(c) <= unit
-          long long c = (unit * ctas) / total;
-          while (stretch(c + 1) <= unit) ++c;
-          while (stretch(c) > unit) --c;
-          return static_cast<int>(c);
-        };
         const int c0 = owner(seg_begin), c1 = owner(seg_end - 1);
-        __threadfence();
         __syncthreads();
         if (tid == 0) {
+          __threadfence();
           unsigned* counter = p.counters + static_cast<int64_t>(cur.b) * hz_all + cur.hz;
           const unsigned before = atomicAdd(counter, 1u);
           arrived = before;
@@ -580,33 +642,70 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
         }
         __syncthreads();
         if (arrived == static_cast<unsigned>(c1 - c0)) {
-          for (int i = tid; i < nheads * (D / 4); i += kThreads) {
-            const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
-            float top = -kInf, sum = 0.0f;
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-              const float* s = p.part + (2 * static_cast<int64_t>(c) + (c == c0 && stretch(c) < seg_begin ? 1 : 0)) * kSlot;
-              const float2 e = __ldcg(reinterpret_cast<const float2*>(s + NT * 8 * D + 2 * h));
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(s + h * D + d));
-              const float up = fmaxf(top, e.x);
-              const float fa = top == -kInf ? 1.0f : ex2(top - up), fb = e.x == -kInf ? 1.0f : ex2(e.x - up);
-              top = up;
-              sum = sum * fa + e.y * fb;
-              acc.x = acc.x * fa + v.x * fb;
-              acc.y = acc.y * fa + v.y * fb;
-              acc.z = acc.z * fa + v.z * fb;
-              acc.w = acc.w * fa + v.w * fb;
-            }
-            finish(h, d, top, sum, acc);
+          // The last to arrive: warp w adds the partials c0 + w, c0 + w + 4, ...
+          // (all heads of a partial in flight together), then the warps join.
+          constexpr int kVec = D / 32;  // elements of a row per lane
+          constexpr int kHeads = NT * 8;
+          float top[kHeads], sum[kHeads], acc[kHeads][kVec];
+#pragma unroll
+          for (int h = 0; h < kHeads; ++h) {
+            top[h] = -kInf;
+            sum[h] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) acc[h][e] = 0.0f;
           }
+          const int first_slot = stretch(c0) < seg_begin ? 1 : 0;
+#pragma unroll(NT == 1 ? 2 : 1)
+          for (int c = c0 + warp; c <= c1; c += kWarps) {
+            const float* s = p.part + (2 * static_cast<int64_t>(c) + (c == c0 ? first_slot : 0)) * kSlot;
+            float2 e[kHeads];
+            float v[kHeads][kVec];
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+              if (h >= nheads) continue;
+              e[h] = __ldcg(reinterpret_cast<const float2*>(s + NT * 8 * D + 2 * h));
+              if (kVec == 4) {
+                const float4 w = __ldcg(reinterpret_cast<const float4*>(s + h * D + lane * 4));
+                v[h][0] = w.x;
+                v[h][1] = w.y;
+                v[h][kVec - 2] = w.z;
+                v[h][kVec - 1] = w.w;
+              } else {
+                const float2 w = __ldcg(reinterpret_cast<const float2*>(s + h * D + lane * 2));
+                v[h][0] = w.x;
+                v[h][1] = w.y;
+              }
+            }
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+              if (h >= nheads) continue;
+              const float up = fmaxf(top[h], e[h].x);
+              const float fa = top[h] == -kInf ? 1.0f : ex2(top[h] - up), fb = e[h].x == -kInf ? 1.0f : ex2(e[h].x - up);
+              top[h] = up;
+              sum[h] = sum[h] * fa + e[h].y * fb;
+#pragma unroll
+              for (int k = 0; k < kVec; ++k) acc[h][k] = acc[h][k] * fa + v[h][k] * fb;
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < kHeads; ++h) {
+            if (h >= nheads) continue;
+            if (lane == 0) {
+              ml[warp][h][0] = top[h];
+              ml[warp][h][1] = sum[h];
+            }
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) o_join[(warp * NT * 8 + h) * S::kOStride + lane * kVec + k] = acc[h][k];
+          }
+          __syncthreads();
+          join(finish);
         }
       }
       __syncthreads();  // the join buffer is free again
       fresh = true;
       seg_begin = seg_end;
     }
-    if (u + 1 < end) advance<S::kTile>(p, cur);
+    cur = next;
   }
   cp_async_wait_group<0>();
 }
