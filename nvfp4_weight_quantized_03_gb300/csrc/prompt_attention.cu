@@ -37,6 +37,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -93,7 +94,41 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Two fp32 operations in one instruction, each rounded as a single one.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 // 16 or 32 columns of this thread's lane without waiting for them.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
@@ -105,6 +140,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
+}
+
+// Ties registers to this place: their readers cannot be moved above it (and so
+// not above the wait for the load that fills them).
+template <int N>
+__device__ __forceinline__ void pin(float* v) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile(""
+                 : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
+                   "+f"(v[i + 6]), "+f"(v[i + 7]));
 }
 
 // Descriptor of an operand whose rows run along the contraction (v: [key][64
@@ -257,6 +303,112 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float kInf = __int_as_float(0x7f800000);
     float mc = -kInf, l = 0.0f;  // the reference in base-2 units and the sum of 2^(s - m)
     bool ok = true;
+    // The values of the diagonal tile (load u of the ring), looked through for
+    // elements that are not finite; a thread takes one key's row.
+    auto clean_values = [&](int u) -> bool {
+      const int s = u % S::kSlots;
+      const bool here = mbar_wait_a(full(s), (u / S::kSlots) & 1, abort_flag, p.status);
+      __syncwarp();
+      if (!here) return false;
+      const uint32_t row = sbase + S::kRing + s * S::kTile + r * 128;
+      bool bad = false;
+#pragma unroll 4
+      for (int q = 0; q < S::kPanels * 8; ++q) {
+        const uint4 w = lds128(row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4));
+        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bad |= (a[e] & 0x7F800000u) == 0x7F800000u || (a[e] & 0x7F80u) == 0x7F80u;
+      }
+      if (bad) {
+        *dirty = 1;
+        for (int q = 0; q < S::kPanels * 8; ++q) {
+          const uint32_t at = row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4);
+          uint4 w = lds128(at);
+          uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if ((a[e] & 0x7F800000u) == 0x7F800000u) a[e] &= 0x0000FFFFu;
+            if ((a[e] & 0x7F80u) == 0x7F80u) a[e] &= 0xFFFF0000u;
+          }
+          sts128(at, make_uint4(a[0], a[1], a[2], a[3]));
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      return true;
+    };
+    // One key tile: scores in, weights out, l and (rarely) the reference moved.
+    auto step = [&](auto masked, int j) {
+      constexpr bool kMasked = decltype(masked)::value;  // the diagonal tile: keys past r are left out
+      float x[128];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32(s_t + q * 32, x + q * 32);
+      if (kMasked) ok = clean_values(2 * j + 1) && ok;  // while the scores arrive
+      tmem_ld_wait();
+      pin<128>(x);
+      if (kMasked) {
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+          if (e > r) x[e] = -kInf;
+      }
+      float t4[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        t4[q] = max3(x[q * 32], x[q * 32 + 1], x[q * 32 + 2]);
+#pragma unroll
+        for (int e = 3; e < 31; e += 2) t4[q] = max3(t4[q], x[q * 32 + e], x[q * 32 + e + 1]);
+        t4[q] = fmaxf(t4[q], x[q * 32 + 31]);
+      }
+      const float top = max3(fmaxf(t4[0], t4[1]), t4[2], t4[3]);
+      const float tc = top == -kInf ? -kInf : top * p.c;
+      if (__any_sync(~0u, tc > mc + kSlack)) {
+        const float up = fmaxf(mc, tc);
+        if (j > 0) {
+          const float f = mc == up ? 1.0f : ex2(mc - up);
+          l *= f;
+#pragma unroll 1
+          for (int q = 0; q < D / 16; ++q) {
+            float v[16];
+            tmem_ld16(o_t + q * 16, v);
+            tmem_ld_wait();
+            pin<16>(v);
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e] * f);
+            tmem_st_x16(o_t + q * 16, w);
+          }
+        }
+        mc = up;
+      }
+      const float sub = mc == -kInf ? 0.0f : mc;
+      const uint64_t c2 = pair(p.c, p.c), sub2 = pair(-sub, -sub);
+      uint64_t sums[2] = {0, 0};  // two chains of two fp32 sums
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float a, b;
+          unpair(fma2(pair(x[q * 32 + 2 * e], x[q * 32 + 2 * e + 1]), c2, sub2), a, b);
+          if (kMasked) {  // once more: c may be 0
+            if (q * 32 + 2 * e > r) a = -kInf;
+            if (q * 32 + 2 * e + 1 > r) b = -kInf;
+          }
+          a = ex2(a);
+          b = ex2(b);
+          sums[e & 1] = add2(sums[e & 1], pair(a, b));
+          w[e] = pack_bf16(a, b);
+        }
+        tmem_st_x16(s_t + q * 16, w);
+      }
+      float s0, s1;
+      unpair(add2(sums[0], sums[1]), s0, s1);
+      l += s0 + s1;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_a(p_full(i));
+    };
     for (int j = 0; j < mine; ++j) {
       if (!mbar_wait_a(s_full(i), j & 1, abort_flag, p.status)) {
         ok = false;
@@ -264,98 +416,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       tc_fence_after();
-      float x[128];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32(s_t + q * 32, x + q * 32);
-      const bool diagonal = j + 1 == mine;
-      if (diagonal) {
-        // Look through this tile's values while the scores arrive.
-        const int u = 2 * j + 1, s = u % S::kSlots;
-        if (!mbar_wait_a(full(s), (u / S::kSlots) & 1, abort_flag, p.status)) ok = false;
-        __syncwarp();
-        if (ok) {
-          const uint32_t row = sbase + S::kRing + s * S::kTile + r * 128;
-          bool bad = false;
-#pragma unroll 4
-          for (int q = 0; q < S::kPanels * 8; ++q) {
-            const uint4 w = lds128(row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4));
-            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              bad |= (a[e] & 0x7F800000u) == 0x7F800000u || (a[e] & 0x7F80u) == 0x7F80u;
-          }
-          if (bad) {
-            *dirty = 1;
-            for (int q = 0; q < S::kPanels * 8; ++q) {
-              const uint32_t at = row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4);
-              uint4 w = lds128(at);
-              uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((a[e] & 0x7F800000u) == 0x7F800000u) a[e] &= 0x0000FFFFu;
-                if ((a[e] & 0x7F80u) == 0x7F80u) a[e] &= 0xFFFF0000u;
-              }
-              sts128(at, make_uint4(a[0], a[1], a[2], a[3]));
-            }
-            fence_proxy_async_smem();
-          }
-        }
-        __syncwarp();
-      }
-      tmem_ld_wait();
-      if (diagonal) {
-#pragma unroll
-        for (int e = 0; e < 128; ++e)
-          if (e > r) x[e] = -kInf;
-      }
-      float top = fmaxf(x[0], x[1]);
-#pragma unroll
-      for (int e = 2; e < 128; e += 2) top = fmaxf(top, fmaxf(x[e], x[e + 1]));
-      const float tc = top == -kInf ? -kInf : top * p.c;
-      if (__any_sync(~0u, tc > mc + kSlack)) {
-        const float up = fmaxf(mc, tc);
-        if (j > 0) {
-          const float f = mc == up ? 1.0f : ex2(mc - up);
-          l *= f;
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            float v[32];
-            tmem_ld32(o_t + q * 32, v);
-            tmem_ld_wait();
-            uint32_t w[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(v[e] * f);
-            tmem_st_x32(o_t + q * 32, w);
-          }
-        }
-        mc = up;
-      }
-      const float sub = mc == -kInf ? 0.0f : mc;
-      float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t w[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          float a = fmaf(x[q * 64 + 2 * e], p.c, -sub), b = fmaf(x[q * 64 + 2 * e + 1], p.c, -sub);
-          if (diagonal) {  // also where c is 0
-            if (q * 64 + 2 * e > r) a = -kInf;
-            if (q * 64 + 2 * e + 1 > r) b = -kInf;
-          }
-          a = ex2(a);
-          b = ex2(b);
-          sum0 += a;
-          sum1 += b;
-          w[e] = pack_bf16(a, b);
-        }
-        tmem_st_x32(s_t + q * 32, w);
-      }
-      l += sum0 + sum1;
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_a(p_full(i));
-      if (!ok) break;
+      if (j + 1 < mine)
+        step(std::false_type{}, j);
+      else
+        step(std::true_type{}, j);
     }
     ok = ok && mine > 0 && mbar_wait_a(o_full(i), 0, abort_flag, p.status);
     __syncwarp();
@@ -371,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float v[32];
         tmem_ld32(o_t + q * 32, v);
         tmem_ld_wait();
+        pin<32>(v);
         if (fix && live) {
           for (int j = (n0 - 1) * kRows; j <= rs; ++j) {
             const __nv_bfloat16* src = p.v + static_cast<int64_t>(it.start + j) * p.ldv + kvh * D + q * 32;
