@@ -16,8 +16,8 @@
 //                   the sum l in registers and writes the weights back as bf16
 //                   over the scores, where the second product reads them
 //   warp 8          TMA: q once, then k, v tiles through a ring
-//   warp 9          issues S_i = Q_i K^T and O_i += P_i V
-//   warps 10, 11    idle
+//   warps 9, 10     issue S_i = Q_i K^T and O_i += P_i V of tile 0, tile 1
+//   warp 11         idle
 // Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each).
 //
 // The reference m moves only when a score passes it by 2^8 (base-2 units), so
@@ -50,7 +50,7 @@ namespace {
 
 constexpr int kRows = 128;   // rows of a query tile, keys of a key tile
 constexpr int kBlock = 256;  // query rows of a CTA
-// Two softmax warpgroups and one of which two warps work (the third group
+// Two softmax warpgroups and one of which three warps work (the third group
 // exists so that registers can be moved to the softmax: at launch 384 threads
 // have 168 each; 256 * 224 + 128 * 56 = 384 * 168).
 constexpr int kThreads = 384;
@@ -166,6 +166,39 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
   return d;
 }
 
+// The issuing warps stay converged and one lane's predicate guards each
+// instruction: descriptors then live in uniform registers.  From a branch that
+// one lane takes, every product paid for moving them there (85 instead of 60
+// cycles between products of 64 cycles).
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
+}
+
 // The work of a CTA: query rows [row0, row0 + 256) of one sequence.
 struct Item {
   int start, len, t;  // the sequence's first row and length; the block's index in it
@@ -240,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* gen = smem_raw + (sbase - raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // uniform to the compiler too
 
   Item it;
   if (!find_item(p, static_cast<int64_t>(blockIdx.x) / p.heads, it)) return;  // the whole CTA
@@ -257,24 +290,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto s_full = [&](int i) { return misc + 8u * (1 + i); };
   auto p_full = [&](int i) { return misc + 8u * (3 + i); };
   auto o_full = [&](int i) { return misc + 8u * (5 + i); };
-  const uint32_t done = misc + 8u * 7;
-  const uint32_t tmem_holder = misc + 8u * 8;
+  auto turn = [&](int i) { return misc + 8u * (7 + i); };
+  const uint32_t done = misc + 8u * 9;
+  const uint32_t tmem_holder = misc + 8u * 10;
   uint8_t* misc_gen = gen + S::kBars + 16 * S::kSlots;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc_gen + 8 * 8 + 4);
-  volatile int* dirty = reinterpret_cast<volatile int*>(misc_gen + 8 * 9);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc_gen + 8 * 10 + 4);
+  volatile int* dirty = reinterpret_cast<volatile int*>(misc_gen + 8 * 11);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kSlots; ++s) {
       mbar_init_a(full(s), 1);
-      mbar_init_a(empty(s), 1);
+      mbar_init_a(empty(s), 2);
     }
     mbar_init_a(q_full, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init_a(s_full(i), 1);
       mbar_init_a(p_full(i), 4);
       mbar_init_a(o_full(i), 1);
+      mbar_init_a(turn(i), 1);
     }
-    mbar_init_a(done, 1);
+    mbar_init_a(done, 2);
     *abort_flag = 0;
     *dirty = 0;
     fence_mbarrier_init();
@@ -291,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc_gen + 8 * 8);
+  const uint32_t tmem = __shfl_sync(~0u, *reinterpret_cast<volatile uint32_t*>(misc_gen + 8 * 10), 0);
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -500,60 +535,74 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait_a(full(s), (last / S::kSlots) & 1, &no_abort, p.status);
         }
       }
-    } else if (warp == 9) {
-      if (lane == 0) {
-        const uint32_t id_s = idesc_bf16_f32(128, 128) | (p.negative ? 1u << 13 : 0u);
-        const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // v: rows along the contraction
-        auto slot = [&](int u) { return sbase + S::kRing + (u % S::kSlots) * S::kTile; };
-        auto wait_slot = [&](int u) {
-          return mbar_wait_a(full(u % S::kSlots), (u / S::kSlots) & 1, abort_flag, p.status);
-        };
-        auto scores = [&](int i, int j) {
-          const uint32_t qa = sbase + i * S::kTile, ka = slot(2 * j);
-  #pragma unroll
-          for (int d = 0; d < S::kPanels; ++d)
-  #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_f16(tmem + i * 128, sw128_kmajor_desc(qa + d * kPanel + kk * 32),
-                         sw128_kmajor_desc(ka + d * kPanel + kk * 32), id_s, d + kk > 0 ? 1u : 0u);
-          tc_commit(s_full(i));
-        };
-        auto values = [&](int i, int j) {
-          const uint32_t va = slot(2 * j + 1);
-  #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_f16_ts(tmem + 256 + i * D, tmem + i * 128 + kk * 8, sw128_mnmajor_desc(va + kk * 2048), id_o,
-                          j + kk > 0 ? 1u : 0u);
-        };
-        bool ok = mbar_wait_a(q_full, 0, abort_flag, p.status) && wait_slot(0);
-        if (ok) {
-          tc_fence_after();
-          scores(0, 0);
-          if (n1 > 0) scores(1, 0);
-          tc_commit(empty(0));
+    } else if (warp < 11) {
+      const uint32_t leader = elect_lane();
+      // Warp 9 + i issues the products of query tile i.  An issuer is held up
+      // while the tensor core works its products off; with one issuer for
+      // both tiles its waits left the tensor core idle for a quarter of the
+      // time.
+      const int i = warp - 9;
+      const int mine = i == 0 ? n0 : n1;
+      const uint32_t id_s = idesc_bf16_f32(128, 128) | (p.negative ? 1u << 13 : 0u);
+      const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // v: rows along the contraction
+      auto slot = [&](int u) { return sbase + S::kRing + (u % S::kSlots) * S::kTile; };
+      auto wait_slot = [&](int u) {
+        return mbar_wait_a(full(u % S::kSlots), (u / S::kSlots) & 1, abort_flag, p.status);
+      };
+      auto scores = [&](int j) {
+        const uint32_t qa = sbase + i * S::kTile, ka = slot(2 * j);
+#pragma unroll
+        for (int d = 0; d < S::kPanels; ++d)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss(leader, tmem + i * 128, sw128_kmajor_desc(qa + d * kPanel + kk * 32),
+                       sw128_kmajor_desc(ka + d * kPanel + kk * 32), id_s, d + kk > 0 ? 1u : 0u);
+        commit(leader, s_full(i));
+      };
+      auto values = [&](int j) {
+        const uint32_t va = slot(2 * j + 1);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(leader, tmem + 256 + i * D, tmem + i * 128 + kk * 8, sw128_mnmajor_desc(va + kk * 2048), id_o,
+                        j + kk > 0 ? 1u : 0u);
+      };
+      // A slot is free when both issuers have released it; one whose tile
+      // does not use it (fewer key tiles, or no rows) just arrives.
+      auto release = [&](int u, bool used) {
+        if (used) {
+          commit(leader, empty(u % S::kSlots));
+        } else if (leader) {
+          mbar_arrive_a(empty(u % S::kSlots));
         }
-        for (int j = 0; ok && j < n; ++j) {
-          ok = wait_slot(2 * j + 1) && (j + 1 >= n || wait_slot(2 * j + 2));
-          for (int i = 0; ok && i < 2; ++i) {
-            const int mine = i == 0 ? n0 : n1;
-            if (j >= mine) continue;
-            if (!mbar_wait_a(p_full(i), j & 1, abort_flag, p.status)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            values(i, j);
-            if (j + 1 < mine)
-              scores(i, j + 1);
-            else
-              tc_commit(o_full(i));
-          }
-          if (!ok) break;
-          tc_commit(empty((2 * j + 1) % S::kSlots));
-          if (j + 1 < n) tc_commit(empty((2 * j + 2) % S::kSlots));
-        }
-        tc_commit(done);  // also after an expired wait: arrives once the issued MMAs are done
+      };
+      bool ok = mbar_wait_a(q_full, 0, abort_flag, p.status) && wait_slot(0);
+      __syncwarp();
+      if (ok) {
+        tc_fence_after();
+        if (mine > 0) scores(0);
+        release(0, mine > 0);
       }
+      for (int j = 0; ok && j < n; ++j) {
+        ok = wait_slot(2 * j + 1) && (j + 1 >= n || wait_slot(2 * j + 2));
+        if (!ok) break;
+        if (j < mine) ok = mbar_wait_a(p_full(i), j & 1, abort_flag, p.status);
+        // Turns: tile 0's products of key tile j, then tile 1's, then tile
+        // 0's of j + 1.  Without them the two tiles fall into step, both in
+        // the softmax and then both at the tensor core.
+        if (ok && n1 > 0 && (i == 1 || j > 0)) ok = mbar_wait_a(turn(i), (i == 1 ? j : j - 1) & 1, abort_flag, p.status);
+        if (!ok) break;
+        __syncwarp();
+        if (j < mine) {
+          tc_fence_after();
+          values(j);
+        }
+        release(2 * j + 1, j < mine);
+        if (j + 1 < mine) scores(j + 1);
+        if (n1 > 0 && leader) mbar_arrive_a(turn(1 - i));
+        if (j + 1 == mine) commit(leader, o_full(i));
+        if (j + 1 < n) release(2 * j + 2, j + 1 < mine);
+      }
+      commit(leader, done);  // also after an expired wait: arrives once the issued MMAs are done
     }
   }
   __syncwarp();
