@@ -166,6 +166,25 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
   return d;
 }
 
+// mbar_wait_a that polls: the hand-overs between the softmax and the issuers
+// are on the critical path, and a parked warp takes some 300 cycles to come
+// back.  Bounded in the same way.
+__device__ __forceinline__ bool mbar_poll_a(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (mbar_test_wait_a(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_test_wait_a(bar, parity)) return true;
+    if ((i & 255u) == 0) {
+      if (*abort_flag) return false;
+      if (clock64() - t0 > QERL_WAIT_LIMIT) {
+        *abort_flag = 1;
+        record_error(status, 5);
+        return false;
+      }
+    }
+  }
+}
+
 // The issuing warps stay converged and one lane's predicate guards each
 // instruction: descriptors then live in uniform registers.  From a branch that
 // one lane takes, every product paid for moving them there (85 instead of 60
@@ -288,14 +307,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t misc = bars + 16u * S::kSlots;
   const uint32_t q_full = misc;
   auto s_full = [&](int i) { return misc + 8u * (1 + i); };
-  auto p_full = [&](int i) { return misc + 8u * (3 + i); };
-  auto o_full = [&](int i) { return misc + 8u * (5 + i); };
-  auto turn = [&](int i) { return misc + 8u * (7 + i); };
-  const uint32_t done = misc + 8u * 9;
-  const uint32_t tmem_holder = misc + 8u * 10;
+  auto p_full = [&](int i, int part) { return misc + 8u * (3 + 2 * i + part); };
+  auto o_full = [&](int i) { return misc + 8u * (7 + i); };
+  auto turn = [&](int i) { return misc + 8u * (9 + i); };
+  const uint32_t done = misc + 8u * 11;
+  const uint32_t tmem_holder = misc + 8u * 12;
   uint8_t* misc_gen = gen + S::kBars + 16 * S::kSlots;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc_gen + 8 * 10 + 4);
-  volatile int* dirty = reinterpret_cast<volatile int*>(misc_gen + 8 * 11);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc_gen + 8 * 12 + 4);
+  volatile int* dirty = reinterpret_cast<volatile int*>(misc_gen + 8 * 13);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kSlots; ++s) {
@@ -305,7 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init_a(q_full, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init_a(s_full(i), 1);
-      mbar_init_a(p_full(i), 4);
+      mbar_init_a(p_full(i, 0), 4);
+      mbar_init_a(p_full(i, 1), 4);
       mbar_init_a(o_full(i), 1);
       mbar_init_a(turn(i), 1);
     }
@@ -326,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(~0u, *reinterpret_cast<volatile uint32_t*>(misc_gen + 8 * 10), 0);
+  const uint32_t tmem = __shfl_sync(~0u, *reinterpret_cast<volatile uint32_t*>(misc_gen + 8 * 12), 0);
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -435,14 +455,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           w[e] = pack_bf16(a, b);
         }
         tmem_st_x16(s_t + q * 16, w);
+        if (q == 1 || q == 3) {  // half of the keys: the product with v may begin
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_a(p_full(i, q >> 1));
+        }
       }
       float s0, s1;
       unpair(add2(sums[0], sums[1]), s0, s1);
       l += s0 + s1;
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_a(p_full(i));
     };
     for (int j = 0; j < mine; ++j) {
       if (!mbar_wait_a(s_full(i), j & 1, abort_flag, p.status)) {
@@ -559,10 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                        sw128_kmajor_desc(ka + d * kPanel + kk * 32), id_s, d + kk > 0 ? 1u : 0u);
         commit(leader, s_full(i));
       };
-      auto values = [&](int j) {
+      auto values = [&](int j, int part) {
         const uint32_t va = slot(2 * j + 1);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
+        for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
           mma_ts(leader, tmem + 256 + i * D, tmem + i * 128 + kk * 8, sw128_mnmajor_desc(va + kk * 2048), id_o,
                         j + kk > 0 ? 1u : 0u);
       };
@@ -585,16 +607,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; ok && j < n; ++j) {
         ok = wait_slot(2 * j + 1) && (j + 1 >= n || wait_slot(2 * j + 2));
         if (!ok) break;
-        if (j < mine) ok = mbar_wait_a(p_full(i), j & 1, abort_flag, p.status);
+        if (j < mine) ok = mbar_poll_a(p_full(i, 0), j & 1, abort_flag, p.status);
         // Turns: tile 0's products of key tile j, then tile 1's, then tile
         // 0's of j + 1.  Without them the two tiles fall into step, both in
         // the softmax and then both at the tensor core.
-        if (ok && n1 > 0 && (i == 1 || j > 0)) ok = mbar_wait_a(turn(i), (i == 1 ? j : j - 1) & 1, abort_flag, p.status);
+        if (ok && n1 > 0 && (i == 1 || j > 0)) ok = mbar_poll_a(turn(i), (i == 1 ? j : j - 1) & 1, abort_flag, p.status);
         if (!ok) break;
         __syncwarp();
         if (j < mine) {
           tc_fence_after();
-          values(j);
+          values(j, 0);
+          ok = mbar_poll_a(p_full(i, 1), j & 1, abort_flag, p.status);
+          if (!ok) break;
+          __syncwarp();
+          tc_fence_after();
+          values(j, 1);
         }
         release(2 * j + 1, j < mine);
         if (j + 1 < mine) scores(j + 1);
