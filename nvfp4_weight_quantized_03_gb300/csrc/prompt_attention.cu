@@ -82,7 +82,7 @@ struct Shape {
   static constexpr int kSlots = D == 128 ? 5 : 8;
   static constexpr uint32_t kRing = 2 * kTile;
   static constexpr uint32_t kBars = kRing + kSlots * kTile;
-  static constexpr uint32_t kSmem = 1024 + kBars + 256;
+  static constexpr uint32_t kSmem = 1024 + kBars + 384;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -284,6 +284,10 @@ __device__ __forceinline__ bool find_item(const PromptParams& p, int64_t rank, I
   return false;
 }
 
+// A CTA works through items (query blocks x heads) until none are left; the
+// softmax, the issuers and the loads each run ahead as far as their buffers
+// allow, so an item's first loads and products overlap the end of the one
+// before it.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ PromptMaps maps, const PromptParams p) {
@@ -294,44 +298,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* gen = smem_raw + (sbase - raw);
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // uniform to the compiler too
 
-  Item it;
-  if (!find_item(p, static_cast<int64_t>(blockIdx.x) / p.heads, it)) return;  // the whole CTA
-  const int head = static_cast<int>(blockIdx.x % p.heads), kvh = head / p.group;
-  const int n0 = 2 * it.t + 1;                                         // key tiles of query tile 0
-  const int n1 = it.t * kBlock + kRows < it.len ? 2 * it.t + 2 : 0;    // of query tile 1 (0: no such rows)
-  const int n = max(n0, n1);
-
   const uint32_t bars = sbase + S::kBars;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (S::kSlots + s); };
   const uint32_t misc = bars + 16u * S::kSlots;
-  const uint32_t q_full = misc;
-  auto s_full = [&](int i) { return misc + 8u * (1 + i); };
-  auto p_full = [&](int i, int part) { return misc + 8u * (3 + 2 * i + part); };
-  auto o_full = [&](int i) { return misc + 8u * (7 + i); };
-  auto turn = [&](int i) { return misc + 8u * (9 + i); };
-  const uint32_t done = misc + 8u * 11;
-  const uint32_t tmem_holder = misc + 8u * 12;
+  auto s_full = [&](int i) { return misc + 8u * i; };
+  auto p_full = [&](int i, int part) { return misc + 8u * (2 + 2 * i + part); };
+  auto o_full = [&](int i) { return misc + 8u * (6 + i); };
+  auto turn = [&](int i) { return misc + 8u * (8 + i); };
+  auto q_full = [&](int i) { return misc + 8u * (10 + i); };
+  auto q_empty = [&](int i) { return misc + 8u * (12 + i); };
+  auto item_full = [&](int e) { return misc + 8u * (14 + e); };
+  auto item_empty = [&](int e) { return misc + 8u * (16 + e); };
+  const uint32_t done = misc + 8u * 18;
+  const uint32_t tmem_holder = misc + 8u * 19;
   uint8_t* misc_gen = gen + S::kBars + 16 * S::kSlots;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc_gen + 8 * 12 + 4);
-  volatile int* dirty = reinterpret_cast<volatile int*>(misc_gen + 8 * 13);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc_gen + 8 * 19 + 4);
+  volatile int* dirty = reinterpret_cast<volatile int*>(misc_gen + 8 * 20);         // [4]: item k's at k & 3 is k + 1
+  volatile int* items = reinterpret_cast<volatile int*>(misc_gen + 8 * 20 + 16);    // [2][4]
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kSlots; ++s) {
       mbar_init_a(full(s), 1);
       mbar_init_a(empty(s), 2);
     }
-    mbar_init_a(q_full, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init_a(s_full(i), 1);
       mbar_init_a(p_full(i, 0), 4);
       mbar_init_a(p_full(i, 1), 4);
       mbar_init_a(o_full(i), 1);
       mbar_init_a(turn(i), 1);
+      mbar_init_a(q_full(i), 1);
+      mbar_init_a(q_empty(i), 1);
+      mbar_init_a(item_full(i), 1);
+      mbar_init_a(item_empty(i), 10);  // 8 softmax warps and 2 issuers
     }
     mbar_init_a(done, 2);
     *abort_flag = 0;
-    *dirty = 0;
+    for (int i = 0; i < 4; ++i) dirty[i] = 0;
     fence_mbarrier_init();
   }
   if (warp == 9) {
@@ -346,212 +350,265 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(~0u, *reinterpret_cast<volatile uint32_t*>(misc_gen + 8 * 12), 0);
+  const uint32_t tmem = __shfl_sync(~0u, *reinterpret_cast<volatile uint32_t*>(misc_gen + 8 * 19), 0);
+
+  // The item in hand, read from the ring by a whole warp; false: no more.
+  struct Work {
+    Item it;
+    int head, n0, n1;  // key tiles of query tile 0, 1 (0: it has no rows)
+  };
+  auto take = [&](int k, Work& w) -> bool {
+    const int e = k & 1;
+    if (!mbar_wait_a(item_full(e), (k >> 1) & 1, abort_flag, p.status)) return false;
+    w.it.start = items[e * 4];
+    w.it.len = items[e * 4 + 1];
+    w.it.t = items[e * 4 + 2];
+    w.head = items[e * 4 + 3];
+    w.n0 = 2 * w.it.t + 1;
+    w.n1 = w.it.t * kBlock + kRows < w.it.len ? 2 * w.it.t + 2 : 0;
+    __syncwarp();
+    if (lane == 0) mbar_arrive_a(item_empty(e));
+    return w.it.len > 0;
+  };
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int i = warp >> 2;  // query tile
-    const int mine = i == 0 ? n0 : n1;
+    const int i = warp >> 2;               // query tile
     const int r = (warp & 3) * 32 + lane;  // row of the tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_t = tmem + lanes + i * 128, o_t = tmem + lanes + 256 + i * D;
     const float kInf = __int_as_float(0x7f800000);
-    float mc = -kInf, l = 0.0f;  // the reference in base-2 units and the sum of 2^(s - m)
     bool ok = true;
-    // The values of the diagonal tile (load u of the ring), looked through for
-    // elements that are not finite; a thread takes one key's row.
-    auto clean_values = [&](int u) -> bool {
-      const int s = u % S::kSlots;
-      const bool here = mbar_wait_a(full(s), (u / S::kSlots) & 1, abort_flag, p.status);
-      __syncwarp();
-      if (!here) return false;
-      const uint32_t row = sbase + S::kRing + s * S::kTile + r * 128;
-      bool bad = false;
+    int tiles_done = 0, outputs_done = 0, u0 = 0;  // of this query tile; loads of the ring before this item
+    Work w;
+    for (int k = 0; ok && take(k, w); ++k) {
+      const int mine = i == 0 ? w.n0 : w.n1;
+      float mc = -kInf, l = 0.0f;  // the reference in base-2 units and the sum of 2^(s - m)
+      // The values of the diagonal tile (load u of the ring), looked through for
+      // elements that are not finite; a thread takes one key's row.
+      auto clean_values = [&](int u) -> bool {
+        const int s = u % S::kSlots;
+        const bool here = mbar_wait_a(full(s), (u / S::kSlots) & 1, abort_flag, p.status);
+        __syncwarp();
+        if (!here) return false;
+        const uint32_t row = sbase + S::kRing + s * S::kTile + r * 128;
+        bool bad = false;
 #pragma unroll 4
-      for (int q = 0; q < S::kPanels * 8; ++q) {
-        const uint4 w = lds128(row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4));
-        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) bad |= (a[e] & 0x7F800000u) == 0x7F800000u || (a[e] & 0x7F80u) == 0x7F80u;
-      }
-      if (bad) {
-        *dirty = 1;
         for (int q = 0; q < S::kPanels * 8; ++q) {
-          const uint32_t at = row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4);
-          uint4 w = lds128(at);
-          uint32_t a[4] = {w.x, w.y, w.z, w.w};
+          const uint4 w = lds128(row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4));
+          const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if ((a[e] & 0x7F800000u) == 0x7F800000u) a[e] &= 0x0000FFFFu;
-            if ((a[e] & 0x7F80u) == 0x7F80u) a[e] &= 0xFFFF0000u;
+          for (int e = 0; e < 4; ++e) bad |= (a[e] & 0x7F800000u) == 0x7F800000u || (a[e] & 0x7F80u) == 0x7F80u;
+        }
+        if (bad) {
+          dirty[k & 3] = k + 1;
+          for (int q = 0; q < S::kPanels * 8; ++q) {
+            const uint32_t at = row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4);
+            uint4 w = lds128(at);
+            uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if ((a[e] & 0x7F800000u) == 0x7F800000u) a[e] &= 0x0000FFFFu;
+              if ((a[e] & 0x7F80u) == 0x7F80u) a[e] &= 0xFFFF0000u;
+            }
+            sts128(at, make_uint4(a[0], a[1], a[2], a[3]));
           }
-          sts128(at, make_uint4(a[0], a[1], a[2], a[3]));
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
-      }
-      __syncwarp();
-      return true;
-    };
-    // One key tile: scores in, weights out, l and (rarely) the reference moved.
-    auto step = [&](auto masked, int j) {
-      constexpr bool kMasked = decltype(masked)::value;  // the diagonal tile: keys past r are left out
-      float x[128];
+        __syncwarp();
+        return true;
+      };
+      // One key tile: scores in, weights out, l and (rarely) the reference moved.
+      auto step = [&](auto masked, int j) {
+        constexpr bool kMasked = decltype(masked)::value;  // the diagonal tile: keys past r are left out
+        float x[128];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32(s_t + q * 32, x + q * 32);
-      if (kMasked) ok = clean_values(2 * j + 1) && ok;  // while the scores arrive
-      tmem_ld_wait();
-      pin<128>(x);
-      if (kMasked) {
-#pragma unroll
-        for (int e = 0; e < 128; ++e)
-          if (e > r) x[e] = -kInf;
-      }
-      float t4[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        t4[q] = max3(x[q * 32], x[q * 32 + 1], x[q * 32 + 2]);
-#pragma unroll
-        for (int e = 3; e < 31; e += 2) t4[q] = max3(t4[q], x[q * 32 + e], x[q * 32 + e + 1]);
-        t4[q] = fmaxf(t4[q], x[q * 32 + 31]);
-      }
-      const float top = max3(fmaxf(t4[0], t4[1]), t4[2], t4[3]);
-      const float tc = top == -kInf ? -kInf : top * p.c;
-      if (__any_sync(~0u, tc > mc + kSlack)) {
-        const float up = fmaxf(mc, tc);
-        if (j > 0) {
-          const float f = mc == up ? 1.0f : ex2(mc - up);
-          l *= f;
-#pragma unroll 1
-          for (int q = 0; q < D / 16; ++q) {
-            float v[16];
-            tmem_ld16(o_t + q * 16, v);
-            tmem_ld_wait();
-            pin<16>(v);
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e] * f);
-            tmem_st_x16(o_t + q * 16, w);
-          }
-        }
-        mc = up;
-      }
-      const float sub = mc == -kInf ? 0.0f : mc;
-      const uint64_t c2 = pair(p.c, p.c), sub2 = pair(-sub, -sub);
-      uint64_t sums[2] = {0, 0};  // two chains of two fp32 sums
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float a, b;
-          unpair(fma2(pair(x[q * 32 + 2 * e], x[q * 32 + 2 * e + 1]), c2, sub2), a, b);
-          if (kMasked) {  // once more: c may be 0
-            if (q * 32 + 2 * e > r) a = -kInf;
-            if (q * 32 + 2 * e + 1 > r) b = -kInf;
-          }
-          a = ex2(a);
-          b = ex2(b);
-          sums[e & 1] = add2(sums[e & 1], pair(a, b));
-          w[e] = pack_bf16(a, b);
-        }
-        tmem_st_x16(s_t + q * 16, w);
-        if (q == 1 || q == 3) {  // half of the keys: the product with v may begin
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_a(p_full(i, q >> 1));
-        }
-      }
-      float s0, s1;
-      unpair(add2(sums[0], sums[1]), s0, s1);
-      l += s0 + s1;
-    };
-    for (int j = 0; j < mine; ++j) {
-      if (!mbar_wait_a(s_full(i), j & 1, abort_flag, p.status)) {
-        ok = false;
-        break;
-      }
-      __syncwarp();
-      tc_fence_after();
-      if (j + 1 < mine)
-        step(std::false_type{}, j);
-      else
-        step(std::true_type{}, j);
-    }
-    ok = ok && mine > 0 && mbar_wait_a(o_full(i), 0, abort_flag, p.status);
-    __syncwarp();
-    if (mine > 0) {
-      tc_fence_after();
-      const int rs = it.t * kBlock + i * kRows + r;  // row in the sequence
-      const bool live = ok && rs < it.len;
-      const bool fix = *dirty != 0;
-      const float f = l == 0.0f ? 0.0f : 1.0f / l;
-      const uint32_t stage = sbase + i * S::kTile + (warp & 3) * 32 * (D * 2);  // this warp's rows of the q tile
-#pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
-        float v[32];
-        tmem_ld32(o_t + q * 32, v);
+        for (int q = 0; q < 4; ++q) tmem_ld32(s_t + q * 32, x + q * 32);
+        if (kMasked) ok = clean_values(u0 + 2 * j + 1) && ok;  // while the scores arrive
         tmem_ld_wait();
-        pin<32>(v);
-        if (fix && live) {
-          for (int j = (n0 - 1) * kRows; j <= rs; ++j) {
-            const __nv_bfloat16* src = p.v + static_cast<int64_t>(it.start + j) * p.ldv + kvh * D + q * 32;
+        pin<128>(x);
+        if (kMasked) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float y = __bfloat162float(src[e]);
-              if (!(fabsf(y) < kInf)) v[e] += y;
+          for (int e = 0; e < 128; ++e)
+            if (e > r) x[e] = -kInf;
+        }
+        float t4[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          t4[q] = max3(x[q * 32], x[q * 32 + 1], x[q * 32 + 2]);
+#pragma unroll
+          for (int e = 3; e < 31; e += 2) t4[q] = max3(t4[q], x[q * 32 + e], x[q * 32 + e + 1]);
+          t4[q] = fmaxf(t4[q], x[q * 32 + 31]);
+        }
+        const float top = max3(fmaxf(t4[0], t4[1]), t4[2], t4[3]);
+        const float tc = top == -kInf ? -kInf : top * p.c;
+        if (__any_sync(~0u, tc > mc + kSlack)) {
+          const float up = fmaxf(mc, tc);
+          if (j > 0) {
+            const float f = mc == up ? 1.0f : ex2(mc - up);
+            l *= f;
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              float v[16];
+              tmem_ld16(o_t + q * 16, v);
+              tmem_ld_wait();
+              pin<16>(v);
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e] * f);
+              tmem_st_x16(o_t + q * 16, w);
             }
           }
+          mc = up;
         }
+        const float sub = mc == -kInf ? 0.0f : mc;
+        const uint64_t c2 = pair(p.c, p.c), sub2 = pair(-sub, -sub);
+        uint64_t sums[2] = {0, 0};  // two chains of two fp32 sums
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint4 w = make_uint4(pack_bf16(v[8 * e] * f, v[8 * e + 1] * f), pack_bf16(v[8 * e + 2] * f, v[8 * e + 3] * f),
-                                     pack_bf16(v[8 * e + 4] * f, v[8 * e + 5] * f),
-                                     pack_bf16(v[8 * e + 6] * f, v[8 * e + 7] * f));
-          sts128(stage + lane * (D * 2) + (((q * 4 + e) ^ (lane & 7)) << 4), w);
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float a, b;
+            unpair(fma2(pair(x[q * 32 + 2 * e], x[q * 32 + 2 * e + 1]), c2, sub2), a, b);
+            if (kMasked) {  // once more: c may be 0
+              if (q * 32 + 2 * e > r) a = -kInf;
+              if (q * 32 + 2 * e + 1 > r) b = -kInf;
+            }
+            a = ex2(a);
+            b = ex2(b);
+            sums[e & 1] = add2(sums[e & 1], pair(a, b));
+            w[e] = pack_bf16(a, b);
+          }
+          tmem_st_x16(s_t + q * 16, w);
+          if (q == 1 || q == 3) {  // half of the keys: the product with v may begin
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_a(p_full(i, q >> 1));
+          }
         }
+        float s0, s1;
+        unpair(add2(sums[0], sums[1]), s0, s1);
+        l += s0 + s1;
+      };
+
+      for (int j = 0; j < mine; ++j) {
+        if (!mbar_wait_a(s_full(i), (tiles_done + j) & 1, abort_flag, p.status)) ok = false;
+        __syncwarp();
+        if (!ok) break;
+        tc_fence_after();
+        if (j + 1 < mine)
+          step(std::false_type{}, j);
+        else
+          step(std::true_type{}, j);
       }
-      if (live && p.lse != nullptr)
-        p.lse[static_cast<int64_t>(it.start + rs) * p.heads + head] =
-            l == 0.0f ? -kInf : (mc + log2f(l)) * 0.69314718055994530942f;
-      __syncwarp();
-      // Rows of D * 2 bytes, D / 8 lanes a row.
-      constexpr int kPer = 32 / (D / 8);
-      const int first = it.t * kBlock + i * kRows + (warp & 3) * 32;
-#pragma unroll 4
-      for (int q = 0; q < 32; q += kPer) {
-        const int row = q + lane / (D / 8), ch = lane % (D / 8);
-        const uint4 w = lds128(stage + row * (D * 2) + ((ch ^ (row & 7)) << 4));
-        if (ok && first + row < it.len)
-          *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(it.start + first + row) * p.ldo + head * D + ch * 8) = w;
+      tiles_done += mine;
+      u0 += 2 * max(w.n0, w.n1);
+      if (mine > 0) {
+        ok = ok && mbar_wait_a(o_full(i), outputs_done & 1, abort_flag, p.status);
+        ++outputs_done;
+        __syncwarp();
+        tc_fence_after();
+        const int rs = w.it.t * kBlock + i * kRows + r;  // row in the sequence
+        const bool live = ok && rs < w.it.len;
+        const bool fix = dirty[k & 3] == k + 1;
+        const float f = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t row = static_cast<int64_t>(w.it.start) + rs;
+        __nv_bfloat16* dst = p.out + row * p.ldo + w.head * D;
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          float v[32];
+          tmem_ld32(o_t + q * 32, v);
+          tmem_ld_wait();
+          pin<32>(v);
+          if (fix && live) {
+            for (int j = (w.n0 - 1) * kRows; j <= rs; ++j) {
+              const __nv_bfloat16* src =
+                  p.v + static_cast<int64_t>(w.it.start + j) * p.ldv + w.head / p.group * D + q * 32;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float y = __bfloat162float(src[e]);
+                if (!(fabsf(y) < kInf)) v[e] += y;
+              }
+            }
+          }
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(dst + q * 32 + e * 8) =
+                  make_uint4(pack_bf16(v[8 * e] * f, v[8 * e + 1] * f), pack_bf16(v[8 * e + 2] * f, v[8 * e + 3] * f),
+                             pack_bf16(v[8 * e + 4] * f, v[8 * e + 5] * f),
+                             pack_bf16(v[8 * e + 6] * f, v[8 * e + 7] * f));
+          }
+        }
+        if (live && p.lse != nullptr)
+          p.lse[row * p.heads + w.head] = l == 0.0f ? -kInf : (mc + log2f(l)) * 0.69314718055994530942f;
+        __syncwarp();
       }
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8) {
-      if (lane == 0) {
-        const int row0 = it.start + it.t * kBlock;
-        const int tiles = n1 > 0 ? 2 : 1;
-        mbar_arrive_expect_tx_a(q_full, tiles * S::kTile);
-        for (int i = 0; i < tiles; ++i)
-  #pragma unroll
-          for (int d = 0; d < S::kPanels; ++d)
-            tma_load_2d(sbase + i * S::kTile + d * kPanel, &maps.q, head * D + d * 64, row0 + i * kRows, q_full);
-        int issued = 0;
-        for (int u = 0; u < 2 * n; ++u) {  // k, v, k, v, ...
-          const int s = u % S::kSlots;
-          if (u >= S::kSlots && !mbar_wait_a(empty(s), ((u / S::kSlots) & 1) ^ 1, abort_flag, p.status)) break;
-          mbar_arrive_expect_tx_a(full(s), S::kTile);
-          const uint32_t dst = sbase + S::kRing + s * S::kTile;
-  #pragma unroll
-          for (int d = 0; d < S::kPanels; ++d)
-            tma_load_2d(dst + d * kPanel, (u & 1) ? &maps.v : &maps.k, kvh * D + d * 64, it.start + (u >> 1) * kRows,
-                        full(s));
-          issued = u + 1;
+      int issued = 0, q_loads[2] = {0, 0};
+      for (int k = 0;; ++k) {
+        // The items are dealt out in rounds, every other round backwards.
+        const int64_t g = gridDim.x, c = blockIdx.x;
+        const int64_t idx = k * g + ((k & 1) ? g - 1 - c : c);
+        Item it;
+        const bool have = find_item(p, idx / p.heads, it);
+        bool more = have;
+        if (lane == 0) {
+          const int head = static_cast<int>(idx % p.heads), e = k & 1;
+          more = k < 2 || mbar_wait_a(item_empty(e), ((k >> 1) & 1) ^ 1, abort_flag, p.status);
+          if (more) {
+            items[e * 4] = it.start;
+            items[e * 4 + 1] = have ? it.len : 0;
+            items[e * 4 + 2] = it.t;
+            items[e * 4 + 3] = head;
+            mbar_arrive_a(item_full(e));
+          }
+          more = more && have;
+          if (more) {
+            const bool second = it.t * kBlock + kRows < it.len;
+            const int n = 2 * it.t + (second ? 2 : 1);
+            for (int u = 0; more && u < 2 * n; ++u) {  // k, v, k, v, ...
+              const int at = issued, s = at % S::kSlots;
+              if (at >= S::kSlots && !mbar_wait_a(empty(s), ((at / S::kSlots) & 1) ^ 1, abort_flag, p.status)) {
+                more = false;
+                break;
+              }
+              mbar_arrive_expect_tx_a(full(s), S::kTile);
+              const uint32_t dst = sbase + S::kRing + s * S::kTile;
+#pragma unroll
+              for (int d = 0; d < S::kPanels; ++d)
+                tma_load_2d(dst + d * kPanel, (u & 1) ? &maps.v : &maps.k, head / p.group * D + d * 64,
+                            it.start + (u >> 1) * kRows, full(s));
+              ++issued;
+              if (u > 0) continue;
+              // After the first keys, the queries (their buffers come free when the last item's last scores are done).
+              for (int i = 0; more && i < (second ? 2 : 1); ++i) {
+                if (q_loads[i] > 0 && !mbar_wait_a(q_empty(i), (q_loads[i] - 1) & 1, abort_flag, p.status)) {
+                  more = false;
+                  break;
+                }
+                mbar_arrive_expect_tx_a(q_full(i), S::kTile);
+#pragma unroll
+                for (int d = 0; d < S::kPanels; ++d)
+                  tma_load_2d(sbase + i * S::kTile + d * kPanel, &maps.q, head * D + d * 64,
+                              it.start + it.t * kBlock + i * kRows, q_full(i));
+                ++q_loads[i];
+              }
+            }
+          }
         }
+        if (!__shfl_sync(~0u, static_cast<int>(more), 0)) break;
+      }
+      if (lane == 0) {
         // Every issued copy lands before the CTA exits (after an expired wait too).
         volatile int no_abort = 0;
-        mbar_wait_a(q_full, 0, &no_abort, p.status);
+        for (int i = 0; i < 2; ++i)
+          if (q_loads[i] > 0) mbar_wait_a(q_full(i), (q_loads[i] - 1) & 1, &no_abort, p.status);
         for (int s = 0; s < min(issued, S::kSlots); ++s) {
           const int last = issued - 1 - ((issued - 1 - s) % S::kSlots);
           mbar_wait_a(full(s), (last / S::kSlots) & 1, &no_abort, p.status);
@@ -564,29 +621,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       // both tiles its waits left the tensor core idle for a quarter of the
       // time.
       const int i = warp - 9;
-      const int mine = i == 0 ? n0 : n1;
       const uint32_t id_s = idesc_bf16_f32(128, 128) | (p.negative ? 1u << 13 : 0u);
       const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // v: rows along the contraction
       auto slot = [&](int u) { return sbase + S::kRing + (u % S::kSlots) * S::kTile; };
       auto wait_slot = [&](int u) {
         return mbar_wait_a(full(u % S::kSlots), (u / S::kSlots) & 1, abort_flag, p.status);
       };
-      auto scores = [&](int j) {
-        const uint32_t qa = sbase + i * S::kTile, ka = slot(2 * j);
+      auto scores = [&](int u) {
+        const uint32_t qa = sbase + i * S::kTile, ka = slot(u);
 #pragma unroll
         for (int d = 0; d < S::kPanels; ++d)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_ss(leader, tmem + i * 128, sw128_kmajor_desc(qa + d * kPanel + kk * 32),
-                       sw128_kmajor_desc(ka + d * kPanel + kk * 32), id_s, d + kk > 0 ? 1u : 0u);
+                   sw128_kmajor_desc(ka + d * kPanel + kk * 32), id_s, d + kk > 0 ? 1u : 0u);
         commit(leader, s_full(i));
       };
-      auto values = [&](int j, int part) {
-        const uint32_t va = slot(2 * j + 1);
+      auto values = [&](int u, int part, bool more) {
+        const uint32_t va = slot(u);
 #pragma unroll
         for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
           mma_ts(leader, tmem + 256 + i * D, tmem + i * 128 + kk * 8, sw128_mnmajor_desc(va + kk * 2048), id_o,
-                        j + kk > 0 ? 1u : 0u);
+                 more || kk > 0 ? 1u : 0u);
       };
       // A slot is free when both issuers have released it; one whose tile
       // does not use it (fewer key tiles, or no rows) just arrives.
@@ -597,37 +653,53 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_a(empty(u % S::kSlots));
         }
       };
-      bool ok = mbar_wait_a(q_full, 0, abort_flag, p.status) && wait_slot(0);
-      __syncwarp();
-      if (ok) {
-        tc_fence_after();
-        if (mine > 0) scores(0);
-        release(0, mine > 0);
-      }
-      for (int j = 0; ok && j < n; ++j) {
-        ok = wait_slot(2 * j + 1) && (j + 1 >= n || wait_slot(2 * j + 2));
-        if (!ok) break;
-        if (j < mine) ok = mbar_poll_a(p_full(i, 0), j & 1, abort_flag, p.status);
-        // Turns: tile 0's products of key tile j, then tile 1's, then tile
-        // 0's of j + 1.  Without them the two tiles fall into step, both in
-        // the softmax and then both at the tensor core.
-        if (ok && n1 > 0 && (i == 1 || j > 0)) ok = mbar_poll_a(turn(i), (i == 1 ? j : j - 1) & 1, abort_flag, p.status);
+      int u0 = 0, tiles_done = 0, turns = 0, q_used = 0;
+      bool ok = true;
+      Work w;
+      for (int k = 0; ok && take(k, w); ++k) {
+        const int mine = i == 0 ? w.n0 : w.n1, n = max(w.n0, w.n1);
+        if (mine > 0) {
+          ok = mbar_wait_a(q_full(i), q_used & 1, abort_flag, p.status);
+          ++q_used;
+        }
+        ok = ok && wait_slot(u0);
         if (!ok) break;
         __syncwarp();
-        if (j < mine) {
-          tc_fence_after();
-          values(j, 0);
-          ok = mbar_poll_a(p_full(i, 1), j & 1, abort_flag, p.status);
+        tc_fence_after();
+        if (mine > 0) scores(u0);
+        if (mine == 1) commit(leader, q_empty(i));
+        release(u0, mine > 0);
+        for (int j = 0; j < n; ++j) {
+          ok = wait_slot(u0 + 2 * j + 1) && (j + 1 >= n || wait_slot(u0 + 2 * j + 2));
+          if (ok && j < mine) ok = mbar_poll_a(p_full(i, 0), (tiles_done + j) & 1, abort_flag, p.status);
+          // Turns: tile 0's products of a key tile, then tile 1's, then tile
+          // 0's of the next.  Without them the two tiles fall into step, both
+          // in the softmax and then both at the tensor core.
+          if (ok && w.n1 > 0) {
+            const int before = turns - (i == 0 ? 1 : 0);
+            if (before >= 0) ok = mbar_poll_a(turn(i), before & 1, abort_flag, p.status);
+            ++turns;
+          }
           if (!ok) break;
           __syncwarp();
-          tc_fence_after();
-          values(j, 1);
+          if (j < mine) {
+            tc_fence_after();
+            values(u0 + 2 * j + 1, 0, j > 0);
+            ok = mbar_poll_a(p_full(i, 1), (tiles_done + j) & 1, abort_flag, p.status);
+            if (!ok) break;
+            __syncwarp();
+            tc_fence_after();
+            values(u0 + 2 * j + 1, 1, true);
+          }
+          release(u0 + 2 * j + 1, j < mine);
+          if (j + 1 < mine) scores(u0 + 2 * j + 2);
+          if (j + 2 == mine) commit(leader, q_empty(i));
+          if (w.n1 > 0 && leader) mbar_arrive_a(turn(1 - i));
+          if (j + 1 == mine) commit(leader, o_full(i));
+          if (j + 1 < n) release(u0 + 2 * j + 2, j + 1 < mine);
         }
-        release(2 * j + 1, j < mine);
-        if (j + 1 < mine) scores(j + 1);
-        if (n1 > 0 && leader) mbar_arrive_a(turn(1 - i));
-        if (j + 1 == mine) commit(leader, o_full(i));
-        if (j + 1 < n) release(2 * j + 2, j + 1 < mine);
+        tiles_done += mine;
+        u0 += 2 * n;
       }
       commit(leader, done);  // also after an expired wait: arrives once the issued MMAs are done
     }
@@ -671,10 +743,8 @@ bool rows_map(CUtensorMap* map, const void* base, int64_t width, int64_t rows, i
 }
 
 template <int D>
-qerl_status launch(const PromptMaps& maps, const PromptParams& p, int64_t grid, cudaStream_t s) {
+qerl_status launch(const PromptMaps& maps, const PromptParams& p, int64_t grid, int dev, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // one bit per device: the attribute belongs to the device's function
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return QERL_ERR_CUDA;
   const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
   if ((ready.load() & bit) == 0) {
     if (cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem) !=
@@ -713,9 +783,13 @@ qerl_status launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t s
   p.status = &static_cast<WsHeader*>(a.workspace)->status;
   // Every sequence has at most one block that is not full.
   const int64_t blocks = a.tokens / kBlock + std::min(a.num_seqs, a.tokens);
-  const int64_t grid = blocks * a.num_heads;
-  if (grid > INT32_MAX) return QERL_ERR_UNSUPPORTED_SHAPE;
-  return a.head_dim == 128 ? launch<128>(maps, p, grid, s) : launch<64>(maps, p, grid, s);
+  if (blocks * a.num_heads > INT32_MAX) return QERL_ERR_UNSUPPORTED_SHAPE;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return QERL_ERR_CUDA;
+  const int64_t grid = std::min<int64_t>(blocks * a.num_heads, sms);  // one resident CTA per SM
+  return a.head_dim == 128 ? launch<128>(maps, p, grid, dev, s) : launch<64>(maps, p, grid, dev, s);
 }
 
 }  // namespace qerl
