@@ -17,7 +17,7 @@
 //                   over the scores, where the second product reads them
 //   warp 8          TMA: q once, then k, v tiles through a ring
 //   warps 9, 10     issue S_i = Q_i K^T and O_i += P_i V of tile 0, tile 1
-//   warp 11         idle
+//   warp 11         finds the CTA's next items
 // Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each).
 //
 // The reference m moves only when a score passes it by 2^8 (base-2 units), so
@@ -37,7 +37,6 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
-#include <type_traits>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -50,9 +49,8 @@ namespace {
 
 constexpr int kRows = 128;   // rows of a query tile, keys of a key tile
 constexpr int kBlock = 256;  // query rows of a CTA
-// Two softmax warpgroups and one of which three warps work (the third group
-// exists so that registers can be moved to the softmax: at launch 384 threads
-// have 168 each; 256 * 224 + 128 * 56 = 384 * 168).
+// Two softmax warpgroups and one for the rest, which gives registers to them:
+// at launch 384 threads have 168 each; 256 * 224 + 128 * 56 = 384 * 168.
 constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 constexpr uint32_t kPanel = kRows * 128;  // 128 rows of 64 bf16, 128-byte swizzle
@@ -79,9 +77,10 @@ template <int D>
 struct Shape {
   static constexpr int kPanels = D / 64;
   static constexpr uint32_t kTile = kPanels * kPanel;
-  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kSlots = D == 128 ? 4 : 8;
   static constexpr uint32_t kRing = 2 * kTile;
-  static constexpr uint32_t kBars = kRing + kSlots * kTile;
+  static constexpr uint32_t kStage = kRing + kSlots * kTile;  // 64 output columns of each query tile
+  static constexpr uint32_t kBars = kStage + 2 * kPanel;
   static constexpr uint32_t kSmem = 1024 + kBars + 384;
 };
 
@@ -98,6 +97,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
+}
+// x * 0 + c for two bf16
+__device__ __forceinline__ uint32_t times0_plus(uint32_t x, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(0u), "r"(c));
+  return d;
 }
 // Two fp32 operations in one instruction, each rounded as a single one.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
@@ -331,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init_a(q_full(i), 1);
       mbar_init_a(q_empty(i), 1);
       mbar_init_a(item_full(i), 1);
-      mbar_init_a(item_empty(i), 10);  // 8 softmax warps and 2 issuers
+      mbar_init_a(item_empty(i), 11);  // 8 softmax warps, the loads and 2 issuers
     }
     mbar_init_a(done, 2);
     *abort_flag = 0;
@@ -392,14 +397,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (!here) return false;
         const uint32_t row = sbase + S::kRing + s * S::kTile + r * 128;
-        bool bad = false;
-#pragma unroll 4
+        // x * 0 + sum is NaN from the first x that is not finite
+        uint32_t sum = 0;
+#pragma unroll
         for (int q = 0; q < S::kPanels * 8; ++q) {
           const uint4 w = lds128(row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4));
-          const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) bad |= (a[e] & 0x7F800000u) == 0x7F800000u || (a[e] & 0x7F80u) == 0x7F80u;
+          sum = times0_plus(w.x, sum);
+          sum = times0_plus(w.y, sum);
+          sum = times0_plus(w.z, sum);
+          sum = times0_plus(w.w, sum);
         }
+        const bool bad = (sum & 0x7FFF7FFFu) != 0;
         if (bad) {
           dirty[k & 3] = k + 1;
           for (int q = 0; q < S::kPanels * 8; ++q) {
@@ -419,18 +427,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       // One key tile: scores in, weights out, l and (rarely) the reference moved.
-      auto step = [&](auto masked, int j) {
-        constexpr bool kMasked = decltype(masked)::value;  // the diagonal tile: keys past r are left out
+      auto step = [&](int j) {
         float x[128];
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32(s_t + q * 32, x + q * 32);
-        if (kMasked) ok = clean_values(u0 + 2 * j + 1) && ok;  // while the scores arrive
         tmem_ld_wait();
         pin<128>(x);
-        if (kMasked) {
+        if (j + 1 == mine) {  // the diagonal tile: keys past r are left out
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (e > r) x[e] = -kInf;
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t keep = r >= q * 32 + 31 ? ~0u : r < q * 32 ? 0u : (2u << (r - q * 32)) - 1;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((keep & (1u << e)) == 0) x[q * 32 + e] = -kInf;
+          }
         }
         float t4[4];
 #pragma unroll
@@ -471,10 +481,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 16; ++e) {
             float a, b;
             unpair(fma2(pair(x[q * 32 + 2 * e], x[q * 32 + 2 * e + 1]), c2, sub2), a, b);
-            if (kMasked) {  // once more: c may be 0
-              if (q * 32 + 2 * e > r) a = -kInf;
-              if (q * 32 + 2 * e + 1 > r) b = -kInf;
-            }
             a = ex2(a);
             b = ex2(b);
             sums[e & 1] = add2(sums[e & 1], pair(a, b));
@@ -494,14 +500,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
 
       for (int j = 0; j < mine; ++j) {
-        if (!mbar_wait_a(s_full(i), (tiles_done + j) & 1, abort_flag, p.status)) ok = false;
+        if (j + 1 == mine) ok = clean_values(u0 + 2 * j + 1);  // while the scores are computed
+        ok = ok && mbar_wait_a(s_full(i), (tiles_done + j) & 1, abort_flag, p.status);
         __syncwarp();
         if (!ok) break;
         tc_fence_after();
-        if (j + 1 < mine)
-          step(std::false_type{}, j);
-        else
-          step(std::true_type{}, j);
+        step(j);
       }
       tiles_done += mine;
       u0 += 2 * max(w.n0, w.n1);
@@ -515,32 +519,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool fix = dirty[k & 3] == k + 1;
         const float f = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t row = static_cast<int64_t>(w.it.start) + rs;
-        __nv_bfloat16* dst = p.out + row * p.ldo + w.head * D;
+        // 64 columns at a time through shared memory, so that a store covers
+        // whole lines (a thread's own row, 16 bytes a store, took 4 times as
+        // long).  Each warp uses its own 32 rows of the buffer.
+        const uint32_t stage = sbase + S::kStage + i * kPanel + (warp & 3) * 32 * 128;
+        const int first = rs - lane;
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          float v[32];
-          tmem_ld32(o_t + q * 32, v);
+        for (int h = 0; h < D / 64; ++h) {
+          float v[64];
+          tmem_ld32(o_t + h * 64, v);
+          tmem_ld32(o_t + h * 64 + 32, v + 32);
           tmem_ld_wait();
-          pin<32>(v);
+          pin<64>(v);
           if (fix && live) {
             for (int j = (w.n0 - 1) * kRows; j <= rs; ++j) {
               const __nv_bfloat16* src =
-                  p.v + static_cast<int64_t>(w.it.start + j) * p.ldv + w.head / p.group * D + q * 32;
+                  p.v + static_cast<int64_t>(w.it.start + j) * p.ldv + w.head / p.group * D + h * 64;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
+              for (int e = 0; e < 64; ++e) {
                 const float y = __bfloat162float(src[e]);
                 if (!(fabsf(y) < kInf)) v[e] += y;
               }
             }
           }
-          if (live) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(dst + q * 32 + e * 8) =
-                  make_uint4(pack_bf16(v[8 * e] * f, v[8 * e + 1] * f), pack_bf16(v[8 * e + 2] * f, v[8 * e + 3] * f),
-                             pack_bf16(v[8 * e + 4] * f, v[8 * e + 5] * f),
-                             pack_bf16(v[8 * e + 6] * f, v[8 * e + 7] * f));
+          for (int e = 0; e < 8; ++e)
+            sts128(stage + lane * 128 + ((e ^ (lane & 7)) << 4),
+                   make_uint4(pack_bf16(v[8 * e] * f, v[8 * e + 1] * f), pack_bf16(v[8 * e + 2] * f, v[8 * e + 3] * f),
+                              pack_bf16(v[8 * e + 4] * f, v[8 * e + 5] * f),
+                              pack_bf16(v[8 * e + 6] * f, v[8 * e + 7] * f)));
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 32; q += 4) {
+            const int at = q + (lane >> 3), ch = lane & 7;
+            const uint4 y = lds128(stage + at * 128 + ((ch ^ (at & 7)) << 4));
+            if (ok && first + at < w.it.len)
+              *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(w.it.start) + first + at) * p.ldo + w.head * D +
+                                        h * 64 + ch * 8) = y;
           }
+          __syncwarp();
         }
         if (live && p.lse != nullptr)
           p.lse[row * p.heads + w.head] = l == 0.0f ? -kInf : (mc + log2f(l)) * 0.69314718055994530942f;
@@ -551,58 +568,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8) {
       int issued = 0, q_loads[2] = {0, 0};
-      for (int k = 0;; ++k) {
-        // The items are dealt out in rounds, every other round backwards.
-        const int64_t g = gridDim.x, c = blockIdx.x;
-        const int64_t idx = k * g + ((k & 1) ? g - 1 - c : c);
-        Item it;
-        const bool have = find_item(p, idx / p.heads, it);
-        bool more = have;
+      Work w;
+      for (int k = 0; take(k, w); ++k) {
+        bool ok = true;
         if (lane == 0) {
-          const int head = static_cast<int>(idx % p.heads), e = k & 1;
-          more = k < 2 || mbar_wait_a(item_empty(e), ((k >> 1) & 1) ^ 1, abort_flag, p.status);
-          if (more) {
-            items[e * 4] = it.start;
-            items[e * 4 + 1] = have ? it.len : 0;
-            items[e * 4 + 2] = it.t;
-            items[e * 4 + 3] = head;
-            mbar_arrive_a(item_full(e));
-          }
-          more = more && have;
-          if (more) {
-            const bool second = it.t * kBlock + kRows < it.len;
-            const int n = 2 * it.t + (second ? 2 : 1);
-            for (int u = 0; more && u < 2 * n; ++u) {  // k, v, k, v, ...
-              const int at = issued, s = at % S::kSlots;
-              if (at >= S::kSlots && !mbar_wait_a(empty(s), ((at / S::kSlots) & 1) ^ 1, abort_flag, p.status)) {
-                more = false;
-                break;
-              }
-              mbar_arrive_expect_tx_a(full(s), S::kTile);
-              const uint32_t dst = sbase + S::kRing + s * S::kTile;
+          const int n = max(w.n0, w.n1);
+          for (int u = 0; ok && u < 2 * n; ++u) {  // k, v, k, v, ...
+            const int s = issued % S::kSlots;
+            if (issued >= S::kSlots) ok = mbar_wait_a(empty(s), ((issued / S::kSlots) & 1) ^ 1, abort_flag, p.status);
+            if (!ok) break;
+            mbar_arrive_expect_tx_a(full(s), S::kTile);
+            const uint32_t dst = sbase + S::kRing + s * S::kTile;
+#pragma unroll
+            for (int d = 0; d < S::kPanels; ++d)
+              tma_load_2d(dst + d * kPanel, (u & 1) ? &maps.v : &maps.k, w.head / p.group * D + d * 64,
+                          w.it.start + (u >> 1) * kRows, full(s));
+            ++issued;
+            if (u > 0) continue;
+            // After the first keys, the queries (their buffers come free with the last scores of the item before).
+            for (int i = 0; ok && i < (w.n1 > 0 ? 2 : 1); ++i) {
+              if (q_loads[i] > 0) ok = mbar_wait_a(q_empty(i), (q_loads[i] - 1) & 1, abort_flag, p.status);
+              if (!ok) break;
+              mbar_arrive_expect_tx_a(q_full(i), S::kTile);
 #pragma unroll
               for (int d = 0; d < S::kPanels; ++d)
-                tma_load_2d(dst + d * kPanel, (u & 1) ? &maps.v : &maps.k, head / p.group * D + d * 64,
-                            it.start + (u >> 1) * kRows, full(s));
-              ++issued;
-              if (u > 0) continue;
-              // After the first keys, the queries (their buffers come free when the last item's last scores are done).
-              for (int i = 0; more && i < (second ? 2 : 1); ++i) {
-                if (q_loads[i] > 0 && !mbar_wait_a(q_empty(i), (q_loads[i] - 1) & 1, abort_flag, p.status)) {
-                  more = false;
-                  break;
-                }
-                mbar_arrive_expect_tx_a(q_full(i), S::kTile);
-#pragma unroll
-                for (int d = 0; d < S::kPanels; ++d)
-                  tma_load_2d(sbase + i * S::kTile + d * kPanel, &maps.q, head * D + d * 64,
-                              it.start + it.t * kBlock + i * kRows, q_full(i));
-                ++q_loads[i];
-              }
+                tma_load_2d(sbase + i * S::kTile + d * kPanel, &maps.q, w.head * D + d * 64,
+                            w.it.start + w.it.t * kBlock + i * kRows, q_full(i));
+              ++q_loads[i];
             }
           }
         }
-        if (!__shfl_sync(~0u, static_cast<int>(more), 0)) break;
+        if (!__shfl_sync(~0u, static_cast<int>(ok), 0)) break;
       }
       if (lane == 0) {
         // Every issued copy lands before the CTA exits (after an expired wait too).
@@ -702,6 +698,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         u0 += 2 * n;
       }
       commit(leader, done);  // also after an expired wait: arrives once the issued MMAs are done
+    } else {
+      // Warp 11 finds the items, ahead of the others.  They are dealt out in
+      // rounds, every other round backwards.
+      for (int k = 0;; ++k) {
+        const int64_t g = gridDim.x, c = blockIdx.x;
+        const int64_t idx = k * g + ((k & 1) ? g - 1 - c : c);
+        const int e = k & 1;
+        Item it{0, 0, 0};
+        const bool have = find_item(p, idx / p.heads, it);
+        if (k >= 2 && !mbar_wait_a(item_empty(e), ((k >> 1) & 1) ^ 1, abort_flag, p.status)) break;
+        if (lane == 0) {
+          items[e * 4] = it.start;
+          items[e * 4 + 1] = have ? it.len : 0;
+          items[e * 4 + 2] = it.t;
+          items[e * 4 + 3] = static_cast<int>(idx % p.heads);
+          mbar_arrive_a(item_full(e));
+        }
+        __syncwarp();
+        if (!have) break;
+      }
     }
   }
   __syncwarp();
@@ -776,7 +792,8 @@ qerl_status launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t s
   p.heads = a.num_heads;
   p.group = a.num_heads / a.num_kv_heads;
   p.negative = a.scale < 0.0f;
-  p.c = (a.scale < 0.0f ? -a.scale : a.scale) * 1.44269504088896340736f;
+  // Not 0: a masked score of -inf times 0 would be NaN (1e-37 times any score below 1e29 is as good as 0).
+  p.c = std::max((a.scale < 0.0f ? -a.scale : a.scale) * 1.44269504088896340736f, 1e-37f);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.ldo = a.ldo;
   p.lse = a.lse;
