@@ -63,7 +63,7 @@ struct DecodeParams {
   __nv_bfloat16* out;
   int64_t ldo;
   float* lse;
-  float* part;         // [CTA][2][NT * 8][D + 2]
+  float* part;         // [CTA][2][NT * 8][D + 2]: of the segment begun before its stretch, of the one begun in it
   unsigned* counters;  // [num_seqs * kv_heads * zgroups], zero between calls
   int* status;
 };
@@ -74,6 +74,10 @@ struct Shape {
   static constexpr int kChunks = kRow / 16;
   static constexpr int kKeys = kRow >= 256 ? 16 : 32;  // per warp and stage
   static constexpr int kTile = kKeys * kWarps;
+  // The line's unit of cost is 16 keys; a (sequence, head) costs about a tile
+  // more for its start and its join.
+  static constexpr int kTileCost = kTile / 16;
+  static constexpr int kSegmentCost = kTileCost;
   static constexpr int kStage = 2 * kKeys * kRow;  // K then V
   static constexpr int kStages = NT == 1 ? (kStage > 4096 ? 3 : 5) : (kStage > 4096 ? 2 : 4);
   static constexpr int kRing = kWarps * kStages * kStage;
@@ -145,10 +149,33 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// A place on the line of work units: key tile `tile` of `tiles` of (sequence
-// b, part hz of its kv_heads * zgroups).
+// cp_async_16 with an L2 cache policy.
+__device__ __forceinline__ void cp_async_16_hint(uint32_t smem_dst, const void* gsrc, uint32_t src_bytes, uint64_t pol) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(smem_dst), "l"(gsrc),
+               "r"(src_bytes), "l"(pol)
+               : "memory");
+}
+
+// Named barriers of the join (0 is __syncthreads), one of each for even and one
+// for odd segments: the warp that joined a segment does not wait before the
+// next one and may be a whole segment ahead, where its arrival must not count
+// for the barrier the others are still at.
+__device__ __forceinline__ int join_full(int segment) { return 1 + (segment & 1); }
+__device__ __forceinline__ int join_free(int segment) { return 3 + (segment & 1); }
+__device__ __forceinline__ void bar_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
+}
+// 2^(m - top); 1 for a part without a finite score, whose sums are 0 (or NaN, which stays).
+__device__ __forceinline__ float weight_of(float m, float top) {
+  return m == -__int_as_float(0x7f800000) ? 1.0f : ex2(m - top);
+}
+
+// A place on the line of work: key tile `tile` of `tiles` of (sequence b, part
+// hz of its kv_heads * zgroups), which begins at `pos`.
 struct Cursor {
   int b, hz, tile, tiles, len;
+  long long pos;
 };
 
 __device__ __forceinline__ int live_length(const DecodeParams& p, int b) {
@@ -156,16 +183,26 @@ __device__ __forceinline__ int live_length(const DecodeParams& p, int b) {
   return n < 0 ? 0 : n > p.capacity ? static_cast<int>(p.capacity) : n;
 }
 
-template <int kTile>
+template <typename S>
+__device__ __forceinline__ int segment_cost(int len) {
+  return (len - 1) / 16 + 1 + S::kSegmentCost;
+}
+
+// The next tile on the line; b == num_seqs past its end.
+template <typename S>
 __device__ __forceinline__ void advance(const DecodeParams& p, Cursor& c) {
-  if (++c.tile < c.tiles) return;
+  if (++c.tile < c.tiles) {
+    c.pos += S::kTileCost;
+    return;
+  }
+  c.pos += segment_cost<S>(c.len) - (c.tiles - 1) * S::kTileCost;
   c.tile = 0;
   if (++c.hz < p.kv_heads * p.zgroups) return;
   c.hz = 0;
   while (++c.b < p.num_seqs) {
     c.len = live_length(p, c.b);
     if (c.len > 0) {
-      c.tiles = (c.len - 1) / kTile + 1;
+      c.tiles = (c.len - 1) / S::kTile + 1;
       return;
     }
   }
@@ -184,18 +221,19 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
   __shared__ long long red[kWarps];
   __shared__ long long found[2];
   __shared__ float ml[kWarps][NT * 8][2];
-  __shared__ unsigned arrived;
+  __shared__ int4 pending[2];  // (b, hz, first CTA, CTAs) of a segment to join, by slot
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hz_all = p.kv_heads * p.zgroups;
   const uint32_t ring = smem_u32(smem) + warp * (S::kStages * S::kStage);
   float* o_join = reinterpret_cast<float*>(smem + S::kRing);
   const float kInf = __int_as_float(0x7f800000);
+  if (tid < 2) pending[tid] = make_int4(0, 0, 0, 0);  // before the loop's first barrier
 
   // ---- this CTA's stretch of the line ---------------------------------------
-  auto units = [&](int b) -> long long {
+  auto cost = [&](int b) -> long long {
     if (b >= p.num_seqs) return 0;
     const int n = live_length(p, b);
-    return n > 0 ? static_cast<long long>((n - 1) / S::kTile + 1) * hz_all : 0;
+    return n > 0 ? static_cast<long long>(segment_cost<S>(n)) * hz_all : 0;
   };
   auto scan = [&](long long v) -> long long {  // inclusive over the warp
 #pragma unroll
@@ -217,11 +255,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
   }
   long long total = 0, incl = 0, mine = 0;
   if (p.num_seqs <= 32) {  // every warp for itself, no barrier
-    mine = units(lane);
+    mine = cost(lane);
     incl = scan(mine);
     total = __shfl_sync(~0u, incl, 31);
   } else {
-    for (int b = tid; b < p.num_seqs; b += kThreads) total += units(b);
+    for (int b = tid; b < p.num_seqs; b += kThreads) total += cost(b);
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) total += __shfl_xor_sync(~0u, total, i);
     if (lane == 0) red[warp] = total;
@@ -231,18 +269,20 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
     for (int i = 0; i < kWarps; ++i) total += red[i];
   }
   if (total == 0) return;
-  // Even stretches; no CTA without a unit between two that have one (the join
-  // counts the CTAs of a range).
-  const long long ctas = total < gridDim.x ? total : gridDim.x;
+  // Even stretches of the line; a tile belongs to the stretch in which it
+  // begins.  None is shorter than a tile, so that every CTA between the owners
+  // of a segment's first and last tile has a tile of it (the join counts them).
+  const long long most = quotient(total, S::kTileCost);
+  const long long ctas = most < 1 ? 1 : most < gridDim.x ? most : gridDim.x;
   if (blockIdx.x >= ctas) return;
-  const long long each = quotient(total, ctas), extra = total - each * ctas;  // the first `extra` CTAs get one more
+  const long long each = quotient(total, ctas), extra = total - each * ctas;  // the first `extra` are one longer
   auto stretch = [&](long long c) -> long long { return each * c + (c < extra ? c : extra); };
-  auto owner = [&](long long unit) -> int {  // the CTA that holds a unit
+  auto owner = [&](long long pos) -> int {  // the CTA whose stretch holds a place
     const long long wide = extra * (each + 1);
-    return static_cast<int>(unit < wide ? quotient(unit, each + 1) : extra + quotient(unit - wide, each));
+    return static_cast<int>(pos < wide ? quotient(pos, each + 1) : extra + quotient(pos - wide, each));
   };
   const long long begin = stretch(blockIdx.x), end = stretch(blockIdx.x + 1);
-  // The sequence that holds unit `begin`, and the unit's place in it.
+  // The sequence that holds `begin`, and the place in it.
   Cursor cur;
   long long inside;
   if (p.num_seqs <= 32) {
@@ -252,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
   } else {
     long long base = 0;
     for (int b0 = 0;; b0 += kThreads) {
-      mine = units(b0 + tid);
+      mine = cost(b0 + tid);
       incl = scan(mine);
       __syncthreads();
       if (lane == 31) red[warp] = incl;
@@ -279,8 +319,19 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
   }
   cur.len = live_length(p, cur.b);
   cur.tiles = (cur.len - 1) / S::kTile + 1;
-  cur.hz = static_cast<int>(quotient(inside, cur.tiles));
-  cur.tile = static_cast<int>(inside - static_cast<long long>(cur.hz) * cur.tiles);
+  {
+    const int segment = segment_cost<S>(cur.len);
+    cur.hz = static_cast<int>(quotient(inside, segment));
+    const int in_segment = static_cast<int>(inside - static_cast<long long>(cur.hz) * segment);
+    cur.tile = (in_segment + S::kTileCost - 1) / S::kTileCost;  // the first that begins here or later
+    cur.pos = begin - in_segment + cur.tile * S::kTileCost;
+    if (cur.tile >= cur.tiles) {
+      cur.tile = cur.tiles - 1;
+      cur.pos = begin - in_segment + cur.tile * S::kTileCost;
+      advance<S>(p, cur);
+    }
+  }
+  if (cur.b >= p.num_seqs || cur.pos >= end) return;  // no tile begins in this stretch
 
   // ---- loads ----------------------------------------------------------------
   // Byte offset of this lane's key row of the cursor's tile; -1 past the length
@@ -297,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
     return ((page * p.kv_heads + c.hz / p.zgroups) * p.page_size + (key - static_cast<int64_t>(pi) * p.page_size)) *
            S::kRow;
   };
+  const uint64_t once = l2_policy_evict_first();  // the stream leaves the kernel's code in L2
   auto issue = [&](int stage, int64_t off) {
     const uint32_t base_a = ring + stage * S::kStage;
     constexpr int kPer = S::kKeys * S::kChunks / 32;
@@ -306,29 +358,30 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
       const int64_t o = __shfl_sync(~0u, off, row);
       const uint32_t dst = base_a + at_chunk<S::kRow>(row, chunk);
       const int64_t from = o < 0 ? 0 : o + chunk * 16;
-      cp_async_16(dst, p.kp + from, o < 0 ? 0 : 16);
-      cp_async_16(dst + S::kKeys * S::kRow, p.vp + from, o < 0 ? 0 : 16);
+      cp_async_16_hint(dst, p.kp + from, o < 0 ? 0 : 16, once);
+      cp_async_16_hint(dst + S::kKeys * S::kRow, p.vp + from, o < 0 ? 0 : 16, once);
     }
   };
   // The page numbers of the first stages are fetched together, later ones a
   // step before their rows.
+  // The page numbers of the first stages are fetched together, later ones a
+  // step before their rows.
   Cursor ahead = cur;
-  long long to_load = end - begin;
   int64_t offs[S::kStages];
+  bool more[S::kStages];
 #pragma unroll
   for (int s = 0; s < S::kStages; ++s) {
-    if (s > 0 && s < to_load) advance<S::kTile>(p, ahead);
-    offs[s] = s < to_load ? lookup(ahead) : -1;
+    if (s > 0 && more[s - 1]) advance<S>(p, ahead);
+    more[s] = (s == 0 || more[s - 1]) && ahead.b < p.num_seqs && ahead.pos < end;
+    offs[s] = more[s] ? lookup(ahead) : -1;
   }
 #pragma unroll
   for (int s = 0; s < S::kStages - 1; ++s) {
-    if (s < end - begin) {
-      issue(s, offs[s]);
-      --to_load;
-    }
+    if (more[s]) issue(s, offs[s]);
     cp_async_commit();
   }
   int64_t off = offs[S::kStages - 1];
+  bool to_load = more[S::kStages - 1];
 
   // ---- the key loop ----------------------------------------------------------
   constexpr int KS = D / 16;  // 16-element steps of a head
@@ -369,14 +422,30 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
   load_q(cur, qn);
   bool fresh = true;
   int stage = 0;
-  long long seg_begin = begin - cur.tile;  // first unit of the segment
-  for (long long u = begin; u < end; ++u) {
+  const long long first_pos = cur.pos;
+  constexpr int64_t kSlot = static_cast<int64_t>(NT * 8) * S::kPartRow;
+  // Output elements d .. d + 3 of the h-th head of a segment from its (m, l, o).
+  auto finish = [&](int b, int hz, int h, int d, float top, float sum, const float4& v) {
+    const int kv = hz / p.zgroups;
+    const int head = kv * p.group + (hz - kv * p.zgroups) * p.zheads + h;
+    const float vs = kFp8 && p.v_scale != nullptr ? p.v_scale[kv] : 1.0f;
+    const float f = sum == 0.0f ? 0.0f : vs / sum;
+    uint2 w;
+    w.x = pack_bf16(v.x * f, v.y * f);
+    w.y = pack_bf16(v.z * f, v.w * f);
+    *reinterpret_cast<uint2*>(p.out + b * p.ldo + static_cast<int64_t>(head) * D + d) = w;
+    if (d == 0 && p.lse != nullptr)
+      p.lse[static_cast<int64_t>(b) * p.heads + head] = sum == 0.0f ? -kInf : (top + log2f(sum)) * 0.69314718055994530942f;
+  };
+  int segments = 0;
+  bool last = false;
+  while (!last) {
     const int kvh = cur.hz / p.zgroups, z = cur.hz - kvh * p.zgroups;
     const int head0 = kvh * p.group + z * p.zheads;
     const int nheads = min(p.zheads, p.group - z * p.zheads);
     if (fresh) {
       fresh = false;
-      if (!kAheadQ && u > begin) load_q(cur, qn);
+      if (!kAheadQ && cur.pos != first_pos) load_q(cur, qn);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (!kFp8) {
@@ -419,19 +488,17 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
     }
     const bool last_tile = cur.tile + 1 == cur.tiles;
     Cursor next = cur;
-    if (u + 1 < end) {
-      advance<S::kTile>(p, next);
-      if (kAheadQ && last_tile) load_q(next, qn);
-    }
+    advance<S>(p, next);
+    last = next.b >= p.num_seqs || next.pos >= end;
+    if (kAheadQ && last_tile && !last) load_q(next, qn);
     // Refill the stage the previous step emptied, then wait for this one.
     {
       const int fill = stage == 0 ? S::kStages - 1 : stage - 1;
-      if (to_load > 0) {
+      if (to_load) {
         issue(fill, off);
-        if (--to_load > 0) {
-          advance<S::kTile>(p, ahead);
-          off = lookup(ahead);
-        }
+        advance<S>(p, ahead);
+        to_load = ahead.b < p.num_seqs && ahead.pos < end;
+        if (to_load) off = lookup(ahead);
       }
       cp_async_commit();
       cp_async_wait_group<S::kStages - 1>();
@@ -561,9 +628,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
 
     // ---- end of a (sequence, head) or of the stretch -------------------------
-    if (last_tile || u + 1 == end) {
-      const long long seg_end = seg_begin + cur.tiles;
-      const bool whole = seg_begin >= begin && seg_end <= end;
+    // The warps leave their (m, l, o) in shared memory and go on; one of them,
+    // another each time, waits for the others' and joins them.
+    if (last_tile || last) {
+      if (segments > 0 && warp != ((segments - 1) & (kWarps - 1))) bar_sync(join_free(segments));  // its last joiner has read it
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -584,23 +652,16 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
             dst[ks * 16 + (kFp8 ? 2 * g8 + 1 : g8 + 8)] = o[nt][ks][c + 2];
           }
         }
-      __syncthreads();
-      const float vs = kFp8 && p.v_scale != nullptr ? p.v_scale[kvh] : 1.0f;
-      auto finish = [&](int h, int d, float top, float sum, const float4& v) {
-        const int head = head0 + h;
-        const float f = sum == 0.0f ? 0.0f : vs / sum;
-        uint2 w;
-        w.x = pack_bf16(v.x * f, v.y * f);
-        w.y = pack_bf16(v.z * f, v.w * f);
-        *reinterpret_cast<uint2*>(p.out + cur.b * p.ldo + static_cast<int64_t>(head) * D + d) = w;
-        if (d == 0 && p.lse != nullptr)
-          p.lse[static_cast<int64_t>(cur.b) * p.heads + head] =
-              sum == 0.0f ? -kInf : (top + log2f(sum)) * 0.69314718055994530942f;
-      };
-      constexpr int64_t kSlot = static_cast<int64_t>(NT * 8) * S::kPartRow;
-      // The warps' (m, l, o) of a head joined, in warp order, and handed on.
-      auto join = [&](auto&& use) {
-        for (int i = tid; i < nheads * (D / 4); i += kThreads) {
+      __syncwarp();
+      if (warp != (segments & (kWarps - 1))) {
+        bar_arrive(join_full(segments));
+      } else {
+        bar_sync(join_full(segments));
+        const long long seg_begin = cur.pos - static_cast<long long>(cur.tile) * S::kTileCost;  // its first tile
+        const bool whole = seg_begin >= begin && last_tile;
+        const int slot_index = seg_begin < begin ? 0 : 1;
+        float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + slot_index) * kSlot;
+        for (int i = lane; i < nheads * (D / 4); i += 32) {
           const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
           float top = -kInf;
 #pragma unroll
@@ -609,8 +670,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
           float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            // a warp without a finite score has sums of 0 (or NaN, which stays)
-            const float f = ml[w][h][0] == -kInf ? 1.0f : ex2(ml[w][h][0] - top);
+            const float f = weight_of(ml[w][h][0], top);
             const float4 v = *reinterpret_cast<const float4*>(o_join + (w * NT * 8 + h) * S::kOStride + d);
             sum += f * ml[w][h][1];
             acc.x += f * v.x;
@@ -618,96 +678,89 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
             acc.z += f * v.z;
             acc.w += f * v.w;
           }
-          use(h, d, top, sum, acc);
+          if (whole) {
+            finish(cur.b, cur.hz, h, d, top, sum, acc);
+          } else {
+            __stcg(reinterpret_cast<float4*>(slot + h * D + d), acc);
+            if (d == 0) __stcg(reinterpret_cast<float2*>(slot + NT * 8 * D + 2 * h), make_float2(top, sum));
+          }
         }
-      };
-      if (whole) {
-        join(finish);
-      } else {
-        float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (seg_begin <= begin ? 0 : 1)) * kSlot;
-        join([&](int h, int d, float top, float sum, const float4& v) {
-          __stcg(reinterpret_cast<float4*>(slot + h * D + d), v);
-          if (d == 0) __stcg(reinterpret_cast<float2*>(slot + NT * 8 * D + 2 * h), make_float2(top, sum));
-        });
-        // The CTAs that hold units of this segment: those of its first and last unit.
-        const int c0 = owner(seg_begin), c1 = owner(seg_end - 1);
-        __syncthreads();
-        if (tid == 0) {
-          __threadfence();
+        __syncwarp();
+        if (!last) bar_arrive(join_free(segments + 1));
+        if (!whole && lane == 0) {
+          // The CTAs that hold tiles of this segment; the last of them to come
+          // here adds their partials when its own tiles are done.
+          const int c0 = owner(seg_begin), c1 = owner(seg_begin + static_cast<long long>(cur.tiles - 1) * S::kTileCost);
           unsigned* counter = p.counters + static_cast<int64_t>(cur.b) * hz_all + cur.hz;
-          const unsigned before = atomicAdd(counter, 1u);
-          arrived = before;
-          if (before == static_cast<unsigned>(c1 - c0)) *counter = 0;  // ready for the next call
           __threadfence();
+          if (atomicAdd(counter, 1u) == static_cast<unsigned>(c1 - c0)) {
+            *counter = 0;  // ready for the next call
+            __threadfence();
+            pending[slot_index] = make_int4(cur.b, cur.hz, c0, c1 - c0 + 1);
+          }
         }
-        __syncthreads();
-        if (arrived == static_cast<unsigned>(c1 - c0)) {
-          // The last to arrive: warp w adds the partials c0 + w, c0 + w + 4, ...
-          // (all heads of a partial in flight together), then the warps join.
-          constexpr int kVec = D / 32;  // elements of a row per lane
-          constexpr int kHeads = NT * 8;
-          float top[kHeads], sum[kHeads], acc[kHeads][kVec];
-#pragma unroll
-          for (int h = 0; h < kHeads; ++h) {
-            top[h] = -kInf;
-            sum[h] = 0.0f;
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) acc[h][e] = 0.0f;
-          }
-          const int first_slot = stretch(c0) < seg_begin ? 1 : 0;
-#pragma unroll(NT == 1 ? 2 : 1)
-          for (int c = c0 + warp; c <= c1; c += kWarps) {
-            const float* s = p.part + (2 * static_cast<int64_t>(c) + (c == c0 ? first_slot : 0)) * kSlot;
-            float2 e[kHeads];
-            float v[kHeads][kVec];
-#pragma unroll
-            for (int h = 0; h < kHeads; ++h) {
-              if (h >= nheads) continue;
-              e[h] = __ldcg(reinterpret_cast<const float2*>(s + NT * 8 * D + 2 * h));
-              if (kVec == 4) {
-                const float4 w = __ldcg(reinterpret_cast<const float4*>(s + h * D + lane * 4));
-                v[h][0] = w.x;
-                v[h][1] = w.y;
-                v[h][kVec - 2] = w.z;
-                v[h][kVec - 1] = w.w;
-              } else {
-                const float2 w = __ldcg(reinterpret_cast<const float2*>(s + h * D + lane * 2));
-                v[h][0] = w.x;
-                v[h][1] = w.y;
-              }
-            }
-#pragma unroll
-            for (int h = 0; h < kHeads; ++h) {
-              if (h >= nheads) continue;
-              const float up = fmaxf(top[h], e[h].x);
-              const float fa = top[h] == -kInf ? 1.0f : ex2(top[h] - up), fb = e[h].x == -kInf ? 1.0f : ex2(e[h].x - up);
-              top[h] = up;
-              sum[h] = sum[h] * fa + e[h].y * fb;
-#pragma unroll
-              for (int k = 0; k < kVec; ++k) acc[h][k] = acc[h][k] * fa + v[h][k] * fb;
-            }
-          }
-#pragma unroll
-          for (int h = 0; h < kHeads; ++h) {
-            if (h >= nheads) continue;
-            if (lane == 0) {
-              ml[warp][h][0] = top[h];
-              ml[warp][h][1] = sum[h];
-            }
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) o_join[(warp * NT * 8 + h) * S::kOStride + lane * kVec + k] = acc[h][k];
-          }
-          __syncthreads();
-          join(finish);
-        }
+        __syncwarp();
       }
-      __syncthreads();  // the join buffer is free again
+      ++segments;
       fresh = true;
-      seg_begin = seg_end;
     }
     cur = next;
   }
   cp_async_wait_group<0>();
+
+  // ---- segments whose last partial this CTA brought --------------------------
+  __syncthreads();
+  // Kept short: this code runs once, and its fetch is part of its time.
+  for (int s = 0; s < 2; ++s) {
+    const int4 job = pending[s];
+    if (job.w == 0) continue;
+    const int part0 = job.y % p.zgroups, nheads = min(p.zheads, p.group - part0 * p.zheads);
+#pragma unroll 1
+    for (int i = tid; i < nheads * (D / 4); i += kThreads) {
+      const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+      // Its first CTA began the segment (slot 1); the others came to it from before (slot 0).
+      const float* first = p.part + (2 * static_cast<int64_t>(job.z) + 1) * kSlot;
+      float top = -kInf, sum = 0.0f;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      constexpr int kBatch = 16;  // partials in flight
+#pragma unroll 1
+      for (int c0 = 0; c0 < job.w; c0 += kBatch) {
+        float2 e[kBatch];
+        float4 v[kBatch];
+        float up = top;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const int c = c0 + q;
+          const float* slot = first + (c == 0 ? 0 : 2 * c - 1) * kSlot;
+          e[q] = make_float2(-kInf, 0.0f);
+          v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (c < job.w) {
+            e[q] = __ldcg(reinterpret_cast<const float2*>(slot + NT * 8 * D + 2 * h));
+            v[q] = __ldcg(reinterpret_cast<const float4*>(slot + h * D + d));
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) up = fmaxf(up, e[q].x);
+        const float f0 = weight_of(top, up);
+        top = up;
+        sum *= f0;
+        acc.x *= f0;
+        acc.y *= f0;
+        acc.z *= f0;
+        acc.w *= f0;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const float f = weight_of(e[q].x, top);
+          sum += f * e[q].y;
+          acc.x += f * v[q].x;
+          acc.y += f * v[q].y;
+          acc.z += f * v[q].z;
+          acc.w += f * v[q].w;
+        }
+      }
+      finish(job.x, job.y, h, d, top, sum, acc);
+    }
+  }
 }
 
 template <int D, bool kFp8, int NT>

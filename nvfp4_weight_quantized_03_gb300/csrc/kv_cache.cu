@@ -84,30 +84,24 @@ __global__ void __launch_bounds__(512) rope_append_kernel(const AppendParams p) 
   const int per_head = p.dim >> 4;  // items of a head
   const int rot_items = p.half >> 3;
   const int items = (p.heads + 2 * p.kv_heads) * per_head;
+  // The place of token t in the cache: its page number, or -1.
+  auto page_of = [&](int64_t t, int pos) -> int {
+    if (p.k_pages == nullptr || pos < 0) return -1;
+    const int64_t s = p.seq_ids != nullptr ? p.seq_ids[t] : t;
+    const int64_t pi = pos / p.page_size;
+    return s >= 0 && s < p.num_seqs && pi < p.max_pages ? p.table[s * p.ld_table + pi] : -1;
+  };
   int buf = 0;
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-    const int pos = p.positions[t];
+  // A token's position and page number, which depend on one another, are
+  // fetched while the tokens before it are worked on.
+  int64_t t = blockIdx.x;
+  int pos = p.positions[t], pos_next = t + gridDim.x < p.tokens ? p.positions[t + gridDim.x] : -1;
+  int page = page_of(t, pos);
+  for (int page_next = -1, pos_later = -1; t < p.tokens; t += gridDim.x, pos = pos_next, page = page_next, pos_next = pos_later) {
+    const int64_t t1 = t + gridDim.x, t2 = t1 + gridDim.x;
+    page_next = t1 < p.tokens ? page_of(t1, pos_next) : -1;
+    pos_later = t2 < p.tokens ? p.positions[t2] : -1;
     if (pos < 0) continue;  // padding: uniform over the CTA
-    if (tid < p.half) {
-      const uint64_t a = turn * static_cast<uint64_t>(pos);
-      // the top 32 bits as a signed fraction of half a turn, in [-1, 1)
-      const float x = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077392578125e-10f;
-      sincospif(x, &sn[buf][tid], &cs[buf][tid]);
-    }
-    // The cache row of this token.
-    int64_t row = -1;
-    if (p.k_pages != nullptr) {
-      const int64_t s = p.seq_ids != nullptr ? p.seq_ids[t] : t;
-      const int64_t pi = pos / p.page_size;
-      int64_t page = -1;
-      if (s >= 0 && s < p.num_seqs && pi < p.max_pages) page = p.table[s * p.ld_table + pi];
-      if (page < 0 || page >= p.num_pages) {
-        if (tid == 0) record_error(p.status, QERL_ERR_RANGE);
-      } else {
-        row = page * p.kv_heads * p.page_size + (pos - pi * p.page_size);
-      }
-    }
-    // The first item's loads go out before the barrier that publishes the angles.
     for (int it = tid, first = 1;; it += blockDim.x, first = 0) {
       const int head = it / per_head, sub = it - head * per_head;
       // 0: q, 1: k, 2: v
@@ -117,7 +111,7 @@ __global__ void __launch_bounds__(512) rope_append_kernel(const AppendParams p) 
       // element offsets of the item's two chunks within the head
       const int e0 = rot ? sub * 8 : kind == 2 ? sub * 16 : 2 * p.half + (sub - rot_items) * 16;
       const int e1 = rot ? p.half + sub * 8 : e0 + 8;
-      const bool live = it < items && (kind < 2 || row >= 0);
+      const bool live = it < items && (kind < 2 || p.k_pages != nullptr);
       uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
       if (live) {
         const __nv_bfloat16* src = kind == 0 ? p.q + t * p.ldq : kind == 1 ? p.k + t * p.ldk : p.v + t * p.ldv;
@@ -125,9 +119,18 @@ __global__ void __launch_bounds__(512) rope_append_kernel(const AppendParams p) 
         w0 = *reinterpret_cast<const uint4*>(src + e0);
         w1 = *reinterpret_cast<const uint4*>(src + e1);
       }
-      if (first) __syncthreads();  // the angles of this token; two buffers, so one barrier a token
+      if (first) {  // while the first item's rows arrive
+        if (tid < p.half) {
+          const uint64_t a = turn * static_cast<uint64_t>(pos);
+          // the top 32 bits as a signed fraction of half a turn, in [-1, 1)
+          const float x = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077392578125e-10f;
+          sincospif(x, &sn[buf][tid], &cs[buf][tid]);
+        }
+        __syncthreads();  // the angles of this token; two buffers, so one barrier a token
+      }
       if (it >= items) break;
       if (!live) continue;
+      const bool placed = page >= 0 && page < p.num_pages;
       float a[8], b[8];
       unpack8(w0, a);
       unpack8(w1, b);
@@ -156,9 +159,10 @@ __global__ void __launch_bounds__(512) rope_append_kernel(const AppendParams p) 
         *reinterpret_cast<uint4*>(dst + e0) = w0;
         *reinterpret_cast<uint4*>(dst + e1) = w1;
       }
-      if (kind >= 1 && row >= 0) {
+      if (kind >= 1 && placed) {
         uint8_t* pages = kind == 1 ? p.k_pages : p.v_pages;
-        const int64_t at = (row + static_cast<int64_t>(hh) * p.page_size) * p.dim;
+        const int64_t at =
+            ((static_cast<int64_t>(page) * p.kv_heads + hh) * p.page_size + pos % p.page_size) * p.dim;
         if (kE4m3) {
           const float* sc = kind == 1 ? p.k_scale : p.v_scale;
           const float scale = sc != nullptr ? sc[hh] : 1.0f;
@@ -171,6 +175,7 @@ __global__ void __launch_bounds__(512) rope_append_kernel(const AppendParams p) 
         }
       }
     }
+    if (tid == 0 && p.k_pages != nullptr && (page < 0 || page >= p.num_pages)) record_error(p.status, QERL_ERR_RANGE);
     buf ^= 1;
   }
 }
