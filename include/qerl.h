@@ -499,7 +499,7 @@ typedef struct {
  *   q        bf16 rows of num_heads * head_dim, row stride ldq, or NULL.
  *   k, v     bf16 rows of num_kv_heads * head_dim, row strides ldk, ldv.
  *   positions  device int32 [tokens]; a negative one marks padding: nothing of
- *            that token is read or written.
+ *            that token is written.
  *   seq_ids  device int32 [tokens], the token's row of the page table; NULL:
  *            token t belongs to sequence t.
  *   inv_freq device double [rot_dim / 2], radians per position, finite.

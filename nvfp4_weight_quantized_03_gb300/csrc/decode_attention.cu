@@ -33,6 +33,7 @@
 #include "qerl_internal.h"
 #include "qerl_ptx.cuh"
 
+#include <algorithm>
 #include <atomic>
 #include <cuda_bf16.h>
 
@@ -74,12 +75,18 @@ struct Shape {
   static constexpr int kChunks = kRow / 16;
   static constexpr int kKeys = kRow >= 256 ? 16 : 32;  // per warp and stage
   static constexpr int kTile = kKeys * kWarps;
-  // The line's unit of cost is 16 keys; a (sequence, head) costs about a tile
-  // more for its start and its join.
+  // The line's unit of cost is 16 keys; a (sequence, head) costs about one and a
+  // half tiles more for its start and its join (heads of 64, 256 sequences of
+  // 93 to 1500 rows: half a tile 65 us, one 59 us, one and a half 55.5 us, two
+  // 56.6 us).
   static constexpr int kTileCost = kTile / 16;
-  static constexpr int kSegmentCost = kTileCost;
+  static constexpr int kSegmentCost = kTileCost * 3 / 2;
   static constexpr int kStage = 2 * kKeys * kRow;  // K then V
-  static constexpr int kStages = NT == 1 ? (kStage > 4096 ? 3 : 5) : (kStage > 4096 ? 2 : 4);
+  // CTAs per SM and stages per warp fill the shared memory.  Short rows leave
+  // the warps waiting on their own chain of steps more than on memory: three
+  // CTAs with 2 stages (51 us) beat two with 3 (55.5 us).
+  static constexpr int kCtas = D == 64 && NT == 1 ? 3 : 2;
+  static constexpr int kStages = kStage == 4096 ? 4 : NT == 1 && D == 128 ? 3 : 2;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kOStride = D + 4;  // columns 2c, 2c+1 of 8 rows fall in 32 banks
   static constexpr int kJoin = kWarps * NT * 8 * kOStride * 4;
@@ -215,7 +222,7 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 }
 
 template <int D, bool kFp8, int NT>
-__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_kernel(const DecodeParams p) {
   using S = Shape<D, kFp8, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long red[kWarps];
@@ -774,7 +781,7 @@ qerl_status launch(const DecodeParams& p, int sms, int dev, cudaStream_t s) {
       return QERL_ERR_CUDA;
     ready.fetch_or(bit);
   }
-  int64_t grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+  int64_t grid = std::min(S::kCtas * sms, kMaxCtas);
   const int64_t most =
       static_cast<int64_t>(p.num_seqs) * p.kv_heads * p.zgroups * ((p.capacity + S::kTile - 1) / S::kTile);
   if (most < grid) grid = most > 0 ? most : 1;
