@@ -163,6 +163,12 @@ __device__ __forceinline__ void cp_async_16_hint(uint32_t smem_dst, const void* 
                : "memory");
 }
 
+__device__ __forceinline__ unsigned atomic_add_acq_rel(unsigned* p, unsigned v) {
+  unsigned old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+
 // Named barriers of the join (0 is __syncthreads), one of each for even and one
 // for odd segments: the warp that joined a segment does not wait before the
 // next one and may be a whole segment ahead, where its arrival must not count
@@ -235,6 +241,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
   float* o_join = reinterpret_cast<float*>(smem + S::kRing);
   const float kInf = __int_as_float(0x7f800000);
   if (tid < 2) pending[tid] = make_int4(0, 0, 0, 0);  // before the loop's first barrier
+
+  griddep_wait();
 
   // ---- this CTA's stretch of the line ---------------------------------------
   auto cost = [&](int b) -> long long {
@@ -699,10 +707,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
           // here adds their partials when its own tiles are done.
           const int c0 = owner(seg_begin), c1 = owner(seg_begin + static_cast<long long>(cur.tiles - 1) * S::kTileCost);
           unsigned* counter = p.counters + static_cast<int64_t>(cur.b) * hz_all + cur.hz;
-          __threadfence();
-          if (atomicAdd(counter, 1u) == static_cast<unsigned>(c1 - c0)) {
+          // Release of this warp's partial, acquire of the others'.
+          if (atomic_add_acq_rel(counter, 1u) == static_cast<unsigned>(c1 - c0)) {
             *counter = 0;  // ready for the next call
-            __threadfence();
             pending[slot_index] = make_int4(cur.b, cur.hz, c0, c1 - c0 + 1);
           }
         }
@@ -785,8 +792,8 @@ qerl_status launch(const DecodeParams& p, int sms, int dev, cudaStream_t s) {
   const int64_t most =
       static_cast<int64_t>(p.num_seqs) * p.kv_heads * p.zgroups * ((p.capacity + S::kTile - 1) / S::kTile);
   if (most < grid) grid = most > 0 ? most : 1;
-  decode_kernel<D, kFp8, NT><<<static_cast<unsigned>(grid), kThreads, S::kSmem, s>>>(p);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(
+      launch_dependent(decode_kernel<D, kFp8, NT>, dim3(static_cast<unsigned>(grid)), kThreads, S::kSmem, s, p));
 }
 
 struct Split {

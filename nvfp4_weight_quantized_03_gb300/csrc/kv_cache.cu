@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(512, kThreadsPerSm / 512) rope_append_kernel(c
   // position keeps exactly the bits below one turn, so far positions lose
   // nothing (an fp32 angle would be off by 1e-3 rad at position 1e4).
   uint64_t turn = 0;
+  griddep_wait();
   if (tid < p.half) {
     const double t = p.inv_freq[tid] * 0.15915494309189533577;  // 1 / (2 pi)
     turn = static_cast<uint64_t>(__double2ull_rn((t - floor(t)) * 18446744073709551616.0));
@@ -249,11 +250,8 @@ qerl_status launch_rope_append(const RopeAppendArgs& a, cudaStream_t s) {
       return QERL_ERR_CUDA;
     ready[e4m3].fetch_or(bit);
   }
-  if (e4m3)
-    rope_append_kernel<true><<<grid, threads, smem, s>>>(p);
-  else
-    rope_append_kernel<false><<<grid, threads, smem, s>>>(p);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(
+      launch_dependent(e4m3 ? rope_append_kernel<true> : rope_append_kernel<false>, grid, threads, smem, s, p));
 }
 
 }  // namespace qerl

@@ -357,6 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, *reinterpret_cast<volatile uint32_t*>(misc_gen + 8 * 19), 0);
 
+  griddep_wait();
+
   // The item in hand, read from the ring by a whole warp; false: no more.
   struct Work {
     Item it;
@@ -783,8 +785,8 @@ qerl_status launch(const PromptMaps& maps, const PromptParams& p, int64_t grid, 
       return QERL_ERR_CUDA;
     ready.fetch_or(bit);
   }
-  prompt_kernel<D><<<static_cast<unsigned>(grid), kThreads, Shape<D>::kSmem, s>>>(maps, p);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(
+      launch_dependent(prompt_kernel<D>, dim3(static_cast<unsigned>(grid)), kThreads, Shape<D>::kSmem, s, maps, p));
 }
 
 }  // namespace

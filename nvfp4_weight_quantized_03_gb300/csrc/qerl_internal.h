@@ -5,6 +5,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include <utility>
+
 #include "../../include/qerl.h"
 
 namespace qerl {
@@ -172,6 +174,25 @@ struct PromptAttentionArgs {
 size_t prompt_attention_workspace_bytes(int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
                                         int64_t num_seqs);
 qerl_status launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t s);
+
+// A launch whose CTAs may start while the kernel before it in the stream ends
+// (programmatic dependent launch): every kernel launched through it begins with
+// griddep_wait(), before it reads or writes global memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                             Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
 
 // api.cu: the argument checks shared by every linear entry point.
 qerl_status prepare_linear_group(const void* x, int64_t m, int64_t k, int64_t ldx, const float* z,
