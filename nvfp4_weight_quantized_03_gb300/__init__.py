@@ -523,7 +523,7 @@ def kv_cache(k, v, page_table, k_scale=None, v_scale=None):
     c.k_scale, c.v_scale = _p(k_scale), _p(v_scale)
     c.page_table = _p(page_table)
     c.num_seqs, c.max_pages = page_table.shape
-    c.ld_table = max(page_table.stride(0), c.max_pages)
+    c.ld_table = page_table.stride(0) if c.num_seqs > 1 else max(page_table.stride(0), c.max_pages)
     c.tensors = (k, v, page_table, k_scale, v_scale)
     return c
 

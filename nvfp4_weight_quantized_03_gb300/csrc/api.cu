@@ -528,7 +528,7 @@ qerl_status qerl_rope_append(const qerl_kv_cache* cache, const void* q, int64_t 
 
 size_t qerl_decode_attention_workspace_size(int64_t num_seqs, int num_heads, int num_kv_heads, int head_dim) {
   if (num_seqs < 0 || check_heads(num_heads, num_kv_heads, head_dim) != QERL_OK) return 0;
-  return qerl::decode_attention_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim);
+  return qerl::decode_attention_workspace_bytes(num_seqs, num_heads, num_kv_heads);
 }
 
 qerl_status qerl_decode_attention(const qerl_kv_cache* cache, const void* q, int64_t ldq, int num_heads,
@@ -545,8 +545,7 @@ qerl_status qerl_decode_attention(const qerl_kv_cache* cache, const void* q, int
   if ((st = check_rows(q, ldq, width)) != QERL_OK || (st = check_rows(out, ldo, width)) != QERL_OK) return st;
   if (!aligned(lengths, 4) || !aligned(lse, 4)) return QERL_ERR_MISALIGNED;
   st = check_ws(workspace, ws_bytes,
-                qerl::decode_attention_workspace_bytes(cache->num_seqs, num_heads, cache->num_kv_heads,
-                                                       cache->head_dim));
+                qerl::decode_attention_workspace_bytes(cache->num_seqs, num_heads, cache->num_kv_heads));
   if (st != QERL_OK) return st;
   qerl::DecodeAttentionArgs a{};
   a.cache = cache;

@@ -42,7 +42,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxCtas = 1024;
+// Partials at the front of the workspace, in a region of one size for every
+// shape: the counters behind it then lie at the same place for all calls that
+// share a workspace, and are zero between them.
+constexpr size_t kPartBytes = size_t{6} << 20;
 // How far (base 2) a score may pass the reference m before m moves: 2^8 keeps
 // the fp32 sums and the fp16 probabilities in range, and most steps then skip
 // the maximum's reduction and the rescaling.
@@ -372,9 +375,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
       const int row = (i * 32 + lane) / S::kChunks, chunk = lane % S::kChunks;
       const int64_t o = __shfl_sync(~0u, off, row);
       const uint32_t dst = base_a + at_chunk<S::kRow>(row, chunk);
-      const int64_t from = o < 0 ? 0 : o + chunk * 16;
-      cp_async_16_hint(dst, p.kp + from, o < 0 ? 0 : 16, once);
-      cp_async_16_hint(dst + S::kKeys * S::kRow, p.vp + from, o < 0 ? 0 : 16, once);
+      // a row of zeros: nothing is read, from an address that is memory all the same
+      const bool real = o >= 0;
+      const void* none = p.q;
+      cp_async_16_hint(dst, real ? p.kp + o + chunk * 16 : none, real ? 16 : 0, once);
+      cp_async_16_hint(dst + S::kKeys * S::kRow, real ? p.vp + o + chunk * 16 : none, real ? 16 : 0, once);
     }
   };
   // The page numbers of the first stages are fetched together, later ones a
@@ -788,7 +793,8 @@ qerl_status launch(const DecodeParams& p, int sms, int dev, cudaStream_t s) {
       return QERL_ERR_CUDA;
     ready.fetch_or(bit);
   }
-  int64_t grid = std::min(S::kCtas * sms, kMaxCtas);
+  constexpr int kFit = static_cast<int>(kPartBytes / (2 * NT * 8 * S::kPartRow * sizeof(float)));
+  int64_t grid = std::min(S::kCtas * sms, kFit);
   const int64_t most =
       static_cast<int64_t>(p.num_seqs) * p.kv_heads * p.zgroups * ((p.capacity + S::kTile - 1) / S::kTile);
   if (most < grid) grid = most > 0 ? most : 1;
@@ -816,10 +822,9 @@ size_t counter_bytes(int64_t num_seqs, int num_kv_heads, const Split& s) {
 
 }  // namespace
 
-size_t decode_attention_workspace_bytes(int64_t num_seqs, int num_heads, int num_kv_heads, int head_dim) {
+size_t decode_attention_workspace_bytes(int64_t num_seqs, int num_heads, int num_kv_heads) {
   const Split s = split_heads(num_heads / num_kv_heads);
-  return kWsHeaderBytes + counter_bytes(num_seqs, num_kv_heads, s) +
-         static_cast<size_t>(kMaxCtas) * 2 * (s.tiles * 8) * (head_dim + 2) * sizeof(float);
+  return kWsHeaderBytes + kPartBytes + counter_bytes(num_seqs, num_kv_heads, s);
 }
 
 qerl_status launch_decode_attention(const DecodeAttentionArgs& a, cudaStream_t s) {
@@ -855,8 +860,8 @@ qerl_status launch_decode_attention(const DecodeAttentionArgs& a, cudaStream_t s
   p.lse = a.lse;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.status = &reinterpret_cast<WsHeader*>(ws)->status;
-  p.counters = reinterpret_cast<unsigned*>(ws + kWsHeaderBytes);
-  p.part = reinterpret_cast<float*>(ws + kWsHeaderBytes + counter_bytes(c.num_seqs, c.num_kv_heads, sp));
+  p.part = reinterpret_cast<float*>(ws + kWsHeaderBytes);
+  p.counters = reinterpret_cast<unsigned*>(ws + kWsHeaderBytes + kPartBytes);
   const bool f8 = c.dtype == QERL_E4M3;
   const bool one = sp.tiles == 1;
   if (c.head_dim == 128) {

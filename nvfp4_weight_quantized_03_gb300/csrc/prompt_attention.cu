@@ -222,63 +222,53 @@ struct Item {
 __device__ __forceinline__ int blocks_of(const PromptParams& p, int s, int& start, int& len) {
   start = p.cu[s];
   const int end = p.cu[s + 1];
-  len = end - start;
   if (start < 0 || end < start || end > p.tokens) {
     record_error(p.status, QERL_ERR_RANGE);
     len = 0;
+    return 0;
   }
+  len = end - start;
   return (len + kBlock - 1) / kBlock;
 }
 
-// The rank-th block of all sequences' blocks, longest key range first (the
-// blocks with index t in their sequence, t descending): the last blocks to
-// start are then the cheapest.  Every warp works it out for itself.
-__device__ __forceinline__ bool find_item(const PromptParams& p, int64_t rank, Item& it) {
-  const int lane = threadIdx.x & 31;
-  int start, len;
-  int most = 0;
-  for (int s = lane; s < p.num_seqs; s += 32) most = max(most, blocks_of(p, s, start, len));
-  most = __reduce_max_sync(~0u, most);
-  // count(t): blocks of index >= t.  The largest t with count(t) > rank.
-  auto count = [&](int t) -> int64_t {
-    long long n = 0;
-    for (int s = lane; s < p.num_seqs; s += 32) n += max(0, blocks_of(p, s, start, len) - t);
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) n += __shfl_xor_sync(~0u, n, i);
-    return n;
-  };
-  if (p.num_seqs == 1) {
-    it.t = most - 1 - static_cast<int>(rank);
-    if (rank >= most) return false;
-    blocks_of(p, 0, it.start, it.len);
-    return true;
+// All sequences' blocks in the order of their cost: those of index `level`
+// within their sequence in the order of the sequences, level descending (the
+// last blocks to start are the cheapest).  find() is called by a whole warp
+// with ranks that do not decrease and goes on from where it was, so a CTA's
+// calls together look at each (level, sequence) once.
+struct Finder {
+  int level, s0;
+  int64_t passed;  // blocks before sequence s0 of this level
+
+  __device__ __forceinline__ void begin(const PromptParams& p) {
+    int most = 0, start, len;
+    for (int s = threadIdx.x & 31; s < p.num_seqs; s += 32) most = max(most, blocks_of(p, s, start, len));
+    level = __reduce_max_sync(~0u, most) - 1;
+    s0 = 0;
+    passed = 0;
   }
-  if (count(0) <= rank) return false;
-  int lo = 0, hi = most;  // count(lo) > rank >= count(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (count(mid) > rank)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  int64_t left = rank - count(lo + 1);  // the left-th sequence with more than lo blocks
-  for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-    const int s = s0 + lane;
-    const bool has = s < p.num_seqs && blocks_of(p, s, start, len) > lo;
-    const unsigned mask = __ballot_sync(~0u, has);
-    const int n = __popc(mask);
-    if (left < n) {
-      const int src = __fns(mask, 0, static_cast<int>(left) + 1);
-      it.t = lo;
-      it.start = __shfl_sync(~0u, start, src);
-      it.len = __shfl_sync(~0u, len, src);
-      return true;
+  __device__ __forceinline__ bool find(const PromptParams& p, int64_t rank, Item& it) {
+    const int lane = threadIdx.x & 31;
+    for (; level >= 0; --level, s0 = 0) {
+      for (; s0 < p.num_seqs; s0 += 32) {
+        int start = 0, len = 0;
+        const bool has = s0 + lane < p.num_seqs && blocks_of(p, s0 + lane, start, len) > level;
+        const unsigned mask = __ballot_sync(~0u, has);
+        const int n = __popc(mask);
+        if (rank - passed < n) {
+          const unsigned mine = __ballot_sync(~0u, has && __popc(mask & ((1u << lane) - 1)) == rank - passed);
+          const int src = __ffs(mine) - 1;
+          it.t = level;
+          it.start = __shfl_sync(~0u, start, src);
+          it.len = __shfl_sync(~0u, len, src);
+          return true;
+        }
+        passed += n;
+      }
     }
-    left -= n;
+    return false;
   }
-  return false;
-}
+};
 
 // A CTA works through items (query blocks x heads) until none are left; the
 // softmax, the issuers and the loads each run ahead as far as their buffers
@@ -709,12 +699,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // Warp 11 finds the items, ahead of the others.  They are dealt out in
       // rounds, every other round backwards.
+      Finder finder;
+      finder.begin(p);
       for (int k = 0;; ++k) {
         const int64_t g = gridDim.x, c = blockIdx.x;
         const int64_t idx = k * g + ((k & 1) ? g - 1 - c : c);
         const int e = k & 1;
         Item it{0, 0, 0};
-        const bool have = find_item(p, idx / p.heads, it);
+        const bool have = finder.find(p, idx / p.heads, it);
         if (k >= 2 && !mbar_wait_a(item_empty(e), ((k >> 1) & 1) ^ 1, abort_flag, p.status)) break;
         if (lane == 0) {
           items[e * 4] = it.start;

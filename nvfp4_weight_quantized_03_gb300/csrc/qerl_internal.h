@@ -154,7 +154,7 @@ struct DecodeAttentionArgs {
   float* lse;
   void* workspace;
 };
-size_t decode_attention_workspace_bytes(int64_t num_seqs, int num_heads, int num_kv_heads, int head_dim);
+size_t decode_attention_workspace_bytes(int64_t num_seqs, int num_heads, int num_kv_heads);
 qerl_status launch_decode_attention(const DecodeAttentionArgs& a, cudaStream_t s);
 
 // prompt_attention.cu: causal attention of packed whole prompts.

@@ -252,3 +252,40 @@ def test_bad_pages_and_lengths_are_recorded(q_):
         _check([40] * 3, q[ok], [rows[i] for i in ok], ks, vs, 0.125, out[ok], lse[ok])
         if lengths[1] < 0:
             assert (out[1] == 0).all() and (lse[1] == -math.inf).all()
+
+
+def test_one_workspace_for_many_shapes(q_):
+    """Calls of different shapes take turns on one workspace, which is zero-filled once."""
+    shapes = [([900, 3, 77], 28, 4, 128, F8), ([5000], 12, 1, 128, BF), ([40] * 300, 8, 2, 64, BF),
+              ([1, 2000], 45, 3, 64, BF)]
+    need = max(q_.qerl_decode_attention_workspace_size(len(l), h, hk, d) for l, h, hk, d, _ in shapes)
+    ws = q_.workspace(need)
+    made = [_setup(q_, l, h, hk, d, 16, t, seed=i) for i, (l, h, hk, d, t) in enumerate(shapes)]
+    for _ in range(2):
+        for (lens, *_rest), (cache, q, rows, ks, vs) in zip(shapes, made):
+            out, lse = _run(q_, cache, q, lens, 0.1, ws=ws)
+            _check(lens, q, rows, ks, vs, 0.1, out, lse)
+
+
+def test_a_table_whose_rows_overlap_is_refused(q_):
+    cache, q, *_ = _setup(q_, [20, 20], 8, 2, 64, 16, BF)
+    shared = q_.kv_cache(cache.tensors[0], cache.tensors[1], cache.tensors[2][:1].expand(2, -1))
+    ws = q_.workspace(q_.qerl_decode_attention_workspace_size(2, 8, 2, 64))
+    st = q_.qerl_decode_attention(shared, q, torch.ones(2, dtype=torch.int32, device="cuda"), 0.1, torch.empty_like(q),
+                                  None, ws)
+    assert q_.STATUS_NAMES[st] == "QERL_ERR_INVALID_ARGUMENT"
+
+
+def test_no_lse_and_no_pages(q_):
+    """lse may be left out; a cache without pages or table columns gives empty rows."""
+    cache, q, rows, ks, vs = _setup(q_, [50, 300], 8, 2, 64, 16, BF)
+    out, lse = _run(q_, cache, q, [50, 300], 0.1)
+    ws = q_.workspace(q_.qerl_decode_attention_workspace_size(2, 8, 2, 64))
+    again = torch.empty_like(out)
+    lengths = torch.tensor([50, 300], dtype=torch.int32, device="cuda")
+    q_.check(q_.qerl_decode_attention(cache, q, lengths, 0.1, again, None, ws))
+    assert q_.qerl_read_status(ws) == 0 and torch.equal(out, again)
+    none = torch.empty((0, 2, 16, 64), dtype=BF, device="cuda")
+    empty = q_.kv_cache(none, none, torch.zeros((2, 0), dtype=torch.int32, device="cuda"))
+    q_.check(q_.qerl_decode_attention(empty, q, lengths * 0, 0.1, out, lse, ws))
+    assert q_.qerl_read_status(ws) == 0 and (out == 0).all() and (lse == -math.inf).all()

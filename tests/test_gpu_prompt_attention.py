@@ -157,6 +157,31 @@ def test_many_short_prompts(q_):
     _check(q, k, v, cu_list, 0.125, out, lse)
 
 
+def test_many_empty_and_equal_prompts(q_):
+    """Hundreds of sequences, most of them empty, some a block, some two: every block is found once."""
+    lens = [0] * 400
+    for i in range(0, 400, 3):
+        lens[i] = 1 + (i * 11) % 40
+    lens[200], lens[7] = 300, 513
+    g = torch.Generator(device="cuda").manual_seed(10)
+    t = sum(lens)
+    q, k, v = _rows(t, 4, 64, g, 1.5), _rows(t, 2, 64, g), _rows(t, 2, 64, g)
+    cu, cu_list = _cu(lens)
+    out, lse = _run(q_, q, k, v, cu, 0.125)
+    _check(q, k, v, cu_list, 0.125, out, lse)
+
+
+def test_no_lse(q_):
+    g = torch.Generator(device="cuda").manual_seed(11)
+    q, k, v = _rows(300, 4, 128, g), _rows(300, 2, 128, g), _rows(300, 2, 128, g)
+    cu, _ = _cu([300])
+    out, _ = _run(q_, q, k, v, cu, 0.09)
+    again = torch.empty_like(out)
+    ws = q_.workspace(q_.qerl_prompt_attention_workspace_size(300, 4, 2, 128, 1))
+    q_.check(q_.qerl_prompt_attention(q, k, v, cu, 0.09, again, None, ws))
+    assert q_.qerl_read_status(ws) == 0 and torch.equal(out, again)
+
+
 def test_bad_offsets_are_recorded(q_):
     g = torch.Generator(device="cuda").manual_seed(8)
     t = 100
