@@ -310,7 +310,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init_a(s_full(i), 1);
+#ifdef QERL_TEST_HOOKS
+      mbar_init_a(p_full(i, 0), 4 + (g_test_extra_arrival ? 1 : 0));
+#else
       mbar_init_a(p_full(i, 0), 4);
+#endif
       mbar_init_a(p_full(i, 1), 4);
       mbar_init_a(o_full(i), 1);
       mbar_init_a(turn(i), 1);
@@ -810,3 +814,13 @@ qerl_status launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t s
 }
 
 }  // namespace qerl
+
+#ifdef QERL_TEST_HOOKS
+// Test-only build: this file's wait limit, and one arrival too many expected on
+// the barriers that announce the first half of a tile's weights.
+extern "C" QERL_API int qerl_test_set_prompt_hooks(long long wait_limit_cycles, int extra_arrival) {
+  if (cudaMemcpyToSymbol(qerl::g_test_wait_limit, &wait_limit_cycles, sizeof(wait_limit_cycles)) != cudaSuccess)
+    return 1;
+  return cudaMemcpyToSymbol(qerl::g_test_extra_arrival, &extra_arrival, sizeof(extra_arrival)) != cudaSuccess ? 1 : 0;
+}
+#endif
