@@ -217,13 +217,15 @@ def _p(t):
     return t.data_ptr()
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream() builds an object: 3 us a call
+# current_stream() builds an object (3 us a call), current_device() looks whether CUDA is up each time.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -239,7 +241,7 @@ def _wdtype(W):
 
 
 def _nbytes(t):
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 # ---- C entry points ---------------------------------------------------------
@@ -486,16 +488,17 @@ def _heads(name, t, shape):
 
 def _vector(name, t, dtype, n):
     """Raises unless t is a contiguous CUDA vector of n entries of this type."""
-    if t.dtype is not dtype or not t.is_cuda or t.dim() != 1:
+    if t.dtype is not dtype or not t.is_cuda:
         _expect(name, t, dtype, 1)
-    if t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name}: expected {n} contiguous entries, got {tuple(t.shape)} with strides {t.stride()}")
 
 
 def _heads_shape(name, t):
-    if t.dim() != 3:
-        raise ValueError(f"{name}: expected [rows, heads, head_dim], got {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name}: expected [rows, heads, head_dim], got {tuple(shape)}")
+    return shape
 
 
 def kv_cache(k, v, page_table, k_scale=None, v_scale=None):
@@ -542,9 +545,11 @@ def qerl_rope_append(cache, q, k, v, positions, inv_freq, q_out, k_out, workspac
     ldk = _heads("k", k, shape)
     h = ldq = ldqo = ldv = ldko = 0
     if q is not None:
-        h = _heads_shape("q", q)[1]
-        ldq = _heads("q", q, (tokens, h, d))
-        ldqo = _heads("q_out", q_out, (tokens, h, d))
+        wide = _heads_shape("q", q)
+        h = wide[1]
+        if wide[0] != tokens or wide[2] != d:
+            raise ValueError(f"q: expected k's tokens and head_dim, got {tuple(wide)}")
+        ldq, ldqo = _heads("q", q, wide), _heads("q_out", q_out, wide)
     if v is not None:
         ldv = _heads("v", v, shape)
     if k_out is not None:
@@ -554,10 +559,11 @@ def qerl_rope_append(cache, q, k, v, positions, inv_freq, q_out, k_out, workspac
     _vector("inv_freq", inv_freq, _F64, half)
     if seq_ids is not None:
         _vector("seq_ids", seq_ids, _I32, tokens)
-    return (_lib or lib()).qerl_rope_append(cache, _p(q), ldq, h, k.data_ptr(), ldk, _p(v), ldv, hk, d, tokens,
-                                            _p(seq_ids), positions.data_ptr(), inv_freq.data_ptr(), 2 * half,
-                                            _p(q_out), ldqo, _p(k_out), ldko, workspace.data_ptr(),
-                                            _nbytes(workspace), _stream(stream))
+    return (_lib or lib()).qerl_rope_append(
+        cache, None if q is None else q.data_ptr(), ldq, h, k.data_ptr(), ldk, None if v is None else v.data_ptr(), ldv,
+        hk, d, tokens, None if seq_ids is None else seq_ids.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
+        2 * half, None if q is None else q_out.data_ptr(), ldqo, None if k_out is None else k_out.data_ptr(), ldko,
+        workspace.data_ptr(), workspace.nbytes, _stream(stream))
 
 
 def qerl_decode_attention_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
@@ -565,7 +571,7 @@ def qerl_decode_attention_workspace_size(num_seqs: int, num_heads: int, num_kv_h
 
 
 def _lse(lse, rows, heads):
-    if lse.dtype is not _F32 or not lse.is_cuda or lse.dim() != 2:
+    if lse.dtype is not _F32 or not lse.is_cuda:
         _expect("lse", lse, _F32, 2)
     if lse.shape != (rows, heads) or not lse.is_contiguous():
         raise ValueError("lse: contiguous [rows, num_heads]")
@@ -583,7 +589,7 @@ def qerl_decode_attention(cache, q, lengths, scale, out, lse, workspace, stream=
     _vector("lengths", lengths, _I32, n)
     return (_lib or lib()).qerl_decode_attention(cache, q.data_ptr(), ldq, h, lengths.data_ptr(), scale,
                                                  out.data_ptr(), ldo, None if lse is None else _lse(lse, n, h),
-                                                 workspace.data_ptr(), _nbytes(workspace), _stream(stream))
+                                                 workspace.data_ptr(), workspace.nbytes, _stream(stream))
 
 
 def qerl_prompt_attention_workspace_size(tokens: int, num_heads: int, num_kv_heads: int, head_dim: int,
