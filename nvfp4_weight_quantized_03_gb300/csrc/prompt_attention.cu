@@ -351,7 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto take = [&](int k, Work& w) -> bool {
     const int e = k & 1;
-    if (!mbar_wait_a(item_full(e), (k >> 1) & 1, abort_flag, p.status)) return false;
+    // (a warp goes on or gives up as a whole, here and at every wait of a whole warp)
+    if (!__all_sync(~0u, mbar_wait_a(item_full(e), (k >> 1) & 1, abort_flag, p.status))) return false;
     w.it.start = items[e * 4];
     w.it.len = items[e * 4 + 1];
     w.it.t = items[e * 4 + 2];
@@ -380,9 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // elements that are not finite; a thread takes one key's row.
       auto clean_values = [&](int u) -> bool {
         const int s = u % S::kSlots;
-        const bool here = mbar_wait_a(full(s), (u / S::kSlots) & 1, abort_flag, p.status);
-        __syncwarp();
-        if (!here) return false;
+        if (!__all_sync(~0u, mbar_wait_a(full(s), (u / S::kSlots) & 1, abort_flag, p.status))) return false;
         const uint32_t row = sbase + S::kRing + s * S::kTile + r * 128;
         // x * 0 + sum is NaN from the first x that is not finite
         uint32_t sum = 0;
@@ -503,8 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       for (int j = 0; j < mine; ++j) {
         if (j + 1 == mine) ok = clean_values(u0 + 2 * j + 1);  // while the scores are computed
-        ok = ok && mbar_wait_a(s_full(i), (tiles_done + j) & 1, abort_flag, p.status);
-        __syncwarp();
+        ok = __all_sync(~0u, ok && mbar_wait_a(s_full(i), (tiles_done + j) & 1, abort_flag, p.status));
         if (!ok) break;
         tc_fence_after();
         step(j);
@@ -512,9 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tiles_done += mine;
       u0 += 2 * max(w.n0, w.n1);
       if (mine > 0) {
-        ok = ok && mbar_wait_a(o_full(i), outputs_done & 1, abort_flag, p.status);
+        ok = __all_sync(~0u, ok && mbar_wait_a(o_full(i), outputs_done & 1, abort_flag, p.status));
         ++outputs_done;
-        __syncwarp();
         tc_fence_after();
         const int rs = w.it.t * kBlock + i * kRows + r;  // row in the sequence
         const bool live = ok && rs < w.it.len;
@@ -660,9 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait_a(q_full(i), q_used & 1, abort_flag, p.status);
           ++q_used;
         }
-        ok = ok && wait_slot(u0);
+        ok = __all_sync(~0u, ok && wait_slot(u0));
         if (!ok) break;
-        __syncwarp();
         tc_fence_after();
         if (mine > 0) scores(u0);
         if (mine == 1) commit(leader, q_empty(i));
@@ -678,14 +674,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++turns;
           }
           if (ok && j < mine) ok = mbar_wait_a(p_full(i, 0), (tiles_done + j) & 1, abort_flag, p.status);
+          ok = __all_sync(~0u, ok);
           if (!ok) break;
-          __syncwarp();
           if (j < mine) {
             tc_fence_after();
             values(u0 + 2 * j + 1, 0, j > 0);
-            ok = mbar_wait_a(p_full(i, 1), (tiles_done + j) & 1, abort_flag, p.status);
+            ok = __all_sync(~0u, mbar_wait_a(p_full(i, 1), (tiles_done + j) & 1, abort_flag, p.status));
             if (!ok) break;
-            __syncwarp();
             tc_fence_after();
             values(u0 + 2 * j + 1, 1, true);
           }
@@ -711,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = k & 1;
         Item it{0, 0, 0};
         const bool have = finder.find(p, idx / p.heads, it);
-        if (k >= 2 && !mbar_wait_a(item_empty(e), ((k >> 1) & 1) ^ 1, abort_flag, p.status)) break;
+        const bool free = k < 2 || mbar_wait_a(item_empty(e), ((k >> 1) & 1) ^ 1, abort_flag, p.status);
+        if (!__all_sync(~0u, free)) break;
         if (lane == 0) {
           items[e * 4] = it.start;
           items[e * 4 + 1] = have ? it.len : 0;
