@@ -9,13 +9,22 @@
 // output stay in registers.
 //
 // Bound: bytes of the cache (G multiply-adds per byte).  The work is cut by
-// bytes, not by sequences: all (sequence, key-value head, key tile) units in
-// order form one line that the resident CTAs share out evenly, computed on the
+// cost, not by sequences: all (sequence, key-value head, key tile) units in
+// order form one line, weighted by their rows and the cost of a segment's start
+// and join, that the resident CTAs share out evenly.  It is computed on the
 // device from the lengths, so ragged batches balance and no host copy of the
 // lengths is needed.  A CTA whose stretch begins or ends inside a (sequence,
 // head) leaves its partial (m, l, o) in the workspace; the last of that
 // head's CTAs to arrive joins the partials in CTA order (the result does not
 // depend on the arrival order).
+//
+// Measured: 128 x 6000 rows, 40/8 heads of 128, E4M3: 247 us = 0.94 of the copy
+// rate; 64 ragged to 8192, 28/4, bf16: 73 us = 0.88; 1 x 100003, 40/8, bf16:
+// 73 us = 0.83 (3 us before the first rows, the CTAs finish 12 us apart, 5 us
+// of join); 256 ragged to 1500, 32/8 heads of 64: 50 us = 0.83.  Steps: joins
+// with one partial in flight 96 -> 84 us on the long sequence; the stretch by
+// cost, the join by one warp while the others go on, and the stream marked
+// evict-first (it leaves the code and the partials in L2) 84 -> 73 us.
 //
 // A warp owns kKeys keys of every tile and its own ring of cp.async stages, so
 // the key loop has no CTA barrier.  Products run on mma.sync.m16n8k16 with the

@@ -289,3 +289,31 @@ def test_no_lse_and_no_pages(q_):
     empty = q_.kv_cache(none, none, torch.zeros((2, 0), dtype=torch.int32, device="cuda"))
     q_.check(q_.qerl_decode_attention(empty, q, lengths * 0, 0.1, out, lse, ws))
     assert q_.qerl_read_status(ws) == 0 and (out == 0).all() and (lse == -math.inf).all()
+
+
+def test_binding_refuses_what_the_library_cannot_see(q_):
+    """Types, shapes and strides that a raw pointer does not tell."""
+    cache, q, *_ = _setup(q_, [20, 20], 8, 2, 64, 16, BF)
+    n, h, d = q.shape
+    ws = q_.workspace(q_.qerl_decode_attention_workspace_size(n, h, 2, d))
+    good = dict(q=q, lengths=torch.tensor([20, 20], dtype=torch.int32, device="cuda"), out=torch.empty_like(q),
+                lse=torch.empty((n, h), device="cuda"))
+    call = lambda **kw: q_.qerl_decode_attention(cache, scale=0.1, workspace=ws, **{**good, **kw})
+    assert call() == 0
+    for kw, error in [(dict(q=q.float()), TypeError), (dict(out=good["out"].half()), TypeError),
+                      (dict(lengths=good["lengths"].long()), TypeError), (dict(lengths=good["lengths"].cpu()), TypeError),
+                      (dict(lse=good["lse"].double()), TypeError), (dict(lengths=good["lengths"][:1]), ValueError),
+                      (dict(q=q[:1]), ValueError), (dict(out=good["out"][:, :4]), ValueError),
+                      (dict(lse=torch.empty((h, n), device="cuda")), ValueError),
+                      (dict(q=q.transpose(0, 1).contiguous().transpose(0, 1)), ValueError),
+                      (dict(lengths=torch.zeros(4, dtype=torch.int32, device="cuda")[::2]), ValueError)]:
+        with pytest.raises(error):
+            call(**kw)
+    k, v, table = cache.tensors[:3]
+    for args, error in [((k.float(), v.float(), table), TypeError), ((k, v, table.long()), TypeError),
+                        ((k, v[:-1], table), ValueError), ((k.transpose(1, 2), v.transpose(1, 2), table), ValueError),
+                        ((k, v.view(torch.int16), table), TypeError), ((k, v, table.T.contiguous().T), ValueError),
+                        ((k.view(torch.uint8)[..., :64].contiguous().view(F8), v.view(torch.uint8)[..., :64].contiguous()
+                          .view(F8), table, torch.ones(3, device="cuda")), ValueError)]:
+        with pytest.raises(error):
+            q_.kv_cache(*args)
