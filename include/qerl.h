@@ -507,7 +507,8 @@ typedef struct {
  *   k_out    bf16 rows or NULL; may be k itself (same stride).
  *   cache    NULL: rotation only (v, seq_ids are then not read; k_out required).
  * The cache gets the fp32 rotated k (and v) rounded once to its type: bf16, or
- * E4M3(value / scale), nearest even, saturating at +-448, NaN kept.
+ * E4M3(value * (1 / scale)) with an fp32 reciprocal, nearest even, saturating
+ * at +-448, NaN kept.
  * Pointers of q, k, v, q_out, k_out 16-byte aligned, strides multiples of 8.
  * rot_dim % 16 == 0, 0 <= rot_dim <= head_dim.  The num_kv_heads and head_dim
  * arguments equal the cache's.  Two tokens of one call at one place of the

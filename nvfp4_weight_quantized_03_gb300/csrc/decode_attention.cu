@@ -55,6 +55,11 @@ constexpr int kThreads = 32 * kWarps;
 // shape: the counters behind it then lie at the same place for all calls that
 // share a workspace, and are zero between them.
 constexpr size_t kPartBytes = size_t{6} << 20;
+constexpr int kMaxCtas = 1024;
+constexpr size_t kGroupBytes = 2 * kMaxCtas * sizeof(unsigned);
+// A segment of more CTAs than kDirect is joined in groups of kGroup CTAs first,
+// by the last of each group to arrive: one CTA alone took 9 us for 76 partials.
+constexpr int kDirect = 16, kGroup = 8;
 // How far (base 2) a score may pass the reference m before m moves: 2^8 keeps
 // the fp32 sums and the fp16 probabilities in range, and most steps then skip
 // the maximum's reduction and the rescaling.
@@ -76,8 +81,9 @@ struct DecodeParams {
   __nv_bfloat16* out;
   int64_t ldo;
   float* lse;
-  float* part;         // [CTA][2][NT * 8][D + 2]: of the segment begun before its stretch, of the one begun in it
+  float* part;         // [CTA][2][NT * 8][D + 4]: of the segment begun before its stretch, of the one begun in it
   unsigned* counters;  // [num_seqs * kv_heads * zgroups], zero between calls
+  unsigned* group_counters;  // [CTA][2], zero between calls
   int* status;
 };
 
@@ -95,15 +101,16 @@ struct Shape {
   static constexpr int kSegmentCost = kTileCost * 3 / 2;
   static constexpr int kStage = 2 * kKeys * kRow;  // K then V
   // CTAs per SM and stages per warp fill the shared memory.  Short rows leave
-  // the warps waiting on their own chain of steps more than on memory: three
-  // CTAs with 2 stages (51 us) beat two with 3 (55.5 us).
-  static constexpr int kCtas = D == 64 && NT == 1 ? 3 : 2;
-  static constexpr int kStages = kStage == 4096 ? 4 : NT == 1 && D == 128 ? 3 : 2;
+  // the warps waiting on their own chain of steps more than on memory: heads of
+  // 64, bf16, three CTAs with 2 stages 51 us, two with 3 55.5 us; E4M3 (64 x
+  // 6000 rows, 32/8 heads) four with 2 stages 75 us, three with 4 79 us.
+  static constexpr int kCtas = kStage == 4096 ? (NT == 1 ? 4 : 3) : D == 64 && NT == 1 ? 3 : 2;
+  static constexpr int kStages = kStage == 4096 ? (NT == 1 ? 2 : 3) : NT == 1 && D == 128 ? 3 : 2;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kOStride = D + 4;  // columns 2c, 2c+1 of 8 rows fall in 32 banks
   static constexpr int kJoin = kWarps * NT * 8 * kOStride * 4;
   static constexpr int kSmem = kRing + kJoin;
-  static constexpr int kPartRow = D + 2;
+  static constexpr int kPartRow = D + 4;  // o; (m, l) of a CTA's partial; (m, l) of a group's sum
 };
 
 // Physical 16-byte chunk of a row in shared memory: 8 rows of one logical
@@ -720,11 +727,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
           // The CTAs that hold tiles of this segment; the last of them to come
           // here adds their partials when its own tiles are done.
           const int c0 = owner(seg_begin), c1 = owner(seg_begin + static_cast<long long>(cur.tiles - 1) * S::kTileCost);
-          unsigned* counter = p.counters + static_cast<int64_t>(cur.b) * hz_all + cur.hz;
+          const int parts = c1 - c0 + 1;
+          const int lead = parts <= kDirect ? 0 : (static_cast<int>(blockIdx.x) - c0) / kGroup * kGroup;
+          const int group = parts <= kDirect ? parts : min(kGroup, parts - lead);
+          unsigned* counter = parts <= kDirect ? p.counters + static_cast<int64_t>(cur.b) * hz_all + cur.hz
+                                               : p.group_counters + 2 * (c0 + lead) + (lead == 0 ? 1 : 0);
           // Release of this warp's partial, acquire of the others'.
-          if (atomic_add_acq_rel(counter, 1u) == static_cast<unsigned>(c1 - c0)) {
+          if (atomic_add_acq_rel(counter, 1u) == static_cast<unsigned>(group - 1)) {
             *counter = 0;  // ready for the next call
-            pending[slot_index] = make_int4(cur.b, cur.hz, c0, c1 - c0 + 1);
+            pending[slot_index] = make_int4(cur.b, cur.hz, c0 + lead, parts <= kDirect ? parts : group | lead << 8 | parts << 18);
           }
         }
         __syncwarp();
@@ -736,58 +747,94 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
   }
   cp_async_wait_group<0>();
 
-  // ---- segments whose last partial this CTA brought --------------------------
+  // ---- segments (or groups of their CTAs) whose last partial this CTA brought --
+  // A partial's slot is 1 in the CTA that began the segment and 0 in the others,
+  // which came to it from before.  Kept short: this code runs once, and its
+  // fetch is part of its time.
   __syncthreads();
-  // Kept short: this code runs once, and its fetch is part of its time.
+#pragma unroll 1
   for (int s = 0; s < 2; ++s) {
     const int4 job = pending[s];
     if (job.w == 0) continue;
+    // .w: the number of partials, or group | lead << 8 | parts << 18
+    const bool grouped = job.w > kDirect;
+    const int parts = job.w >> 18, lead = (job.w >> 8) & 1023;
+    int first_cta = job.z, first_slot = grouped && lead > 0 ? 0 : 1, count = grouped ? job.w & 255 : job.w, stride = 1;
+    bool sums_of_groups = false;  // the second level
     const int part0 = job.y % p.zgroups, nheads = min(p.zheads, p.group - part0 * p.zheads);
 #pragma unroll 1
-    for (int i = tid; i < nheads * (D / 4); i += kThreads) {
-      const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
-      // Its first CTA began the segment (slot 1); the others came to it from before (slot 0).
-      const float* first = p.part + (2 * static_cast<int64_t>(job.z) + 1) * kSlot;
-      float top = -kInf, sum = 0.0f;
-      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      constexpr int kBatch = 16;  // partials in flight
+    for (;;) {
+      float* first = p.part + (2 * static_cast<int64_t>(first_cta) + first_slot) * kSlot;
+      const int ml_at = NT * 8 * (sums_of_groups ? D + 2 : D);
+      const bool last_level = !grouped || sums_of_groups;
 #pragma unroll 1
-      for (int c0 = 0; c0 < job.w; c0 += kBatch) {
-        float2 e[kBatch];
-        float4 v[kBatch];
-        float up = top;
+      for (int i = tid; i < nheads * (D / 4); i += kThreads) {
+        const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+        float top = -kInf, sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        constexpr int kBatch = 16;  // partials in flight
+#pragma unroll 1
+        for (int c0 = 0; c0 < count; c0 += kBatch) {
+          float2 e[kBatch];
+          float4 v[kBatch];
+          float up = top;
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const int c = c0 + q;
-          const float* slot = first + (c == 0 ? 0 : 2 * c - 1) * kSlot;
-          e[q] = make_float2(-kInf, 0.0f);
-          v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (c < job.w) {
-            e[q] = __ldcg(reinterpret_cast<const float2*>(slot + NT * 8 * D + 2 * h));
-            v[q] = __ldcg(reinterpret_cast<const float4*>(slot + h * D + d));
+          for (int q = 0; q < kBatch; ++q) {
+            const int c = c0 + q;
+            const float* slot = first + (c == 0 ? 0 : 2 * c * stride - first_slot) * kSlot;
+            e[q] = make_float2(-kInf, 0.0f);
+            v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (c < count) {
+              e[q] = __ldcg(reinterpret_cast<const float2*>(slot + ml_at + 2 * h));
+              v[q] = __ldcg(reinterpret_cast<const float4*>(slot + h * D + d));
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q) up = fmaxf(up, e[q].x);
+          const float f0 = weight_of(top, up);
+          top = up;
+          sum *= f0;
+          acc.x *= f0;
+          acc.y *= f0;
+          acc.z *= f0;
+          acc.w *= f0;
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q) {
+            const float f = weight_of(e[q].x, top);
+            sum += f * e[q].y;
+            acc.x += f * v[q].x;
+            acc.y += f * v[q].y;
+            acc.z += f * v[q].z;
+            acc.w += f * v[q].w;
           }
         }
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) up = fmaxf(up, e[q].x);
-        const float f0 = weight_of(top, up);
-        top = up;
-        sum *= f0;
-        acc.x *= f0;
-        acc.y *= f0;
-        acc.z *= f0;
-        acc.w *= f0;
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const float f = weight_of(e[q].x, top);
-          sum += f * e[q].y;
-          acc.x += f * v[q].x;
-          acc.y += f * v[q].y;
-          acc.z += f * v[q].z;
-          acc.w += f * v[q].w;
+        if (last_level) {
+          finish(job.x, job.y, h, d, top, sum, acc);
+        } else {
+          // into the first partial's slot; its (m, l), which other threads still read, stays
+          __stcg(reinterpret_cast<float4*>(first + h * D + d), acc);
+          if (d == 0) __stcg(reinterpret_cast<float2*>(first + NT * 8 * (D + 2) + 2 * h), make_float2(top, sum));
         }
       }
-      finish(job.x, job.y, h, d, top, sum, acc);
+      if (last_level) break;
+      // The group's sum is there; the last group of the segment goes on to join them.
+      __syncthreads();
+      if (tid == 0) {
+        const int groups = (parts + kGroup - 1) / kGroup;
+        unsigned* counter = p.counters + static_cast<int64_t>(job.x) * hz_all + job.y;
+        const bool mine = atomic_add_acq_rel(counter, 1u) == static_cast<unsigned>(groups - 1);
+        if (mine) *counter = 0;
+        found[0] = mine;
+      }
+      __syncthreads();
+      if (!found[0]) break;
+      first_cta = job.z - lead;
+      first_slot = 1;
+      count = (parts + kGroup - 1) / kGroup;
+      stride = kGroup;
+      sums_of_groups = true;
     }
+    __syncthreads();  // found is free
   }
 }
 
@@ -803,7 +850,7 @@ qerl_status launch(const DecodeParams& p, int sms, int dev, cudaStream_t s) {
     ready.fetch_or(bit);
   }
   constexpr int kFit = static_cast<int>(kPartBytes / (2 * NT * 8 * S::kPartRow * sizeof(float)));
-  int64_t grid = std::min(S::kCtas * sms, kFit);
+  int64_t grid = std::min({S::kCtas * sms, kFit, kMaxCtas});
   const int64_t most =
       static_cast<int64_t>(p.num_seqs) * p.kv_heads * p.zgroups * ((p.capacity + S::kTile - 1) / S::kTile);
   if (most < grid) grid = most > 0 ? most : 1;
@@ -833,7 +880,7 @@ size_t counter_bytes(int64_t num_seqs, int num_kv_heads, const Split& s) {
 
 size_t decode_attention_workspace_bytes(int64_t num_seqs, int num_heads, int num_kv_heads) {
   const Split s = split_heads(num_heads / num_kv_heads);
-  return kWsHeaderBytes + kPartBytes + counter_bytes(num_seqs, num_kv_heads, s);
+  return kWsHeaderBytes + kPartBytes + kGroupBytes + counter_bytes(num_seqs, num_kv_heads, s);
 }
 
 qerl_status launch_decode_attention(const DecodeAttentionArgs& a, cudaStream_t s) {
@@ -870,7 +917,8 @@ qerl_status launch_decode_attention(const DecodeAttentionArgs& a, cudaStream_t s
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.status = &reinterpret_cast<WsHeader*>(ws)->status;
   p.part = reinterpret_cast<float*>(ws + kWsHeaderBytes);
-  p.counters = reinterpret_cast<unsigned*>(ws + kWsHeaderBytes + kPartBytes);
+  p.group_counters = reinterpret_cast<unsigned*>(ws + kWsHeaderBytes + kPartBytes);
+  p.counters = p.group_counters + 2 * kMaxCtas;
   const bool f8 = c.dtype == QERL_E4M3;
   const bool one = sp.tiles == 1;
   if (c.head_dim == 128) {

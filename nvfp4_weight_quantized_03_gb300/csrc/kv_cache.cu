@@ -56,9 +56,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// Two fp32 values -> E4M3 (nearest even, saturating, NaN kept) of value / scale, in the low 16 bits.
-__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi, float scale) {
-  const float a = __fdiv_rn(lo, scale), b = __fdiv_rn(hi, scale);
+// Two fp32 values times `inverse` -> E4M3 (nearest even, saturating, NaN kept), in the low 16 bits.
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi, float inverse) {
+  const float a = lo * inverse, b = hi * inverse;
   uint32_t h;
   asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
       : "=r"(h)
@@ -100,10 +100,12 @@ __global__ void __launch_bounds__(512, kThreadsPerSm / 512) rope_append_kernel(c
   const int64_t ldd = kind == 0 ? p.ldqo : p.ldko;
   if (dst != nullptr) dst += head * p.dim + blockIdx.x * ldd;
   uint8_t* pages = kind == 1 ? p.k_pages : kind == 2 ? p.v_pages : nullptr;
-  float scale = 1.0f;
+  // One division a thread: 16 per item and token took longer than the rows
+  // (16000 tokens of 40 + 2 x 8 heads: 66 us, so 0.59 of the copy rate).
+  float inverse = 1.0f;
   if (kE4m3 && active && kind > 0) {
     const float* sc = kind == 1 ? p.k_scale : p.v_scale;
-    if (sc != nullptr) scale = sc[head];
+    if (sc != nullptr) inverse = 1.0f / sc[head];
   }
   // The place of token t in the cache: its page number, or -1.
   auto page_of = [&](int64_t t, int pos) -> int {
@@ -168,8 +170,8 @@ __global__ void __launch_bounds__(512, kThreadsPerSm / 512) rope_append_kernel(c
           b[i] = pack_bf16(yl, yh);
         }
         if (kE4m3 && kind > 0) {
-          c0[i >> 1] |= pack_e4m3(xl, xh, scale) << (16 * (i & 1));
-          c1[i >> 1] |= pack_e4m3(yl, yh, scale) << (16 * (i & 1));
+          c0[i >> 1] |= pack_e4m3(xl, xh, inverse) << (16 * (i & 1));
+          c1[i >> 1] |= pack_e4m3(yl, yh, inverse) << (16 * (i & 1));
         }
       }
       if (dst != nullptr) {
