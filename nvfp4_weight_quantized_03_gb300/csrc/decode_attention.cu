@@ -20,11 +20,13 @@
 //
 // Measured: 128 x 6000 rows, 40/8 heads of 128, E4M3: 247 us = 0.94 of the copy
 // rate; 64 ragged to 8192, 28/4, bf16: 73 us = 0.88; 1 x 100003, 40/8, bf16:
-// 73 us = 0.83 (3 us before the first rows, the CTAs finish 12 us apart, 5 us
-// of join); 256 ragged to 1500, 32/8 heads of 64: 50 us = 0.83.  Steps: joins
-// with one partial in flight 96 -> 84 us on the long sequence; the stretch by
-// cost, the join by one warp while the others go on, and the stream marked
-// evict-first (it leaves the code and the partials in L2) 84 -> 73 us.
+// 72 us = 0.84 (3 us before the first rows, the CTAs finish 12 us apart, 5 us
+// of join); 256 ragged to 1500, 32/8 heads of 64: 50 us = 0.84.  Steps: the
+// join with more than one partial in flight 96 -> 84 us on the long sequence;
+// the stretch by cost, the segments' joins by one warp while the others go on,
+// and the stream marked evict-first (it leaves the code and the partials in L2)
+// 84 -> 73 us; many partials joined in two levels 73 -> 72 us (one sequence of
+// 8000 rows 18.3 -> 12.8 us).
 //
 // A warp owns kKeys keys of every tile and its own ring of cp.async stages, so
 // the key loop has no CTA barrier.  Products run on mma.sync.m16n8k16 with the
