@@ -87,7 +87,7 @@ template <int D>
 struct Shape {
   static constexpr int kPanels = D / 64;
   static constexpr uint32_t kTile = kPanels * kPanel;
-  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr unsigned kSlots = D == 128 ? 4 : 8;
   static constexpr uint32_t kRing = 2 * kTile;
   static constexpr uint32_t kStage = kRing + kSlots * kTile;  // 64 output columns of each query tile
   static constexpr uint32_t kBars = kStage + 2 * kPanel;
@@ -214,6 +214,17 @@ __device__ __forceinline__ void commit(uint32_t leader, uint32_t bar) {
       : "memory");
 }
 
+// Where the counters of the ring's loads and of a tile's steps begin.  A CTA
+// counts over all its items, so they may pass 2^32: they are unsigned, and only
+// their residues (slot and phase) are used, which the wrap keeps because 2^32 is
+// a multiple of two laps of the ring.  The start is too.
+#ifdef QERL_TEST_HOOKS
+__device__ unsigned g_test_first_count = 0;
+#define QERL_FIRST_COUNT g_test_first_count
+#else
+#define QERL_FIRST_COUNT 0u
+#endif
+
 // The work of a CTA: query rows [row0, row0 + 256) of one sequence.
 struct Item {
   int start, len, t;  // the sequence's first row and length; the block's index in it
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* items = reinterpret_cast<volatile int*>(misc_gen + 8 * 20 + 16);    // [2][4]
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kSlots; ++s) {
+    for (unsigned s = 0; s < S::kSlots; ++s) {
       mbar_init_a(full(s), 1);
       mbar_init_a(empty(s), 2);
     }
@@ -372,15 +383,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_t = tmem + lanes + i * 128, o_t = tmem + lanes + 256 + i * D;
     const float kInf = __int_as_float(0x7f800000);
     bool ok = true;
-    int tiles_done = 0, outputs_done = 0, u0 = 0;  // of this query tile; loads of the ring before this item
+    unsigned tiles_done = QERL_FIRST_COUNT, u0 = QERL_FIRST_COUNT;  // of this query tile; loads of the ring before this item
+    int outputs_done = 0;
     Work w;
     for (int k = 0; ok && take(k, w); ++k) {
       const int mine = i == 0 ? w.n0 : w.n1;
       float mc = -kInf, l = 0.0f;  // the reference in base-2 units and the sum of 2^(s - m)
       // The values of the diagonal tile (load u of the ring), looked through for
       // elements that are not finite; a thread takes one key's row.
-      auto clean_values = [&](int u) -> bool {
-        const int s = u % S::kSlots;
+      auto clean_values = [&](unsigned u) -> bool {
+        const unsigned s = u % S::kSlots;
         if (!__all_sync(~0u, mbar_wait_a(full(s), (u / S::kSlots) & 1, abort_flag, p.status))) return false;
         const uint32_t row = sbase + S::kRing + s * S::kTile + r * 128;
         // x * 0 + sum is NaN from the first x that is not finite
@@ -566,15 +578,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8) {
-      int issued = 0, q_loads[2] = {0, 0};
+      unsigned issued = QERL_FIRST_COUNT, used = 0;  // loads; slots of the ring that hold one
+      int q_loads[2] = {0, 0};
       Work w;
       for (int k = 0; take(k, w); ++k) {
         bool ok = true;
         if (lane == 0) {
           const int n = max(w.n0, w.n1);
           for (int u = 0; ok && u < 2 * n; ++u) {  // k, v, k, v, ...
-            const int s = issued % S::kSlots;
-            if (issued >= S::kSlots) ok = mbar_wait_a(empty(s), ((issued / S::kSlots) & 1) ^ 1, abort_flag, p.status);
+            const unsigned s = issued % S::kSlots;
+            if (used == S::kSlots) ok = mbar_wait_a(empty(s), ((issued / S::kSlots) & 1) ^ 1, abort_flag, p.status);
             if (!ok) break;
             mbar_arrive_expect_tx_a(full(s), S::kTile);
             const uint32_t dst = sbase + S::kRing + s * S::kTile;
@@ -583,6 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d(dst + d * kPanel, (u & 1) ? &maps.v : &maps.k, w.head / p.group * D + d * 64,
                           w.it.start + (u >> 1) * kRows, full(s));
             ++issued;
+            if (used < S::kSlots) ++used;
             if (u > 0) continue;
             // After the first keys, the queries (their buffers come free with the last scores of the item before).
             for (int i = 0; ok && i < (w.n1 > 0 ? 2 : 1); ++i) {
@@ -604,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         volatile int no_abort = 0;
         for (int i = 0; i < 2; ++i)
           if (q_loads[i] > 0) mbar_wait_a(q_full(i), (q_loads[i] - 1) & 1, &no_abort, p.status);
-        for (int s = 0; s < min(issued, S::kSlots); ++s) {
-          const int last = issued - 1 - ((issued - 1 - s) % S::kSlots);
+        for (unsigned s = 0; s < used; ++s) {
+          const unsigned last = issued - 1 - ((issued - 1 - s) % S::kSlots);
           mbar_wait_a(full(s), (last / S::kSlots) & 1, &no_abort, p.status);
         }
       }
@@ -618,11 +632,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i = warp - 9;
       const uint32_t id_s = idesc_bf16_f32(128, 128) | (p.negative ? 1u << 13 : 0u);
       const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // v: rows along the contraction
-      auto slot = [&](int u) { return sbase + S::kRing + (u % S::kSlots) * S::kTile; };
-      auto wait_slot = [&](int u) {
+      auto slot = [&](unsigned u) { return sbase + S::kRing + (u % S::kSlots) * S::kTile; };
+      auto wait_slot = [&](unsigned u) {
         return mbar_wait_a(full(u % S::kSlots), (u / S::kSlots) & 1, abort_flag, p.status);
       };
-      auto scores = [&](int u) {
+      auto scores = [&](unsigned u) {
         const uint32_t qa = sbase + i * S::kTile, ka = slot(u);
 #pragma unroll
         for (int d = 0; d < S::kPanels; ++d)
@@ -632,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    sw128_kmajor_desc(ka + d * kPanel + kk * 32), id_s, d + kk > 0 ? 1u : 0u);
         commit(leader, s_full(i));
       };
-      auto values = [&](int u, int part, bool more) {
+      auto values = [&](unsigned u, int part, bool more) {
         const uint32_t va = slot(u);
 #pragma unroll
         for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
@@ -641,15 +655,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // A slot is free when both issuers have released it; one whose tile
       // does not use it (fewer key tiles, or no rows) just arrives.
-      auto release = [&](int u, bool used) {
+      auto release = [&](unsigned u, bool used) {
         if (used) {
           commit(leader, empty(u % S::kSlots));
         } else if (leader) {
           mbar_arrive_a(empty(u % S::kSlots));
         }
       };
-      int u0 = 0, tiles_done = 0, turns = 0, q_used = 0;
-      bool ok = true;
+      unsigned u0 = QERL_FIRST_COUNT, tiles_done = QERL_FIRST_COUNT, turns = QERL_FIRST_COUNT;
+      int q_used = 0;
+      bool ok = true, first_turn = i == 0;  // of tile 0: nobody hands it over
       Work w;
       for (int k = 0; ok && take(k, w); ++k) {
         const int mine = i == 0 ? w.n0 : w.n1, n = max(w.n0, w.n1);
@@ -669,8 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 0's of the next.  Without them the two tiles fall into step, both
           // in the softmax and then both at the tensor core.
           if (ok && w.n1 > 0) {
-            const int before = turns - (i == 0 ? 1 : 0);
-            if (before >= 0) ok = mbar_wait_a(turn(i), before & 1, abort_flag, p.status);
+            if (!first_turn) ok = mbar_wait_a(turn(i), (turns - (i == 0 ? 1 : 0)) & 1, abort_flag, p.status);
+            first_turn = false;
             ++turns;
           }
           if (ok && j < mine) ok = mbar_wait_a(p_full(i, 0), (tiles_done + j) & 1, abort_flag, p.status);
@@ -812,6 +827,12 @@ qerl_status launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t s
 }  // namespace qerl
 
 #ifdef QERL_TEST_HOOKS
+// Test-only build: where the counters begin (a multiple of 16).
+extern "C" QERL_API int qerl_test_set_prompt_first_count(unsigned count) {
+  if (count % 16 != 0) return 1;
+  return cudaMemcpyToSymbol(qerl::g_test_first_count, &count, sizeof(count)) != cudaSuccess ? 1 : 0;
+}
+
 // Test-only build: this file's wait limit, and one arrival too many expected on
 // the barriers that announce the first half of a tile's weights.
 extern "C" QERL_API int qerl_test_set_prompt_hooks(long long wait_limit_cycles, int extra_arrival) {
