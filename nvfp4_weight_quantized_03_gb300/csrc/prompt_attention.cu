@@ -65,6 +65,11 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 constexpr uint32_t kPanel = kRows * 128;  // 128 rows of 64 bf16, 128-byte swizzle
 constexpr float kSlack = 8.0f;
+// The longest sequence.  A wait may last two items (the loads and the finder are
+// done that much before the last outputs), and an item takes 1430 cycles per key
+// tile: 2^24 rows stay 5 times below the wait limit of 4e9 cycles, which would
+// otherwise report a timeout for a call that is only long.
+constexpr int kMaxRows = 1 << 24;
 
 struct PromptParams {
   const __nv_bfloat16* v;  // for the epilogue of a tile with non-finite values
@@ -233,7 +238,7 @@ struct Item {
 __device__ __forceinline__ int blocks_of(const PromptParams& p, int s, int& start, int& len) {
   start = p.cu[s];
   const int end = p.cu[s + 1];
-  if (start < 0 || end < start || end > p.tokens) {
+  if (start < 0 || end < start || end > p.tokens || end - start > kMaxRows) {
     record_error(p.status, QERL_ERR_RANGE);
     len = 0;
     return 0;
