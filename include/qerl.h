@@ -560,9 +560,8 @@ QERL_API qerl_status qerl_decode_attention(const qerl_kv_cache* cache, const voi
  *   q, out   bf16 rows of num_heads * head_dim, strides ldq, ldo.
  *   k, v     bf16 rows of num_kv_heads * head_dim, strides ldk, ldv.
  *   cu_seqlens  device int32 [num_seqs + 1], not decreasing, within 0 ..
- *            tokens; a sequence has at most 2^24 rows.  A sequence that breaks
- *            this records QERL_ERR_RANGE and is skipped; the other sequences'
- *            rows may then be skipped too.
+ *            tokens; a sequence has at most 2^24 rows.  Offsets that break
+ *            this record QERL_ERR_RANGE, and no row of the call is written.
  *            Empty sequences are allowed; rows of no sequence are left as they
  *            are in out and lse.
  *   lse      float [tokens][num_heads] or NULL.

@@ -235,14 +235,12 @@ struct Item {
   int start, len, t;  // the sequence's first row and length; the block's index in it
 };
 
+// The blocks of sequence s; -1 if its offsets break the rules.
 __device__ __forceinline__ int blocks_of(const PromptParams& p, int s, int& start, int& len) {
   start = p.cu[s];
   const int end = p.cu[s + 1];
-  if (start < 0 || end < start || end > p.tokens || end - start > kMaxRows) {
-    record_error(p.status, QERL_ERR_RANGE);
-    len = 0;
-    return 0;
-  }
+  len = 0;
+  if (start < 0 || end < start || end > p.tokens || end - start > kMaxRows) return -1;
   len = end - start;
   return (len + kBlock - 1) / kBlock;
 }
@@ -256,10 +254,19 @@ struct Finder {
   int level, s0;
   int64_t passed;  // blocks before sequence s0 of this level
 
+  // One sequence that breaks the rules leaves nothing to find: the offsets
+  // around it may lie before those of other sequences, and two CTAs would then
+  // write the same rows.
   __device__ __forceinline__ void begin(const PromptParams& p) {
     int most = 0, start, len;
-    for (int s = threadIdx.x & 31; s < p.num_seqs; s += 32) most = max(most, blocks_of(p, s, start, len));
-    level = __reduce_max_sync(~0u, most) - 1;
+    bool bad = false;
+    for (int s = threadIdx.x & 31; s < p.num_seqs; s += 32) {
+      const int n = blocks_of(p, s, start, len);
+      most = max(most, n);
+      bad |= n < 0;
+    }
+    if (bad) record_error(p.status, QERL_ERR_RANGE);
+    level = __any_sync(~0u, bad) ? -1 : __reduce_max_sync(~0u, most) - 1;
     s0 = 0;
     passed = 0;
   }
