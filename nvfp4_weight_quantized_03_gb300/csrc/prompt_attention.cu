@@ -249,31 +249,55 @@ __device__ __forceinline__ int blocks_of(const PromptParams& p, int s, int& star
 // within their sequence in the order of the sequences, level descending (the
 // last blocks to start are the cheapest).  find() is called by a whole warp
 // with ranks that do not decrease and goes on from where it was, so a CTA's
-// calls together look at each (level, sequence) once.
+// calls together look at each (level, sequence) once at most.  The sequences are
+// taken in up to 32 groups, and a level passes over the groups that have no
+// block in it.  A group that is looked through has one, so the ranks between a
+// CTA's items bound the steps between them: of 2^20 sequences with one long one
+// among them a level takes 1024 steps where all of them take 32768 (at a few
+// hundred cycles a step, the 304 levels that may lie between two items of one
+// head would take most of the 4e9 cycles that a wait may last).
 struct Finder {
   int level, s0;
-  int64_t passed;  // blocks before sequence s0 of this level
+  int group_shift;  // a group: 32 << group_shift sequences
+  int group_most;   // lane g's: the most blocks of a sequence of group g
+  int64_t passed;   // blocks before sequence s0 of this level
 
   // One sequence that breaks the rules leaves nothing to find: the offsets
   // around it may lie before those of other sequences, and two CTAs would then
   // write the same rows.
   __device__ __forceinline__ void begin(const PromptParams& p) {
-    int most = 0, start, len;
+    const int lane = threadIdx.x & 31;
+    int start, len;
     bool bad = false;
-    for (int s = threadIdx.x & 31; s < p.num_seqs; s += 32) {
-      const int n = blocks_of(p, s, start, len);
-      most = max(most, n);
-      bad |= n < 0;
+    group_shift = 0;
+    while ((1024 << group_shift) < p.num_seqs) ++group_shift;
+    group_most = 0;
+    for (int g = 0; (g << group_shift) * 32 < p.num_seqs; ++g) {
+      const int end = min(((g + 1) << group_shift) * 32, p.num_seqs);
+      int most = 0;
+      for (int s = ((g << group_shift) * 32) + lane; s < end; s += 32) {
+        const int n = blocks_of(p, s, start, len);
+        most = max(most, n);
+        bad |= n < 0;
+      }
+      most = __reduce_max_sync(~0u, most);
+      if (lane == g) group_most = most;
     }
     if (bad) record_error(p.status, QERL_ERR_RANGE);
-    level = __any_sync(~0u, bad) ? -1 : __reduce_max_sync(~0u, most) - 1;
+    level = __any_sync(~0u, bad) ? -1 : __reduce_max_sync(~0u, group_most) - 1;
     s0 = 0;
     passed = 0;
   }
   __device__ __forceinline__ bool find(const PromptParams& p, int64_t rank, Item& it) {
     const int lane = threadIdx.x & 31;
     for (; level >= 0; --level, s0 = 0) {
+      const unsigned groups = __ballot_sync(~0u, group_most > level);
       for (; s0 < p.num_seqs; s0 += 32) {
+        const int g = s0 >> (group_shift + 5);
+        if ((groups >> g & 1) == 0) {  // to the group's end
+          s0 = (((g + 1) << group_shift) - 1) * 32;
+          continue;
+        }
         int start = 0, len = 0;
         const bool has = s0 + lane < p.num_seqs && blocks_of(p, s0 + lane, start, len) > level;
         const unsigned mask = __ballot_sync(~0u, has);
