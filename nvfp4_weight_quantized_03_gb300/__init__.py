@@ -70,6 +70,7 @@ class KvCache(ctypes.Structure):
                 ("num_pages", ctypes.c_int64), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
                 ("page_table", ctypes.c_void_p), ("num_seqs", ctypes.c_int64), ("max_pages", ctypes.c_int64),
                 ("ld_table", ctypes.c_int64)]
+    device = None  # the device number of the memory, where kv_cache() made the descriptor
 
 
 QERL_OK = 0
@@ -222,10 +223,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(_device())
+            return _raw_stream(_device() if dev is None else dev)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -463,18 +464,20 @@ def qerl_rmsnorm_noise(h, w_norm, Z, delta, out, stream=None) -> int:
 _BF16, _I32, _F32, _F64 = torch.bfloat16, torch.int32, torch.float32, torch.float64
 
 
-def _expect(name, t, dtype, dims):
-    """Raises unless t is a CUDA tensor of this type and dimension count: a raw pointer of another type
-    would be misread."""
+def _expect(name, t, dtype, dims, dev=None):
+    """Raises unless t is a CUDA tensor of this type and dimension count, on device number dev (if given): a
+    raw pointer of another type would be misread, one of other memory would fault."""
     if t.dtype is not dtype or not t.is_cuda or t.dim() != dims:
         raise TypeError(f"{name}: expected a {dims}-d CUDA tensor of {dtype}, got {tuple(t.shape)} {t.dtype} on "
                         f"{t.device}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
 
 
-def _heads(name, t, shape):
+def _heads(name, t, shape, dev):
     """Row stride of bf16 rows of heads [rows, heads, head_dim], of this shape, whose heads lie side by side."""
-    if t.dtype is not _BF16 or not t.is_cuda:
-        _expect(name, t, _BF16, 3)
+    if t.dtype is not _BF16 or t.get_device() != dev:
+        _expect(name, t, _BF16, 3, dev)
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     ld, s1, s2 = t.stride()
@@ -486,12 +489,20 @@ def _heads(name, t, shape):
     return ld
 
 
-def _vector(name, t, dtype, n):
-    """Raises unless t is a contiguous CUDA vector of n entries of this type."""
-    if t.dtype is not dtype or not t.is_cuda:
-        _expect(name, t, dtype, 1)
+def _vector(name, t, dtype, n, dev):
+    """Raises unless t is a contiguous vector of n entries of this type on device number dev."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _expect(name, t, dtype, 1, dev)
     if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name}: expected {n} contiguous entries, got {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _memory(ws, cache, dev):
+    """Raises unless the workspace, and the cache if there is one, are memory of device number dev."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous memory on cuda:{dev}, got strides {ws.stride()} on {ws.device}")
+    if cache is not None and cache.device is not None and cache.device != dev:
+        raise ValueError(f"cache: on cuda:{cache.device}, expected cuda:{dev}")
 
 
 def _heads_shape(name, t):
@@ -508,8 +519,9 @@ def kv_cache(k, v, page_table, k_scale=None, v_scale=None):
     if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
         raise TypeError("k: the cache holds bfloat16 or float8_e4m3fn")
     _expect("k", k, k.dtype, 4)
-    _expect("v", v, k.dtype, 4)
-    _expect("page_table", page_table, torch.int32, 2)
+    dev = k.get_device()
+    _expect("v", v, k.dtype, 4, dev)
+    _expect("page_table", page_table, torch.int32, 2, dev)
     if v.shape != k.shape or not k.is_contiguous() or not v.is_contiguous():
         raise ValueError("k and v: contiguous pages of one shape")
     if page_table.shape[1] > 1 and page_table.stride(1) != 1:
@@ -518,7 +530,7 @@ def kv_cache(k, v, page_table, k_scale=None, v_scale=None):
     c.num_pages, c.num_kv_heads, c.page_size, c.head_dim = k.shape
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
         if t is not None:
-            _expect(name, t, torch.float32, 1)
+            _expect(name, t, torch.float32, 1, dev)
             if t.numel() != c.num_kv_heads or not t.is_contiguous():
                 raise ValueError(f"{name}: one contiguous float per key-value head")
     c.k, c.v = _p(k), _p(v)
@@ -528,6 +540,7 @@ def kv_cache(k, v, page_table, k_scale=None, v_scale=None):
     c.num_seqs, c.max_pages = page_table.shape
     c.ld_table = page_table.stride(0) if c.num_seqs > 1 else max(page_table.stride(0), c.max_pages)
     c.tensors = (k, v, page_table, k_scale, v_scale)
+    c.device = dev
     return c
 
 
@@ -542,37 +555,40 @@ def qerl_rope_append(cache, q, k, v, positions, inv_freq, q_out, k_out, workspac
     cache None: rotation only (v may be None)."""
     shape = _heads_shape("k", k)
     tokens, hk, d = shape
-    ldk = _heads("k", k, shape)
+    dev = _device()  # where the launch goes
+    ldk = _heads("k", k, shape, dev)
     h = ldq = ldqo = ldv = ldko = 0
     if q is not None:
         wide = _heads_shape("q", q)
         h = wide[1]
         if wide[0] != tokens or wide[2] != d:
             raise ValueError(f"q: expected k's tokens and head_dim, got {tuple(wide)}")
-        ldq, ldqo = _heads("q", q, wide), _heads("q_out", q_out, wide)
+        ldq, ldqo = _heads("q", q, wide, dev), _heads("q_out", q_out, wide, dev)
     if v is not None:
-        ldv = _heads("v", v, shape)
+        ldv = _heads("v", v, shape, dev)
     if k_out is not None:
-        ldko = _heads("k_out", k_out, shape)
-    _vector("positions", positions, _I32, tokens)
+        ldko = _heads("k_out", k_out, shape, dev)
+    _vector("positions", positions, _I32, tokens, dev)
     half = inv_freq.numel()
-    _vector("inv_freq", inv_freq, _F64, half)
+    _vector("inv_freq", inv_freq, _F64, half, dev)
     if seq_ids is not None:
-        _vector("seq_ids", seq_ids, _I32, tokens)
+        _vector("seq_ids", seq_ids, _I32, tokens, dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous() or cache is not None and cache.device != dev:
+        _memory(workspace, cache, dev)
     return (_lib or lib()).qerl_rope_append(
         cache, None if q is None else q.data_ptr(), ldq, h, k.data_ptr(), ldk, None if v is None else v.data_ptr(), ldv,
         hk, d, tokens, None if seq_ids is None else seq_ids.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
         2 * half, None if q is None else q_out.data_ptr(), ldqo, None if k_out is None else k_out.data_ptr(), ldko,
-        workspace.data_ptr(), workspace.nbytes, _stream(stream))
+        workspace.data_ptr(), workspace.nbytes, _stream(stream, dev))
 
 
 def qerl_decode_attention_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
     return lib().qerl_decode_attention_workspace_size(int(num_seqs), int(num_heads), int(num_kv_heads), int(head_dim))
 
 
-def _lse(lse, rows, heads):
-    if lse.dtype is not _F32 or not lse.is_cuda:
-        _expect("lse", lse, _F32, 2)
+def _lse(lse, rows, heads, dev):
+    if lse.dtype is not _F32 or lse.get_device() != dev:
+        _expect("lse", lse, _F32, 2, dev)
     if lse.shape != (rows, heads) or not lse.is_contiguous():
         raise ValueError("lse: contiguous [rows, num_heads]")
     return lse.data_ptr()
@@ -585,11 +601,15 @@ def qerl_decode_attention(cache, q, lengths, scale, out, lse, workspace, stream=
     n, h, d = shape
     if n != cache.num_seqs or d != cache.head_dim:
         raise ValueError("q: [num_seqs, num_heads, head_dim] of the cache")
-    ldq, ldo = _heads("q", q, shape), _heads("out", out, shape)
-    _vector("lengths", lengths, _I32, n)
+    dev = _device()  # where the launch goes
+    ldq, ldo = _heads("q", q, shape, dev), _heads("out", out, shape, dev)
+    _vector("lengths", lengths, _I32, n, dev)
+    lse_p = None if lse is None else _lse(lse, n, h, dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous() or cache.device != dev:
+        _memory(workspace, cache, dev)
     return (_lib or lib()).qerl_decode_attention(cache, q.data_ptr(), ldq, h, lengths.data_ptr(), scale,
-                                                 out.data_ptr(), ldo, None if lse is None else _lse(lse, n, h),
-                                                 workspace.data_ptr(), workspace.nbytes, _stream(stream))
+                                                 out.data_ptr(), ldo, lse_p, workspace.data_ptr(), workspace.nbytes,
+                                                 _stream(stream, dev))
 
 
 def qerl_prompt_attention_workspace_size(tokens: int, num_heads: int, num_kv_heads: int, head_dim: int,
@@ -605,16 +625,19 @@ def qerl_prompt_attention(q, k, v, cu_seqlens, scale, out, lse, workspace, strea
     shape = _heads_shape("q", q)
     t, h, d = shape
     hk = _heads_shape("k", k)[1]
-    ldq, ldo = _heads("q", q, shape), _heads("out", out, shape)
-    ldk, ldv = _heads("k", k, (t, hk, d)), _heads("v", v, (t, hk, d))
+    dev = _device()  # where the launch goes
+    ldq, ldo = _heads("q", q, shape, dev), _heads("out", out, shape, dev)
+    ldk, ldv = _heads("k", k, (t, hk, d), dev), _heads("v", v, (t, hk, d), dev)
     n = cu_seqlens.numel()
-    _vector("cu_seqlens", cu_seqlens, _I32, n)
+    _vector("cu_seqlens", cu_seqlens, _I32, n, dev)
     if n < 1:
         raise ValueError("cu_seqlens: [num_seqs + 1]")
+    lse_p = None if lse is None else _lse(lse, t, h, dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _memory(workspace, None, dev)
     return (_lib or lib()).qerl_prompt_attention(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, t, h, hk, d,
-                                                 cu_seqlens.data_ptr(), n - 1, scale, out.data_ptr(), ldo,
-                                                 None if lse is None else _lse(lse, t, h), workspace.data_ptr(),
-                                                 _nbytes(workspace), _stream(stream))
+                                                 cu_seqlens.data_ptr(), n - 1, scale, out.data_ptr(), ldo, lse_p,
+                                                 workspace.data_ptr(), workspace.nbytes, _stream(stream, dev))
 
 
 def qerl_read_status(workspace, stream=None) -> int:
