@@ -45,8 +45,8 @@ struct AppendParams {
   int heads, kv_heads, dim, half;
   const int *seq_ids, *positions;
   const double* inv_freq;
-  // The cache; k_pages null: rotation only.
-  uint8_t *k_pages, *v_pages;
+  bool has_cache;  // false: rotation only
+  uint8_t *k_pages, *v_pages;  // null for a cache of no pages
   const float *k_scale, *v_scale;
   const int* table;
   int64_t num_seqs, ld_table, num_pages, max_pages;
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(512, kThreadsPerSm<kE4m3> / 512) rope_append_k
   const bool rot = kind < 2 && sub < rot_items;
   const int e0 = rot ? sub * 8 : kind == 2 ? sub * 16 : 2 * p.half + (sub - rot_items) * 16;
   const int e1 = rot ? p.half + sub * 8 : e0 + 8;
-  const bool active = item < items && (kind < 2 || p.k_pages != nullptr);
+  const bool active = item < items && (kind < 2 || p.has_cache);
   const int64_t step = gridDim.x;
   const __nv_bfloat16* src = (kind == 0 ? p.q : kind == 1 ? p.k : p.v) + head * p.dim;
   const int64_t ld = kind == 0 ? p.ldq : kind == 1 ? p.ldk : p.ldv;
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(512, kThreadsPerSm<kE4m3> / 512) rope_append_k
   }
   // The place of token t in the cache: its page number, or -1.
   auto page_of = [&](int64_t t, int pos) -> int {
-    if (p.k_pages == nullptr || pos < 0) return -1;
+    if (!p.has_cache || pos < 0) return -1;
     const int64_t s = p.seq_ids != nullptr ? p.seq_ids[t] : t;
     const int pi = pos / p.page_size;
     return s >= 0 && s < p.num_seqs && pi < p.max_pages ? p.table[s * p.ld_table + pi] : -1;
@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(512, kThreadsPerSm<kE4m3> / 512) rope_append_k
     buf ^= 1;
     angles(pos_next, buf);  // of the next one, so that nobody waits for them
     if (pos < 0) continue;  // padding
-    const bool placed = page >= 0 && page < p.num_pages;  // (never without a cache)
-    if (tid == 0 && p.k_pages != nullptr && !placed) record_error(p.status, QERL_ERR_RANGE);
+    const bool placed = page >= 0 && page < p.num_pages;  // never without pages
+    if (tid == 0 && p.has_cache && !placed) record_error(p.status, QERL_ERR_RANGE);
     if (active) {
       uint32_t a[4] = {w0.x, w0.y, w0.z, w0.w}, b[4] = {w1.x, w1.y, w1.z, w1.w}, c0[2] = {0, 0}, c1[2] = {0, 0};
 #pragma unroll
@@ -224,6 +224,7 @@ qerl_status launch_rope_append(const RopeAppendArgs& a, cudaStream_t s) {
   if (a.cache != nullptr) {
     const qerl_kv_cache& c = *a.cache;
     e4m3 = c.dtype == QERL_E4M3;
+    p.has_cache = true;
     p.k_pages = static_cast<uint8_t*>(c.k);
     p.v_pages = static_cast<uint8_t*>(c.v);
     p.k_scale = c.k_scale;
