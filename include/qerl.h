@@ -464,7 +464,8 @@ QERL_API qerl_status qerl_lora_linear_noalloc(const void* x, int64_t m, int64_t 
  *   k, v     device, [num_pages][num_kv_heads][page_size][head_dim] of dtype
  *            (QERL_BF16 or QERL_E4M3), 16-byte aligned.
  *   k_scale, v_scale  device float [num_kv_heads] or NULL (1): a QERL_E4M3
- *            cache holds value / scale.  NULL for QERL_BF16.
+ *            cache holds value / scale (see qerl_rope_append for the
+ *            rounding).  NULL for QERL_BF16.
  *   page_table  device int32, row s (stride ld_table) holds the page numbers
  *            of sequence s: position p lies in page page_table[s][p /
  *            page_size], row p % page_size.  Entries past a sequence's last
@@ -507,7 +508,8 @@ typedef struct {
  *   k_out    bf16 rows or NULL; may be k itself (same stride).
  *   cache    NULL: rotation only (v, seq_ids are then not read; k_out required).
  * The cache gets the fp32 rotated k (and v) rounded once to its type: bf16, or
- * E4M3(value * (1 / scale)) with an fp32 reciprocal, nearest even, saturating
+ * E4M3(value * (1 / scale)) with an fp32 reciprocal (for scales below 2^-64 or
+ * above 2^64 of value and scale times 2^64 or 2^-64), nearest even, saturating
  * at +-448, NaN kept.
  * Pointers of q, k, v, q_out, k_out 16-byte aligned, strides multiples of 8.
  * rot_dim % 16 == 0, 0 <= rot_dim <= head_dim.  The num_kv_heads and head_dim

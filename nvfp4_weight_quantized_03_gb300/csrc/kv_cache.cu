@@ -5,7 +5,8 @@
 //   theta = p * inv_freq[i]
 //   (x[i], x[i + half]) -> (x[i] cos - x[i + half] sin, x[i + half] cos + x[i] sin)
 // in fp32 with one rounding to bf16 (and, for the cache, one rounding of the
-// fp32 value to the cache's type: the 8-bit cache holds sat(value / scale)).
+// fp32 value to the cache's type: the 8-bit cache holds sat(value * (1 / scale)),
+// the reciprocal taken once in fp32).
 //
 // Bound: bytes.  Every q, k, v element is read once and written once or twice.
 // A CTA takes one token at a time (grid-stride); a thread takes the same item of
@@ -105,11 +106,19 @@ __global__ void __launch_bounds__(512, kThreadsPerSm<kE4m3> / 512) rope_append_k
   if (dst != nullptr) dst += head * p.dim + blockIdx.x * ldd;
   uint8_t* pages = kind == 1 ? p.k_pages : kind == 2 ? p.v_pages : nullptr;
   // One division a thread: 16 per item and token took longer than the rows
-  // (16000 tokens of 40 + 2 x 8 heads: 66 us, so 0.59 of the copy rate).
-  float inverse = 1.0f;
+  // (16000 tokens of 40 + 2 x 8 heads: 66 us, so 0.59 of the copy rate).  The
+  // reciprocal of a scale near either end of fp32's range leaves it (that of a
+  // subnormal scale is infinite, and would make NaN of a zero): such a scale,
+  // and then every value, is first moved by 2^64.  That is exact but for values
+  // whose quotients saturate or are far below E4M3's smallest.
+  float inverse = 1.0f, move = 1.0f;
   if (kE4m3 && active && kind > 0) {
     const float* sc = kind == 1 ? p.k_scale : p.v_scale;
-    if (sc != nullptr) inverse = 1.0f / sc[head];
+    if (sc != nullptr) {
+      const float scale = sc[head];
+      move = fabsf(scale) < 0x1p-64f ? 0x1p64f : fabsf(scale) > 0x1p64f ? 0x1p-64f : 1.0f;
+      inverse = 1.0f / (scale * move);
+    }
   }
   // The place of token t in the cache: its page number, or -1.
   auto page_of = [&](int64_t t, int pos) -> int {
@@ -174,6 +183,12 @@ __global__ void __launch_bounds__(512, kThreadsPerSm<kE4m3> / 512) rope_append_k
           b[i] = pack_bf16(yl, yh);
         }
         if (kE4m3 && kind > 0) {
+          if (move != 1.0f) {
+            xl *= move;
+            xh *= move;
+            yl *= move;
+            yh *= move;
+          }
           c0[i >> 1] |= pack_e4m3(xl, xh, inverse) << (16 * (i & 1));
           c1[i >> 1] |= pack_e4m3(yl, yh, inverse) << (16 * (i & 1));
         }

@@ -1,4 +1,4 @@
-"""The append at its edges: a cache without pages."""
+"""The append at its edges: a cache without pages, and scales whose reciprocal leaves fp32's range."""
 import pytest
 import torch
 
@@ -38,3 +38,28 @@ def test_a_cache_without_pages_records_the_lost_tokens(q_, dtype):
     q_.check(q_.qerl_decode_attention(cache, q, pos + 5, 0.1, out, lse, dws))
     assert q_.STATUS_NAMES[q_.qerl_read_status(dws)] == "QERL_ERR_RANGE"
     assert (out == 0).all()
+
+
+# Scales of every size; values whose quotients are 0, E4M3 values, or past its largest, so nothing is rounded.
+@pytest.mark.parametrize("exponent", [-149, -140, -130, -127, -126, -120, -64, -9, 0, 30, 64, 100, 126, 127])
+def test_scales_whose_reciprocal_is_out_of_range(q_, exponent):
+    dim = 128
+    quotients = [0.0] + [(1.0 + (i % 8) / 8.0) * 2.0 ** (i // 8 - 6) * (-1) ** i for i in range(1, 120)]
+    quotients += [2.0 ** e for e in (10, 16, 17, 20, 30, 60, 100, -11)]
+    x = torch.tensor(quotients, dtype=torch.float64) * 2.0 ** exponent
+    held = (x.abs() < 2.0 ** 128) & (x.to(BF).double() == x)  # by bf16, subnormals included
+    x = torch.where(held, x, 0.0)
+    want = (x / 2.0 ** exponent).clamp(-448, 448).float()
+    want[want.abs() == 2.0 ** -11] = 0.0  # half of E4M3's smallest step is 2^-10
+    k = x.to(BF).view(1, 1, dim).cuda()
+    assert (want == 0).any() and (want != 0).sum() >= (3 if exponent < -135 else 20)
+    kp, vp = (torch.full((1, 1, 1, dim), 0x7F, dtype=torch.uint8, device="cuda").view(F8) for _ in range(2))
+    scale = torch.tensor([2.0 ** exponent], dtype=torch.float64).float().cuda()
+    assert scale.item() == 2.0 ** exponent
+    cache = q_.kv_cache(kp, vp, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), scale, scale)
+    ws = q_.workspace(q_.qerl_rope_append_workspace_size())
+    q_.check(q_.qerl_rope_append(cache, None, k, k, torch.zeros(1, dtype=torch.int32, device="cuda"), _no_freq(), None,
+                                 None, ws))
+    assert q_.qerl_read_status(ws) == 0
+    for pages in (kp, vp):
+        assert torch.equal(pages.float().flatten().cpu(), want)
