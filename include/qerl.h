@@ -539,7 +539,8 @@ QERL_API qerl_status qerl_rope_append(const qerl_kv_cache* cache, const void* q,
  *            that; either records QERL_ERR_RANGE.
  *   out      bf16 rows, stride ldo; lse float [num_seqs][num_heads] or NULL.
  * q and out 16-byte aligned, strides multiples of 8.  Scores, softmax and sums
- * are fp32; for a QERL_E4M3 cache the softmax weights are rounded to fp16.  A
+ * are fp32; for a QERL_E4M3 cache the softmax weights are rounded to fp16 for the
+ * product with v (by half a step, 2^-11, or by 2^-32 of the largest).  A
  * non-finite q, k or v in use makes the outputs it reaches non-finite.
  * A page number outside the cache records QERL_ERR_RANGE and its rows read as
  * zeros.  The result does not depend on timing (partial sums are joined in a

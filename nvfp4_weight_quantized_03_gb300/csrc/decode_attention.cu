@@ -40,7 +40,10 @@
 // 16 keys where the memory is the bound anyway.  E4M3 cache: keys and values
 // are exact in fp16, q is scaled by a power of two per head to fp16 (exact
 // unless an element is 2^14 below the head's largest), 2^(s - m) is rounded to
-// fp16 (half a step 2^-11).
+// fp16 (half a step 2^-11).  There m lies 2^7 below the maximum it was taken
+// from, so that weights up to 2^15 use fp16's range: one is lost to the product
+// only below 2^-32 of the largest (with m at the maximum below 2^-25, and
+// 100000 of those are a third of a percent of the sum, which keeps them).
 #include "qerl_internal.h"
 #include "qerl_ptx.cuh"
 
@@ -66,6 +69,9 @@ constexpr int kDirect = 16, kGroup = 8;
 // the fp32 sums and the fp16 probabilities in range, and most steps then skip
 // the maximum's reduction and the rescaling.
 constexpr float kSlack = 8.0f;
+// How far m lies below the maximum when it moves.
+template <bool kFp8>
+constexpr float kBelow = kFp8 ? 7.0f : 0.0f;
 
 struct DecodeParams {
   const __nv_bfloat16* q;
@@ -589,19 +595,20 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
           x[nt][mt][i] = v;
           top[i & 1] = fmaxf(top[i & 1], v);
         }
-      grow |= top[0] > m[nt][0] + kSlack || top[1] > m[nt][1] + kSlack;
+      grow |= top[0] > m[nt][0] + (kBelow<kFp8> + kSlack) || top[1] > m[nt][1] + (kBelow<kFp8> + kSlack);
     }
     if (__any_sync(~0u, grow)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float top = m[nt][c];
+          float top = -kInf;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(x[nt][mt][c], x[nt][mt][c + 2]));
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+          top = fmaxf(m[nt][c], top - kBelow<kFp8>);
           const float f = m[nt][c] == -kInf ? 1.0f : ex2(m[nt][c] - top);  // no sum yet (or NaN, kept) at -inf
           m[nt][c] = top;
           l[nt][c] *= f;
