@@ -38,12 +38,13 @@
 // Roundings: scores, m, l and o are fp32.  bf16 cache: 2^(s - m) enters the
 // value product as bf16 high + bf16 low (16 bits), which costs 8 more MMAs per
 // 16 keys where the memory is the bound anyway.  E4M3 cache: keys and values
-// are exact in fp16, q is scaled by a power of two per head to fp16 (exact
-// unless an element is 2^14 below the head's largest), 2^(s - m) is rounded to
-// fp16 (half a step 2^-11).  There m lies 2^7 below the maximum it was taken
-// from, so that weights up to 2^15 use fp16's range: one is lost to the product
-// only below 2^-32 of the largest (with m at the maximum below 2^-25, and
-// 100000 of those are a third of a percent of the sum, which keeps them).
+// are exact in fp16, q is scaled by a power of two per head to the top of
+// fp16's range (exact unless an element is 2^31 below the head's largest),
+// 2^(s - m) is rounded to fp16 (half a step 2^-11).  There m lies 2^7 below the
+// maximum it was taken from, so that weights up to 2^15 use fp16's range: one
+// is lost to the product only below 2^-32 of the largest (with m at the maximum
+// below 2^-25, and 100000 of those are a third of a percent of the sum, which
+// keeps them).
 #include "qerl_internal.h"
 #include "qerl_ptx.cuh"
 
@@ -508,11 +509,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
           }
           amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
           amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
-          // 2^-e for amax in [2^e, 2^(e+1)), kept in the normal range
-          int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-          e = amax == 0.0f || e > 127 ? 0 : e < -126 ? -126 : e > 126 ? 126 : e;
-          const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          // amax in [2^e, 2^(e+1)) goes to [2^14, 2^15); beside an infinite
+          // element the finite ones are scaled as if of its size, and stay
+          // finite.  Both factors are normal numbers.
+          const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -112), 127);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+          const float up = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
             qf[nt][ks][0] = pack_f16(bf_lo(qn[nt][ks][0]) * down, bf_hi(qn[nt][ks][0]) * down);
