@@ -1,4 +1,4 @@
-"""The append at its edges: a cache without pages, and scales whose reciprocal leaves fp32's range."""
+"""The append at its edges: a cache without pages, scales whose reciprocal leaves fp32's range, no queries."""
 import pytest
 import torch
 
@@ -63,3 +63,18 @@ def test_scales_whose_reciprocal_is_out_of_range(q_, exponent):
     assert q_.qerl_read_status(ws) == 0
     for pages in (kp, vp):
         assert torch.equal(pages.float().flatten().cpu(), want)
+
+
+def test_rope_append_without_queries(q_):
+    """The Python call takes no q where the entry point does."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k = torch.randn((5, 2, 64), generator=g, device="cuda").to(BF)
+    pages = [torch.zeros((2, 2, 4, 64), dtype=BF, device="cuda") for _ in range(2)]
+    cache = q_.kv_cache(*pages, torch.tensor([[1, 0]], dtype=torch.int32, device="cuda"))
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")
+    freq = torch.linspace(1, 0.01, 32, dtype=torch.float64, device="cuda")
+    none, k_out = q_.rope_append(cache, None, k, k, pos, freq, seq_ids=torch.zeros_like(pos))
+    assert none is None
+    q_out, k_too = q_.rope_append(None, k, k, None, pos, freq)
+    assert torch.equal(k_out, k_too) and torch.equal(q_out, k_too)
+    assert torch.equal(pages[0][1].transpose(0, 1), k_out[:4]) and torch.equal(pages[1][0, :, 0], k[4])
