@@ -1,4 +1,5 @@
-"""The append at its edges: a cache without pages, scales whose reciprocal leaves fp32's range, no queries."""
+"""The append at its edges: a cache without pages, scales whose reciprocal leaves fp32's range, no queries, and
+the 8-bit values bit for bit."""
 import pytest
 import torch
 
@@ -78,3 +79,32 @@ def test_rope_append_without_queries(q_):
     q_out, k_too = q_.rope_append(None, k, k, None, pos, freq)
     assert torch.equal(k_out, k_too) and torch.equal(q_out, k_too)
     assert torch.equal(pages[0][1].transpose(0, 1), k_out[:4]) and torch.equal(pages[1][0, :, 0], k[4])
+
+
+@pytest.mark.parametrize("hk,dim", [(1, 64), (8, 128), (3, 64)])
+def test_8_bit_values_bit_for_bit(q_, hk, dim):
+    """v is not rotated: its bytes are those of value * (1 / scale), both steps in fp32, rounded to nearest
+    even and clamped to +-448."""
+    tokens, page = 700, 16
+    g = torch.Generator(device="cuda").manual_seed(hk)
+    v = (torch.randn((tokens, hk, dim), generator=g, device="cuda") *
+         2.0 ** torch.randint(-14, 6, (tokens, 1, 1), generator=g, device="cuda")).to(BF)
+    v[0] = 0.0
+    v[1] = -0.0
+    vs = torch.rand(hk, generator=g, device="cuda") * 0.01 + 0.003
+    vs[0] = 1.0 / 64  # quotients that are exact, so midpoints between E4M3 values are met
+    v[2:200, 0] = (torch.randint(-256, 257, (198, dim), generator=g, device="cuda") / 512.0).to(BF)
+    kp, vp = (torch.zeros((-(-tokens // page), hk, page, dim), dtype=torch.uint8, device="cuda").view(F8)
+              for _ in range(2))
+    table = torch.arange(kp.shape[0], dtype=torch.int32, device="cuda")[None]
+    cache = q_.kv_cache(kp, vp, table, vs, vs)
+    ws = q_.workspace(q_.qerl_rope_append_workspace_size())
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    q_.check(q_.qerl_rope_append(cache, None, v, v, pos, _no_freq(), None, None, ws, seq_ids=torch.zeros_like(pos)))
+    assert q_.qerl_read_status(ws) == 0
+    quotient = v.float() * (1.0 / vs)[None, :, None]
+    want = quotient.clamp(-448, 448).to(F8).view(torch.uint8)
+    assert ((quotient * 2.0 ** 12).frac() == 0).any()
+    for pages in (kp, vp):
+        got = pages.view(torch.uint8).transpose(1, 2).reshape(-1, hk, dim)[:tokens]
+        assert torch.equal(got, want)
