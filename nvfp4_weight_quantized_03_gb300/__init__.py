@@ -722,9 +722,10 @@ def lora_linear(x, wpacked, tensor_scale, n, z=None, A=None, B=None, alpha=0.0, 
 
 
 def rope_append(cache, q, k, v, positions, inv_freq, seq_ids=None, ws=None):
-    """Rotated copies (q, k) of q (or None) and k, with k and v appended to the cache (see qerl_rope_append)."""
-    q_out = None if q is None else torch.empty_like(q, memory_format=torch.contiguous_format)
-    k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    """Rotated copies (q, k) of q (or None) and k, with k and v appended to the cache (see qerl_rope_append);
+    rows of padding are 0."""
+    q_out = None if q is None else torch.zeros_like(q, memory_format=torch.contiguous_format)
+    k_out = torch.zeros_like(k, memory_format=torch.contiguous_format)
     ws = workspace(qerl_rope_append_workspace_size(), k.device) if ws is None else ws
     check(qerl_rope_append(cache, q, k, v, positions, inv_freq, q_out, k_out, ws, seq_ids), "qerl_rope_append")
     return q_out, k_out

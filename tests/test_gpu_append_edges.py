@@ -81,6 +81,22 @@ def test_rope_append_without_queries(q_):
     assert torch.equal(pages[0][1].transpose(0, 1), k_out[:4]) and torch.equal(pages[1][0, :, 0], k[4])
 
 
+def test_rope_append_gives_zeros_for_padding(q_):
+    """Not what the memory held before."""
+    k = torch.ones((4000, 8, 128), dtype=BF, device="cuda")
+    pos = torch.full((4000,), -1, dtype=torch.int32, device="cuda")
+    pos[7] = 3
+    for _ in range(2):
+        dirt = torch.full_like(k, float("nan")), torch.full_like(k, float("nan"))
+        torch.cuda.synchronize()
+        del dirt  # the allocator hands the same memory out again
+        q_out, k_out = q_.rope_append(None, k, k, None, pos, _no_freq())
+        for x in (q_out, k_out):
+            assert (x[7] == 1).all()
+            x[7] = 0
+            assert (x == 0).all()
+
+
 @pytest.mark.parametrize("hk,dim", [(1, 64), (8, 128), (3, 64)])
 def test_8_bit_values_bit_for_bit(q_, hk, dim):
     """v is not rotated: its bytes are those of value * (1 / scale), both steps in fp32, rounded to nearest
