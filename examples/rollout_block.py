@@ -51,6 +51,7 @@ class AttentionHalf:
         self.inv_freq = (1e6 ** (-torch.arange(dim // 2, dtype=torch.float64) / (dim // 2))).cuda()
         self.append_ws = q.workspace(q.qerl_rope_append_workspace_size())
         self.decode_ws = q.workspace(q.qerl_decode_attention_workspace_size(seqs, heads, kv_heads, dim))
+        self.prompt_ws = []  # one per prompt pass, until its status is read
 
     def buffers(self, rows):
         """What one pass over `rows` rows writes, allocated once."""
@@ -86,6 +87,7 @@ class AttentionHalf:
         b = self.buffers(h.shape[0])
         qh, kh, vh, att = self._project(h, b, positions, seq_ids)
         ws = q.workspace(q.qerl_prompt_attention_workspace_size(h.shape[0], self.heads, self.kv_heads, self.dim, len(lens)))
+        self.prompt_ws.append(ws)
         q.check(q.qerl_prompt_attention(qh, kh, vh, cu.cuda(), self.scale, att, b["lse"], ws), "prompt attention")
         return self._output(h, b)
 
@@ -96,7 +98,10 @@ class AttentionHalf:
         return self._output(h, b)
 
     def status(self):
-        return [q.qerl_read_status(w) for w in (self.append_ws, self.decode_ws)]
+        """What the device recorded since the last call: the first error, or QERL_OK.  Synchronises."""
+        found = [q.qerl_read_status(w) for w in (self.append_ws, self.decode_ws, *self.prompt_ws)]
+        self.prompt_ws.clear()
+        return next((s for s in found if s != q.QERL_OK), q.QERL_OK)
 
 
 def rollout(heads=8, kv_heads=2, dim=128, lens=(37, 5, 130, 64), steps=6, cache_dtype=torch.bfloat16, seed=0):
@@ -122,10 +127,10 @@ def rollout(heads=8, kv_heads=2, dim=128, lens=(37, 5, 130, 64), steps=6, cache_
         h.copy_(torch.stack([hidden[s + m + t] for s, m in zip(start, lens)]))
         graph.replay()
         got.append(out.clone())
-    torch.cuda.synchronize()
-    assert half.status() == [q.QERL_OK, q.QERL_OK]
+    q.check(half.status(), "prompts and steps")
 
     whole = half.prompts(hidden, total)
+    q.check(half.status(), "the whole sequences")
     want = [torch.stack([whole[s + m + t] for s, m in zip(start, lens)]) for t in range(steps)]
     begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     lengths -= steps  # the timed replays write the same rows again

@@ -548,7 +548,7 @@ QERL_API qerl_status qerl_rope_append(const qerl_kv_cache* cache, const void* q,
  * workspace >= qerl_decode_attention_workspace_size(), 256-byte aligned,
  * zero-filled before its first use.  Calls of any shapes may share one if they
  * are ordered and it is used for nothing else (counters in it stay zero between
- * calls). */
+ * calls) but the status word of the other two attention calls. */
 QERL_API size_t qerl_decode_attention_workspace_size(int64_t num_seqs, int num_heads, int num_kv_heads,
                                                      int head_dim);
 QERL_API qerl_status qerl_decode_attention(const qerl_kv_cache* cache, const void* q, int64_t ldq, int num_heads,

@@ -28,10 +28,16 @@ The functions named like the C entry points take torch tensors:
 `linear_descs()` builds the descriptor array of a group once; passing it
 instead of the list skips that marshalling on every call.
 
-and return the qerl_status integer (QERL_OK == 0).  `check()` turns a
-non-zero status into an exception.  `quantize()`, `pack()` and
-`lora_linear()` are conveniences that allocate the outputs with torch (the
-library itself never allocates).
+The functions return the qerl_status integer (QERL_OK == 0); `check()` turns a
+non-zero status into an exception.  `quantize()`, `pack()`, `lora_linear()`,
+`rope_append()`, `decode_attention()` and `prompt_attention()` are conveniences
+that allocate the outputs with torch (the library itself never allocates).
+
+What only the device sees (a page number outside the cache, offsets that step
+back, a wait that ran out) is recorded in the call's workspace, for
+`qerl_read_status(workspace)`.  A convenience makes a workspace of its own where
+it is given none, and that record is lost with it: pass `ws` and read its status
+wherever lengths, positions or pages may be wrong.
 """
 import ctypes
 import os
@@ -723,7 +729,7 @@ def lora_linear(x, wpacked, tensor_scale, n, z=None, A=None, B=None, alpha=0.0, 
 
 def rope_append(cache, q, k, v, positions, inv_freq, seq_ids=None, ws=None):
     """Rotated copies (q, k) of q (or None) and k, with k and v appended to the cache (see qerl_rope_append);
-    rows of padding are 0."""
+    rows of padding are 0.  A token outside the page table or the cache is not appended and is recorded in ws."""
     q_out = None if q is None else torch.zeros_like(q, memory_format=torch.contiguous_format)
     k_out = torch.zeros_like(k, memory_format=torch.contiguous_format)
     ws = workspace(qerl_rope_append_workspace_size(), k.device) if ws is None else ws
@@ -732,7 +738,8 @@ def rope_append(cache, q, k, v, positions, inv_freq, seq_ids=None, ws=None):
 
 
 def decode_attention(cache, q, lengths, scale, ws=None):
-    """(out, lse) of one new token per sequence over the cache (see qerl_decode_attention)."""
+    """(out, lse) of one new token per sequence over the cache (see qerl_decode_attention).  Lengths and pages
+    outside the cache are recorded in ws."""
     n, h, d = q.shape
     out = torch.empty((n, h, d), dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((n, h), dtype=torch.float32, device=q.device)
@@ -743,7 +750,7 @@ def decode_attention(cache, q, lengths, scale, ws=None):
 
 def prompt_attention(q, k, v, cu_seqlens, scale, ws=None):
     """(out, lse) of causal attention of packed sequences (see qerl_prompt_attention); rows of no sequence
-    are 0 and -inf."""
+    are 0 and -inf, and so is every row where the offsets step back or out, which is recorded in ws."""
     t, h, d = q.shape
     out = torch.zeros((t, h, d), dtype=torch.bfloat16, device=q.device)
     lse = torch.full((t, h), -float("inf"), dtype=torch.float32, device=q.device)
