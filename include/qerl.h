@@ -513,8 +513,9 @@ typedef struct {
  * at +-448, NaN kept.
  * Pointers of q, k, v, q_out, k_out 16-byte aligned, strides multiples of 8.
  * rot_dim % 16 == 0, 0 <= rot_dim <= head_dim.  The num_kv_heads and head_dim
- * arguments equal the cache's.  Two tokens of one call at one place of the
- * cache give either's row.
+ * arguments equal the cache's.  Where two tokens of one call have one place of
+ * the cache, what that place then holds is not specified: its k and v rows may
+ * be pieces of both tokens'.
  * A sequence number or position outside the page table, or a page number
  * outside the cache, records QERL_ERR_RANGE: that token is not appended.
  * workspace >= qerl_rope_append_workspace_size(), 256-byte aligned, zero-filled
