@@ -18,10 +18,14 @@
 // head's CTAs to arrive joins the partials in CTA order (the result does not
 // depend on the arrival order).
 //
-// Measured: 128 x 6000 rows, 40/8 heads of 128, E4M3: 247 us = 0.94 of the copy
-// rate; 64 ragged to 8192, 28/4, bf16: 73 us = 0.88; 1 x 100003, 40/8, bf16:
-// 72 us = 0.84 (3 us before the first rows, the CTAs finish 12 us apart, 5 us
-// of join); 256 ragged to 1500, 32/8 heads of 64: 50 us = 0.84.  Steps: the
+// Measured (in a captured graph): 128 x 6000 rows, 40/8 heads of 128, E4M3:
+// 249 us = 0.93 of the copy rate; 64 ragged to 8192, 28/4, bf16: 72 us = 0.88;
+// 1 x 100003, 40/8, bf16: 71 us = 0.85 (3 us before the first rows, the CTAs
+// finish 12 us apart, 5 us of join); 256 ragged to 1500, 32/8 heads of 64: 49 us
+// = 0.85.  Furthest from the rate are two column tiles over an E4M3 cache (64 x
+// 6000 rows: 12/1 heads of 128 31 us = 0.48, 45/3 heads of 64 42 us = 0.52): 255
+// and 168 registers leave 2 and 3 warps to a scheduler, which issues in 35% and
+// 49% of its cycles and otherwise waits for each warp's chain.  Steps: the
 // join with more than one partial in flight 96 -> 84 us on the long sequence;
 // the stretch by cost, the segments' joins by one warp while the others go on,
 // and the stream marked evict-first (it leaves the code and the partials in L2)
@@ -407,8 +411,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
       cp_async_16_hint(dst + S::kKeys * S::kRow, real ? p.vp + o + chunk * 16 : none, real ? 16 : 0, once);
     }
   };
-  // The page numbers of the first stages are fetched together, later ones a
-  // step before their rows.
   // The page numbers of the first stages are fetched together, later ones a
   // step before their rows.
   Cursor ahead = cur;

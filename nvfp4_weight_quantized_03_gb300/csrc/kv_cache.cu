@@ -18,7 +18,9 @@
 // ahead.  Measured on 10517 tokens of 28 + 2 x 4 heads of 128 (205 MB, 30 us at
 // the copy rate): page after position after token 68 us, fetched ahead 58 us,
 // rows through shared memory at 5 CTAs per SM 42 us, the angles a token ahead
-// 37 us (5.5 TB/s).
+// 37 us (5.5 TB/s).  An E4M3 cache: 9132 tokens of 40 + 2 x 8 heads (262 MB,
+// 38.5 us) 56 us; with fewer threads and the same two stages less is in flight,
+// and warps wait for loads in a third of their cycles.
 #include "qerl_internal.h"
 #include "qerl_ptx.cuh"
 
@@ -32,8 +34,9 @@ namespace {
 constexpr int kMaxHalf = 64;  // rot_dim / 2
 constexpr int kStages = 2;
 // Threads per SM that the launch bounds leave room for.  The E4M3 conversions
-// need the registers of two thirds (16000 tokens of 40 + 2 x 8 heads: 56.6 us,
-// with 1536 threads 60.1 us); without them more threads win (37 us against 39).
+// need the registers of two thirds (9132 tokens of 40 + 2 x 8 heads: 56 us, with
+// 1536 threads 60 us); without them more threads win (10517 tokens of 28 + 2 x 4
+// heads: 37 us against 39).
 template <bool kE4m3>
 constexpr int kThreadsPerSm = kE4m3 ? 1024 : 1536;
 
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(512, kThreadsPerSm<kE4m3> / 512) rope_append_k
   if (dst != nullptr) dst += head * p.dim + blockIdx.x * ldd;
   uint8_t* pages = kind == 1 ? p.k_pages : kind == 2 ? p.v_pages : nullptr;
   // One division a thread: 16 per item and token took longer than the rows
-  // (16000 tokens of 40 + 2 x 8 heads: 66 us, so 0.59 of the copy rate).  The
+  // (9132 tokens of 40 + 2 x 8 heads: 66 us, so 0.59 of the copy rate).  The
   // reciprocal of a scale near either end of fp32's range leaves it (that of a
   // subnormal scale is infinite, and would make NaN of a zero): such a scale,
   // and then every value, is first moved by 2^64.  That is exact but for values

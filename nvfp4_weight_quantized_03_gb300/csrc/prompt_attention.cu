@@ -37,7 +37,11 @@
 // large bf16 product): one issuer for both tiles 594 us, an issuer each with
 // descriptors in uniform registers 502 us, the value product begun at half of
 // the weights 492 us, persistent CTAs 467 us, items found ahead and outputs in
-// whole lines 421 us (1.63 PFLOP/s).  What is left is the tiles' own chain
+// whole lines 421 us in a captured graph, 428 us a call (1.61 to 1.63 PFLOP/s).
+// Short prompts are further away (28/4 heads: 4 of 2000 rows 91 us = 0.66 of the
+// rate, 12 to 3001 0.56, 16 to 500 29 us = 0.31): half of a diagonal tile's
+// products are masked, and an item's end, where the softmax warps also write the
+// outputs, takes about 2000 cycles.  What is left is the tiles' own chain
 // (scores, softmax, weights, products: 2860 cycles a pair of tiles where the
 // products take 2048).  Heads of 64 have half the products per exponential and
 // are held by the softmax: 2400 cycles a pair, of which the exponentials of

@@ -29,7 +29,7 @@ def test_status_of_every_pass():
 
 
 def test_one_workspace_for_the_three_calls():
-    """As the README has it."""
+    """They write only the status word of it, or leave it as it was: they take turns on one."""
     import nvfp4_weight_quantized_03_gb300 as q
     heads, kv_heads, dim, page, lens = 8, 2, 64, 16, [37, 20]
     g = torch.Generator(device="cuda").manual_seed(1)
