@@ -585,6 +585,113 @@ QERL_API qerl_status qerl_prompt_attention(const void* q, int64_t ldq, const voi
                                            void* out, int64_t ldo, float* lse, void* workspace, size_t ws_bytes,
                                            void* stream);
 
+/* The two calls above within a window of `window` rows, with the first `sinks`
+ * rows of a sequence visible from everywhere (a row of neither has no weight):
+ *   qerl_window_decode_attention: rows j >= lengths[s] - window or j < sinks.
+ *     The table's entries of pages without such a row are not read.
+ *   qerl_window_prompt_attention: row i attends to rows j <= i with
+ *     i - j < window or j < sinks.
+ * window >= 1, sinks >= 0.  Everything else as for the call of all rows, its
+ * workspace included; a window that no sequence outgrows gives its result. */
+QERL_API qerl_status qerl_window_decode_attention(const qerl_kv_cache* cache, const void* q, int64_t ldq,
+                                                  int num_heads, const int32_t* lengths, int32_t window,
+                                                  int32_t sinks, float scale, void* out, int64_t ldo, float* lse,
+                                                  void* workspace, size_t ws_bytes, void* stream);
+QERL_API qerl_status qerl_window_prompt_attention(const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                                  const void* v, int64_t ldv, int64_t tokens, int num_heads,
+                                                  int num_kv_heads, int head_dim, const int32_t* cu_seqlens,
+                                                  int64_t num_seqs, int32_t window, int32_t sinks, float scale,
+                                                  void* out, int64_t ldo, float* lse, void* workspace,
+                                                  size_t ws_bytes, void* stream);
+
+/* Attention of several new tokens per sequence over the cache and over one
+ * another, to verify drafted tokens (a tree or a chain) in one pass.  Sequence s
+ * has the rows cu_tokens[s] .. cu_tokens[s + 1] - 1 of q, k, v (rotated, not yet
+ * in the cache) and lengths[s] rows in the cache; its new token t attends to all
+ * of those rows and to the new tokens j of its sequence that it sees:
+ *   s_tj = scale * q_t . k_j;  lse_t = ln sum_j exp(s_tj);
+ *   out_t = sum_j exp(s_tj - lse_t) v_j.
+ * What is accepted is appended afterwards (qerl_rope_append with rot_dim 0, a
+ * negative position for what is not).
+ *   q, out   bf16 [tokens] rows of num_heads * head_dim, strides ldq, ldo.
+ *   k, v     bf16 [tokens] rows of num_kv_heads * head_dim, strides ldk, ldv.
+ *   cu_tokens  device int32 [num_seqs + 1], not decreasing, within 0 .. tokens; a
+ *            sequence has at most 2^20 new tokens.  Offsets that break this record
+ *            QERL_ERR_RANGE, and no row of the call is written.  Sequences without
+ *            new tokens are allowed; rows of no sequence are left as they are.
+ *   lengths  device int32 [num_seqs], 0 allowed.  Below 0 counts as 0, above
+ *            max_pages * page_size as that; either records QERL_ERR_RANGE.
+ *   mask     device int64 [tokens][mask_words] or NULL: bit j % 64 of word j / 64
+ *            of row t is set where t sees new token j of its sequence (itself
+ *            included, only if set).  Bits past the sequence's tokens count as 0;
+ *            tokens past 64 * mask_words are seen by none, which records
+ *            QERL_ERR_RANGE.  NULL: t sees j <= t.
+ *   lse      float [tokens][num_heads] or NULL.
+ * q, k, v, out 16-byte aligned, strides multiples of 8; mask 8-byte aligned;
+ * tokens <= 2^30, 1 <= mask_words <= 2^14.  out overlaps none of q, k, v.  Keys
+ * that a token does not attend to do not change it, whatever they hold; a token
+ * that sees nothing (or only s_tj = -inf) gives out = 0, lse = -inf.  Scores,
+ * softmax and sums are fp32; the softmax weights are rounded to bf16 for the
+ * product with v.  For a QERL_E4M3 cache, whose value scales are to lie within
+ * 2^-64 .. 2^64, the new tokens' k and v are used as they are, not rounded to its
+ * type.  A page number outside the cache records QERL_ERR_RANGE and its rows read
+ * as zeros.  The result does not depend on timing.
+ * workspace >= qerl_tree_attention_workspace_size(), 256-byte aligned, its header
+ * (256 bytes) zero-filled before its first use; ordered calls may share it. */
+QERL_API size_t qerl_tree_attention_workspace_size(int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
+                                                   int64_t num_seqs);
+QERL_API qerl_status qerl_tree_attention(const qerl_kv_cache* cache, const void* q, int64_t ldq, const void* k,
+                                         int64_t ldk, const void* v, int64_t ldv, int64_t tokens, int num_heads,
+                                         const int32_t* cu_tokens, const int32_t* lengths, const int64_t* mask,
+                                         int mask_words, float scale, void* out, int64_t ldo, float* lse,
+                                         void* workspace, size_t ws_bytes, void* stream);
+
+/* Pages of the cache.  Both calls read and write the descriptor's page_table and
+ * pages, whatever their type, and take no notice of the scales.
+ *
+ * qerl_kv_fork: sequence children[i] becomes a copy of the first lengths[i] rows of
+ * sequence parents[i], i < count (rollouts of one prompt).  Its table row takes
+ * the parent's entries of full pages, which the two then share; where lengths[i]
+ * is no multiple of page_size, its next entry becomes new_pages[i] and the rows
+ * of the parent's last page are copied there (the rest of that page is left as
+ * it is).  Otherwise new_pages[i] is not used.  Later entries are left alone.
+ *   parents, children, lengths, new_pages  device int32 [count].
+ * A parent may have many children.  No child is a parent of the same call, and
+ * no two items have one child or one new page, nor is a new page one that the
+ * call copies from: what such items leave in the child's table row and in these
+ * pages is not specified.  A sequence number, length or page number outside the
+ * cache, or a child that is its own parent, records QERL_ERR_RANGE; nothing of
+ * that item is written.
+ * workspace >= qerl_kv_fork_workspace_size(), 256-byte aligned, zero-filled before
+ * its first use (status word only). */
+QERL_API size_t qerl_kv_fork_workspace_size(void);
+QERL_API qerl_status qerl_kv_fork(const qerl_kv_cache* cache, const int32_t* parents, const int32_t* children,
+                                  const int32_t* lengths, const int32_t* new_pages, int64_t count, void* workspace,
+                                  size_t ws_bytes, void* stream);
+
+/* qerl_kv_compact: moves the pages in use to the front of the pool.  In use are the
+ * pages that the entries of a sequence's first lengths[s] rows name (negative
+ * entries name none: a page given up, e.g. behind a window).  With L of them in
+ * use, the i-th page in use (by number, from 0) at or past L moves to the i-th
+ * unused number below L; then numbers 0 .. L - 1 are in use and the rest of the
+ * pool is free.  A page that no sequence holds, one of length 0 among them, is
+ * thereby freed.
+ *   lengths    device int32 [num_seqs]; below 0 counts as 0, above max_pages *
+ *              page_size as that, and either records QERL_ERR_RANGE.
+ *   new_table  device int32 [num_seqs] rows of max_pages entries, stride ld_new:
+ *              the entries with the new numbers; those of no page (past a
+ *              sequence's last page, negative, or outside the pool, which
+ *              records QERL_ERR_RANGE) are copied.  May be page_table itself
+ *              (same stride); page_table is not written otherwise.
+ *   live_pages device int32: L.
+ * Pages past L keep their contents.  workspace >=
+ * qerl_kv_compact_workspace_size(num_pages), 256-byte aligned, its header (256
+ * bytes) zero-filled before its first use; ordered calls may share it. */
+QERL_API size_t qerl_kv_compact_workspace_size(int64_t num_pages);
+QERL_API qerl_status qerl_kv_compact(const qerl_kv_cache* cache, const int32_t* lengths, int32_t* new_table,
+                                     int64_t ld_new, int32_t* live_pages, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
 /* Synchronizes `stream`, returns the status word recorded in `workspace` by
  * the kernels of earlier calls (QERL_OK if none failed) and resets it to
  * QERL_OK.  A failing CUDA call returns QERL_ERR_CUDA. */

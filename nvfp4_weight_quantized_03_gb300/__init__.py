@@ -22,6 +22,11 @@ The functions named like the C entry points take torch tensors:
     qerl_rope_append(cache, q, k, v, positions, inv_freq, q_out, k_out, workspace, seq_ids)
     qerl_decode_attention(cache, q, lengths, scale, out, lse, workspace)
     qerl_prompt_attention(q, k, v, cu_seqlens, scale, out, lse, workspace)
+    qerl_window_decode_attention(cache, q, lengths, window, sinks, scale, out, lse, workspace)
+    qerl_window_prompt_attention(q, k, v, cu_seqlens, window, sinks, scale, out, lse, workspace)
+    qerl_tree_attention(cache, q, k, v, cu_tokens, lengths, mask, scale, out, lse, workspace)
+    qerl_kv_fork(cache, parents, children, lengths, new_pages, workspace)
+    qerl_kv_compact(cache, lengths, new_table, live_pages, workspace)
     qerl_read_status(workspace)
 
 `kv_cache()` builds the descriptor of a paged key-value cache once, and
@@ -30,8 +35,8 @@ instead of the list skips that marshalling on every call.
 
 The functions return the qerl_status integer (QERL_OK == 0); `check()` turns a
 non-zero status into an exception.  `quantize()`, `pack()`, `lora_linear()`,
-`rope_append()`, `decode_attention()` and `prompt_attention()` are conveniences
-that allocate the outputs with torch (the library itself never allocates).
+`rope_append()`, `decode_attention()`, `prompt_attention()`, their window forms,
+`tree_attention()`, `kv_fork()` and `kv_compact()` are conveniences that allocate the outputs with torch (the library itself never allocates).
 
 What only the device sees (a page number outside the cache, offsets that step
 back, a wait that ran out) is recorded in the call's workspace, for
@@ -60,6 +65,10 @@ __all__ = [
     "QERL_E4M3", "KvCache", "kv_cache", "qerl_rope_append", "qerl_rope_append_workspace_size",
     "qerl_decode_attention", "qerl_decode_attention_workspace_size", "rope_append", "decode_attention",
     "qerl_prompt_attention", "qerl_prompt_attention_workspace_size", "prompt_attention",
+    "qerl_window_decode_attention", "qerl_window_prompt_attention", "window_decode_attention",
+    "window_prompt_attention", "qerl_kv_fork", "qerl_kv_fork_workspace_size", "kv_fork", "qerl_kv_compact",
+    "qerl_kv_compact_workspace_size", "kv_compact", "qerl_tree_attention", "qerl_tree_attention_workspace_size",
+    "tree_attention",
 ]
 
 class LinearDesc(ctypes.Structure):
@@ -201,6 +210,27 @@ def lib():
             L.qerl_prompt_attention.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, ctypes.c_int, ctypes.c_int,
                                                 ctypes.c_int, _vp, _i64, ctypes.c_float, _vp, _i64, _vp, _vp,
                                                 ctypes.c_size_t, _vp]
+            _i32 = ctypes.c_int32
+            L.qerl_window_decode_attention.restype = ctypes.c_int
+            L.qerl_window_decode_attention.argtypes = [_c, _vp, _i64, ctypes.c_int, _vp, _i32, _i32, ctypes.c_float,
+                                                       _vp, _i64, _vp, _vp, ctypes.c_size_t, _vp]
+            L.qerl_window_prompt_attention.restype = ctypes.c_int
+            L.qerl_window_prompt_attention.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, ctypes.c_int,
+                                                       ctypes.c_int, ctypes.c_int, _vp, _i64, _i32, _i32,
+                                                       ctypes.c_float, _vp, _i64, _vp, _vp, ctypes.c_size_t, _vp]
+            L.qerl_tree_attention_workspace_size.restype = ctypes.c_size_t
+            L.qerl_tree_attention_workspace_size.argtypes = [_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64]
+            L.qerl_tree_attention.restype = ctypes.c_int
+            L.qerl_tree_attention.argtypes = [_c, _vp, _i64, _vp, _i64, _vp, _i64, _i64, ctypes.c_int, _vp, _vp, _vp,
+                                              ctypes.c_int, ctypes.c_float, _vp, _i64, _vp, _vp, ctypes.c_size_t, _vp]
+            L.qerl_kv_fork_workspace_size.restype = ctypes.c_size_t
+            L.qerl_kv_fork_workspace_size.argtypes = []
+            L.qerl_kv_fork.restype = ctypes.c_int
+            L.qerl_kv_fork.argtypes = [_c, _vp, _vp, _vp, _vp, _i64, _vp, ctypes.c_size_t, _vp]
+            L.qerl_kv_compact_workspace_size.restype = ctypes.c_size_t
+            L.qerl_kv_compact_workspace_size.argtypes = [_i64]
+            L.qerl_kv_compact.restype = ctypes.c_int
+            L.qerl_kv_compact.argtypes = [_c, _vp, _vp, _i64, _vp, _vp, ctypes.c_size_t, _vp]
             L.qerl_read_status.restype = ctypes.c_int
             L.qerl_read_status.argtypes = [_vp, _vp]
             _lib = L
@@ -603,6 +633,23 @@ def _lse(lse, rows, heads, dev):
 def qerl_decode_attention(cache, q, lengths, scale, out, lse, workspace, stream=None) -> int:
     """q, out [num_seqs, num_heads, head_dim] bf16 (strided rows), lengths [num_seqs] int32, lse [num_seqs,
     num_heads] float32 or None: one new token per sequence over the cache's first lengths[s] rows."""
+    return _decode(cache, q, lengths, None, scale, out, lse, workspace, stream)
+
+
+def qerl_window_decode_attention(cache, q, lengths, window, sinks, scale, out, lse, workspace, stream=None) -> int:
+    """qerl_decode_attention over the last `window` of the lengths[s] rows and the first `sinks`."""
+    return _decode(cache, q, lengths, (_int32("window", window), _int32("sinks", sinks)), scale, out, lse, workspace,
+                   stream)
+
+
+def _int32(name, n):
+    """ctypes drops the high bits of a larger number without a word."""
+    if not -2**31 <= n < 2**31:
+        raise ValueError(f"{name}: {n} is no 32-bit number")
+    return n
+
+
+def _decode(cache, q, lengths, window, scale, out, lse, workspace, stream):
     shape = _heads_shape("q", q)
     n, h, d = shape
     if n != cache.num_seqs or d != cache.head_dim:
@@ -613,9 +660,13 @@ def qerl_decode_attention(cache, q, lengths, scale, out, lse, workspace, stream=
     lse_p = None if lse is None else _lse(lse, n, h, dev)
     if workspace.get_device() != dev or not workspace.is_contiguous() or cache.device != dev:
         _memory(workspace, cache, dev)
-    return (_lib or lib()).qerl_decode_attention(cache, q.data_ptr(), ldq, h, lengths.data_ptr(), scale,
-                                                 out.data_ptr(), ldo, lse_p, workspace.data_ptr(), workspace.nbytes,
-                                                 _stream(stream, dev))
+    if window is None:
+        return (_lib or lib()).qerl_decode_attention(cache, q.data_ptr(), ldq, h, lengths.data_ptr(), scale,
+                                                     out.data_ptr(), ldo, lse_p, workspace.data_ptr(),
+                                                     workspace.nbytes, _stream(stream, dev))
+    return (_lib or lib()).qerl_window_decode_attention(cache, q.data_ptr(), ldq, h, lengths.data_ptr(), *window, scale,
+                                                        out.data_ptr(), ldo, lse_p, workspace.data_ptr(),
+                                                        workspace.nbytes, _stream(stream, dev))
 
 
 def qerl_prompt_attention_workspace_size(tokens: int, num_heads: int, num_kv_heads: int, head_dim: int,
@@ -628,6 +679,16 @@ def qerl_prompt_attention(q, k, v, cu_seqlens, scale, out, lse, workspace, strea
     """q, out [tokens, num_heads, head_dim], k, v [tokens, num_kv_heads, head_dim] bf16 (strided rows),
     cu_seqlens [num_seqs + 1] int32, lse [tokens, num_heads] float32 or None: causal attention of the
     packed sequences."""
+    return _prompt(q, k, v, cu_seqlens, None, scale, out, lse, workspace, stream)
+
+
+def qerl_window_prompt_attention(q, k, v, cu_seqlens, window, sinks, scale, out, lse, workspace, stream=None) -> int:
+    """qerl_prompt_attention in which row i attends to rows i - window + 1 .. i and to the first `sinks`."""
+    return _prompt(q, k, v, cu_seqlens, (_int32("window", window), _int32("sinks", sinks)), scale, out, lse, workspace,
+                   stream)
+
+
+def _prompt(q, k, v, cu_seqlens, window, scale, out, lse, workspace, stream):
     shape = _heads_shape("q", q)
     t, h, d = shape
     hk = _heads_shape("k", k)[1]
@@ -641,9 +702,88 @@ def qerl_prompt_attention(q, k, v, cu_seqlens, scale, out, lse, workspace, strea
     lse_p = None if lse is None else _lse(lse, t, h, dev)
     if workspace.get_device() != dev or not workspace.is_contiguous():
         _memory(workspace, None, dev)
-    return (_lib or lib()).qerl_prompt_attention(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, t, h, hk, d,
-                                                 cu_seqlens.data_ptr(), n - 1, scale, out.data_ptr(), ldo, lse_p,
-                                                 workspace.data_ptr(), workspace.nbytes, _stream(stream, dev))
+    if window is None:
+        return (_lib or lib()).qerl_prompt_attention(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, t, h, hk, d,
+                                                     cu_seqlens.data_ptr(), n - 1, scale, out.data_ptr(), ldo, lse_p,
+                                                     workspace.data_ptr(), workspace.nbytes, _stream(stream, dev))
+    return (_lib or lib()).qerl_window_prompt_attention(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, t, h, hk,
+                                                        d, cu_seqlens.data_ptr(), n - 1, *window, scale, out.data_ptr(),
+                                                        ldo, lse_p, workspace.data_ptr(), workspace.nbytes,
+                                                        _stream(stream, dev))
+
+
+def qerl_tree_attention_workspace_size(tokens: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                       num_seqs: int) -> int:
+    return lib().qerl_tree_attention_workspace_size(int(tokens), int(num_heads), int(num_kv_heads), int(head_dim),
+                                                    int(num_seqs))
+
+
+def qerl_tree_attention(cache, q, k, v, cu_tokens, lengths, mask, scale, out, lse, workspace, stream=None) -> int:
+    """q, out [tokens, num_heads, head_dim], k, v [tokens, num_kv_heads, head_dim] bf16 (strided rows), cu_tokens
+    [num_seqs + 1] and lengths [num_seqs] int32, mask [tokens, words] int64 or None, lse [tokens, num_heads]
+    float32 or None: the new tokens of every sequence over its lengths[s] rows of the cache and over one another
+    (bit j of a token's words: it sees the j-th new token of its sequence; None: those up to itself)."""
+    shape = _heads_shape("q", q)
+    t, h, d = shape
+    n, hk = cache.num_seqs, cache.num_kv_heads
+    if d != cache.head_dim:
+        raise ValueError("q: [tokens, num_heads, head_dim] of the cache")
+    dev = _device()  # where the launch goes
+    ldq, ldo = _heads("q", q, shape, dev), _heads("out", out, shape, dev)
+    ldk, ldv = _heads("k", k, (t, hk, d), dev), _heads("v", v, (t, hk, d), dev)
+    _vector("cu_tokens", cu_tokens, _I32, n + 1, dev)
+    _vector("lengths", lengths, _I32, n, dev)
+    words, mask_p = 0, None
+    if mask is not None:
+        if mask.dtype is not torch.int64 or mask.get_device() != dev:
+            _expect("mask", mask, torch.int64, 2, dev)
+        if mask.dim() != 2 or mask.shape[0] != t or not mask.is_contiguous():
+            raise ValueError(f"mask: expected contiguous [{t}, words], got {tuple(mask.shape)}")
+        words, mask_p = mask.shape[1], mask.data_ptr()
+    lse_p = None if lse is None else _lse(lse, t, h, dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous() or cache.device != dev:
+        _memory(workspace, cache, dev)
+    return (_lib or lib()).qerl_tree_attention(cache, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, t, h,
+                                               cu_tokens.data_ptr(), lengths.data_ptr(), mask_p, words, scale,
+                                               out.data_ptr(), ldo, lse_p, workspace.data_ptr(), workspace.nbytes,
+                                               _stream(stream, dev))
+
+
+def qerl_kv_fork_workspace_size() -> int:
+    return lib().qerl_kv_fork_workspace_size()
+
+
+def qerl_kv_fork(cache, parents, children, lengths, new_pages, workspace, stream=None) -> int:
+    """parents, children, lengths, new_pages [count] int32: sequence children[i] becomes a copy of the first
+    lengths[i] rows of sequence parents[i]; a last page that is not full is copied to page new_pages[i]."""
+    n = parents.numel()
+    dev = _device()  # where the launch goes
+    for name, t in (("parents", parents), ("children", children), ("lengths", lengths), ("new_pages", new_pages)):
+        _vector(name, t, _I32, n, dev)
+    _memory(workspace, cache, dev)
+    return lib().qerl_kv_fork(cache, parents.data_ptr(), children.data_ptr(), lengths.data_ptr(), new_pages.data_ptr(), n,
+                              workspace.data_ptr(), workspace.nbytes, _stream(stream, dev))
+
+
+def qerl_kv_compact_workspace_size(num_pages: int) -> int:
+    return lib().qerl_kv_compact_workspace_size(int(num_pages))
+
+
+def qerl_kv_compact(cache, lengths, new_table, live_pages, workspace, stream=None) -> int:
+    """lengths [num_seqs] int32, new_table [num_seqs, max_pages] int32 (strided rows; may be the cache's page
+    table), live_pages [1] int32: the pages in use moved to the front of the pool."""
+    n, most = cache.num_seqs, cache.max_pages
+    dev = _device()  # where the launch goes
+    _vector("lengths", lengths, _I32, n, dev)
+    _vector("live_pages", live_pages, _I32, 1, dev)
+    _expect("new_table", new_table, _I32, 2, dev)
+    if new_table.shape != (n, most) or most > 1 and new_table.stride(1) != 1:
+        raise ValueError(f"new_table: expected {(n, most)} with contiguous rows, got {tuple(new_table.shape)} with "
+                         f"strides {new_table.stride()}")
+    ld = new_table.stride(0) if n > 1 else max(new_table.stride(0), most)
+    _memory(workspace, cache, dev)
+    return lib().qerl_kv_compact(cache, lengths.data_ptr(), new_table.data_ptr(), ld, live_pages.data_ptr(),
+                                 workspace.data_ptr(), workspace.nbytes, _stream(stream, dev))
 
 
 def qerl_read_status(workspace, stream=None) -> int:
@@ -740,21 +880,76 @@ def rope_append(cache, q, k, v, positions, inv_freq, seq_ids=None, ws=None):
 def decode_attention(cache, q, lengths, scale, ws=None):
     """(out, lse) of one new token per sequence over the cache (see qerl_decode_attention).  Lengths and pages
     outside the cache are recorded in ws."""
+    out, lse, ws = _decode_outputs(cache, q, ws)
+    check(qerl_decode_attention(cache, q, lengths, scale, out, lse, ws), "qerl_decode_attention")
+    return out, lse
+
+
+def window_decode_attention(cache, q, lengths, window, sinks, scale, ws=None):
+    """decode_attention() over the last `window` rows and the first `sinks` (see qerl_window_decode_attention)."""
+    out, lse, ws = _decode_outputs(cache, q, ws)
+    check(qerl_window_decode_attention(cache, q, lengths, window, sinks, scale, out, lse, ws),
+          "qerl_window_decode_attention")
+    return out, lse
+
+
+def _decode_outputs(cache, q, ws):
     n, h, d = q.shape
     out = torch.empty((n, h, d), dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((n, h), dtype=torch.float32, device=q.device)
-    ws = workspace(qerl_decode_attention_workspace_size(n, h, cache.num_kv_heads, d), q.device) if ws is None else ws
-    check(qerl_decode_attention(cache, q, lengths, scale, out, lse, ws), "qerl_decode_attention")
-    return out, lse
+    if ws is None:
+        ws = workspace(qerl_decode_attention_workspace_size(n, h, cache.num_kv_heads, d), q.device)
+    return out, lse, ws
 
 
 def prompt_attention(q, k, v, cu_seqlens, scale, ws=None):
     """(out, lse) of causal attention of packed sequences (see qerl_prompt_attention); rows of no sequence
     are 0 and -inf, and so is every row where the offsets step back or out, which is recorded in ws."""
+    out, lse, ws = _prompt_outputs(q, k, cu_seqlens, ws)
+    check(qerl_prompt_attention(q, k, v, cu_seqlens, scale, out, lse, ws), "qerl_prompt_attention")
+    return out, lse
+
+
+def window_prompt_attention(q, k, v, cu_seqlens, window, sinks, scale, ws=None):
+    """prompt_attention() within a window, with sinks (see qerl_window_prompt_attention)."""
+    out, lse, ws = _prompt_outputs(q, k, cu_seqlens, ws)
+    check(qerl_window_prompt_attention(q, k, v, cu_seqlens, window, sinks, scale, out, lse, ws),
+          "qerl_window_prompt_attention")
+    return out, lse
+
+
+def _prompt_outputs(q, k, cu_seqlens, ws):
     t, h, d = q.shape
     out = torch.zeros((t, h, d), dtype=torch.bfloat16, device=q.device)
     lse = torch.full((t, h), -float("inf"), dtype=torch.float32, device=q.device)
-    n = cu_seqlens.numel() - 1
-    ws = workspace(qerl_prompt_attention_workspace_size(t, h, k.shape[1], d, n), q.device) if ws is None else ws
-    check(qerl_prompt_attention(q, k, v, cu_seqlens, scale, out, lse, ws), "qerl_prompt_attention")
+    if ws is None:
+        ws = workspace(qerl_prompt_attention_workspace_size(t, h, k.shape[1], d, cu_seqlens.numel() - 1), q.device)
+    return out, lse, ws
+
+
+def tree_attention(cache, q, k, v, cu_tokens, lengths, mask, scale, ws=None):
+    """(out, lse) of several new tokens per sequence over the cache and one another (see qerl_tree_attention); rows
+    of no sequence are 0 and -inf, and so is every row where the offsets step back or out, which is recorded in ws."""
+    t, h, d = q.shape
+    out = torch.zeros((t, h, d), dtype=torch.bfloat16, device=q.device)
+    lse = torch.full((t, h), -float("inf"), dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = workspace(qerl_tree_attention_workspace_size(t, h, cache.num_kv_heads, d, cache.num_seqs), q.device)
+    check(qerl_tree_attention(cache, q, k, v, cu_tokens, lengths, mask, scale, out, lse, ws), "qerl_tree_attention")
     return out, lse
+
+
+def kv_fork(cache, parents, children, lengths, new_pages, ws=None):
+    """Children of sequences in the cache (see qerl_kv_fork).  Numbers outside the cache are recorded in ws."""
+    ws = workspace(qerl_kv_fork_workspace_size(), parents.device) if ws is None else ws
+    check(qerl_kv_fork(cache, parents, children, lengths, new_pages, ws), "qerl_kv_fork")
+
+
+def kv_compact(cache, lengths, ws=None):
+    """(new_table, live_pages) with the pages in use moved to the front of the pool (see qerl_kv_compact).  Lengths
+    and page numbers outside the cache are recorded in ws."""
+    new_table = torch.empty((cache.num_seqs, cache.max_pages), dtype=torch.int32, device=lengths.device)
+    live = torch.empty(1, dtype=torch.int32, device=lengths.device)
+    ws = workspace(qerl_kv_compact_workspace_size(cache.num_pages), lengths.device) if ws is None else ws
+    check(qerl_kv_compact(cache, lengths, new_table, live, ws), "qerl_kv_compact")
+    return new_table, live

@@ -531,9 +531,10 @@ size_t qerl_decode_attention_workspace_size(int64_t num_seqs, int num_heads, int
   return qerl::decode_attention_workspace_bytes(num_seqs, num_heads, num_kv_heads);
 }
 
-qerl_status qerl_decode_attention(const qerl_kv_cache* cache, const void* q, int64_t ldq, int num_heads,
-                                  const int32_t* lengths, float scale, void* out, int64_t ldo, float* lse,
-                                  void* workspace, size_t ws_bytes, void* stream) {
+// window 0: every row.
+static qerl_status decode_attention(const qerl_kv_cache* cache, const void* q, int64_t ldq, int num_heads,
+                                    const int32_t* lengths, int window, int sinks, float scale, void* out, int64_t ldo,
+                                    float* lse, void* workspace, size_t ws_bytes, void* stream) {
   if (cache == nullptr) return QERL_ERR_INVALID_ARGUMENT;
   qerl_status st = check_heads(num_heads, cache->num_kv_heads, cache->head_dim);
   if (st != QERL_OK) return st;
@@ -553,6 +554,8 @@ qerl_status qerl_decode_attention(const qerl_kv_cache* cache, const void* q, int
   a.ldq = ldq;
   a.num_heads = num_heads;
   a.lengths = lengths;
+  a.window = window;
+  a.sinks = sinks;
   a.scale = scale;
   a.out = out;
   a.ldo = ldo;
@@ -561,16 +564,32 @@ qerl_status qerl_decode_attention(const qerl_kv_cache* cache, const void* q, int
   return qerl::launch_decode_attention(a, as_stream(stream));
 }
 
+qerl_status qerl_decode_attention(const qerl_kv_cache* cache, const void* q, int64_t ldq, int num_heads,
+                                  const int32_t* lengths, float scale, void* out, int64_t ldo, float* lse,
+                                  void* workspace, size_t ws_bytes, void* stream) {
+  return decode_attention(cache, q, ldq, num_heads, lengths, 0, 0, scale, out, ldo, lse, workspace, ws_bytes, stream);
+}
+
+qerl_status qerl_window_decode_attention(const qerl_kv_cache* cache, const void* q, int64_t ldq, int num_heads,
+                                         const int32_t* lengths, int32_t window, int32_t sinks, float scale, void* out,
+                                         int64_t ldo, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  if (window < 1 || sinks < 0) return QERL_ERR_INVALID_ARGUMENT;
+  return decode_attention(cache, q, ldq, num_heads, lengths, window, sinks, scale, out, ldo, lse, workspace, ws_bytes,
+                          stream);
+}
+
 size_t qerl_prompt_attention_workspace_size(int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
                                             int64_t num_seqs) {
   if (tokens < 0 || num_seqs < 0 || check_heads(num_heads, num_kv_heads, head_dim) != QERL_OK) return 0;
   return qerl::prompt_attention_workspace_bytes(tokens, num_heads, num_kv_heads, head_dim, num_seqs);
 }
 
-qerl_status qerl_prompt_attention(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
-                                  int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
-                                  const int32_t* cu_seqlens, int64_t num_seqs, float scale, void* out, int64_t ldo,
-                                  float* lse, void* workspace, size_t ws_bytes, void* stream) {
+// window 0: every row j <= i.
+static qerl_status prompt_attention(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                    int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
+                                    const int32_t* cu_seqlens, int64_t num_seqs, int window, int sinks, float scale,
+                                    void* out, int64_t ldo, float* lse, void* workspace, size_t ws_bytes,
+                                    void* stream) {
   if (tokens < 0 || num_seqs < 0) return QERL_ERR_INVALID_ARGUMENT;
   qerl_status st = check_heads(num_heads, num_kv_heads, head_dim);
   if (st != QERL_OK) return st;
@@ -603,12 +622,137 @@ qerl_status qerl_prompt_attention(const void* q, int64_t ldq, const void* k, int
   a.head_dim = head_dim;
   a.cu_seqlens = cu_seqlens;
   a.num_seqs = num_seqs;
+  a.window = window;
+  a.sinks = sinks;
   a.scale = scale;
   a.out = out;
   a.ldo = ldo;
   a.lse = lse;
   a.workspace = workspace;
   return qerl::launch_prompt_attention(a, as_stream(stream));
+}
+
+qerl_status qerl_prompt_attention(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                  int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
+                                  const int32_t* cu_seqlens, int64_t num_seqs, float scale, void* out, int64_t ldo,
+                                  float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  return prompt_attention(q, ldq, k, ldk, v, ldv, tokens, num_heads, num_kv_heads, head_dim, cu_seqlens, num_seqs, 0, 0,
+                          scale, out, ldo, lse, workspace, ws_bytes, stream);
+}
+
+qerl_status qerl_window_prompt_attention(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                                         int64_t ldv, int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
+                                         const int32_t* cu_seqlens, int64_t num_seqs, int32_t window, int32_t sinks,
+                                         float scale, void* out, int64_t ldo, float* lse, void* workspace,
+                                         size_t ws_bytes, void* stream) {
+  if (window < 1 || sinks < 0) return QERL_ERR_INVALID_ARGUMENT;
+  return prompt_attention(q, ldq, k, ldk, v, ldv, tokens, num_heads, num_kv_heads, head_dim, cu_seqlens, num_seqs,
+                          window, sinks, scale, out, ldo, lse, workspace, ws_bytes, stream);
+}
+
+size_t qerl_tree_attention_workspace_size(int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
+                                          int64_t num_seqs) {
+  if (tokens < 0 || tokens > (1 << 30) || num_seqs < 0 || check_heads(num_heads, num_kv_heads, head_dim) != QERL_OK)
+    return 0;
+  return qerl::tree_attention_workspace_bytes(tokens, num_heads, num_kv_heads, head_dim);
+}
+
+qerl_status qerl_tree_attention(const qerl_kv_cache* cache, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                const void* v, int64_t ldv, int64_t tokens, int num_heads, const int32_t* cu_tokens,
+                                const int32_t* lengths, const int64_t* mask, int mask_words, float scale, void* out,
+                                int64_t ldo, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  if (cache == nullptr || tokens < 0) return QERL_ERR_INVALID_ARGUMENT;
+  qerl_status st = check_heads(num_heads, cache->num_kv_heads, cache->head_dim);
+  if (st != QERL_OK) return st;
+  if ((st = check_cache(cache)) != QERL_OK) return st;
+  if (!std::isfinite(scale) || (mask != nullptr && mask_words < 1)) return QERL_ERR_INVALID_ARGUMENT;
+  if (tokens > (1 << 30) || (mask != nullptr && mask_words > (1 << 14))) return QERL_ERR_UNSUPPORTED_SHAPE;
+  if (tokens == 0 || cache->num_seqs == 0) return QERL_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || out == nullptr || cu_tokens == nullptr || lengths == nullptr)
+    return QERL_ERR_INVALID_ARGUMENT;
+  const int64_t q_width = static_cast<int64_t>(num_heads) * cache->head_dim;
+  const int64_t kv_width = static_cast<int64_t>(cache->num_kv_heads) * cache->head_dim;
+  if ((st = check_rows(q, ldq, q_width)) != QERL_OK || (st = check_rows(k, ldk, kv_width)) != QERL_OK ||
+      (st = check_rows(v, ldv, kv_width)) != QERL_OK || (st = check_rows(out, ldo, q_width)) != QERL_OK)
+    return st;
+  if (!aligned(cu_tokens, 4) || !aligned(lengths, 4) || !aligned(mask, 8) || !aligned(lse, 4))
+    return QERL_ERR_MISALIGNED;
+  st = check_ws(workspace, ws_bytes,
+                qerl::tree_attention_workspace_bytes(tokens, num_heads, cache->num_kv_heads, cache->head_dim));
+  if (st != QERL_OK) return st;
+  qerl::TreeAttentionArgs a{};
+  a.cache = cache;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.tokens = tokens;
+  a.num_heads = num_heads;
+  a.cu_tokens = cu_tokens;
+  a.lengths = lengths;
+  a.mask = mask;
+  a.mask_words = mask_words;
+  a.scale = scale;
+  a.out = out;
+  a.ldo = ldo;
+  a.lse = lse;
+  a.workspace = workspace;
+  return qerl::launch_tree_attention(a, as_stream(stream));
+}
+
+size_t qerl_kv_fork_workspace_size(void) { return kWsHeaderBytes; }
+
+qerl_status qerl_kv_fork(const qerl_kv_cache* cache, const int32_t* parents, const int32_t* children,
+                         const int32_t* lengths, const int32_t* new_pages, int64_t count, void* workspace,
+                         size_t ws_bytes, void* stream) {
+  if (cache == nullptr || count < 0) return QERL_ERR_INVALID_ARGUMENT;
+  qerl_status st = check_heads(cache->num_kv_heads, cache->num_kv_heads, cache->head_dim);
+  if (st != QERL_OK || (st = check_cache(cache)) != QERL_OK) return st;
+  if (count == 0) return QERL_OK;
+  if (count > INT32_MAX) return QERL_ERR_UNSUPPORTED_SHAPE;
+  if (parents == nullptr || children == nullptr || lengths == nullptr || new_pages == nullptr)
+    return QERL_ERR_INVALID_ARGUMENT;
+  if (!aligned(parents, 4) || !aligned(children, 4) || !aligned(lengths, 4) || !aligned(new_pages, 4))
+    return QERL_ERR_MISALIGNED;
+  if ((st = check_ws(workspace, ws_bytes, kWsHeaderBytes)) != QERL_OK) return st;
+  qerl::KvForkArgs a{};
+  a.cache = cache;
+  a.parents = parents;
+  a.children = children;
+  a.lengths = lengths;
+  a.new_pages = new_pages;
+  a.count = count;
+  a.status = &static_cast<qerl::WsHeader*>(workspace)->status;
+  return qerl::launch_kv_fork(a, as_stream(stream));
+}
+
+size_t qerl_kv_compact_workspace_size(int64_t num_pages) {
+  return num_pages < 0 || num_pages > INT32_MAX ? 0 : qerl::kv_compact_workspace_bytes(num_pages);
+}
+
+qerl_status qerl_kv_compact(const qerl_kv_cache* cache, const int32_t* lengths, int32_t* new_table, int64_t ld_new,
+                            int32_t* live_pages, void* workspace, size_t ws_bytes, void* stream) {
+  if (cache == nullptr || live_pages == nullptr) return QERL_ERR_INVALID_ARGUMENT;
+  qerl_status st = check_heads(cache->num_kv_heads, cache->num_kv_heads, cache->head_dim);
+  if (st != QERL_OK || (st = check_cache(cache)) != QERL_OK) return st;
+  if (cache->num_seqs > 0 && lengths == nullptr) return QERL_ERR_INVALID_ARGUMENT;
+  if (cache->num_seqs > 0 && cache->max_pages > 0 && new_table == nullptr) return QERL_ERR_INVALID_ARGUMENT;
+  if (ld_new < cache->max_pages) return QERL_ERR_INVALID_ARGUMENT;
+  if (new_table != nullptr && new_table == cache->page_table && ld_new != cache->ld_table)
+    return QERL_ERR_INVALID_ARGUMENT;
+  if (!aligned(lengths, 4) || !aligned(new_table, 4) || !aligned(live_pages, 4)) return QERL_ERR_MISALIGNED;
+  st = check_ws(workspace, ws_bytes, qerl::kv_compact_workspace_bytes(cache->num_pages));
+  if (st != QERL_OK) return st;
+  qerl::KvCompactArgs a{};
+  a.cache = cache;
+  a.lengths = lengths;
+  a.new_table = new_table;
+  a.ld_new = ld_new;
+  a.live_pages = live_pages;
+  a.workspace = workspace;
+  return qerl::launch_kv_compact(a, as_stream(stream));
 }
 
 qerl_status qerl_read_status(void* workspace, void* stream) {

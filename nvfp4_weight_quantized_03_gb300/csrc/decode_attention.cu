@@ -1,8 +1,10 @@
 // decode_attention.cu -- attention of one new token per sequence over the
-// paged key-value cache.
+// paged key-value cache, or over a window of it.
 //
 //   s_j = scale * q . k_j,  j < len;   o = sum_j exp(s_j - lse) v_j,
 //   lse = log sum_j exp(s_j)
+// (a window of w rows and n sinks: of these j those with j >= len - w or j < n,
+// which the tiles take as if they lay side by side; nothing else differs)
 // for every query head; the G = num_heads / num_kv_heads query heads of a
 // key-value head read its rows together.  One pass: the running reference m
 // (a maximum in base-2 units), the sum l of 2^(s - m) and the unnormalised
@@ -90,6 +92,7 @@ struct DecodeParams {
   int num_seqs, heads, kv_heads, group;
   int zgroups, zheads;  // a key-value head's query heads in zgroups parts of zheads
   const int* lengths;
+  int sinks, seen;  // a window: the rows j < sinks and the last ones, at most `seen` rows in all
   float scale_log2;
   __nv_bfloat16* out;
   int64_t ldo;
@@ -220,12 +223,25 @@ __device__ __forceinline__ float weight_of(float m, float top) {
 // hz of its kv_heads * zgroups), which begins at `pos`.
 struct Cursor {
   int b, hz, tile, tiles, len;
+  int skip;  // the rows that a window leaves out, behind the sinks
   long long pos;
 };
 
-__device__ __forceinline__ int live_length(const DecodeParams& p, int b) {
+__device__ __forceinline__ int kept_length(const DecodeParams& p, int b) {
   const int n = p.lengths[b];
   return n < 0 ? 0 : n > p.capacity ? static_cast<int>(p.capacity) : n;
+}
+// The rows of a sequence that its token attends to.
+template <bool kWindow>
+__device__ __forceinline__ int live_length(const DecodeParams& p, int b) {
+  const int n = kept_length(p, b);
+  return kWindow ? min(n, p.seen) : n;
+}
+template <bool kWindow>
+__device__ __forceinline__ void set_length(const DecodeParams& p, Cursor& c) {
+  const int n = kept_length(p, c.b);
+  c.len = kWindow ? min(n, p.seen) : n;
+  c.skip = n - c.len;
 }
 
 template <typename S>
@@ -234,7 +250,7 @@ __device__ __forceinline__ int segment_cost(int len) {
 }
 
 // The next tile on the line; b == num_seqs past its end.
-template <typename S>
+template <typename S, bool kWindow>
 __device__ __forceinline__ void advance(const DecodeParams& p, Cursor& c) {
   if (++c.tile < c.tiles) {
     c.pos += S::kTileCost;
@@ -245,7 +261,7 @@ __device__ __forceinline__ void advance(const DecodeParams& p, Cursor& c) {
   if (++c.hz < p.kv_heads * p.zgroups) return;
   c.hz = 0;
   while (++c.b < p.num_seqs) {
-    c.len = live_length(p, c.b);
+    set_length<kWindow>(p, c);
     if (c.len > 0) {
       c.tiles = (c.len - 1) / S::kTile + 1;
       return;
@@ -259,7 +275,7 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return a / b;
 }
 
-template <int D, bool kFp8, int NT>
+template <int D, bool kFp8, int NT, bool kWindow>
 __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_kernel(const DecodeParams p) {
   using S = Shape<D, kFp8, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -279,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
   // ---- this CTA's stretch of the line ---------------------------------------
   auto cost = [&](int b) -> long long {
     if (b >= p.num_seqs) return 0;
-    const int n = live_length(p, b);
+    const int n = live_length<kWindow>(p, b);
     return n > 0 ? static_cast<long long>(segment_cost<S>(n)) * hz_all : 0;
   };
   auto scan = [&](long long v) -> long long {  // inclusive over the warp
@@ -364,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
     cur.b = static_cast<int>(found[0]);
     inside = found[1];
   }
-  cur.len = live_length(p, cur.b);
+  set_length<kWindow>(p, cur);
   cur.tiles = (cur.len - 1) / S::kTile + 1;
   {
     const int segment = segment_cost<S>(cur.len);
@@ -375,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
     if (cur.tile >= cur.tiles) {
       cur.tile = cur.tiles - 1;
       cur.pos = begin - in_segment + cur.tile * S::kTileCost;
-      advance<S>(p, cur);
+      advance<S, kWindow>(p, cur);
     }
   }
   if (cur.b >= p.num_seqs || cur.pos >= end) return;  // no tile begins in this stretch
@@ -384,8 +400,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
   // Byte offset of this lane's key row of the cursor's tile; -1 past the length
   // or for a page number outside the cache (the row then reads as zeros).
   auto lookup = [&](const Cursor& c) -> int64_t {
-    const int64_t key = static_cast<int64_t>(c.tile) * S::kTile + warp * S::kKeys + (lane & (S::kKeys - 1));
+    int64_t key = static_cast<int64_t>(c.tile) * S::kTile + warp * S::kKeys + (lane & (S::kKeys - 1));
     if (key >= c.len) return -1;
+    // The tiles run over the visible rows as if they lay side by side.
+    if (kWindow && key >= p.sinks) key += c.skip;
     const int pi = p.page_shift >= 0 ? static_cast<int>(key) >> p.page_shift : static_cast<int>(key) / p.page_size;
     const int64_t page = p.table[c.b * p.ld_table + pi];
     if (page < 0 || page >= p.num_pages) {
@@ -418,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
   bool more[S::kStages];
 #pragma unroll
   for (int s = 0; s < S::kStages; ++s) {
-    if (s > 0 && more[s - 1]) advance<S>(p, ahead);
+    if (s > 0 && more[s - 1]) advance<S, kWindow>(p, ahead);
     more[s] = (s == 0 || more[s - 1]) && ahead.b < p.num_seqs && ahead.pos < end;
     offs[s] = more[s] ? lookup(ahead) : -1;
   }
@@ -536,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
     }
     const bool last_tile = cur.tile + 1 == cur.tiles;
     Cursor next = cur;
-    advance<S>(p, next);
+    advance<S, kWindow>(p, next);
     last = next.b >= p.num_seqs || next.pos >= end;
     if (kAheadQ && last_tile && !last) load_q(next, qn);
     // Refill the stage the previous step emptied, then wait for this one.
@@ -544,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
       const int fill = stage == 0 ? S::kStages - 1 : stage - 1;
       if (to_load) {
         issue(fill, off);
-        advance<S>(p, ahead);
+        advance<S, kWindow>(p, ahead);
         to_load = ahead.b < p.num_seqs && ahead.pos < end;
         if (to_load) off = lookup(ahead);
       }
@@ -851,24 +869,34 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
   }
 }
 
-template <int D, bool kFp8, int NT>
+template <int D, bool kFp8, int NT, bool kWindow>
 qerl_status launch(const DecodeParams& p, int sms, int dev, cudaStream_t s) {
   using S = Shape<D, kFp8, NT>;
   static std::atomic<uint64_t> ready{0};  // one bit per device: the attribute belongs to the device's function
   const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
   if ((ready.load() & bit) == 0) {
-    if (cudaFuncSetAttribute(decode_kernel<D, kFp8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(decode_kernel<D, kFp8, NT, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             S::kSmem) != cudaSuccess)
       return QERL_ERR_CUDA;
     ready.fetch_or(bit);
   }
   constexpr int kFit = static_cast<int>(kPartBytes / (2 * NT * 8 * S::kPartRow * sizeof(float)));
   int64_t grid = std::min({S::kCtas * sms, kFit, kMaxCtas});
-  const int64_t most =
-      static_cast<int64_t>(p.num_seqs) * p.kv_heads * p.zgroups * ((p.capacity + S::kTile - 1) / S::kTile);
+  const int64_t rows = kWindow ? std::min<int64_t>(p.capacity, p.seen) : p.capacity;
+  const int64_t most = static_cast<int64_t>(p.num_seqs) * p.kv_heads * p.zgroups * ((rows + S::kTile - 1) / S::kTile);
   if (most < grid) grid = most > 0 ? most : 1;
   return cuda_status(
-      launch_dependent(decode_kernel<D, kFp8, NT>, dim3(static_cast<unsigned>(grid)), kThreads, S::kSmem, s, p));
+      launch_dependent(decode_kernel<D, kFp8, NT, kWindow>, dim3(static_cast<unsigned>(grid)), kThreads, S::kSmem, s, p));
+}
+
+template <bool kWindow>
+qerl_status launch_for(const DecodeParams& p, int head_dim, bool f8, bool one, int sms, int dev, cudaStream_t s) {
+  if (head_dim == 128) {
+    if (f8) return one ? launch<128, true, 1, kWindow>(p, sms, dev, s) : launch<128, true, 2, kWindow>(p, sms, dev, s);
+    return one ? launch<128, false, 1, kWindow>(p, sms, dev, s) : launch<128, false, 2, kWindow>(p, sms, dev, s);
+  }
+  if (f8) return one ? launch<64, true, 1, kWindow>(p, sms, dev, s) : launch<64, true, 2, kWindow>(p, sms, dev, s);
+  return one ? launch<64, false, 1, kWindow>(p, sms, dev, s) : launch<64, false, 2, kWindow>(p, sms, dev, s);
 }
 
 struct Split {
@@ -934,12 +962,11 @@ qerl_status launch_decode_attention(const DecodeAttentionArgs& a, cudaStream_t s
   p.counters = p.group_counters + 2 * kMaxCtas;
   const bool f8 = c.dtype == QERL_E4M3;
   const bool one = sp.tiles == 1;
-  if (c.head_dim == 128) {
-    if (f8) return one ? launch<128, true, 1>(p, sms, dev, s) : launch<128, true, 2>(p, sms, dev, s);
-    return one ? launch<128, false, 1>(p, sms, dev, s) : launch<128, false, 2>(p, sms, dev, s);
-  }
-  if (f8) return one ? launch<64, true, 1>(p, sms, dev, s) : launch<64, true, 2>(p, sms, dev, s);
-  return one ? launch<64, false, 1>(p, sms, dev, s) : launch<64, false, 2>(p, sms, dev, s);
+  // A window that no sequence outgrows leaves nothing out.
+  p.sinks = a.sinks;
+  p.seen = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(a.window) + a.sinks, INT32_MAX));
+  if (a.window > 0 && p.seen < p.capacity) return launch_for<true>(p, c.head_dim, f8, one, sms, dev, s);
+  return launch_for<false>(p, c.head_dim, f8, one, sms, dev, s);
 }
 
 }  // namespace qerl

@@ -83,6 +83,7 @@ struct PromptParams {
   int tokens, heads, group;
   float c;       // |scale| * log2(e)
   int negative;  // scale < 0: the first product is negated
+  int window, sinks;
   __nv_bfloat16* out;
   int64_t ldo;
   float* lse;
@@ -325,7 +326,11 @@ struct Finder {
 // softmax, the issuers and the loads each run ahead as far as their buffers
 // allow, so an item's first loads and products overlap the end of the one
 // before it.
-template <int D>
+//
+// With a window, an item's key tiles are those of the sinks and those from the
+// first that query tile 0 sees to the diagonal; the tiles between are passed
+// over.  Query tile 1 goes through the same list.
+template <int D, bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ PromptMaps maps, const PromptParams p) {
   using S = Shape<D>;
@@ -399,6 +404,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   struct Work {
     Item it;
     int head, n0, n1;  // key tiles of query tile 0, 1 (0: it has no rows)
+    int sink_tiles, passed;  // with a window: the first tiles of the list, and how many are passed over behind them
+    __device__ __forceinline__ int tile(int j) const { return kWindow && j >= sink_tiles ? j + passed : j; }
+  };
+  // Whether keys of the j-th tile of the list are hidden from rows of query tile i.
+  auto masked = [&](const Work& w, int i, int j) -> bool {
+    if (j + 1 == (i == 0 ? w.n0 : w.n1)) return true;  // the diagonal
+    if (!kWindow) return false;
+    const int key = w.tile(j) * kRows, last_row = w.it.t * kBlock + i * kRows + kRows - 1;
+    return key <= last_row - p.window && key + kRows > p.sinks;
   };
   auto take = [&](int k, Work& w) -> bool {
     const int e = k & 1;
@@ -410,6 +424,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.head = items[e * 4 + 3];
     w.n0 = 2 * w.it.t + 1;
     w.n1 = w.it.t * kBlock + kRows < w.it.len ? 2 * w.it.t + 2 : 0;
+    w.sink_tiles = w.passed = 0;
+    if (kWindow) {
+      const int first = max(w.it.t * kBlock - p.window + 1, 0) / kRows;
+      w.sink_tiles = p.sinks >= first * kRows ? first : (p.sinks + kRows - 1) / kRows;
+      w.passed = first - w.sink_tiles;
+      w.n0 -= w.passed;
+      if (w.n1 > 0) w.n1 -= w.passed;
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive_a(item_empty(e));
     return w.it.len > 0;
@@ -429,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok && take(k, w); ++k) {
       const int mine = i == 0 ? w.n0 : w.n1;
       float mc = -kInf, l = 0.0f;  // the reference in base-2 units and the sum of 2^(s - m)
-      // The values of the diagonal tile (load u of the ring), looked through for
+      // The values of a tile with masked keys (load u of the ring), looked through for
       // elements that are not finite; a thread takes one key's row.
       auto clean_values = [&](unsigned u) -> bool {
         const unsigned s = u % S::kSlots;
@@ -471,7 +493,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < 4; ++q) tmem_ld32(s_t + q * 32, x + q * 32);
         tmem_ld_wait();
         pin<128>(x);
-        if (j + 1 == mine) {  // the diagonal tile: keys past r are left out
+        if (kWindow) {
+          if (masked(w, i, j)) {  // keys past the row, and those before the window that are no sinks
+            const int key = w.tile(j) * kRows, row = w.it.t * kBlock + i * kRows + r;
+            auto below = [](int n) -> uint32_t { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; };
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int at = key + q * 32;
+              const uint32_t keep = below(row + 1 - at) & (~below(row - p.window + 1 - at) | below(p.sinks - at));
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if ((keep & (1u << e)) == 0) x[q * 32 + e] = -kInf;
+            }
+          }
+        } else if (j + 1 == mine) {  // the diagonal tile: keys past r are left out
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t keep = r >= q * 32 + 31 ? ~0u : r < q * 32 ? 0u : (2u << (r - q * 32)) - 1;
@@ -553,8 +588,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
 
       for (int j = 0; j < mine; ++j) {
-        if (j + 1 == mine) ok = clean_values(u0 + 2 * j + 1);  // while the scores are computed
+        // While the scores are computed; but in an item's first tile only after
+        // them: a barrier's phase is only told from the one before, and a query
+        // tile that had no rows may be ahead of the loads by more than a lap
+        // until its issuer, which waits for every load, has computed scores.
+        const bool clean = masked(w, i, j), late = kWindow && j == 0;
+        if (clean && !late) ok = clean_values(u0 + 2 * j + 1);
         ok = __all_sync(~0u, ok && mbar_wait_a(s_full(i), (tiles_done + j) & 1, abort_flag, p.status));
+        if (late && clean && ok) ok = clean_values(u0 + 2 * j + 1);
         if (!ok) break;
         tc_fence_after();
         step(j);
@@ -583,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           pin<64>(v);
           if (fix && live) {
-            for (int j = (w.n0 - 1) * kRows; j <= rs; ++j) {
+            auto add_back = [&](int j) {
               const __nv_bfloat16* src =
                   p.v + static_cast<int64_t>(w.it.start + j) * p.ldv + w.head / p.group * D + h * 64;
 #pragma unroll
@@ -591,6 +632,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float y = __bfloat162float(src[e]);
                 if (!(fabsf(y) < kInf)) v[e] += y;
               }
+            };
+            if (kWindow) {  // of every tile that either query tile may have looked through
+              for (int j = 0; j < max(w.n0, w.n1); ++j) {
+                if (!masked(w, 0, j) && !masked(w, 1, j)) continue;
+                const int key = w.tile(j) * kRows;
+                for (int a = key; a < key + kRows && a <= rs; ++a)
+                  if (a > rs - p.window || a < p.sinks) add_back(a);
+              }
+            } else {
+              for (int j = (w.n0 - 1) * kRows; j <= rs; ++j) add_back(j);
             }
           }
 #pragma unroll
@@ -634,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int d = 0; d < S::kPanels; ++d)
               tma_load_2d(dst + d * kPanel, (u & 1) ? &maps.v : &maps.k, w.head / p.group * D + d * 64,
-                          w.it.start + (u >> 1) * kRows, full(s));
+                          w.it.start + w.tile(u >> 1) * kRows, full(s));
             ++issued;
             if (used < S::kSlots) ++used;
             if (u > 0) continue;
@@ -813,18 +864,18 @@ bool rows_map(CUtensorMap* map, const void* base, int64_t width, int64_t rows, i
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool kWindow>
 qerl_status launch(const PromptMaps& maps, const PromptParams& p, int64_t grid, int dev, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // one bit per device: the attribute belongs to the device's function
   const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
   if ((ready.load() & bit) == 0) {
-    if (cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(prompt_kernel<D, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Shape<D>::kSmem) != cudaSuccess)
       return QERL_ERR_CUDA;
     ready.fetch_or(bit);
   }
-  return cuda_status(
-      launch_dependent(prompt_kernel<D>, dim3(static_cast<unsigned>(grid)), kThreads, Shape<D>::kSmem, s, maps, p));
+  return cuda_status(launch_dependent(prompt_kernel<D, kWindow>, dim3(static_cast<unsigned>(grid)), kThreads,
+                                      Shape<D>::kSmem, s, maps, p));
 }
 
 }  // namespace
@@ -861,7 +912,11 @@ qerl_status launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t s
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return QERL_ERR_CUDA;
   const int64_t grid = std::min<int64_t>(blocks * a.num_heads, sms);  // one resident CTA per SM
-  return a.head_dim == 128 ? launch<128>(maps, p, grid, dev, s) : launch<64>(maps, p, grid, dev, s);
+  p.window = a.window;
+  p.sinks = a.sinks;
+  if (a.window > 0 && a.window < a.tokens)  // else it leaves nothing out
+    return a.head_dim == 128 ? launch<128, true>(maps, p, grid, dev, s) : launch<64, true>(maps, p, grid, dev, s);
+  return a.head_dim == 128 ? launch<128, false>(maps, p, grid, dev, s) : launch<64, false>(maps, p, grid, dev, s);
 }
 
 }  // namespace qerl

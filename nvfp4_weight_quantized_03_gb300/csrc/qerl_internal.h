@@ -148,6 +148,7 @@ struct DecodeAttentionArgs {
   int64_t ldq;
   int num_heads;
   const int* lengths;
+  int window, sinks;  // window 0: every row
   float scale;
   void* out;
   int64_t ldo;
@@ -165,6 +166,7 @@ struct PromptAttentionArgs {
   int num_heads, num_kv_heads, head_dim;
   const int* cu_seqlens;
   int64_t num_seqs;
+  int window, sinks;  // window 0: every row j <= i
   float scale;
   void* out;
   int64_t ldo;
@@ -174,6 +176,44 @@ struct PromptAttentionArgs {
 size_t prompt_attention_workspace_bytes(int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
                                         int64_t num_seqs);
 qerl_status launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t s);
+
+// tree_attention.cu: drafted tokens over the paged cache.
+struct TreeAttentionArgs {
+  const qerl_kv_cache* cache;
+  const void *q, *k, *v;
+  int64_t ldq, ldk, ldv;
+  int64_t tokens;
+  int num_heads;
+  const int *cu_tokens, *lengths;
+  const int64_t* mask;
+  int mask_words;
+  float scale;
+  void* out;
+  int64_t ldo;
+  float* lse;
+  void* workspace;
+};
+size_t tree_attention_workspace_bytes(int64_t tokens, int num_heads, int num_kv_heads, int head_dim);
+qerl_status launch_tree_attention(const TreeAttentionArgs& a, cudaStream_t s);
+
+// cache_pages.cu: sequences forked, the pool compacted.
+struct KvForkArgs {
+  const qerl_kv_cache* cache;
+  const int *parents, *children, *lengths, *new_pages;
+  int64_t count;
+  int* status;
+};
+qerl_status launch_kv_fork(const KvForkArgs& a, cudaStream_t s);
+struct KvCompactArgs {
+  const qerl_kv_cache* cache;
+  const int* lengths;
+  int* new_table;
+  int64_t ld_new;
+  int* live_pages;
+  void* workspace;
+};
+size_t kv_compact_workspace_bytes(int64_t num_pages);
+qerl_status launch_kv_compact(const KvCompactArgs& a, cudaStream_t s);
 
 // A launch whose CTAs may start while the kernel before it in the stream ends
 // (programmatic dependent launch): every kernel launched through it begins with

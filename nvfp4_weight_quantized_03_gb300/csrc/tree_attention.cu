@@ -1,0 +1,1271 @@
+// tree_attention.cu -- attention of several new tokens per sequence (a drafted
+// tree or chain) over the paged key-value cache and over one another.
+//
+//   s_tj = scale * q_t . k_j over the cache's rows j < len and over the new
+//   tokens j that t sees (a mask, or j <= t);
+//   out_t = sum_j exp(s_tj - lse_t) v_j,   lse_t = log sum_j exp(s_tj)
+//
+// Bound: bytes of the cache while rows are few, the two products (4 * head_dim
+// operations per row and key) when they are many.  The new tokens of a sequence
+// and the G query heads of a key-value head are rows of one matrix (row =
+// token * G + head), so that a key read once meets all of them: at a few tokens
+// they fill the 128 rows of a tcgen05 tile.
+//
+// The work is cut by cost: all (sequence, key-value head, 256 rows, key tile)
+// units in order form one line, with the cost of a segment's start and end, that
+// the CTAs, one per SM, share out evenly.  It is computed on the device from the
+// lengths and offsets.  A CTA whose stretch begins or ends inside a segment
+// leaves its partial (m, l, o) in the workspace, and a second small kernel joins
+// the partials in CTA order.
+//
+//   warps 0-3, 4-7  softmax of tile 0, tile 1: a thread owns a row, reads its
+//                   128 scores from tensor memory, keeps the reference m and
+//                   the sum l in registers and writes the weights back as bf16
+//                   over the scores; then the tile's outputs
+//   warps 8-11      loads: q, then k, v tiles through a ring.  Pages may be of
+//                   any size, so rows are gathered with cp.async; bytes of an
+//                   E4M3 cache pass through a ring of their own and are
+//                   widened to bf16 on the way (exact)
+//   warps 12, 13    issue S_i = Q_i K^T and O_i += P_i V of tile 0, tile 1
+//   warp 14         finds the CTA's next items
+// Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each).
+// Of more than 128 rows the two tiles are rows 0-127 and 128-255 and go through
+// all keys.  Up to 128 rows both are the same rows and take every other key
+// tile; their outputs are added at the end.  Either way one tile's products run
+// while the other's softmax is computed.
+//
+// Roundings: scores, m, l, O are fp32; the weights 2^(s - m) are rounded to bf16
+// for the product with v, l sums the unrounded ones.  With an E4M3 cache O is in
+// units of the head's value scale, so the weights of the new tokens, whose values
+// are bf16, are divided by it first.
+//
+// A masked weight is 0, but 0 * NaN is NaN: rows past a length read as zeros, and
+// the values of the new tokens are looked through before the product; elements
+// that are not finite are replaced by 0 there and added back in the end to the
+// rows that do see them.
+#include "qerl_internal.h"
+#include "qerl_ptx.cuh"
+
+#include <algorithm>
+#include <atomic>
+#include <cuda_bf16.h>
+
+namespace qerl {
+namespace {
+
+constexpr int kRows = 128;   // rows of a query tile, keys of a key tile
+constexpr int kBlock = 256;  // rows of a segment
+// At launch 512 threads have 128 registers each: 256 * 184 + 128 * 88 + 128 * 56 = 512 * 128.
+constexpr int kThreads = 512;
+constexpr int kSoftmaxRegs = 184, kLoadRegs = 88, kOtherRegs = 56;
+constexpr uint32_t kPanel = kRows * 128;  // 128 rows of 64 bf16, 128-byte swizzle
+constexpr float kSlack = 8.0f;
+constexpr int kMaxCtas = 160;
+constexpr int kSegmentCost = 2;  // of a segment's start and end, in key tiles
+constexpr int kMaxTokens = 1 << 20;  // of a sequence
+
+struct TreeParams {
+  const __nv_bfloat16 *q, *k, *v;
+  int64_t ldq, ldk, ldv;
+  const uint8_t *kp, *vp;
+  const float *k_scale, *v_scale;
+  const int* table;
+  int64_t ld_table, num_pages;
+  int page_size, page_shift;  // shift < 0: not a power of two
+  int64_t capacity;           // max_pages * page_size
+  const int *cu, *lengths;
+  const unsigned long long* mask;  // null: j <= t
+  int words;
+  int num_seqs, tokens, heads, kv_heads, group;
+  float scale_log2;
+  __nv_bfloat16* out;
+  int64_t ldo;
+  float* lse;
+  int4* jobs;   // [CTA]: (sequence, key-value head, first row, partials) of the segment begun in its stretch; 0: whole
+  float* part;  // [CTA][2]: of the segment begun before its stretch, of the one begun in it; see slot_floats
+  int slot_rows;
+  int* status;
+};
+
+// A partial: o as [head_dim / 4][slot_rows] of 4 floats, then m and l.
+__host__ __device__ __forceinline__ int64_t slot_floats(int slot_rows, int head_dim) {
+  return static_cast<int64_t>(slot_rows) * (head_dim + 2);
+}
+
+template <int D, bool kFp8>
+struct Shape {
+  static constexpr int kPanels = D / 64;
+  static constexpr uint32_t kTile = kPanels * kPanel;
+  static constexpr unsigned kSlots = (kFp8 ? 3 : 5) * (128 / D);
+  static constexpr unsigned kRaw = kFp8 ? 4 * (128 / D) : 0;  // key tiles as they lie in the cache
+  static constexpr uint32_t kRawTile = kRows * D;
+  static constexpr uint32_t kRing = 2 * kTile;
+  static constexpr uint32_t kRawRing = kRing + kSlots * kTile;
+  static constexpr uint32_t kBars = kRawRing + kRaw * kRawTile;
+  static constexpr uint32_t kSmem = 1024 + kBars + 768;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// x * 0 + c for two bf16
+__device__ __forceinline__ uint32_t times0_plus(uint32_t x, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(0u), "r"(c));
+  return d;
+}
+// Two fp32 operations in one instruction, each rounded as a single one.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// 16 or 32 columns of this thread's lane without waiting for them.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Ties registers to this place: their readers cannot be moved above it (and so
+// not above the wait for the load that fills them).
+template <int N>
+__device__ __forceinline__ void pin(float* v) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile(""
+                 : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
+                   "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+
+// Descriptor of an operand whose rows run along the contraction (v: [key][64
+// elements] panels): 128-byte swizzle, 8-key groups 1024 B apart (stride
+// offset), the next 64 elements one panel on (leading offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(kPanel >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// The issuing warps stay converged and one lane's predicate guards each
+// instruction: descriptors then live in uniform registers.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
+}
+
+// Four E4M3 bytes -> four bf16 (exact): the exponent and mantissa as bf16's,
+// which is 2^-120 of the value (subnormals too), times 2^120.  NaN's bits give
+// +-480 here; the caller looks for them.
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);  // each byte atop 16 bits
+  const uint32_t x = (a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), y = (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u);
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(0x7B807B80u));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(0x7B807B80u));
+}
+// NaN where a byte of w is E4M3's NaN.
+__device__ __forceinline__ void nan_bytes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if ((w & 0x7Fu) == 0x7Fu) lo = (lo & 0xFFFF0000u) | 0x7FFFu;
+  if ((w & 0x7F00u) == 0x7F00u) lo = (lo & 0x0000FFFFu) | 0x7FFF0000u;
+  if ((w & 0x7F0000u) == 0x7F0000u) hi = (hi & 0xFFFF0000u) | 0x7FFFu;
+  if ((w & 0x7F000000u) == 0x7F000000u) hi = (hi & 0x0000FFFFu) | 0x7FFF0000u;
+}
+
+// The scheduler is up to two items ahead, and an item may last as long as the
+// cache is long: it waits until another role gives up (or some 2000 s).
+__device__ __forceinline__ bool wait_patiently(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  for (int i = 0; i < (1 << 27); ++i) {
+    if (mbar_try_wait_hint_a(bar, parity, QERL_WAIT_HINT_NS)) return true;
+    if (*abort_flag) return false;
+  }
+  *abort_flag = 1;
+  record_error(status, QERL_ERR_TIMEOUT);
+  return false;
+}
+
+// 2^(m - top); 1 for a part without a finite score, whose sums are 0 (or NaN, which stays).
+__device__ __forceinline__ float weight_of(float m, float top) {
+  return m == -__int_as_float(0x7f800000) ? 1.0f : ex2(m - top);
+}
+
+// A sequence's place on the line.
+struct Sequence {
+  int start, n, len;  // its first new token, their count, its rows in the cache
+  int blocks, ctx, tiles;  // segments per key-value head; key tiles of the cache, of a segment
+  __device__ __forceinline__ long long cost(const TreeParams& p) const {
+    return n > 0 ? static_cast<long long>(p.kv_heads) * blocks * (tiles + kSegmentCost) : 0;
+  }
+};
+// false: its offsets break the rules.
+__device__ __forceinline__ bool sequence(const TreeParams& p, int s, Sequence& q) {
+  q.start = p.cu[s];
+  const int end = p.cu[s + 1], len = p.lengths[s];
+  if (q.start < 0 || end < q.start || end > p.tokens || end - q.start > kMaxTokens) return false;
+  q.n = end - q.start;
+  q.len = len < 0 ? 0 : len > p.capacity ? static_cast<int>(p.capacity) : len;
+  q.blocks = (q.n * p.group + kBlock - 1) / kBlock;
+  q.ctx = q.len == 0 ? 0 : (q.len - 1) / kRows + 1;
+  q.tiles = q.ctx + (q.n + kRows - 1) / kRows;
+  return true;
+}
+
+// a / b for a >= 0, b > 0; the 64-bit division costs several times the 32-bit one.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
+// A piece of a segment: key tiles [t0, t1).
+struct Item {
+  int start, n, len, seq, kv_head, row0, t0, t1, slot;  // slot -1: the whole segment
+};
+constexpr int kItemInts = 12;
+
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+  using S = Shape<D, kFp8>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* gen = smem_raw + (sbase - raw);
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // uniform to the compiler too
+  const float kInf = __int_as_float(0x7f800000);
+
+  const uint32_t bars = sbase + S::kBars;
+  auto full = [&](unsigned s) { return bars + 8u * s; };
+  auto empty = [&](unsigned s) { return bars + 8u * (S::kSlots + s); };
+  const uint32_t misc = bars + 16u * S::kSlots;
+  auto s_full = [&](int i) { return misc + 8u * i; };
+  auto p_full = [&](int i, int part) { return misc + 8u * (2 + 2 * i + part); };
+  auto o_full = [&](int i) { return misc + 8u * (6 + i); };
+  auto turn = [&](int i) { return misc + 8u * (8 + i); };
+  auto q_full = [&](int i) { return misc + 8u * (10 + i); };
+  auto q_empty = [&](int i) { return misc + 8u * (12 + i); };
+  auto ml_full = [&](int i) { return misc + 8u * (14 + i); };
+  auto ml_empty = [&](int i) { return misc + 8u * (16 + i); };
+  auto item_full = [&](int e) { return misc + 8u * (18 + e); };
+  auto item_empty = [&](int e) { return misc + 8u * (20 + e); };
+  const uint32_t done = misc + 8u * 22;
+  const uint32_t tmem_holder = misc + 8u * 23;
+  uint8_t* misc_gen = gen + S::kBars + 16 * S::kSlots;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc_gen + 8 * 23 + 4);
+  volatile int* dirty = reinterpret_cast<volatile int*>(misc_gen + 8 * 24);       // [4]: item k's at k & 3 is k + 1
+  volatile int* items = reinterpret_cast<volatile int*>(misc_gen + 8 * 26);       // [2][kItemInts]
+  volatile long long* sums = reinterpret_cast<volatile long long*>(misc_gen + 8 * 38);  // [16], then the place found
+  volatile int* place = reinterpret_cast<volatile int*>(misc_gen + 8 * 54);       // sequence, bad offsets
+  volatile long long* inside_seq = reinterpret_cast<volatile long long*>(misc_gen + 8 * 55);
+
+  if (threadIdx.x == 0) {
+    for (unsigned s = 0; s < S::kSlots; ++s) {
+      mbar_init_a(full(s), 4);
+      mbar_init_a(empty(s), 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init_a(s_full(i), 1);
+#ifdef QERL_TEST_HOOKS
+      mbar_init_a(p_full(i, 0), 4 + (g_test_extra_arrival ? 1 : 0));
+#else
+      mbar_init_a(p_full(i, 0), 4);
+#endif
+      mbar_init_a(p_full(i, 1), 4);
+      mbar_init_a(o_full(i), 1);
+      mbar_init_a(turn(i), 1);
+      mbar_init_a(q_full(i), 4);
+      mbar_init_a(q_empty(i), 4);
+      mbar_init_a(ml_full(i), 4);
+      mbar_init_a(ml_empty(i), 4);
+      mbar_init_a(item_full(i), 1);
+      mbar_init_a(item_empty(i), 14);  // 8 softmax warps, 4 of the loads and 2 issuers
+    }
+    mbar_init_a(done, 2);
+    *abort_flag = 0;
+    for (int i = 0; i < 4; ++i) dirty[i] = 0;
+    place[1] = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(~0u, *reinterpret_cast<volatile uint32_t*>(misc_gen + 8 * 23), 0);
+
+  griddep_wait();
+
+  // ---- this CTA's stretch of the line ---------------------------------------
+  constexpr int kWarps = kThreads / 32;
+  auto scan = [&](long long v) -> long long {  // inclusive over the block
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const long long up = __shfl_up_sync(~0u, v, i);
+      if (lane >= i) v += up;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    long long w = lane < kWarps ? sums[lane] : 0;
+#pragma unroll
+    for (int i = 1; i < kWarps; i <<= 1) {
+      const long long up = __shfl_up_sync(~0u, w, i);
+      if (lane >= i) w += up;
+    }
+    const long long before = __shfl_sync(~0u, w, warp > 0 ? warp - 1 : 0);
+    return warp > 0 ? v + before : v;
+  };
+  auto total_of = [&]() -> long long {  // of the last scan
+    long long w = lane < kWarps ? sums[lane] : 0;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) w += __shfl_xor_sync(~0u, w, i);
+    return w;
+  };
+  Sequence sq;
+  long long mine = 0, first_cost = 0;
+  for (int b = threadIdx.x; b < p.num_seqs; b += kThreads) {
+    const bool fine = sequence(p, b, sq);
+    // One sequence that breaks the rules leaves nothing to do: the offsets
+    // around it may lie before those of other sequences, and two CTAs would
+    // then write the same rows.
+    if (!fine) place[1] = 1;
+    const long long c = fine ? sq.cost(p) : 0;
+    if (b == threadIdx.x) first_cost = c;
+    mine += c;
+    const int len = p.lengths[b];
+    if (!fine || len < 0 || len > p.capacity || (p.mask != nullptr && sq.n > static_cast<int64_t>(p.words) * 64))
+      record_error(p.status, QERL_ERR_RANGE);
+  }
+  long long incl = scan(mine);
+  const long long total = place[1] ? 0 : total_of();
+  // Even stretches; a tile belongs to the stretch in which its place lies.
+  const long long ctas = total < gridDim.x ? total : gridDim.x;
+  const long long each = ctas > 0 ? quotient(total, ctas) : 0, extra = total - each * ctas;  // the first `extra` are one longer
+  auto stretch = [&](long long c) -> long long { return each * c + (c < extra ? c : extra); };
+  const bool busy = blockIdx.x < ctas;
+  const long long begin = busy ? stretch(blockIdx.x) : 0, end = busy ? stretch(blockIdx.x + 1) : 0;
+  if (p.num_seqs <= kThreads) {
+    if (busy && incl - mine <= begin && begin < incl) {
+      place[0] = threadIdx.x;
+      *inside_seq = begin - (incl - mine);
+    }
+  } else if (busy) {
+    long long base = 0;
+    for (int b0 = 0;; b0 += kThreads) {  // ends: begin < total, the sum of all
+      const int b = b0 + threadIdx.x;
+      mine = b0 == 0 ? first_cost : b < p.num_seqs && sequence(p, b, sq) ? sq.cost(p) : 0;
+      incl = scan(mine) + base;
+      const long long next = base + total_of();
+      if (begin < next) {
+        if (incl - mine <= begin && begin < incl) {
+          place[0] = b;
+          *inside_seq = begin - (incl - mine);
+        }
+        break;
+      }
+      base = next;
+    }
+  }
+  __syncthreads();
+
+  struct Work {
+    Item it;
+    bool shared;  // the two query tiles are the same rows and take every other key tile
+    int ctx;
+    // key tiles of query tile i, and the j-th of them
+    __device__ __forceinline__ int count(int i) const {
+      const int n = it.t1 - it.t0;
+      return shared ? (n + 1 - i) >> 1 : n;
+    }
+    __device__ __forceinline__ int tile(int i, int j) const { return it.t0 + (shared ? 2 * j + i : j); }
+  };
+  auto take = [&](int k, Work& w) -> bool {
+    const int e = k & 1;
+    // (a warp goes on or gives up as a whole, here and at every wait of a whole warp)
+    if (!__all_sync(~0u, mbar_wait_a(item_full(e), (k >> 1) & 1, abort_flag, p.status))) return false;
+    const volatile int* it = items + e * kItemInts;
+    w.it = {it[0], it[1], it[2], it[3], it[4], it[5], it[6], it[7], it[8]};
+    w.shared = w.it.n * p.group - w.it.row0 <= kRows;
+    w.ctx = w.it.len == 0 ? 0 : (w.it.len - 1) / kRows + 1;
+    __syncwarp();
+    if (lane == 0) mbar_arrive_a(item_empty(e));
+    return w.it.n > 0;
+  };
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int i = warp >> 2;               // query tile
+    const int r = (warp & 3) * 32 + lane;  // row of the tile
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_t = tmem + lanes + i * 128, o_t = tmem + lanes + 256 + i * D, o_other = tmem + lanes + 256 + (1 - i) * D;
+    const uint32_t own_q = sbase + i * S::kTile, other_q = sbase + (1 - i) * S::kTile;
+    constexpr uint32_t kMl = 8192;  // of a query tile's buffer when its products are done: outputs, then (m, l)
+    bool ok = true;
+    // Of this query tile; loads of the ring before this item, of which only the
+    // slot and the phase are used (modulo two laps: a CTA may see more than 2^32).
+    unsigned tiles_done = 0, u0 = 0;
+    int outputs_done = 0, exchanges = 0;
+    Work w;
+    for (int k = 0; ok && take(k, w); ++k) {
+      const int mine_n = w.count(i);
+      const int row = w.it.row0 + (w.shared ? 0 : i * kRows) + r;  // of the sequence's rows
+      const int rows = w.it.n * p.group;
+      const int token = row < rows ? row / p.group : 0;
+      float mc = -kInf, l = 0.0f;  // the reference in base-2 units and the sum of 2^(s - m)
+      float v_scale = 1.0f, v_inverse = 1.0f, c_ctx = fabsf(p.scale_log2);
+      if (kFp8) {
+        if (p.k_scale != nullptr) c_ctx = fabsf(p.scale_log2 * p.k_scale[w.it.kv_head]);
+        if (p.v_scale != nullptr) v_scale = p.v_scale[w.it.kv_head];
+        v_inverse = 1.0f / v_scale;
+      }
+      // Not 0: a masked score of -inf times 0 would be NaN (1e-37 times any score below 1e29 is as good as 0).
+      c_ctx = fmaxf(c_ctx, 1e-37f);
+      const float c_new = fmaxf(fabsf(p.scale_log2), 1e-37f);
+      // Bits of the keys 32 q .. 32 q + 31 of key tile t that this row attends to.
+      auto below = [](int n) -> uint32_t { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; };
+      auto sees = [&](int t, int q) -> uint32_t {
+        if (t < w.ctx) return below(w.it.len - t * kRows - q * 32);
+        const int at = (t - w.ctx) * kRows + q * 32;
+        if (row >= rows) return 0;
+        if (p.mask == nullptr) return below(token + 1 - at);
+        const int word = at >> 6;
+        if (word >= p.words) return 0;
+        const unsigned long long m = p.mask[static_cast<int64_t>(w.it.start + token) * p.words + word];
+        return static_cast<uint32_t>(m >> (at & 32)) & below(w.it.n - at);
+      };
+      // The values of a tile of new tokens (load u of the ring), looked through
+      // for elements that are not finite; a thread takes one token's row.
+      auto clean_values = [&](unsigned u) -> bool {
+        const unsigned s = u % S::kSlots;
+        if (!__all_sync(~0u, mbar_wait_a(full(s), (u / S::kSlots) & 1, abort_flag, p.status))) return false;
+        const uint32_t at_row = sbase + S::kRing + s * S::kTile + r * 128;
+        // x * 0 + sum is NaN from the first x that is not finite
+        uint32_t sum = 0;
+#pragma unroll
+        for (int q = 0; q < S::kPanels * 8; ++q) {
+          const uint4 a = lds128(at_row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4));
+          sum = times0_plus(a.x, sum);
+          sum = times0_plus(a.y, sum);
+          sum = times0_plus(a.z, sum);
+          sum = times0_plus(a.w, sum);
+        }
+        if ((sum & 0x7FFF7FFFu) != 0) {
+          dirty[k & 3] = k + 1;
+          for (int q = 0; q < S::kPanels * 8; ++q) {
+            const uint32_t at = at_row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4);
+            const uint4 x = lds128(at);
+            uint32_t a[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if ((a[e] & 0x7F800000u) == 0x7F800000u) a[e] &= 0x0000FFFFu;
+              if ((a[e] & 0x7F80u) == 0x7F80u) a[e] &= 0xFFFF0000u;
+            }
+            sts128(at, make_uint4(a[0], a[1], a[2], a[3]));
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        return true;
+      };
+      // One key tile: scores in, weights out, l and (rarely) the reference moved.
+      auto step = [&](int j, bool masked, bool fresh, const uint32_t (&keep)[4]) {
+        float x[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(s_t + q * 32, x + q * 32);
+        tmem_ld_wait();
+        pin<128>(x);
+        if (masked) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((keep[q] & (1u << e)) == 0) x[q * 32 + e] = -kInf;
+        }
+        const float c = kFp8 && !fresh ? c_ctx : c_new;
+        const uint64_t c2 = pair(c, c);
+        float t4[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          t4[q] = max3(x[q * 32], x[q * 32 + 1], x[q * 32 + 2]);
+#pragma unroll
+          for (int e = 3; e < 31; e += 2) t4[q] = max3(t4[q], x[q * 32 + e], x[q * 32 + e + 1]);
+          t4[q] = fmaxf(t4[q], x[q * 32 + 31]);
+        }
+        const float top = max3(fmaxf(t4[0], t4[1]), t4[2], t4[3]);
+        const float tc = top == -kInf ? -kInf : top * c;
+        if (__any_sync(~0u, tc > mc + kSlack)) {
+          const float up = fmaxf(mc, tc);
+          if (j > 0) {
+            const float f = mc == up ? 1.0f : ex2(mc - up);
+            l *= f;
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              float v[16];
+              tmem_ld16(o_t + q * 16, v);
+              tmem_ld_wait();
+              pin<16>(v);
+              uint32_t y[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(v[e] * f);
+              tmem_st_x16(o_t + q * 16, y);
+            }
+          }
+          mc = up;
+        }
+        uint64_t part[2] = {0, 0};  // two chains of two fp32 sums
+        const float sub = mc == -kInf ? 0.0f : mc;
+        const uint64_t sub2 = pair(-sub, -sub);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t y[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float a, b;
+            unpair(fma2(pair(x[half * 64 + 2 * e], x[half * 64 + 2 * e + 1]), c2, sub2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            part[e & 1] = add2(part[e & 1], pair(a, b));
+            if (kFp8 && fresh) {
+              a *= v_inverse;
+              b *= v_inverse;
+            }
+            y[e] = pack_bf16(a, b);
+          }
+          // half of the keys: the product with v may begin
+          tmem_st_x32(s_t + half * 32, y);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_a(p_full(i, half));
+        }
+        float s0, s1;
+        unpair(add2(part[0], part[1]), s0, s1);
+        l += s0 + s1;
+      };
+
+      for (int j = 0; j < mine_n; ++j) {
+        const int t = w.tile(i, j);
+        const bool fresh = t >= w.ctx, masked = fresh || w.it.len - t * kRows < kRows;
+        uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+        if (masked) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) keep[q] = sees(t, q);
+        }
+        ok = __all_sync(~0u, mbar_wait_a(s_full(i), (tiles_done + j) & 1, abort_flag, p.status));
+        // (after the scores: with the keys in place, and the loads before them,
+        // the values' barrier is in this phase or the one before)
+        if (ok && fresh) ok = clean_values(u0 + 2 * (t - w.it.t0) + 1);
+        if (!ok) break;
+        tc_fence_after();
+        step(j, masked, fresh, keep);
+      }
+      tiles_done += mine_n;
+      u0 = (u0 + 2 * (w.it.t1 - w.it.t0)) % (2 * S::kSlots);
+      // The query tile's buffer is free: its products are done (or, without any, its rows have landed).
+      if (mine_n > 0) {
+        ok = __all_sync(~0u, ok && mbar_wait_a(o_full(i), outputs_done & 1, abort_flag, p.status));
+        ++outputs_done;
+      } else {
+        ok = __all_sync(~0u, ok && mbar_wait_a(q_full(i), k & 1, abort_flag, p.status));
+      }
+      if (!ok) break;
+      tc_fence_after();
+      float f_own = 1.0f, f_other = 0.0f;
+      const bool both = w.shared && w.count(1) > 0;
+      if (both) {
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(own_q + kMl + r * 8), "f"(mc), "f"(l) : "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_a(ml_full(i));
+        ok = __all_sync(~0u, mbar_wait_a(ml_full(1 - i), exchanges & 1, abort_flag, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        float m2, l2;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(m2), "=f"(l2) : "r"(other_q + kMl + r * 8) : "memory");
+        const float top = fmaxf(mc, m2);
+        f_own = weight_of(mc, top);
+        f_other = weight_of(m2, top);
+        // the same sum in the same order on both sides
+        l = i == 0 ? f_own * l + f_other * l2 : f_other * l2 + f_own * l;
+        mc = top;
+      }
+      const bool live = row < rows;
+      const bool fix = dirty[k & 3] == k + 1;
+      const float f = l == 0.0f ? 0.0f : v_scale / l;
+      const bool whole = w.it.slot < 0;
+      float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (whole ? 0 : w.it.slot)) * slot_floats(p.slot_rows, D);
+      const int slot_row = row - w.it.row0;
+      // Shared rows: each tile's warps take half of the columns, tile 0's all of them if tile 1 had no keys.
+      const int c0 = both && i == 1 ? D / 2 : 0, c1 = both ? c0 + D / 2 : w.shared && i == 1 ? 0 : D;
+      const uint32_t stage = own_q + (warp & 3) * 2048;
+      const int head0 = w.it.kv_head * p.group;
+#pragma unroll 1
+      for (int col = c0; col < c1; col += 32) {
+        float v[32];
+        tmem_ld32(o_t + col, v);
+        if (both) {
+          float y[32];
+          tmem_ld32(o_other + col, y);
+          tmem_ld_wait();
+          pin<32>(v);
+          pin<32>(y);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            v[e] = i == 0 ? f_own * v[e] + f_other * y[e] : f_other * y[e] + f_own * v[e];
+        } else {
+          tmem_ld_wait();
+          pin<32>(v);
+        }
+        if (fix && live) {
+          for (int t = max(w.it.t0, w.ctx); t < w.it.t1; ++t)
+            for (int q = 0; q < 4; ++q) {
+              uint32_t keep = sees(t, q);
+              while (keep != 0) {
+                const int node = (t - w.ctx) * kRows + q * 32 + __ffs(keep) - 1;
+                keep &= keep - 1;
+                const __nv_bfloat16* src = p.v + (static_cast<int64_t>(w.it.start) + node) * p.ldv + w.it.kv_head * D + col;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const float y = __bfloat162float(src[e]);
+                  if (!(fabsf(y) < kInf)) v[e] += y * v_inverse;
+                }
+              }
+            }
+        }
+        if (whole) {
+          // Through shared memory, so that a store covers 64 bytes of a row.
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sts128(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4),
+                   make_uint4(pack_bf16(v[8 * e] * f, v[8 * e + 1] * f), pack_bf16(v[8 * e + 2] * f, v[8 * e + 3] * f),
+                              pack_bf16(v[8 * e + 4] * f, v[8 * e + 5] * f),
+                              pack_bf16(v[8 * e + 6] * f, v[8 * e + 7] * f)));
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int at = q * 8 + (lane >> 2), ch = lane & 3;
+            const uint4 y = lds128(stage + at * 64 + ((ch ^ ((at >> 1) & 3)) << 4));
+            const int g = row - lane + at;
+            if (g < rows) {
+              const int tk = g / p.group;
+              *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(w.it.start) + tk) * p.ldo +
+                                        static_cast<int64_t>(head0 + g - tk * p.group) * D + col + ch * 8) = y;
+            }
+          }
+          __syncwarp();
+        } else if (live) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            __stcg(reinterpret_cast<float4*>(slot) + static_cast<int64_t>(col / 4 + e) * p.slot_rows + slot_row,
+                   make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
+        }
+      }
+      if (live && c0 == 0 && c1 > 0) {
+        if (!whole) {
+          __stcg(slot + static_cast<int64_t>(D) * p.slot_rows + slot_row, mc);
+          __stcg(slot + static_cast<int64_t>(D + 1) * p.slot_rows + slot_row, l);
+        } else if (p.lse != nullptr) {
+          p.lse[(static_cast<int64_t>(w.it.start) + token) * p.heads + head0 + row - token * p.group] =
+              l == 0.0f ? -kInf : (mc + log2f(l)) * 0.69314718055994530942f;
+        }
+      }
+      if (both) {  // the other tile's warps still read this tile's outputs and (m, l)
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_a(ml_empty(i));
+        ok = __all_sync(~0u, mbar_wait_a(ml_empty(1 - i), exchanges & 1, abort_flag, p.status));
+        ++exchanges;
+        if (!ok) break;
+        tc_fence_after();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_a(q_empty(i));
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+    // Each warp brings 32 rows of every tile; a barrier takes one arrival of each.
+    const int lw = warp - 8;
+    unsigned issued = 0, told = 0;  // loads of the ring: begun, announced
+    unsigned raw_begun = 0, raw_done = 0;
+    bool ok = true;
+    auto arrive = [&](uint32_t bar) {
+      fence_proxy_async_smem();  // each thread's writes, before the tensor core reads them
+      __syncwarp();
+      if (lane == 0) mbar_arrive_a(bar);
+    };
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+      return __all_sync(~0u, mbar_wait_a(bar, parity, abort_flag, p.status));
+    };
+    auto wait_free = [&](unsigned u) -> bool {  // the slot of load u
+      return u < S::kSlots || wait(empty(u % S::kSlots), ((u / S::kSlots) & 1) ^ 1);
+    };
+    // 16-byte chunks of this warp's 32 rows of a tile of bf16 rows (lane x's row at src; null: zeros).
+    auto copy_rows = [&](uint32_t tile_at, const void* src) {
+      constexpr int kChunks = D / 8;
+#pragma unroll
+      for (int q = 0; q < kChunks; ++q) {
+        const int at = (q * 32 + lane) / kChunks, ch = lane % kChunks, row = lw * 32 + at;
+        const uint8_t* from =
+            reinterpret_cast<const uint8_t*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(src), at));
+        const bool real = from != nullptr;
+        cp_async_16(tile_at + (ch >> 3) * kPanel + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                    real ? from + ch * 16 : reinterpret_cast<const uint8_t*>(p.q), real ? 16 : 0);
+      }
+    };
+    // The same of E4M3 rows, as they are; every thread reads back what it wrote.
+    constexpr int kRawChunks = D / 16;
+    auto raw_at = [&](unsigned u, int q) {
+      return sbase + S::kRawRing + (u % (kFp8 ? S::kRaw : 1)) * S::kRawTile + (q * 128 + lw * 32 + lane) * 16;
+    };
+    auto copy_raw = [&](unsigned u, const void* src) {
+#pragma unroll
+      for (int q = 0; q < kRawChunks; ++q) {
+        const int at = (q * 32 + lane) / kRawChunks, ch = lane % kRawChunks;
+        const uint8_t* from =
+            reinterpret_cast<const uint8_t*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(src), at));
+        const bool real = from != nullptr;
+        cp_async_16(raw_at(u, q), real ? from + ch * 16 : reinterpret_cast<const uint8_t*>(p.q), real ? 16 : 0);
+      }
+    };
+    auto widen = [&]() -> bool {  // the oldest raw tile, which has landed, into its slot
+      if (!wait_free(told)) return false;
+      const uint32_t tile_at = sbase + S::kRing + (told % S::kSlots) * S::kTile;
+#pragma unroll
+      for (int q = 0; q < kRawChunks; ++q) {
+        const uint4 x = lds128(raw_at(raw_done, q));
+        const int ch = 2 * (lane % kRawChunks), row = lw * 32 + (q * 32 + lane) / kRawChunks;
+        const uint32_t a[4] = {x.x, x.y, x.z, x.w};
+        uint32_t y[8];
+        uint32_t nan = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          e4m3x4_to_bf16(a[e], y[2 * e], y[2 * e + 1]);
+          nan |= (a[e] & 0x7F7F7F7Fu) + 0x01010101u;
+        }
+        if (nan & 0x80808080u) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) nan_bytes_to_bf16(a[e], y[2 * e], y[2 * e + 1]);
+        }
+        const uint32_t to = tile_at + (ch >> 3) * kPanel + row * 128;
+        sts128(to + (((ch & 7) ^ (row & 7)) << 4), make_uint4(y[0], y[1], y[2], y[3]));
+        sts128(to + ((((ch + 1) & 7) ^ (row & 7)) << 4), make_uint4(y[4], y[5], y[6], y[7]));
+      }
+      arrive(full(told % S::kSlots));
+      ++told;
+      ++raw_done;
+      return true;
+    };
+    // Everything begun is announced.  Called before any wait for the others:
+    // what they need to go on is then there.
+    auto settle = [&]() -> bool {
+      cp_async_wait_group<0>();
+      if (kFp8) {
+        while (raw_done != raw_begun)
+          if (!widen()) return false;
+      } else {
+        for (; told != issued; ++told) arrive(full(told % S::kSlots));
+      }
+      return true;
+    };
+    // Only slots, phases and whether the first lap is over are used: two to four laps stay.
+    auto drop_laps = [&]() {
+      if (told < 4 * S::kSlots) return;
+      const unsigned laps = (told / (2 * S::kSlots) - 1) * (2 * S::kSlots);
+      told -= laps;
+      issued -= laps;
+    };
+    constexpr unsigned kAhead = kFp8 ? S::kRaw - 1 : S::kSlots - 2;  // loads in flight
+    Work w;
+    for (int k = 0; ok && take(k, w); ++k) {
+      const Item& it = w.it;
+      // Lane x's rows of keys and values of key tile t: key 32 lw + x.
+      const void *src_k = nullptr, *src_v = nullptr;
+      auto look_up = [&](int t) {
+        src_k = src_v = nullptr;
+        if (t >= it.t1) return;
+        if (t < w.ctx) {
+          const int key = t * kRows + lw * 32 + lane;
+          if (key >= it.len) return;
+          const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+          const int64_t page = p.table[it.seq * p.ld_table + pi];
+          if (page < 0 || page >= p.num_pages) {
+            record_error(p.status, QERL_ERR_RANGE);
+            return;
+          }
+          const int64_t at = ((page * p.kv_heads + it.kv_head) * p.page_size + (key - static_cast<int64_t>(pi) * p.page_size)) *
+                             (D * (kFp8 ? 1 : 2));
+          src_k = p.kp + at;
+          src_v = p.vp + at;
+        } else {
+          const int node = (t - w.ctx) * kRows + lw * 32 + lane;
+          if (node >= it.n) return;
+          src_k = p.k + (static_cast<int64_t>(it.start) + node) * p.ldk + it.kv_head * D;
+          src_v = p.v + (static_cast<int64_t>(it.start) + node) * p.ldv + it.kv_head * D;
+        }
+      };
+      auto load_queries = [&]() {
+        // (the buffers come free with the outputs of the item before)
+        for (int i = 0; ok && i < 2; ++i) {
+          if (k > 0 && !__all_sync(~0u, mbar_try_wait_a(q_empty(i), (k - 1) & 1)))
+            ok = settle() && wait(q_empty(i), (k - 1) & 1);
+          if (!ok) break;
+          const int row = it.row0 + (w.shared ? 0 : i * kRows) + lw * 32 + lane;
+          const void* src = nullptr;
+          if (row < it.n * p.group) {
+            const int token = row / p.group;
+            src = p.q + (static_cast<int64_t>(it.start) + token) * p.ldq +
+                  static_cast<int64_t>(it.kv_head * p.group + row - token * p.group) * D;
+          }
+          copy_rows(sbase + i * S::kTile, src);
+        }
+        cp_async_commit();
+        ok = ok && settle();
+        if (ok)
+          for (int i = 0; i < 2; ++i) arrive(q_full(i));
+      };
+      drop_laps();
+      look_up(it.t0);
+      bool asked = false;  // for the queries
+      for (int t = it.t0; ok && t < it.t1; ++t) {
+        const void* tile_src[2] = {src_k, src_v};
+        const bool direct = !kFp8 || t >= w.ctx;  // bf16 rows
+        if (kFp8 && direct) ok = settle();
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {  // k, then v
+          if (!ok) break;
+          if (direct) {
+            if (issued >= S::kSlots &&
+                !__all_sync(~0u, mbar_try_wait_a(empty(issued % S::kSlots), ((issued / S::kSlots) & 1) ^ 1)))
+              ok = settle() && wait_free(issued);
+            if (!ok) break;
+            copy_rows(sbase + S::kRing + (issued % S::kSlots) * S::kTile, tile_src[part]);
+          } else {
+            copy_raw(raw_begun++, tile_src[part]);
+          }
+          ++issued;
+          cp_async_commit();
+          if (part == 0) look_up(t + 1);
+          if (kFp8) {
+            if (!direct && raw_begun - raw_done == kAhead + 1) {
+              cp_async_wait_group<kAhead>();
+              ok = widen();
+            }
+          } else if (issued - told == kAhead + 1) {
+            cp_async_wait_group<kAhead>();
+            arrive(full(told % S::kSlots));
+            ++told;
+          }
+        }
+        if (kFp8 && direct && ok) {
+          cp_async_wait_group<0>();
+          for (; told != issued; ++told) arrive(full(told % S::kSlots));
+        }
+        // The queries after the first keys and values are on their way, of which
+        // no more may be announced without them than there are slots.
+        if (ok && !asked && (t + 1 == it.t1 || t - it.t0 == (S::kSlots >= 4 ? 1 : 0))) {
+          asked = true;
+          load_queries();
+        }
+      }
+    }
+    if (ok) settle();
+    cp_async_wait_group<0>();  // every copy lands before the CTA exits
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp < 14) {
+      const uint32_t leader = elect_lane();
+      // Warp 12 + i issues the products of query tile i.
+      const int i = warp - 12;
+      const uint32_t id_s = idesc_bf16_f32(128, 128);
+      const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // v: rows along the contraction
+      auto slot = [&](unsigned u) { return sbase + S::kRing + (u % S::kSlots) * S::kTile; };
+      auto wait_slot = [&](unsigned u) {
+        return mbar_wait_a(full(u % S::kSlots), (u / S::kSlots) & 1, abort_flag, p.status);
+      };
+      // A slot is free after two arrivals: one of each issuer where both use it,
+      // or both of the one that does.
+      auto release = [&](unsigned u, bool alone) {
+        commit(leader, empty(u % S::kSlots));
+        if (alone && leader) mbar_arrive_a(empty(u % S::kSlots));
+      };
+      unsigned u0 = 0, tiles_done = 0, turns = 0;
+      bool ok = true, first_turn = i == 0;  // of tile 0: nobody hands it over
+      Work w;
+      for (int k = 0; ok && take(k, w); ++k) {
+        const int n = w.count(i);
+        // Of every item, with or without tiles of this one: a barrier's phase is
+        // only told from the one before, and with the queries all loads of the
+        // items before are announced, so the slots' phases are no further off.
+        ok = __all_sync(~0u, mbar_wait_a(q_full(i), k & 1, abort_flag, p.status));
+        if (!ok) break;
+        if (n > 0) {
+          const float ks = kFp8 && p.k_scale != nullptr ? p.k_scale[w.it.kv_head] : 1.0f;
+          auto load_of = [&](int j) { return u0 + 2 * (w.tile(i, j) - w.it.t0); };
+          auto scores = [&](int j) {
+            const unsigned u = load_of(j);
+            const uint32_t qa = sbase + i * S::kTile, ka = slot(u);
+            // a negative factor of the scores: the product is negated
+            const bool negative = p.scale_log2 < 0.0f != (w.tile(i, j) < w.ctx && ks < 0.0f);
+            const uint32_t id = id_s | (negative ? 1u << 13 : 0u);
+#pragma unroll
+            for (int d = 0; d < S::kPanels; ++d)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ss(leader, tmem + i * 128, sw128_kmajor_desc(qa + d * kPanel + kk * 32),
+                       sw128_kmajor_desc(ka + d * kPanel + kk * 32), id, d + kk > 0 ? 1u : 0u);
+            commit(leader, s_full(i));
+            release(u, w.shared);
+          };
+          auto values = [&](unsigned u, int part, bool more) {
+            const uint32_t va = slot(u);
+#pragma unroll
+            for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
+              mma_ts(leader, tmem + 256 + i * D, tmem + i * 128 + kk * 8, sw128_mnmajor_desc(va + kk * 2048), id_o,
+                     more || kk > 0 ? 1u : 0u);
+          };
+          ok = __all_sync(~0u, wait_slot(load_of(0)));
+          if (!ok) break;
+          tc_fence_after();
+          scores(0);
+          for (int j = 0; j < n; ++j) {
+            const unsigned u = load_of(j) + 1;
+            ok = wait_slot(u);
+            if (!w.shared) {
+              // Turns, as the two tiles would fall into step: both in the softmax, then both at the tensor core.
+              ok = ok && (j + 1 >= n || wait_slot(load_of(j + 1)));
+              if (ok && !first_turn) ok = mbar_wait_a(turn(i), (turns - (i == 0 ? 1 : 0)) & 1, abort_flag, p.status);
+              first_turn = false;
+              ++turns;
+            }
+            ok = __all_sync(~0u, ok && mbar_wait_a(p_full(i, 0), (tiles_done + j) & 1, abort_flag, p.status));
+            if (!ok) break;
+            tc_fence_after();
+            values(u, 0, j > 0);
+            ok = __all_sync(~0u, mbar_wait_a(p_full(i, 1), (tiles_done + j) & 1, abort_flag, p.status));
+            if (!ok) break;
+            tc_fence_after();
+            values(u, 1, true);
+            release(u, w.shared);
+            if (j + 1 < n) {
+              if (w.shared) {
+                ok = __all_sync(~0u, wait_slot(load_of(j + 1)));
+                if (!ok) break;
+                tc_fence_after();
+              }
+              scores(j + 1);
+            } else {
+              commit(leader, o_full(i));
+            }
+            if (!w.shared && leader) mbar_arrive_a(turn(1 - i));
+          }
+        }
+        tiles_done += n;
+        u0 = (u0 + 2 * (w.it.t1 - w.it.t0)) % (2 * S::kSlots);
+      }
+      commit(leader, done);  // also after an expired wait: arrives once the issued MMAs are done
+    } else if (warp == 14) {
+      // The items of this CTA's stretch, ahead of the others.
+      auto owner = [&](long long pos) -> int {  // the CTA whose stretch holds a place
+        const long long wide = extra * (each + 1);
+        return static_cast<int>(pos < wide ? quotient(pos, each + 1) : extra + quotient(pos - wide, each));
+      };
+      int4 job = make_int4(0, 0, 0, 0);
+      int k = 0;
+      auto put = [&](const Item& it) -> bool {
+        const int e = k & 1;
+        if (k >= 2 && !__all_sync(~0u, wait_patiently(item_empty(e), ((k >> 1) & 1) ^ 1, abort_flag, p.status)))
+          return false;
+        if (lane == 0) {
+          const int v[9] = {it.start, it.n, it.len, it.seq, it.kv_head, it.row0, it.t0, it.t1, it.slot};
+#pragma unroll
+          for (int x = 0; x < 9; ++x) items[e * kItemInts + x] = v[x];
+          mbar_arrive_a(item_full(e));
+        }
+        __syncwarp();
+        ++k;
+        return true;
+      };
+      bool go = busy;
+      if (go) {
+        int b = place[0];
+        sequence(p, b, sq);
+        const int wide = sq.tiles + kSegmentCost;
+        long long seg = quotient(*inside_seq, wide);
+        int t = static_cast<int>(*inside_seq - seg * wide);
+        int kv_head = static_cast<int>(quotient(seg, sq.blocks)), block = static_cast<int>(seg - static_cast<long long>(kv_head) * sq.blocks);
+        for (long long pos = begin; go && pos < end;) {
+          const long long base = pos - t;
+          // In order, a block sees the new tokens up to its last row's.
+          int needed = sq.tiles;
+          if (p.mask == nullptr) {
+            const int last_row = min((block + 1) * kBlock, sq.n * p.group) - 1;
+            needed = sq.ctx + last_row / p.group / kRows + 1;
+          }
+          const int t1 = static_cast<int>(min(static_cast<long long>(needed), t + (end - pos)));
+          if (t < t1) {
+            const bool whole = t == 0 && t1 == needed;
+            if (t == 0 && !whole)
+              job = make_int4(b, kv_head, block * kBlock, owner(base + needed - 1) - static_cast<int>(blockIdx.x) + 1);
+            go = put({sq.start, sq.n, sq.len, b, kv_head, block * kBlock, t, t1, whole ? -1 : t == 0 ? 1 : 0});
+          }
+          pos = base + sq.tiles + kSegmentCost;
+          t = 0;
+          if (++block == sq.blocks) {
+            block = 0;
+            if (++kv_head == p.kv_heads) {
+              kv_head = 0;
+              for (++b; b < p.num_seqs; b += 32) {  // the next sequence with new tokens
+                const bool some = b + lane < p.num_seqs && p.cu[b + lane + 1] > p.cu[b + lane];
+                const unsigned which = __ballot_sync(~0u, some);
+                if (which != 0) {
+                  b += __ffs(which) - 1;
+                  break;
+                }
+              }
+              if (b >= p.num_seqs) break;
+              sequence(p, b, sq);
+            }
+          }
+        }
+      }
+      if (lane == 0) p.jobs[blockIdx.x] = job;
+      if (!busy || go) put({0, 0, 0, 0, 0, 0, 0, 0, 0});
+    }
+  }
+  __syncwarp();
+  {  // every MMA is done before the tensor memory goes back (bounded)
+    volatile int no_abort = 0;
+    mbar_wait_a(done, 0, &no_abort, p.status);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+// Block (c, y): 16 columns of the segment that CTA c began and others went on with.
+template <int D>
+__global__ void __launch_bounds__(kBlock) join_kernel(const __grid_constant__ TreeParams p, const int has_scale) {
+  griddep_wait();
+  const int4 job = p.jobs[blockIdx.x];
+  if (job.w == 0) return;
+  const int start = p.cu[job.x], rows = (p.cu[job.x + 1] - start) * p.group;
+  const int row = job.z + threadIdx.x;
+  if (row >= rows) return;
+  const float kInf = __int_as_float(0x7f800000);
+  const int64_t slot = slot_floats(p.slot_rows, D);
+  // The first partial is in the second slot of its CTA, the others in the first of theirs.
+  auto part = [&](int c) { return p.part + (2 * (static_cast<int64_t>(blockIdx.x) + c) + (c == 0 ? 1 : 0)) * slot; };
+  constexpr int kBatch = 4;  // partials in flight
+  float top = -kInf, sum = 0.0f;
+  float acc[16] = {};
+  for (int c0 = 0; c0 < job.w; c0 += kBatch) {
+    float m[kBatch], l[kBatch];
+    float4 v[kBatch][4];
+    float up = top;
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      m[q] = -kInf;
+      l[q] = 0.0f;
+      if (c0 + q < job.w) {
+        const float* src = part(c0 + q);
+        m[q] = __ldcg(src + static_cast<int64_t>(D) * p.slot_rows + threadIdx.x);
+        l[q] = __ldcg(src + static_cast<int64_t>(D + 1) * p.slot_rows + threadIdx.x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[q][e] = __ldcg(reinterpret_cast<const float4*>(src) +
+                           static_cast<int64_t>(blockIdx.y * 4 + e) * p.slot_rows + threadIdx.x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[q][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) up = fmaxf(up, m[q]);
+    const float f0 = weight_of(top, up);
+    top = up;
+    sum *= f0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] *= f0;
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const float f = weight_of(m[q], top);
+      sum += f * l[q];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[4 * e] += f * v[q][e].x;
+        acc[4 * e + 1] += f * v[q][e].y;
+        acc[4 * e + 2] += f * v[q][e].z;
+        acc[4 * e + 3] += f * v[q][e].w;
+      }
+    }
+  }
+  const int token = row / p.group, head = job.y * p.group + row - token * p.group;
+  const float f = sum == 0.0f ? 0.0f : (has_scale ? p.v_scale[job.y] : 1.0f) / sum;
+  uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(start) + token) * p.ldo +
+                                        static_cast<int64_t>(head) * D + blockIdx.y * 16);
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    dst[e] = make_uint4(pack_bf16(acc[8 * e] * f, acc[8 * e + 1] * f), pack_bf16(acc[8 * e + 2] * f, acc[8 * e + 3] * f),
+                        pack_bf16(acc[8 * e + 4] * f, acc[8 * e + 5] * f),
+                        pack_bf16(acc[8 * e + 6] * f, acc[8 * e + 7] * f));
+  if (blockIdx.y == 0 && p.lse != nullptr)
+    p.lse[(static_cast<int64_t>(start) + token) * p.heads + head] =
+        sum == 0.0f ? -kInf : (top + log2f(sum)) * 0.69314718055994530942f;
+}
+
+template <int D, bool kFp8>
+qerl_status launch(const TreeParams& p, int grid, int dev, cudaStream_t s) {
+  using S = Shape<D, kFp8>;
+  static std::atomic<uint64_t> ready{0};  // one bit per device: the attribute belongs to the device's function
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if ((ready.load() & bit) == 0) {
+    if (cudaFuncSetAttribute(tree_kernel<D, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) !=
+        cudaSuccess)
+      return QERL_ERR_CUDA;
+    ready.fetch_or(bit);
+  }
+  if (launch_dependent(tree_kernel<D, kFp8>, dim3(static_cast<unsigned>(grid)), kThreads, S::kSmem, s, p) != cudaSuccess)
+    return QERL_ERR_CUDA;
+  return cuda_status(launch_dependent(join_kernel<D>, dim3(static_cast<unsigned>(grid), D / 16), kBlock, 0, s, p,
+                                      static_cast<int>(kFp8 && p.v_scale != nullptr)));
+}
+
+// Rows of a partial: no segment has more.
+int slot_rows(int64_t tokens, int group) {
+  return static_cast<int>(std::min<int64_t>(kBlock, (tokens * group + 31) / 32 * 32));
+}
+
+}  // namespace
+
+size_t tree_attention_workspace_bytes(int64_t tokens, int num_heads, int num_kv_heads, int head_dim) {
+  const size_t slot = slot_floats(slot_rows(tokens, num_heads / num_kv_heads), head_dim) * sizeof(float);
+  return kWsHeaderBytes + align_up(kMaxCtas * sizeof(int4), 256) + 2 * kMaxCtas * slot;
+}
+
+qerl_status launch_tree_attention(const TreeAttentionArgs& a, cudaStream_t s) {
+  const qerl_kv_cache& c = *a.cache;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return QERL_ERR_CUDA;
+  TreeParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.k = static_cast<const __nv_bfloat16*>(a.k);
+  p.v = static_cast<const __nv_bfloat16*>(a.v);
+  p.ldq = a.ldq;
+  p.ldk = a.ldk;
+  p.ldv = a.ldv;
+  p.kp = static_cast<const uint8_t*>(c.k);
+  p.vp = static_cast<const uint8_t*>(c.v);
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.table = c.page_table;
+  p.ld_table = c.ld_table;
+  p.num_pages = c.num_pages;
+  p.page_size = c.page_size;
+  p.page_shift = (c.page_size & (c.page_size - 1)) == 0 ? __builtin_ctz(c.page_size) : -1;
+  p.capacity = c.max_pages * c.page_size;
+  p.cu = a.cu_tokens;
+  p.lengths = a.lengths;
+  p.mask = reinterpret_cast<const unsigned long long*>(a.mask);
+  p.words = a.mask_words;
+  p.num_seqs = static_cast<int>(c.num_seqs);
+  p.tokens = static_cast<int>(a.tokens);
+  p.heads = a.num_heads;
+  p.kv_heads = c.num_kv_heads;
+  p.group = a.num_heads / c.num_kv_heads;
+  p.scale_log2 = a.scale * 1.44269504088896340736f;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.ldo = a.ldo;
+  p.lse = a.lse;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.status = &reinterpret_cast<WsHeader*>(ws)->status;
+  p.jobs = reinterpret_cast<int4*>(ws + kWsHeaderBytes);
+  p.part = reinterpret_cast<float*>(ws + kWsHeaderBytes + align_up(kMaxCtas * sizeof(int4), 256));
+  p.slot_rows = slot_rows(a.tokens, p.group);
+  const int grid = std::min(sms, kMaxCtas);
+  if (c.head_dim == 128)
+    return c.dtype == QERL_E4M3 ? launch<128, true>(p, grid, dev, s) : launch<128, false>(p, grid, dev, s);
+  return c.dtype == QERL_E4M3 ? launch<64, true>(p, grid, dev, s) : launch<64, false>(p, grid, dev, s);
+}
+
+}  // namespace qerl
+
+#ifdef QERL_TEST_HOOKS
+// Test-only build: this file's wait limit, and one arrival too many expected on
+// the barriers that announce the first half of a tile's weights.
+extern "C" QERL_API int qerl_test_set_tree_hooks(long long wait_limit_cycles, int extra_arrival) {
+  if (cudaMemcpyToSymbol(qerl::g_test_wait_limit, &wait_limit_cycles, sizeof(wait_limit_cycles)) != cudaSuccess)
+    return 1;
+  return cudaMemcpyToSymbol(qerl::g_test_extra_arrival, &extra_arrival, sizeof(extra_arrival)) != cudaSuccess ? 1 : 0;
+}
+#endif
