@@ -22,10 +22,10 @@
 //                   128 scores from tensor memory, keeps the reference m and
 //                   the sum l in registers and writes the weights back as bf16
 //                   over the scores; then the tile's outputs
-//   warps 8-11      loads: q, then k, v tiles through a ring.  Pages may be of
-//                   any size, so rows are gathered with cp.async; bytes of an
-//                   E4M3 cache pass through a ring of their own and are
-//                   widened to bf16 on the way (exact)
+//   warps 8-11      loads: q and k, v tiles through a ring.  Pages may be of any
+//                   size, so rows are gathered with cp.async; bytes of an E4M3
+//                   cache pass through a ring of their own and are widened to
+//                   bf16 on the way (exact)
 //   warps 12, 13    issue S_i = Q_i K^T and O_i += P_i V of tile 0, tile 1
 //   warp 14         finds the CTA's next items
 // Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each).
@@ -101,7 +101,9 @@ struct Shape {
   static constexpr uint32_t kRawTile = kRows * D;
   static constexpr uint32_t kRing = 2 * kTile;
   static constexpr uint32_t kRawRing = kRing + kSlots * kTile;
-  static constexpr uint32_t kBars = kRawRing + kRaw * kRawTile;
+  // (m, l) of shared rows, 1 KB a query tile, behind the outputs in the second buffer of the queries if they fit.
+  static constexpr uint32_t kMl = kTile >= 18432 ? kTile + 16384 : kRawRing + kRaw * kRawTile;
+  static constexpr uint32_t kBars = kRawRing + kRaw * kRawTile + (kTile >= 18432 ? 0 : 2048);
   static constexpr uint32_t kSmem = 1024 + kBars + 768;
 };
 
@@ -232,6 +234,12 @@ __device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& lo, uint32_
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(0x7B807B80u));
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(0x7B807B80u));
 }
+// The barrier takes this thread's arrival when its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // NaN where a byte of w is E4M3's NaN.
 __device__ __forceinline__ void nan_bytes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if ((w & 0x7Fu) == 0x7Fu) lo = (lo & 0xFFFF0000u) | 0x7FFFu;
@@ -308,8 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   auto p_full = [&](int i, int part) { return misc + 8u * (2 + 2 * i + part); };
   auto o_full = [&](int i) { return misc + 8u * (6 + i); };
   auto turn = [&](int i) { return misc + 8u * (8 + i); };
-  auto q_full = [&](int i) { return misc + 8u * (10 + i); };
-  auto q_empty = [&](int i) { return misc + 8u * (12 + i); };
+  const uint32_t q_full = misc + 8u * 10;
+  const uint32_t q_free = misc + 8u * 11;    // the last scores are computed
+  auto out_free = [&](int e) { return misc + 8u * (12 + e); };  // the outputs of an even, odd item have left
   auto ml_full = [&](int i) { return misc + 8u * (14 + i); };
   auto ml_empty = [&](int i) { return misc + 8u * (16 + i); };
   auto item_full = [&](int e) { return misc + 8u * (18 + e); };
@@ -323,10 +332,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   volatile long long* sums = reinterpret_cast<volatile long long*>(misc_gen + 8 * 38);  // [16], then the place found
   volatile int* place = reinterpret_cast<volatile int*>(misc_gen + 8 * 54);       // sequence, bad offsets
   volatile long long* inside_seq = reinterpret_cast<volatile long long*>(misc_gen + 8 * 55);
+  volatile unsigned* begun = reinterpret_cast<volatile unsigned*>(misc_gen + 8 * 56);
+  // Waits for a load of the ring: the u-th by its slot and phase, the `count`-th
+  // of all (modulo 2^32).  A barrier's phase is only told from the one before,
+  // and where the tiles take turns at the ring an issuer does not look at every
+  // load: so first that the slot was given to this load, then that it is there.
+  auto wait_load = [&](unsigned u, unsigned count) -> bool {
+    if (static_cast<int>(*begun - count) <= 0) {
+      const long long t0 = clock64();
+      for (unsigned n = 1; static_cast<int>(*begun - count) <= 0; ++n) {
+        if ((n & 255u) != 0) continue;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > QERL_WAIT_LIMIT) {
+          *abort_flag = 1;
+          record_error(p.status, QERL_ERR_TIMEOUT);
+          return false;
+        }
+      }
+    }
+    return mbar_wait_a(full(u % S::kSlots), (u / S::kSlots) & 1, abort_flag, p.status);
+  };
 
   if (threadIdx.x == 0) {
     for (unsigned s = 0; s < S::kSlots; ++s) {
-      mbar_init_a(full(s), 4);
+      mbar_init_a(full(s), 128);
       mbar_init_a(empty(s), 2);
     }
     for (int i = 0; i < 2; ++i) {
@@ -339,13 +368,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       mbar_init_a(p_full(i, 1), 4);
       mbar_init_a(o_full(i), 1);
       mbar_init_a(turn(i), 1);
-      mbar_init_a(q_full(i), 4);
-      mbar_init_a(q_empty(i), 4);
       mbar_init_a(ml_full(i), 4);
       mbar_init_a(ml_empty(i), 4);
       mbar_init_a(item_full(i), 1);
       mbar_init_a(item_empty(i), 14);  // 8 softmax warps, 4 of the loads and 2 issuers
     }
+    mbar_init_a(q_full, 128);
+    mbar_init_a(q_free, 2);
+    mbar_init_a(out_free(0), 8);
+    mbar_init_a(out_free(1), 8);
+    *begun = 0;
     mbar_init_a(done, 2);
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) dirty[i] = 0;
@@ -390,51 +422,84 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     return w;
   };
   Sequence sq;
-  long long mine = 0, first_cost = 0;
-  for (int b = threadIdx.x; b < p.num_seqs; b += kThreads) {
+  long long total = 0, begin = 0, end = 0, each = 0, extra = 0, inside = 0;
+  int seq = 0;
+  bool busy = false;
+  auto stretch = [&](long long c) -> long long { return each * c + (c < extra ? c : extra); };
+  // Even stretches; a tile belongs to the stretch in which its place lies.
+  auto divide = [&]() {
+    const long long ctas = total < gridDim.x ? total : gridDim.x;
+    each = ctas > 0 ? quotient(total, ctas) : 0;
+    extra = total - each * ctas;  // the first `extra` are one longer
+    busy = blockIdx.x < ctas;
+    begin = stretch(blockIdx.x);
+    end = stretch(blockIdx.x + 1);
+  };
+  // One sequence that breaks the rules leaves nothing to do: the offsets around
+  // it may lie before those of other sequences, and two CTAs would then write
+  // the same rows.
+  auto cost_of = [&](int b, bool& bad) -> long long {
     const bool fine = sequence(p, b, sq);
-    // One sequence that breaks the rules leaves nothing to do: the offsets
-    // around it may lie before those of other sequences, and two CTAs would
-    // then write the same rows.
-    if (!fine) place[1] = 1;
-    const long long c = fine ? sq.cost(p) : 0;
-    if (b == threadIdx.x) first_cost = c;
-    mine += c;
     const int len = p.lengths[b];
     if (!fine || len < 0 || len > p.capacity || (p.mask != nullptr && sq.n > static_cast<int64_t>(p.words) * 64))
       record_error(p.status, QERL_ERR_RANGE);
-  }
-  long long incl = scan(mine);
-  const long long total = place[1] ? 0 : total_of();
-  // Even stretches; a tile belongs to the stretch in which its place lies.
-  const long long ctas = total < gridDim.x ? total : gridDim.x;
-  const long long each = ctas > 0 ? quotient(total, ctas) : 0, extra = total - each * ctas;  // the first `extra` are one longer
-  auto stretch = [&](long long c) -> long long { return each * c + (c < extra ? c : extra); };
-  const bool busy = blockIdx.x < ctas;
-  const long long begin = busy ? stretch(blockIdx.x) : 0, end = busy ? stretch(blockIdx.x + 1) : 0;
-  if (p.num_seqs <= kThreads) {
-    if (busy && incl - mine <= begin && begin < incl) {
-      place[0] = threadIdx.x;
-      *inside_seq = begin - (incl - mine);
-    }
-  } else if (busy) {
-    long long base = 0;
-    for (int b0 = 0;; b0 += kThreads) {  // ends: begin < total, the sum of all
-      const int b = b0 + threadIdx.x;
-      mine = b0 == 0 ? first_cost : b < p.num_seqs && sequence(p, b, sq) ? sq.cost(p) : 0;
-      incl = scan(mine) + base;
-      const long long next = base + total_of();
-      if (begin < next) {
-        if (incl - mine <= begin && begin < incl) {
-          place[0] = b;
-          *inside_seq = begin - (incl - mine);
-        }
-        break;
+    bad |= !fine;
+    return fine ? sq.cost(p) : 0;
+  };
+  if (p.num_seqs <= 32) {  // the warp that finds the items alone, without a barrier
+    if (warp == 14) {
+      bool bad = false;
+      const long long mine = lane < p.num_seqs ? cost_of(lane, bad) : 0;
+      long long incl = mine;
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) {
+        const long long up = __shfl_up_sync(~0u, incl, i);
+        if (lane >= i) incl += up;
       }
-      base = next;
+      total = __any_sync(~0u, bad) ? 0 : __shfl_sync(~0u, incl, 31);
+      divide();
+      const unsigned hit = __ballot_sync(~0u, incl - mine <= begin && begin < incl);
+      seq = hit != 0 ? __ffs(hit) - 1 : 0;
+      inside = begin - __shfl_sync(~0u, incl - mine, seq);
     }
+  } else {
+    bool bad = false;
+    long long mine = 0, first_cost = 0;
+    for (int b = threadIdx.x; b < p.num_seqs; b += kThreads) {
+      const long long c = cost_of(b, bad);
+      if (b == threadIdx.x) first_cost = c;
+      mine += c;
+    }
+    if (bad) place[1] = 1;
+    long long incl = scan(mine);
+    total = place[1] ? 0 : total_of();
+    divide();
+    if (p.num_seqs <= kThreads) {
+      if (busy && incl - mine <= begin && begin < incl) {
+        place[0] = threadIdx.x;
+        *inside_seq = begin - (incl - mine);
+      }
+    } else if (busy) {
+      long long base = 0;
+      for (int b0 = 0;; b0 += kThreads) {  // ends: begin < total, the sum of all
+        const int b = b0 + threadIdx.x;
+        mine = b0 == 0 ? first_cost : b < p.num_seqs && sequence(p, b, sq) ? sq.cost(p) : 0;
+        incl = scan(mine) + base;
+        const long long next = base + total_of();
+        if (begin < next) {
+          if (incl - mine <= begin && begin < incl) {
+            place[0] = b;
+            *inside_seq = begin - (incl - mine);
+          }
+          break;
+        }
+        base = next;
+      }
+    }
+    __syncthreads();
+    seq = place[0];
+    inside = *inside_seq;
   }
-  __syncthreads();
 
   struct Work {
     Item it;
@@ -466,12 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     const int r = (warp & 3) * 32 + lane;  // row of the tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_t = tmem + lanes + i * 128, o_t = tmem + lanes + 256 + i * D, o_other = tmem + lanes + 256 + (1 - i) * D;
-    const uint32_t own_q = sbase + i * S::kTile, other_q = sbase + (1 - i) * S::kTile;
-    constexpr uint32_t kMl = 8192;  // of a query tile's buffer when its products are done: outputs, then (m, l)
     bool ok = true;
     // Of this query tile; loads of the ring before this item, of which only the
     // slot and the phase are used (modulo two laps: a CTA may see more than 2^32).
-    unsigned tiles_done = 0, u0 = 0;
+    unsigned tiles_done = 0, u0 = 0, count0 = 0;  // (count0: the loads before this item, modulo 2^32)
     int outputs_done = 0, exchanges = 0;
     Work w;
     for (int k = 0; ok && take(k, w); ++k) {
@@ -501,11 +564,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const unsigned long long m = p.mask[static_cast<int64_t>(w.it.start + token) * p.words + word];
         return static_cast<uint32_t>(m >> (at & 32)) & below(w.it.n - at);
       };
-      // The values of a tile of new tokens (load u of the ring), looked through
+      // The values of a tile of new tokens, looked through
       // for elements that are not finite; a thread takes one token's row.
-      auto clean_values = [&](unsigned u) -> bool {
-        const unsigned s = u % S::kSlots;
-        if (!__all_sync(~0u, mbar_wait_a(full(s), (u / S::kSlots) & 1, abort_flag, p.status))) return false;
+      auto clean_values = [&](unsigned u) -> bool {  // the u-th load of the item
+        if (!__all_sync(~0u, wait_load(u0 + u, count0 + u))) return false;
+        const unsigned s = (u0 + u) % S::kSlots;
         const uint32_t at_row = sbase + S::kRing + s * S::kTile + r * 128;
         // x * 0 + sum is NaN from the first x that is not finite
         uint32_t sum = 0;
@@ -620,28 +683,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           for (int q = 0; q < 4; ++q) keep[q] = sees(t, q);
         }
         ok = __all_sync(~0u, mbar_wait_a(s_full(i), (tiles_done + j) & 1, abort_flag, p.status));
-        // (after the scores: with the keys in place, and the loads before them,
-        // the values' barrier is in this phase or the one before)
-        if (ok && fresh) ok = clean_values(u0 + 2 * (t - w.it.t0) + 1);
+        if (ok && fresh) ok = clean_values(2 * (t - w.it.t0) + 1);
         if (!ok) break;
         tc_fence_after();
         step(j, masked, fresh, keep);
       }
       tiles_done += mine_n;
       u0 = (u0 + 2 * (w.it.t1 - w.it.t0)) % (2 * S::kSlots);
-      // The query tile's buffer is free: its products are done (or, without any, its rows have landed).
+      count0 += 2 * (w.it.t1 - w.it.t0);
       if (mine_n > 0) {
         ok = __all_sync(~0u, ok && mbar_wait_a(o_full(i), outputs_done & 1, abort_flag, p.status));
         ++outputs_done;
-      } else {
-        ok = __all_sync(~0u, ok && mbar_wait_a(q_full(i), k & 1, abort_flag, p.status));
       }
       if (!ok) break;
       tc_fence_after();
       float f_own = 1.0f, f_other = 0.0f;
       const bool both = w.shared && w.count(1) > 0;
       if (both) {
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(own_q + kMl + r * 8), "f"(mc), "f"(l) : "memory");
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sbase + S::kMl + i * 1024 + r * 8), "f"(mc), "f"(l) : "memory");
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_a(ml_full(i));
@@ -649,7 +708,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (!ok) break;
         tc_fence_after();
         float m2, l2;
-        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(m2), "=f"(l2) : "r"(other_q + kMl + r * 8) : "memory");
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(m2), "=f"(l2)
+                     : "r"(sbase + S::kMl + (1 - i) * 1024 + r * 8)
+                     : "memory");
         const float top = fmaxf(mc, m2);
         f_own = weight_of(mc, top);
         f_other = weight_of(m2, top);
@@ -665,7 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const int slot_row = row - w.it.row0;
       // Shared rows: each tile's warps take half of the columns, tile 0's all of them if tile 1 had no keys.
       const int c0 = both && i == 1 ? D / 2 : 0, c1 = both ? c0 + D / 2 : w.shared && i == 1 ? 0 : D;
-      const uint32_t stage = own_q + (warp & 3) * 2048;
+      // Outputs pass through the tile's own queries, or through the buffer that shared rows leave free.
+      const uint32_t stage = sbase + (w.shared ? S::kTile + i * 8192 : i * S::kTile) + (warp & 3) * 2048;
       const int head0 = w.it.kv_head * p.group;
 #pragma unroll 1
       for (int col = c0; col < c1; col += 32) {
@@ -748,36 +811,39 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_a(q_empty(i));
+      if (lane == 0) mbar_arrive_a(out_free(k & 1));
     }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-    // Each warp brings 32 rows of every tile; a barrier takes one arrival of each.
+    // Each warp brings 32 rows of every tile; a barrier takes an arrival of every
+    // thread, which comes by itself when the thread's copies have landed.
     const int lw = warp - 8;
-    unsigned issued = 0, told = 0;  // loads of the ring: begun, announced
+    unsigned told = 0;         // loads that were given a slot, but for laps dropped
+    unsigned slots_given = 0;  // all of them (modulo 2^32)
     unsigned raw_begun = 0, raw_done = 0;
     bool ok = true;
-    auto arrive = [&](uint32_t bar) {
-      fence_proxy_async_smem();  // each thread's writes, before the tensor core reads them
-      __syncwarp();
-      if (lane == 0) mbar_arrive_a(bar);
-    };
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
       return __all_sync(~0u, mbar_wait_a(bar, parity, abort_flag, p.status));
     };
-    auto wait_free = [&](unsigned u) -> bool {  // the slot of load u
-      return u < S::kSlots || wait(empty(u % S::kSlots), ((u / S::kSlots) & 1) ^ 1);
+    auto passed = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(~0u, mbar_test_wait_a(bar, parity)); };
+    auto next_slot = [&]() -> bool {  // waits for the slot of load `told`
+      if (told >= S::kSlots && !wait(empty(told % S::kSlots), ((told / S::kSlots) & 1) ^ 1)) return false;
+      ++slots_given;
+      if (lw == 0 && lane == 0) *begun = slots_given;
+      return true;
     };
     // 16-byte chunks of this warp's 32 rows of a tile of bf16 rows (lane x's row at src; null: zeros).
     auto copy_rows = [&](uint32_t tile_at, const void* src) {
       constexpr int kChunks = D / 8;
-#pragma unroll
+      const int ch = lane % kChunks;
+      const uint32_t to = tile_at + (ch >> 3) * kPanel;
+#pragma unroll 4
       for (int q = 0; q < kChunks; ++q) {
-        const int at = (q * 32 + lane) / kChunks, ch = lane % kChunks, row = lw * 32 + at;
+        const int at = (q * 32 + lane) / kChunks, row = lw * 32 + at;
         const uint8_t* from =
             reinterpret_cast<const uint8_t*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(src), at));
         const bool real = from != nullptr;
-        cp_async_16(tile_at + (ch >> 3) * kPanel + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+        cp_async_16(to + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
                     real ? from + ch * 16 : reinterpret_cast<const uint8_t*>(p.q), real ? 16 : 0);
       }
     };
@@ -787,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       return sbase + S::kRawRing + (u % (kFp8 ? S::kRaw : 1)) * S::kRawTile + (q * 128 + lw * 32 + lane) * 16;
     };
     auto copy_raw = [&](unsigned u, const void* src) {
-#pragma unroll
+#pragma unroll 4
       for (int q = 0; q < kRawChunks; ++q) {
         const int at = (q * 32 + lane) / kRawChunks, ch = lane % kRawChunks;
         const uint8_t* from =
@@ -797,53 +863,60 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       }
     };
     auto widen = [&]() -> bool {  // the oldest raw tile, which has landed, into its slot
-      if (!wait_free(told)) return false;
-      const uint32_t tile_at = sbase + S::kRing + (told % S::kSlots) * S::kTile;
+      if (!next_slot()) return false;
+      const int ch = 2 * (lane % kRawChunks);
+      const uint32_t to = sbase + S::kRing + (told % S::kSlots) * S::kTile + (ch >> 3) * kPanel;
 #pragma unroll
-      for (int q = 0; q < kRawChunks; ++q) {
-        const uint4 x = lds128(raw_at(raw_done, q));
-        const int ch = 2 * (lane % kRawChunks), row = lw * 32 + (q * 32 + lane) / kRawChunks;
-        const uint32_t a[4] = {x.x, x.y, x.z, x.w};
-        uint32_t y[8];
+      for (int q0 = 0; q0 < kRawChunks; q0 += 4) {  // four chunks at a time, for their latencies
+        uint32_t x[4][4];
         uint32_t nan = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          e4m3x4_to_bf16(a[e], y[2 * e], y[2 * e + 1]);
-          nan |= (a[e] & 0x7F7F7F7Fu) + 0x01010101u;
+        for (int q = 0; q < 4; ++q) {
+          const uint4 v = lds128(raw_at(raw_done, q0 + q));
+          x[q][0] = v.x;
+          x[q][1] = v.y;
+          x[q][2] = v.z;
+          x[q][3] = v.w;
         }
-        if (nan & 0x80808080u) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) nan_bytes_to_bf16(a[e], y[2 * e], y[2 * e + 1]);
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) nan |= (x[q][e] & 0x7F7F7F7Fu) + 0x01010101u;
+        nan &= 0x80808080u;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = lw * 32 + ((q0 + q) * 32 + lane) / kRawChunks;
+          uint32_t y[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) e4m3x4_to_bf16(x[q][e], y[2 * e], y[2 * e + 1]);
+          if (nan) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) nan_bytes_to_bf16(x[q][e], y[2 * e], y[2 * e + 1]);
+          }
+          sts128(to + row * 128 + (((ch & 7) ^ (row & 7)) << 4), make_uint4(y[0], y[1], y[2], y[3]));
+          sts128(to + row * 128 + ((((ch & 7) + 1) ^ (row & 7)) << 4), make_uint4(y[4], y[5], y[6], y[7]));
         }
-        const uint32_t to = tile_at + (ch >> 3) * kPanel + row * 128;
-        sts128(to + (((ch & 7) ^ (row & 7)) << 4), make_uint4(y[0], y[1], y[2], y[3]));
-        sts128(to + ((((ch + 1) & 7) ^ (row & 7)) << 4), make_uint4(y[4], y[5], y[6], y[7]));
       }
-      arrive(full(told % S::kSlots));
+      mbar_arrive_a(full(told % S::kSlots));
       ++told;
       ++raw_done;
       return true;
     };
-    // Everything begun is announced.  Called before any wait for the others:
-    // what they need to go on is then there.
+    // No raw tile is kept back.  Called before any wait for the others, who may need them to go on.
     auto settle = [&]() -> bool {
+      if (!kFp8) return true;
       cp_async_wait_group<0>();
-      if (kFp8) {
-        while (raw_done != raw_begun)
-          if (!widen()) return false;
-      } else {
-        for (; told != issued; ++told) arrive(full(told % S::kSlots));
-      }
+      while (raw_done != raw_begun)
+        if (!widen()) return false;
       return true;
     };
     // Only slots, phases and whether the first lap is over are used: two to four laps stay.
     auto drop_laps = [&]() {
-      if (told < 4 * S::kSlots) return;
-      const unsigned laps = (told / (2 * S::kSlots) - 1) * (2 * S::kSlots);
-      told -= laps;
-      issued -= laps;
+      if (told >= 4 * S::kSlots) told -= (told / (2 * S::kSlots) - 1) * (2 * S::kSlots);
     };
-    constexpr unsigned kAhead = kFp8 ? S::kRaw - 1 : S::kSlots - 2;  // loads in flight
+    // The loads of an item that may begin before its queries are there: nothing gives their slots back without them.
+    constexpr int kFirst = S::kSlots >= 4 ? 4 : 2;
+    bool shared_before = false;
     Work w;
     for (int k = 0; ok && take(k, w); ++k) {
       const Item& it = w.it;
@@ -872,13 +945,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           src_v = p.v + (static_cast<int64_t>(it.start) + node) * p.ldv + it.kv_head * D;
         }
       };
-      auto load_queries = [&]() {
-        // (the buffers come free with the outputs of the item before)
-        for (int i = 0; ok && i < 2; ++i) {
-          if (k > 0 && !__all_sync(~0u, mbar_try_wait_a(q_empty(i), (k - 1) & 1)))
-            ok = settle() && wait(q_empty(i), (k - 1) & 1);
-          if (!ok) break;
-          const int row = it.row0 + (w.shared ? 0 : i * kRows) + lw * 32 + lane;
+      // The buffers of the queries.  Rows that both query tiles share lie in the
+      // first, free with the last scores of the item before if that was such a
+      // one too; outputs pass through the second, or through both.  (The item
+      // before the last is always waited for, so that no barrier is a phase
+      // further than the one asked for.)
+      const bool with_scores = w.shared && shared_before;
+      shared_before = w.shared;
+      auto load_queries = [&](bool block) -> bool {
+        if (k >= 2 && !passed(out_free(k & 1), ((k >> 1) & 1) ^ 1)) {
+          if (!block) return false;
+          ok = settle() && wait(out_free(k & 1), ((k >> 1) & 1) ^ 1);
+        }
+        if (ok && k >= 1) {
+          const uint32_t bar = with_scores ? q_free : out_free((k - 1) & 1);
+          const uint32_t parity = (with_scores ? k - 1 : (k - 1) >> 1) & 1;
+          if (!passed(bar, parity)) {
+            if (!block) return false;
+            ok = settle() && wait(bar, parity);
+          }
+        }
+        if (!ok) return true;
+#pragma unroll 1
+        for (int i = 0; i < (w.shared ? 1 : 2); ++i) {
+          const int row = it.row0 + i * kRows + lw * 32 + lane;
           const void* src = nullptr;
           if (row < it.n * p.group) {
             const int token = row / p.group;
@@ -887,58 +977,45 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           }
           copy_rows(sbase + i * S::kTile, src);
         }
-        cp_async_commit();
-        ok = ok && settle();
-        if (ok)
-          for (int i = 0; i < 2; ++i) arrive(q_full(i));
+        cp_async_arrive(q_full);
+        return true;
       };
       drop_laps();
       look_up(it.t0);
       bool asked = false;  // for the queries
-      for (int t = it.t0; ok && t < it.t1; ++t) {
-        const void* tile_src[2] = {src_k, src_v};
+      const void* src_next = nullptr;
+#pragma unroll 1
+      for (int u = 0; ok && u < 2 * (it.t1 - it.t0); ++u) {
+        if (u >= 1 && !asked) asked = load_queries(u == kFirst);
+        if (!ok) break;
+        const int t = it.t0 + (u >> 1);
         const bool direct = !kFp8 || t >= w.ctx;  // bf16 rows
-        if (kFp8 && direct) ok = settle();
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {  // k, then v
+        const void* src = u & 1 ? src_next : src_k;
+        if ((u & 1) == 0) {
+          src_next = src_v;
+          if (kFp8 && direct) ok = settle();
+        }
+        if (!ok) break;
+        if (direct) {
+          ok = next_slot();
           if (!ok) break;
-          if (direct) {
-            if (issued >= S::kSlots &&
-                !__all_sync(~0u, mbar_try_wait_a(empty(issued % S::kSlots), ((issued / S::kSlots) & 1) ^ 1)))
-              ok = settle() && wait_free(issued);
-            if (!ok) break;
-            copy_rows(sbase + S::kRing + (issued % S::kSlots) * S::kTile, tile_src[part]);
-          } else {
-            copy_raw(raw_begun++, tile_src[part]);
-          }
-          ++issued;
+          copy_rows(sbase + S::kRing + (told % S::kSlots) * S::kTile, src);
+          cp_async_arrive(full(told % S::kSlots));
+          ++told;
+        } else {
+          copy_raw(raw_begun++, src);
           cp_async_commit();
-          if (part == 0) look_up(t + 1);
-          if (kFp8) {
-            if (!direct && raw_begun - raw_done == kAhead + 1) {
-              cp_async_wait_group<kAhead>();
-              ok = widen();
-            }
-          } else if (issued - told == kAhead + 1) {
-            cp_async_wait_group<kAhead>();
-            arrive(full(told % S::kSlots));
-            ++told;
+          if (raw_begun - raw_done == S::kRaw) {
+            cp_async_wait_group<(kFp8 ? static_cast<int>(S::kRaw) - 1 : 0)>();
+            ok = widen();
           }
         }
-        if (kFp8 && direct && ok) {
-          cp_async_wait_group<0>();
-          for (; told != issued; ++told) arrive(full(told % S::kSlots));
-        }
-        // The queries after the first keys and values are on their way, of which
-        // no more may be announced without them than there are slots.
-        if (ok && !asked && (t + 1 == it.t1 || t - it.t0 == (S::kSlots >= 4 ? 1 : 0))) {
-          asked = true;
-          load_queries();
-        }
+        if ((u & 1) == 0) look_up(t + 1);
       }
+      if (ok && !asked) load_queries(true);
     }
     if (ok) settle();
-    cp_async_wait_group<0>();  // every copy lands before the CTA exits
+    cp_async_wait_all();  // every copy lands before the CTA exits
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp < 14) {
@@ -948,31 +1025,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const uint32_t id_s = idesc_bf16_f32(128, 128);
       const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // v: rows along the contraction
       auto slot = [&](unsigned u) { return sbase + S::kRing + (u % S::kSlots) * S::kTile; };
-      auto wait_slot = [&](unsigned u) {
-        return mbar_wait_a(full(u % S::kSlots), (u / S::kSlots) & 1, abort_flag, p.status);
-      };
       // A slot is free after two arrivals: one of each issuer where both use it,
       // or both of the one that does.
       auto release = [&](unsigned u, bool alone) {
         commit(leader, empty(u % S::kSlots));
         if (alone && leader) mbar_arrive_a(empty(u % S::kSlots));
       };
-      unsigned u0 = 0, tiles_done = 0, turns = 0;
+      unsigned u0 = 0, count0 = 0, tiles_done = 0, turns = 0;
       bool ok = true, first_turn = i == 0;  // of tile 0: nobody hands it over
       Work w;
       for (int k = 0; ok && take(k, w); ++k) {
         const int n = w.count(i);
-        // Of every item, with or without tiles of this one: a barrier's phase is
-        // only told from the one before, and with the queries all loads of the
-        // items before are announced, so the slots' phases are no further off.
-        ok = __all_sync(~0u, mbar_wait_a(q_full(i), k & 1, abort_flag, p.status));
+        // Of every item, with or without tiles of this one: a barrier's phase is only told from the one before.
+        ok = __all_sync(~0u, mbar_wait_a(q_full, k & 1, abort_flag, p.status));
         if (!ok) break;
-        if (n > 0) {
+        if (n == 0) {
+          if (leader) mbar_arrive_a(q_free);
+        } else {
           const float ks = kFp8 && p.k_scale != nullptr ? p.k_scale[w.it.kv_head] : 1.0f;
-          auto load_of = [&](int j) { return u0 + 2 * (w.tile(i, j) - w.it.t0); };
+          auto load_of = [&](int j) { return static_cast<unsigned>(2 * (w.tile(i, j) - w.it.t0)); };
+          auto wait_slot = [&](unsigned u) { return wait_load(u0 + u, count0 + u); };
           auto scores = [&](int j) {
-            const unsigned u = load_of(j);
-            const uint32_t qa = sbase + i * S::kTile, ka = slot(u);
+            const unsigned u = u0 + load_of(j);
+            const uint32_t qa = sbase + (w.shared ? 0 : i * S::kTile), ka = slot(u);
             // a negative factor of the scores: the product is negated
             const bool negative = p.scale_log2 < 0.0f != (w.tile(i, j) < w.ctx && ks < 0.0f);
             const uint32_t id = id_s | (negative ? 1u << 13 : 0u);
@@ -984,6 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                        sw128_kmajor_desc(ka + d * kPanel + kk * 32), id, d + kk > 0 ? 1u : 0u);
             commit(leader, s_full(i));
             release(u, w.shared);
+            if (j + 1 == n) commit(leader, q_free);
           };
           auto values = [&](unsigned u, int part, bool more) {
             const uint32_t va = slot(u);
@@ -994,11 +1070,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           };
           ok = __all_sync(~0u, wait_slot(load_of(0)));
           if (!ok) break;
+          // (the loads are ordinary writes of other threads, seen here through the barrier)
+          fence_proxy_async_smem();
           tc_fence_after();
           scores(0);
           for (int j = 0; j < n; ++j) {
-            const unsigned u = load_of(j) + 1;
-            ok = wait_slot(u);
+            const unsigned u = u0 + load_of(j) + 1;
+            ok = wait_slot(load_of(j) + 1);
             if (!w.shared) {
               // Turns, as the two tiles would fall into step: both in the softmax, then both at the tensor core.
               ok = ok && (j + 1 >= n || wait_slot(load_of(j + 1)));
@@ -1008,6 +1086,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             }
             ok = __all_sync(~0u, ok && mbar_wait_a(p_full(i, 0), (tiles_done + j) & 1, abort_flag, p.status));
             if (!ok) break;
+            fence_proxy_async_smem();
             tc_fence_after();
             values(u, 0, j > 0);
             ok = __all_sync(~0u, mbar_wait_a(p_full(i, 1), (tiles_done + j) & 1, abort_flag, p.status));
@@ -1019,6 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               if (w.shared) {
                 ok = __all_sync(~0u, wait_slot(load_of(j + 1)));
                 if (!ok) break;
+                fence_proxy_async_smem();
                 tc_fence_after();
               }
               scores(j + 1);
@@ -1030,6 +1110,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
         tiles_done += n;
         u0 = (u0 + 2 * (w.it.t1 - w.it.t0)) % (2 * S::kSlots);
+        count0 += 2 * (w.it.t1 - w.it.t0);
       }
       commit(leader, done);  // also after an expired wait: arrives once the issued MMAs are done
     } else if (warp == 14) {
@@ -1056,11 +1137,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       };
       bool go = busy;
       if (go) {
-        int b = place[0];
+        int b = seq;
         sequence(p, b, sq);
         const int wide = sq.tiles + kSegmentCost;
-        long long seg = quotient(*inside_seq, wide);
-        int t = static_cast<int>(*inside_seq - seg * wide);
+        long long seg = quotient(inside, wide);
+        int t = static_cast<int>(inside - seg * wide);
         int kv_head = static_cast<int>(quotient(seg, sq.blocks)), block = static_cast<int>(seg - static_cast<long long>(kv_head) * sq.blocks);
         for (long long pos = begin; go && pos < end;) {
           const long long base = pos - t;
