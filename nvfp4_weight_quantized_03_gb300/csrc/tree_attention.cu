@@ -77,6 +77,7 @@ struct TreeParams {
   const unsigned long long* mask;  // null: j <= t
   int words;
   int num_seqs, tokens, heads, kv_heads, group;
+  unsigned group_inverse;  // ceil(2^32 / group), 0 for a group of 1
   float scale_log2;
   __nv_bfloat16* out;
   int64_t ldo;
@@ -248,6 +249,21 @@ __device__ __forceinline__ void nan_bytes_to_bf16(uint32_t w, uint32_t& lo, uint
   if ((w & 0x7F000000u) == 0x7F000000u) hi = (hi & 0x0000FFFFu) | 0x7FFF0000u;
 }
 
+// mbar_wait_a in fewer instructions: this kernel waits in some thirty places, and
+// what runs once an item is fetched cold.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait_hint_a(bar, parity, QERL_WAIT_HINT_NS)) {
+    if (*abort_flag) return false;
+    if (clock64() - t0 > QERL_WAIT_LIMIT) {
+      *abort_flag = 1;
+      record_error(status, QERL_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
 // The scheduler is up to two items ahead, and an item may last as long as the
 // cache is long: it waits until another role gives up (or some 2000 s).
 __device__ __forceinline__ bool wait_patiently(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
@@ -292,10 +308,18 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return a / b;
 }
 
-// A piece of a segment: key tiles [t0, t1).
+// A piece of a segment: key tiles [t0, t1).  Its rows begin at row0 = token0 * group + head0.
 struct Item {
-  int start, n, len, seq, kv_head, row0, t0, t1, slot;  // slot -1: the whole segment
+  int start, n, len, seq, kv_head, row0, t0, t1, slot, token0, head0;  // slot -1: the whole segment
 };
+// Token and head (within the group) of row row0 + x of the sequence's, x < 256.
+// The product with the rounded inverse is exact for numerators below 2^32 / 1024.
+__device__ __forceinline__ int token_of(const TreeParams& p, const Item& it, int x, int& head) {
+  const unsigned n = it.head0 + x;
+  const int q = p.group_inverse == 0 ? n : __umulhi(n, p.group_inverse);
+  head = n - q * p.group;
+  return it.token0 + q;
+}
 constexpr int kItemInts = 12;
 
 template <int D, bool kFp8>
@@ -350,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
       }
     }
-    return mbar_wait_a(full(u % S::kSlots), (u / S::kSlots) & 1, abort_flag, p.status);
+    return wait_for(full(u % S::kSlots), (u / S::kSlots) & 1, abort_flag, p.status);
   };
 
   if (threadIdx.x == 0) {
@@ -515,9 +539,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   auto take = [&](int k, Work& w) -> bool {
     const int e = k & 1;
     // (a warp goes on or gives up as a whole, here and at every wait of a whole warp)
-    if (!__all_sync(~0u, mbar_wait_a(item_full(e), (k >> 1) & 1, abort_flag, p.status))) return false;
+    if (!__all_sync(~0u, wait_for(item_full(e), (k >> 1) & 1, abort_flag, p.status))) return false;
     const volatile int* it = items + e * kItemInts;
-    w.it = {it[0], it[1], it[2], it[3], it[4], it[5], it[6], it[7], it[8]};
+    w.it = {it[0], it[1], it[2], it[3], it[4], it[5], it[6], it[7], it[8], it[9], it[10]};
     w.shared = w.it.n * p.group - w.it.row0 <= kRows;
     w.ctx = w.it.len == 0 ? 0 : (w.it.len - 1) / kRows + 1;
     __syncwarp();
@@ -541,7 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const int mine_n = w.count(i);
       const int row = w.it.row0 + (w.shared ? 0 : i * kRows) + r;  // of the sequence's rows
       const int rows = w.it.n * p.group;
-      const int token = row < rows ? row / p.group : 0;
+      int row_head;
+      const int row_token = token_of(p, w.it, row - w.it.row0, row_head);
+      const int token = row < rows ? row_token : 0;
       float mc = -kInf, l = 0.0f;  // the reference in base-2 units and the sum of 2^(s - m)
       float v_scale = 1.0f, v_inverse = 1.0f, c_ctx = fabsf(p.scale_log2);
       if (kFp8) {
@@ -564,6 +590,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const unsigned long long m = p.mask[static_cast<int64_t>(w.it.start + token) * p.words + word];
         return static_cast<uint32_t>(m >> (at & 32)) & below(w.it.n - at);
       };
+      // The mask's words are on their way to the L1 cache during the tiles before.
+      if (p.mask != nullptr && row < rows)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.mask + (static_cast<int64_t>(w.it.start) + token) * p.words));
       // The values of a tile of new tokens, looked through
       // for elements that are not finite; a thread takes one token's row.
       auto clean_values = [&](unsigned u) -> bool {  // the u-th load of the item
@@ -682,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll
           for (int q = 0; q < 4; ++q) keep[q] = sees(t, q);
         }
-        ok = __all_sync(~0u, mbar_wait_a(s_full(i), (tiles_done + j) & 1, abort_flag, p.status));
+        ok = __all_sync(~0u, wait_for(s_full(i), (tiles_done + j) & 1, abort_flag, p.status));
         if (ok && fresh) ok = clean_values(2 * (t - w.it.t0) + 1);
         if (!ok) break;
         tc_fence_after();
@@ -692,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       u0 = (u0 + 2 * (w.it.t1 - w.it.t0)) % (2 * S::kSlots);
       count0 += 2 * (w.it.t1 - w.it.t0);
       if (mine_n > 0) {
-        ok = __all_sync(~0u, ok && mbar_wait_a(o_full(i), outputs_done & 1, abort_flag, p.status));
+        ok = __all_sync(~0u, ok && wait_for(o_full(i), outputs_done & 1, abort_flag, p.status));
         ++outputs_done;
       }
       if (!ok) break;
@@ -704,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_a(ml_full(i));
-        ok = __all_sync(~0u, mbar_wait_a(ml_full(1 - i), exchanges & 1, abort_flag, p.status));
+        ok = __all_sync(~0u, wait_for(ml_full(1 - i), exchanges & 1, abort_flag, p.status));
         if (!ok) break;
         tc_fence_after();
         float m2, l2;
@@ -777,11 +806,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const int at = q * 8 + (lane >> 2), ch = lane & 3;
             const uint4 y = lds128(stage + at * 64 + ((ch ^ ((at >> 1) & 3)) << 4));
             const int g = row - lane + at;
-            if (g < rows) {
-              const int tk = g / p.group;
+            int hd;
+            const int tk = token_of(p, w.it, g - w.it.row0, hd);
+            if (g < rows)
               *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(w.it.start) + tk) * p.ldo +
-                                        static_cast<int64_t>(head0 + g - tk * p.group) * D + col + ch * 8) = y;
-            }
+                                        static_cast<int64_t>(head0 + hd) * D + col + ch * 8) = y;
           }
           __syncwarp();
         } else if (live) {
@@ -796,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           __stcg(slot + static_cast<int64_t>(D) * p.slot_rows + slot_row, mc);
           __stcg(slot + static_cast<int64_t>(D + 1) * p.slot_rows + slot_row, l);
         } else if (p.lse != nullptr) {
-          p.lse[(static_cast<int64_t>(w.it.start) + token) * p.heads + head0 + row - token * p.group] =
+          p.lse[(static_cast<int64_t>(w.it.start) + token) * p.heads + head0 + row_head] =
               l == 0.0f ? -kInf : (mc + log2f(l)) * 0.69314718055994530942f;
         }
       }
@@ -804,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_a(ml_empty(i));
-        ok = __all_sync(~0u, mbar_wait_a(ml_empty(1 - i), exchanges & 1, abort_flag, p.status));
+        ok = __all_sync(~0u, wait_for(ml_empty(1 - i), exchanges & 1, abort_flag, p.status));
         ++exchanges;
         if (!ok) break;
         tc_fence_after();
@@ -823,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     unsigned raw_begun = 0, raw_done = 0;
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-      return __all_sync(~0u, mbar_wait_a(bar, parity, abort_flag, p.status));
+      return __all_sync(~0u, wait_for(bar, parity, abort_flag, p.status));
     };
     auto passed = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(~0u, mbar_test_wait_a(bar, parity)); };
     auto next_slot = [&]() -> bool {  // waits for the slot of load `told`
@@ -864,7 +893,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     };
     auto widen = [&]() -> bool {  // the oldest raw tile, which has landed, into its slot
       if (!next_slot()) return false;
+      // A chunk becomes two, of which a lane of the second panel writes the later
+      // one first: the eight lanes of a row then fall into eight bank groups.
       const int ch = 2 * (lane % kRawChunks);
+      const bool swap = (ch >> 3) != 0;
       const uint32_t to = sbase + S::kRing + (told % S::kSlots) * S::kTile + (ch >> 3) * kPanel;
 #pragma unroll
       for (int q0 = 0; q0 < kRawChunks; q0 += 4) {  // four chunks at a time, for their latencies
@@ -873,41 +905,34 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const uint4 v = lds128(raw_at(raw_done, q0 + q));
-          x[q][0] = v.x;
-          x[q][1] = v.y;
-          x[q][2] = v.z;
-          x[q][3] = v.w;
+          x[q][0] = swap ? v.z : v.x;
+          x[q][1] = swap ? v.w : v.y;
+          x[q][2] = swap ? v.x : v.z;
+          x[q][3] = swap ? v.y : v.w;
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e) nan |= (x[q][e] & 0x7F7F7F7Fu) + 0x01010101u;
-        nan &= 0x80808080u;
+        const bool some = (nan & 0x80808080u) != 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int row = lw * 32 + ((q0 + q) * 32 + lane) / kRawChunks;
           uint32_t y[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) e4m3x4_to_bf16(x[q][e], y[2 * e], y[2 * e + 1]);
-          if (nan) {
+          if (some) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) nan_bytes_to_bf16(x[q][e], y[2 * e], y[2 * e + 1]);
           }
-          sts128(to + row * 128 + (((ch & 7) ^ (row & 7)) << 4), make_uint4(y[0], y[1], y[2], y[3]));
-          sts128(to + row * 128 + ((((ch & 7) + 1) ^ (row & 7)) << 4), make_uint4(y[4], y[5], y[6], y[7]));
+          const uint32_t first = to + row * 128 + ((((ch & 7) + (swap ? 1 : 0)) ^ (row & 7)) << 4);
+          sts128(first, make_uint4(y[0], y[1], y[2], y[3]));
+          sts128(first ^ 16, make_uint4(y[4], y[5], y[6], y[7]));
         }
       }
       mbar_arrive_a(full(told % S::kSlots));
       ++told;
       ++raw_done;
-      return true;
-    };
-    // No raw tile is kept back.  Called before any wait for the others, who may need them to go on.
-    auto settle = [&]() -> bool {
-      if (!kFp8) return true;
-      cp_async_wait_group<0>();
-      while (raw_done != raw_begun)
-        if (!widen()) return false;
       return true;
     };
     // Only slots, phases and whether the first lap is over are used: two to four laps stay.
@@ -916,26 +941,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     };
     // The loads of an item that may begin before its queries are there: nothing gives their slots back without them.
     constexpr int kFirst = S::kSlots >= 4 ? 4 : 2;
-    bool shared_before = false;
+    bool shared_before = false, more = true;
     Work w;
-    for (int k = 0; ok && take(k, w); ++k) {
+    for (int k = 0; ok && more; ++k) {
+      more = take(k, w);
       const Item& it = w.it;
-      // Lane x's rows of keys and values of key tile t: key 32 lw + x.
+      // Lane x's rows of keys and values of key tile t: key 32 lw + x.  Its page's
+      // number is fetched a tile ahead and looked at when its rows are due.
+      int page_next = 0;
+      auto page_index = [&](int key) { return p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size; };
+      auto fetch_page = [&](int t) {
+        const int key = t * kRows + lw * 32 + lane;
+        if (t < it.t1 && t < w.ctx && key < it.len) page_next = p.table[it.seq * p.ld_table + page_index(key)];
+      };
       const void *src_k = nullptr, *src_v = nullptr;
-      auto look_up = [&](int t) {
+      auto find_rows = [&](int t) {
         src_k = src_v = nullptr;
-        if (t >= it.t1) return;
         if (t < w.ctx) {
           const int key = t * kRows + lw * 32 + lane;
           if (key >= it.len) return;
-          const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-          const int64_t page = p.table[it.seq * p.ld_table + pi];
+          const int64_t page = page_next;
           if (page < 0 || page >= p.num_pages) {
             record_error(p.status, QERL_ERR_RANGE);
             return;
           }
-          const int64_t at = ((page * p.kv_heads + it.kv_head) * p.page_size + (key - static_cast<int64_t>(pi) * p.page_size)) *
-                             (D * (kFp8 ? 1 : 2));
+          const int64_t row = key - static_cast<int64_t>(page_index(key)) * p.page_size;
+          const int64_t at = ((page * p.kv_heads + it.kv_head) * p.page_size + row) * (D * (kFp8 ? 1 : 2));
           src_k = p.kp + at;
           src_v = p.vp + at;
         } else {
@@ -952,50 +983,62 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // further than the one asked for.)
       const bool with_scores = w.shared && shared_before;
       shared_before = w.shared;
-      auto load_queries = [&](bool block) -> bool {
-        if (k >= 2 && !passed(out_free(k & 1), ((k >> 1) & 1) ^ 1)) {
-          if (!block) return false;
-          ok = settle() && wait(out_free(k & 1), ((k >> 1) & 1) ^ 1);
+      auto queries_free = [&](bool block) -> bool {
+        if (k >= 2) {
+          const uint32_t bar = out_free(k & 1), parity = ((k >> 1) & 1) ^ 1;
+          if (!(block ? wait(bar, parity) : passed(bar, parity))) return false;
         }
-        if (ok && k >= 1) {
-          const uint32_t bar = with_scores ? q_free : out_free((k - 1) & 1);
-          const uint32_t parity = (with_scores ? k - 1 : (k - 1) >> 1) & 1;
-          if (!passed(bar, parity)) {
-            if (!block) return false;
-            ok = settle() && wait(bar, parity);
-          }
-        }
-        if (!ok) return true;
-#pragma unroll 1
-        for (int i = 0; i < (w.shared ? 1 : 2); ++i) {
-          const int row = it.row0 + i * kRows + lw * 32 + lane;
-          const void* src = nullptr;
-          if (row < it.n * p.group) {
-            const int token = row / p.group;
-            src = p.q + (static_cast<int64_t>(it.start) + token) * p.ldq +
-                  static_cast<int64_t>(it.kv_head * p.group + row - token * p.group) * D;
-          }
-          copy_rows(sbase + i * S::kTile, src);
-        }
-        cp_async_arrive(q_full);
-        return true;
+        if (k == 0) return true;
+        const uint32_t bar = with_scores ? q_free : out_free((k - 1) & 1);
+        const uint32_t parity = (with_scores ? k - 1 : (k - 1) >> 1) & 1;
+        return block ? wait(bar, parity) : passed(bar, parity);
       };
       drop_laps();
-      look_up(it.t0);
-      bool asked = false;  // for the queries
-      const void* src_next = nullptr;
+      const int loads = more ? 2 * (it.t1 - it.t0) : 0;
+      if (more) fetch_page(it.t0);
+      bool asked = !more;  // for the queries
 #pragma unroll 1
-      for (int u = 0; ok && u < 2 * (it.t1 - it.t0); ++u) {
-        if (u >= 1 && !asked) asked = load_queries(u == kFirst);
-        if (!ok) break;
+      for (int u = 0; u <= loads; ++u) {
+        const bool tail = u == loads;
         const int t = it.t0 + (u >> 1);
         const bool direct = !kFp8 || t >= w.ctx;  // bf16 rows
-        const void* src = u & 1 ? src_next : src_k;
-        if ((u & 1) == 0) {
-          src_next = src_v;
-          if (kFp8 && direct) ok = settle();
+        const bool due = !asked && (u == kFirst || tail);
+        bool ask = !asked && u >= 1 && queries_free(false);
+        // Raw tiles stay in flight but before a wait for the others, who may need them to go on, and a load past them.
+        if (kFp8) {
+          const bool all = !more || (due && !ask) || (!tail && direct);
+          if (all) {
+            cp_async_wait_group<0>();
+          } else {
+            cp_async_wait_group<(kFp8 ? static_cast<int>(S::kRaw) - 1 : 0)>();
+          }
+#pragma unroll 1
+          while (ok && raw_begun - raw_done > (all ? 0 : S::kRaw - 1)) ok = widen();
         }
+        if (ok && due && !ask) ask = ok = queries_free(true);
         if (!ok) break;
+        if (ask) {
+          asked = true;
+#pragma unroll 1
+          for (int i = 0; i < (w.shared ? 1 : 2); ++i) {
+            const int row = it.row0 + i * kRows + lw * 32 + lane;
+            const void* src = nullptr;
+            if (row < it.n * p.group) {
+              int head;
+              const int token = token_of(p, it, row - it.row0, head);
+              src = p.q + (static_cast<int64_t>(it.start) + token) * p.ldq +
+                    static_cast<int64_t>(it.kv_head * p.group + head) * D;
+            }
+            copy_rows(sbase + i * S::kTile, src);
+          }
+          cp_async_arrive(q_full);
+        }
+        if (tail) break;
+        if ((u & 1) == 0) {
+          find_rows(t);
+          fetch_page(t + 1);
+        }
+        const void* src = u & 1 ? src_v : src_k;
         if (direct) {
           ok = next_slot();
           if (!ok) break;
@@ -1005,16 +1048,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         } else {
           copy_raw(raw_begun++, src);
           cp_async_commit();
-          if (raw_begun - raw_done == S::kRaw) {
-            cp_async_wait_group<(kFp8 ? static_cast<int>(S::kRaw) - 1 : 0)>();
-            ok = widen();
-          }
         }
-        if ((u & 1) == 0) look_up(t + 1);
       }
-      if (ok && !asked) load_queries(true);
     }
-    if (ok) settle();
     cp_async_wait_all();  // every copy lands before the CTA exits
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -1037,7 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       for (int k = 0; ok && take(k, w); ++k) {
         const int n = w.count(i);
         // Of every item, with or without tiles of this one: a barrier's phase is only told from the one before.
-        ok = __all_sync(~0u, mbar_wait_a(q_full, k & 1, abort_flag, p.status));
+        ok = __all_sync(~0u, wait_for(q_full, k & 1, abort_flag, p.status));
         if (!ok) break;
         if (n == 0) {
           if (leader) mbar_arrive_a(q_free);
@@ -1080,16 +1116,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             if (!w.shared) {
               // Turns, as the two tiles would fall into step: both in the softmax, then both at the tensor core.
               ok = ok && (j + 1 >= n || wait_slot(load_of(j + 1)));
-              if (ok && !first_turn) ok = mbar_wait_a(turn(i), (turns - (i == 0 ? 1 : 0)) & 1, abort_flag, p.status);
+              if (ok && !first_turn) ok = wait_for(turn(i), (turns - (i == 0 ? 1 : 0)) & 1, abort_flag, p.status);
               first_turn = false;
               ++turns;
             }
-            ok = __all_sync(~0u, ok && mbar_wait_a(p_full(i, 0), (tiles_done + j) & 1, abort_flag, p.status));
+            ok = __all_sync(~0u, ok && wait_for(p_full(i, 0), (tiles_done + j) & 1, abort_flag, p.status));
             if (!ok) break;
             fence_proxy_async_smem();
             tc_fence_after();
             values(u, 0, j > 0);
-            ok = __all_sync(~0u, mbar_wait_a(p_full(i, 1), (tiles_done + j) & 1, abort_flag, p.status));
+            ok = __all_sync(~0u, wait_for(p_full(i, 1), (tiles_done + j) & 1, abort_flag, p.status));
             if (!ok) break;
             tc_fence_after();
             values(u, 1, true);
@@ -1126,9 +1162,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (k >= 2 && !__all_sync(~0u, wait_patiently(item_empty(e), ((k >> 1) & 1) ^ 1, abort_flag, p.status)))
           return false;
         if (lane == 0) {
-          const int v[9] = {it.start, it.n, it.len, it.seq, it.kv_head, it.row0, it.t0, it.t1, it.slot};
+          const int v[11] = {it.start, it.n,  it.len,  it.seq,    it.kv_head, it.row0,
+                             it.t0,    it.t1, it.slot, it.token0, it.head0};
 #pragma unroll
-          for (int x = 0; x < 9; ++x) items[e * kItemInts + x] = v[x];
+          for (int x = 0; x < 11; ++x) items[e * kItemInts + x] = v[x];
           mbar_arrive_a(item_full(e));
         }
         __syncwarp();
@@ -1156,7 +1193,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const bool whole = t == 0 && t1 == needed;
             if (t == 0 && !whole)
               job = make_int4(b, kv_head, block * kBlock, owner(base + needed - 1) - static_cast<int>(blockIdx.x) + 1);
-            go = put({sq.start, sq.n, sq.len, b, kv_head, block * kBlock, t, t1, whole ? -1 : t == 0 ? 1 : 0});
+            go = put({sq.start, sq.n, sq.len, b, kv_head, block * kBlock, t, t1, whole ? -1 : t == 0 ? 1 : 0,
+                      block * kBlock / p.group, block * kBlock % p.group});
           }
           pos = base + sq.tiles + kSegmentCost;
           t = 0;
@@ -1179,13 +1217,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
       }
       if (lane == 0) p.jobs[blockIdx.x] = job;
-      if (!busy || go) put({0, 0, 0, 0, 0, 0, 0, 0, 0});
+      if (!busy || go) put({});
     }
   }
   __syncwarp();
   {  // every MMA is done before the tensor memory goes back (bounded)
     volatile int no_abort = 0;
-    mbar_wait_a(done, 0, &no_abort, p.status);
+    wait_for(done, 0, &no_abort, p.status);
   }
   tc_fence_before();
   __syncthreads();
@@ -1324,6 +1362,7 @@ qerl_status launch_tree_attention(const TreeAttentionArgs& a, cudaStream_t s) {
   p.heads = a.num_heads;
   p.kv_heads = c.num_kv_heads;
   p.group = a.num_heads / c.num_kv_heads;
+  p.group_inverse = p.group == 1 ? 0 : static_cast<unsigned>(((uint64_t{1} << 32) + p.group - 1) / p.group);
   p.scale_log2 = a.scale * 1.44269504088896340736f;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.ldo = a.ldo;
