@@ -364,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   auto wait_load = [&](unsigned u, unsigned count) -> bool {
     if (static_cast<int>(*begun - count) <= 0) {
       const long long t0 = clock64();
-      for (unsigned n = 1; static_cast<int>(*begun - count) <= 0; ++n) {
-        if ((n & 255u) != 0) continue;
+      while (static_cast<int>(*begun - count) <= 0) {
+        __nanosleep(40);  // (a warp that polls takes issue slots and instruction fetches from the loads)
         if (*abort_flag) return false;
         if (clock64() - t0 > QERL_WAIT_LIMIT) {
           *abort_flag = 1;
@@ -628,30 +628,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         return true;
       };
       // One key tile: scores in, weights out, l and (rarely) the reference moved.
-      auto step = [&](int j, bool masked, bool fresh, const uint32_t (&keep)[4]) {
-        float x[128];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(s_t + q * 32, x + q * 32);
-        tmem_ld_wait();
-        pin<128>(x);
-        if (masked) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
+      // Both passes are loops over 32 keys, which read the scores twice: code
+      // that runs through once a tile is fetched as slowly as it runs.
+      auto step = [&](int j, int t, bool masked, bool fresh) {
+        auto load = [&](int q, float (&x)[32]) {
+          tmem_ld32(s_t + q * 32, x);
+          tmem_ld_wait();
+          pin<32>(x);
+          if (masked) {
+            const uint32_t keep = sees(t, q);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if ((keep[q] & (1u << e)) == 0) x[q * 32 + e] = -kInf;
+              if ((keep & (1u << e)) == 0) x[e] = -kInf;
+          }
+        };
+        float top = -kInf;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          float x[32];
+          load(q, x);
+          float t2[2] = {top, x[0]};
+#pragma unroll
+          for (int e = 1; e < 29; e += 4) {
+            t2[0] = max3(t2[0], x[e], x[e + 1]);
+            t2[1] = max3(t2[1], x[e + 2], x[e + 3]);
+          }
+          t2[0] = max3(t2[0], x[29], x[30]);
+          top = max3(t2[0], t2[1], x[31]);
         }
         const float c = kFp8 && !fresh ? c_ctx : c_new;
         const uint64_t c2 = pair(c, c);
-        float t4[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          t4[q] = max3(x[q * 32], x[q * 32 + 1], x[q * 32 + 2]);
-#pragma unroll
-          for (int e = 3; e < 31; e += 2) t4[q] = max3(t4[q], x[q * 32 + e], x[q * 32 + e + 1]);
-          t4[q] = fmaxf(t4[q], x[q * 32 + 31]);
-        }
-        const float top = max3(fmaxf(t4[0], t4[1]), t4[2], t4[3]);
         const float tc = top == -kInf ? -kInf : top * c;
         if (__any_sync(~0u, tc > mc + kSlack)) {
           const float up = fmaxf(mc, tc);
@@ -675,28 +681,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         uint64_t part[2] = {0, 0};  // two chains of two fp32 sums
         const float sub = mc == -kInf ? 0.0f : mc;
         const uint64_t sub2 = pair(-sub, -sub);
+        const float by = kFp8 && fresh ? v_inverse : 1.0f;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          float x[32];
+          load(q, x);
+          uint32_t y[16];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t y[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
+          for (int e = 0; e < 16; ++e) {
             float a, b;
-            unpair(fma2(pair(x[half * 64 + 2 * e], x[half * 64 + 2 * e + 1]), c2, sub2), a, b);
+            unpair(fma2(pair(x[2 * e], x[2 * e + 1]), c2, sub2), a, b);
             a = ex2(a);
             b = ex2(b);
             part[e & 1] = add2(part[e & 1], pair(a, b));
-            if (kFp8 && fresh) {
-              a *= v_inverse;
-              b *= v_inverse;
-            }
+            if (kFp8) unpair(fma2(pair(a, b), pair(by, by), 0), a, b);
             y[e] = pack_bf16(a, b);
           }
-          // half of the keys: the product with v may begin
-          tmem_st_x32(s_t + half * 32, y);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_a(p_full(i, half));
+          tmem_st_x16(s_t + q * 16, y);
+          if (q & 1) {  // half of the keys: the product with v may begin
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_a(p_full(i, q >> 1));
+          }
         }
         float s0, s1;
         unpair(add2(part[0], part[1]), s0, s1);
@@ -706,16 +713,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       for (int j = 0; j < mine_n; ++j) {
         const int t = w.tile(i, j);
         const bool fresh = t >= w.ctx, masked = fresh || w.it.len - t * kRows < kRows;
-        uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-        if (masked) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) keep[q] = sees(t, q);
-        }
         ok = __all_sync(~0u, wait_for(s_full(i), (tiles_done + j) & 1, abort_flag, p.status));
         if (ok && fresh) ok = clean_values(2 * (t - w.it.t0) + 1);
         if (!ok) break;
         tc_fence_after();
-        step(j, masked, fresh, keep);
+        step(j, t, masked, fresh);
       }
       tiles_done += mine_n;
       u0 = (u0 + 2 * (w.it.t1 - w.it.t0)) % (2 * S::kSlots);
@@ -898,12 +900,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const int ch = 2 * (lane % kRawChunks);
       const bool swap = (ch >> 3) != 0;
       const uint32_t to = sbase + S::kRing + (told % S::kSlots) * S::kTile + (ch >> 3) * kPanel;
-#pragma unroll
-      for (int q0 = 0; q0 < kRawChunks; q0 += 4) {  // four chunks at a time, for their latencies
-        uint32_t x[4][4];
+      constexpr int kTogether = 2;  // chunks at a time, for their latencies; a loop, as its code would not stay in the cache
+#pragma unroll 1
+      for (int q0 = 0; q0 < kRawChunks; q0 += kTogether) {
+        uint32_t x[kTogether][4];
         uint32_t nan = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < kTogether; ++q) {
           const uint4 v = lds128(raw_at(raw_done, q0 + q));
           x[q][0] = swap ? v.z : v.x;
           x[q][1] = swap ? v.w : v.y;
@@ -911,12 +914,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           x[q][3] = swap ? v.y : v.w;
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < kTogether; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e) nan |= (x[q][e] & 0x7F7F7F7Fu) + 0x01010101u;
         const bool some = (nan & 0x80808080u) != 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < kTogether; ++q) {
           const int row = lw * 32 + ((q0 + q) * 32 + lane) / kRawChunks;
           uint32_t y[8];
 #pragma unroll
