@@ -22,12 +22,12 @@
 //                   128 scores from tensor memory, keeps the reference m and
 //                   the sum l in registers and writes the weights back as bf16
 //                   over the scores; then the tile's outputs
-//   warps 8-11      loads: q and k, v tiles through a ring.  Pages may be of any
+//   4 or 8 more     loads: q and k, v tiles through a ring.  Pages may be of any
 //                   size, so rows are gathered with cp.async; bytes of an E4M3
 //                   cache pass through a ring of their own and are widened to
 //                   bf16 on the way (exact)
-//   warps 12, 13    issue S_i = Q_i K^T and O_i += P_i V of tile 0, tile 1
-//   warp 14         finds the CTA's next items
+//   two more        issue S_i = Q_i K^T and O_i += P_i V of tile 0, tile 1
+//   one more        finds the CTA's next items
 // Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each).
 // Of more than 128 rows the two tiles are rows 0-127 and 128-255 and go through
 // all keys.  Up to 128 rows both are the same rows and take every other key
@@ -55,9 +55,6 @@ namespace {
 
 constexpr int kRows = 128;   // rows of a query tile, keys of a key tile
 constexpr int kBlock = 256;  // rows of a segment
-// At launch 512 threads have 128 registers each: 256 * 184 + 128 * 88 + 128 * 56 = 512 * 128.
-constexpr int kThreads = 512;
-constexpr int kSoftmaxRegs = 184, kLoadRegs = 88, kOtherRegs = 56;
 constexpr uint32_t kPanel = kRows * 128;  // 128 rows of 64 bf16, 128-byte swizzle
 constexpr float kSlack = 8.0f;
 constexpr int kMaxCtas = 160;
@@ -95,6 +92,15 @@ __host__ __device__ __forceinline__ int64_t slot_floats(int slot_rows, int head_
 
 template <int D, bool kFp8>
 struct Shape {
+  // Widening takes the loads of an E4M3 cache twice the warps (64 x 6000 rows, 61
+  // nodes, 28/4 heads: 459 us, with 4 warps 509 us); without it they are slower
+  // (48 sequences to 8192 rows: 104 us, with 4 warps 101 us).
+  static constexpr int kLoadWarps = kFp8 ? 8 : 4;
+  static constexpr int kWarpRows = kRows / kLoadWarps;
+  static constexpr int kThreads = 384 + 32 * kLoadWarps;
+  // At launch 512 threads have 128 registers each, 640 have 96:
+  // 256 * 184 + 128 * 88 + 128 * 56 = 512 * 128, 256 * 136 + 256 * 72 + 128 * 64 = 640 * 96.
+  static constexpr int kSoftmaxRegs = kFp8 ? 136 : 184, kLoadRegs = kFp8 ? 72 : 88, kOtherRegs = kFp8 ? 64 : 56;
   static constexpr int kPanels = D / 64;
   static constexpr uint32_t kTile = kPanels * kPanel;
   static constexpr unsigned kSlots = (kFp8 ? 3 : 5) * (128 / D);
@@ -323,8 +329,10 @@ __device__ __forceinline__ int token_of(const TreeParams& p, const Item& it, int
 constexpr int kItemInts = 12;
 
 template <int D, bool kFp8>
-__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(const __grid_constant__ TreeParams p) {
   using S = Shape<D, kFp8>;
+  constexpr int kThreads = S::kThreads, kLoadWarps = S::kLoadWarps, kWarpRows = S::kWarpRows;
+  constexpr int kIssuer = 8 + kLoadWarps, kFinder = kIssuer + 2;  // warps
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -353,10 +361,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc_gen + 8 * 23 + 4);
   volatile int* dirty = reinterpret_cast<volatile int*>(misc_gen + 8 * 24);       // [4]: item k's at k & 3 is k + 1
   volatile int* items = reinterpret_cast<volatile int*>(misc_gen + 8 * 26);       // [2][kItemInts]
-  volatile long long* sums = reinterpret_cast<volatile long long*>(misc_gen + 8 * 38);  // [16], then the place found
-  volatile int* place = reinterpret_cast<volatile int*>(misc_gen + 8 * 54);       // sequence, bad offsets
-  volatile long long* inside_seq = reinterpret_cast<volatile long long*>(misc_gen + 8 * 55);
-  volatile unsigned* begun = reinterpret_cast<volatile unsigned*>(misc_gen + 8 * 56);
+  volatile long long* sums = reinterpret_cast<volatile long long*>(misc_gen + 8 * 38);  // [20], then the place found
+  volatile int* place = reinterpret_cast<volatile int*>(misc_gen + 8 * 58);       // sequence, bad offsets
+  volatile long long* inside_seq = reinterpret_cast<volatile long long*>(misc_gen + 8 * 59);
+  volatile unsigned* begun = reinterpret_cast<volatile unsigned*>(misc_gen + 8 * 60);
   // Waits for a load of the ring: the u-th by its slot and phase, the `count`-th
   // of all (modulo 2^32).  A barrier's phase is only told from the one before,
   // and where the tiles take turns at the ring an issuer does not look at every
@@ -379,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 
   if (threadIdx.x == 0) {
     for (unsigned s = 0; s < S::kSlots; ++s) {
-      mbar_init_a(full(s), 128);
+      mbar_init_a(full(s), 32 * kLoadWarps);
       mbar_init_a(empty(s), 2);
     }
     for (int i = 0; i < 2; ++i) {
@@ -395,9 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       mbar_init_a(ml_full(i), 4);
       mbar_init_a(ml_empty(i), 4);
       mbar_init_a(item_full(i), 1);
-      mbar_init_a(item_empty(i), 14);  // 8 softmax warps, 4 of the loads and 2 issuers
+      mbar_init_a(item_empty(i), 10 + kLoadWarps);  // 8 softmax warps, the loads and 2 issuers
     }
-    mbar_init_a(q_full, 128);
+    mbar_init_a(q_full, 32 * kLoadWarps);
     mbar_init_a(q_free, 2);
     mbar_init_a(out_free(0), 8);
     mbar_init_a(out_free(1), 8);
@@ -408,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     place[1] = 0;
     fence_mbarrier_init();
   }
-  if (warp == 12) {
+  if (warp == kIssuer) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -471,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     return fine ? sq.cost(p) : 0;
   };
   if (p.num_seqs <= 32) {  // the warp that finds the items alone, without a barrier
-    if (warp == 14) {
+    if (warp == kFinder) {
       bool bad = false;
       const long long mine = lane < p.num_seqs ? cost_of(lane, bad) : 0;
       long long incl = mine;
@@ -550,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   };
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftmaxRegs));
     const int i = warp >> 2;               // query tile
     const int r = (warp & 3) * 32 + lane;  // row of the tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -844,9 +852,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       __syncwarp();
       if (lane == 0) mbar_arrive_a(out_free(k & 1));
     }
-  } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-    // Each warp brings 32 rows of every tile; a barrier takes an arrival of every
+  } else if (warp < kIssuer) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kLoadRegs));
+    // Each warp brings kWarpRows rows of every tile; a barrier takes an arrival of every
     // thread, which comes by itself when the thread's copies have landed.
     const int lw = warp - 8;
     unsigned told = 0;         // loads that were given a slot, but for laps dropped
@@ -863,14 +871,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       if (lw == 0 && lane == 0) *begun = slots_given;
       return true;
     };
-    // 16-byte chunks of this warp's 32 rows of a tile of bf16 rows (lane x's row at src; null: zeros).
+    // 16-byte chunks of this warp's rows of a tile of bf16 rows (lane x's row at src; null: zeros).
     auto copy_rows = [&](uint32_t tile_at, const void* src) {
       constexpr int kChunks = D / 8;
       const int ch = lane % kChunks;
       const uint32_t to = tile_at + (ch >> 3) * kPanel;
 #pragma unroll 4
-      for (int q = 0; q < kChunks; ++q) {
-        const int at = (q * 32 + lane) / kChunks, row = lw * 32 + at;
+      for (int q = 0; q < kChunks * kWarpRows / 32; ++q) {
+        const int at = (q * 32 + lane) / kChunks, row = lw * kWarpRows + at;
         const uint8_t* from =
             reinterpret_cast<const uint8_t*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(src), at));
         const bool real = from != nullptr;
@@ -879,13 +887,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       }
     };
     // The same of E4M3 rows, as they are; every thread reads back what it wrote.
-    constexpr int kRawChunks = D / 16;
+    constexpr int kRawChunks = D / 16, kRawSteps = kRawChunks * kWarpRows / 32;
     auto raw_at = [&](unsigned u, int q) {
-      return sbase + S::kRawRing + (u % (kFp8 ? S::kRaw : 1)) * S::kRawTile + (q * 128 + lw * 32 + lane) * 16;
+      return sbase + S::kRawRing + (u % (kFp8 ? S::kRaw : 1)) * S::kRawTile + ((q * kLoadWarps + lw) * 32 + lane) * 16;
     };
     auto copy_raw = [&](unsigned u, const void* src) {
 #pragma unroll 4
-      for (int q = 0; q < kRawChunks; ++q) {
+      for (int q = 0; q < kRawSteps; ++q) {
         const int at = (q * 32 + lane) / kRawChunks, ch = lane % kRawChunks;
         const uint8_t* from =
             reinterpret_cast<const uint8_t*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(src), at));
@@ -902,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const uint32_t to = sbase + S::kRing + (told % S::kSlots) * S::kTile + (ch >> 3) * kPanel;
       constexpr int kTogether = 2;  // chunks at a time, for their latencies; a loop, as its code would not stay in the cache
 #pragma unroll 1
-      for (int q0 = 0; q0 < kRawChunks; q0 += kTogether) {
+      for (int q0 = 0; q0 < kRawSteps; q0 += kTogether) {
         uint32_t x[kTogether][4];
         uint32_t nan = 0;
 #pragma unroll
@@ -920,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const bool some = (nan & 0x80808080u) != 0;
 #pragma unroll
         for (int q = 0; q < kTogether; ++q) {
-          const int row = lw * 32 + ((q0 + q) * 32 + lane) / kRawChunks;
+          const int row = lw * kWarpRows + ((q0 + q) * 32 + lane) / kRawChunks;
           uint32_t y[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) e4m3x4_to_bf16(x[q][e], y[2 * e], y[2 * e + 1]);
@@ -949,19 +957,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     for (int k = 0; ok && more; ++k) {
       more = take(k, w);
       const Item& it = w.it;
-      // Lane x's rows of keys and values of key tile t: key 32 lw + x.  Its page's
-      // number is fetched a tile ahead and looked at when its rows are due.
+      // Lane x's rows of keys and values of key tile t: key kWarpRows lw + x.  Its
+      // page's number is fetched a tile ahead and looked at when its rows are due.
       int page_next = 0;
       auto page_index = [&](int key) { return p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size; };
       auto fetch_page = [&](int t) {
-        const int key = t * kRows + lw * 32 + lane;
+        const int key = t * kRows + lw * kWarpRows + lane % kWarpRows;
         if (t < it.t1 && t < w.ctx && key < it.len) page_next = p.table[it.seq * p.ld_table + page_index(key)];
       };
       const void *src_k = nullptr, *src_v = nullptr;
       auto find_rows = [&](int t) {
         src_k = src_v = nullptr;
         if (t < w.ctx) {
-          const int key = t * kRows + lw * 32 + lane;
+          const int key = t * kRows + lw * kWarpRows + lane % kWarpRows;
           if (key >= it.len) return;
           const int64_t page = page_next;
           if (page < 0 || page >= p.num_pages) {
@@ -973,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           src_k = p.kp + at;
           src_v = p.vp + at;
         } else {
-          const int node = (t - w.ctx) * kRows + lw * 32 + lane;
+          const int node = (t - w.ctx) * kRows + lw * kWarpRows + lane % kWarpRows;
           if (node >= it.n) return;
           src_k = p.k + (static_cast<int64_t>(it.start) + node) * p.ldk + it.kv_head * D;
           src_v = p.v + (static_cast<int64_t>(it.start) + node) * p.ldv + it.kv_head * D;
@@ -1024,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           asked = true;
 #pragma unroll 1
           for (int i = 0; i < (w.shared ? 1 : 2); ++i) {
-            const int row = it.row0 + i * kRows + lw * 32 + lane;
+            const int row = it.row0 + i * kRows + lw * kWarpRows + lane % kWarpRows;
             const void* src = nullptr;
             if (row < it.n * p.group) {
               int head;
@@ -1056,11 +1064,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     }
     cp_async_wait_all();  // every copy lands before the CTA exits
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp < 14) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOtherRegs));
+    if (warp < kFinder) {
       const uint32_t leader = elect_lane();
-      // Warp 12 + i issues the products of query tile i.
-      const int i = warp - 12;
+      // Each issues the products of one query tile.
+      const int i = warp - kIssuer;
       const uint32_t id_s = idesc_bf16_f32(128, 128);
       const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // v: rows along the contraction
       auto slot = [&](unsigned u) { return sbase + S::kRing + (u % S::kSlots) * S::kTile; };
@@ -1152,7 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         count0 += 2 * (w.it.t1 - w.it.t0);
       }
       commit(leader, done);  // also after an expired wait: arrives once the issued MMAs are done
-    } else if (warp == 14) {
+    } else if (warp == kFinder) {
       // The items of this CTA's stretch, ahead of the others.
       auto owner = [&](long long pos) -> int {  // the CTA whose stretch holds a place
         const long long wide = extra * (each + 1);
@@ -1230,7 +1238,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == kIssuer) tmem_dealloc(tmem, 512);
 }
 
 // Block (c, y): 16 columns of the segment that CTA c began and others went on with.
@@ -1315,7 +1323,8 @@ qerl_status launch(const TreeParams& p, int grid, int dev, cudaStream_t s) {
       return QERL_ERR_CUDA;
     ready.fetch_or(bit);
   }
-  if (launch_dependent(tree_kernel<D, kFp8>, dim3(static_cast<unsigned>(grid)), kThreads, S::kSmem, s, p) != cudaSuccess)
+  if (launch_dependent(tree_kernel<D, kFp8>, dim3(static_cast<unsigned>(grid)), S::kThreads, S::kSmem, s, p) !=
+      cudaSuccess)
     return QERL_ERR_CUDA;
   return cuda_status(launch_dependent(join_kernel<D>, dim3(static_cast<unsigned>(grid), D / 16), kBlock, 0, s, p,
                                       static_cast<int>(kFp8 && p.v_scale != nullptr)));
