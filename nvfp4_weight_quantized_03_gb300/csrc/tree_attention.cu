@@ -92,19 +92,22 @@ __host__ __device__ __forceinline__ int64_t slot_floats(int slot_rows, int head_
 
 template <int D, bool kFp8>
 struct Shape {
-  // Widening takes the loads of an E4M3 cache twice the warps (64 x 6000 rows, 61
-  // nodes, 28/4 heads: 459 us, with 4 warps 509 us); without it they are slower
-  // (48 sequences to 8192 rows: 104 us, with 4 warps 101 us).
+  // Four warps bring the keys and then the values of a tile; of an E4M3 cache,
+  // which takes them longer, four the keys and four the values.
   static constexpr int kLoadWarps = kFp8 ? 8 : 4;
-  static constexpr int kWarpRows = kRows / kLoadWarps;
   static constexpr int kThreads = 384 + 32 * kLoadWarps;
   // At launch 512 threads have 128 registers each, 640 have 96:
   // 256 * 184 + 128 * 88 + 128 * 56 = 512 * 128, 256 * 136 + 256 * 72 + 128 * 64 = 640 * 96.
   static constexpr int kSoftmaxRegs = kFp8 ? 136 : 184, kLoadRegs = kFp8 ? 72 : 88, kOtherRegs = kFp8 ? 64 : 56;
   static constexpr int kPanels = D / 64;
   static constexpr uint32_t kTile = kPanels * kPanel;
-  static constexpr unsigned kSlots = (kFp8 ? 3 : 5) * (128 / D);
-  static constexpr unsigned kRaw = kFp8 ? 4 * (128 / D) : 0;  // key tiles as they lie in the cache
+  // Slots of the keys' and of the values' ring.
+  static constexpr unsigned kKeySlots = kFp8 ? 2 * (128 / D) : D == 128 ? 2 : 5;
+  static constexpr unsigned kValueSlots = kFp8 ? 2 * (128 / D) : D == 128 ? 3 : 5;
+  static constexpr unsigned kSlots = kKeySlots + kValueSlots;
+  // Slots and phases of a tile's loads repeat after so many tiles.
+  static constexpr unsigned kLaps = 2 * kKeySlots * kValueSlots;
+  static constexpr unsigned kRaw = kFp8 ? 2 : 0;  // tiles as they lie in the cache: keys, values
   static constexpr uint32_t kRawTile = kRows * D;
   static constexpr uint32_t kRing = 2 * kTile;
   static constexpr uint32_t kRawRing = kRing + kSlots * kTile;
@@ -331,7 +334,7 @@ constexpr int kItemInts = 12;
 template <int D, bool kFp8>
 __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(const __grid_constant__ TreeParams p) {
   using S = Shape<D, kFp8>;
-  constexpr int kThreads = S::kThreads, kLoadWarps = S::kLoadWarps, kWarpRows = S::kWarpRows;
+  constexpr int kThreads = S::kThreads, kLoadWarps = S::kLoadWarps;
   constexpr int kIssuer = 8 + kLoadWarps, kFinder = kIssuer + 2;  // warps
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -365,14 +368,18 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
   volatile int* place = reinterpret_cast<volatile int*>(misc_gen + 8 * 58);       // sequence, bad offsets
   volatile long long* inside_seq = reinterpret_cast<volatile long long*>(misc_gen + 8 * 59);
   volatile unsigned* begun = reinterpret_cast<volatile unsigned*>(misc_gen + 8 * 60);
-  // Waits for a load of the ring: the u-th by its slot and phase, the `count`-th
-  // of all (modulo 2^32).  A barrier's phase is only told from the one before,
-  // and where the tiles take turns at the ring an issuer does not look at every
-  // load: so first that the slot was given to this load, then that it is there.
-  auto wait_load = [&](unsigned u, unsigned count) -> bool {
-    if (static_cast<int>(*begun - count) <= 0) {
+  // Tile n's keys (part 0) and values (part 1): slot and phase of the barriers.
+  auto slot_of = [&](int part, unsigned n) { return part == 0 ? n % S::kKeySlots : S::kKeySlots + n % S::kValueSlots; };
+  auto phase_of = [&](int part, unsigned n) { return (part == 0 ? n / S::kKeySlots : n / S::kValueSlots) & 1; };
+  auto slot_at = [&](int part, unsigned n) { return sbase + S::kRing + slot_of(part, n) * S::kTile; };
+  // Waits for a load of tile n, the `count`-th of all (modulo 2^32).  A barrier's
+  // phase is only told from the one before, and where the tiles take turns an
+  // issuer does not look at every load: so first that the slot was given to this
+  // load, then that it is there.
+  auto wait_load = [&](int part, unsigned n, unsigned count) -> bool {
+    if (static_cast<int>(begun[part] - count) <= 0) {
       const long long t0 = clock64();
-      while (static_cast<int>(*begun - count) <= 0) {
+      while (static_cast<int>(begun[part] - count) <= 0) {
         __nanosleep(40);  // (a warp that polls takes issue slots and instruction fetches from the loads)
         if (*abort_flag) return false;
         if (clock64() - t0 > QERL_WAIT_LIMIT) {
@@ -382,12 +389,12 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         }
       }
     }
-    return wait_for(full(u % S::kSlots), (u / S::kSlots) & 1, abort_flag, p.status);
+    return wait_for(full(slot_of(part, n)), phase_of(part, n), abort_flag, p.status);
   };
 
   if (threadIdx.x == 0) {
     for (unsigned s = 0; s < S::kSlots; ++s) {
-      mbar_init_a(full(s), 32 * kLoadWarps);
+      mbar_init_a(full(s), 128);
       mbar_init_a(empty(s), 2);
     }
     for (int i = 0; i < 2; ++i) {
@@ -405,11 +412,11 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       mbar_init_a(item_full(i), 1);
       mbar_init_a(item_empty(i), 10 + kLoadWarps);  // 8 softmax warps, the loads and 2 issuers
     }
-    mbar_init_a(q_full, 32 * kLoadWarps);
+    mbar_init_a(q_full, 128);
     mbar_init_a(q_free, 2);
     mbar_init_a(out_free(0), 8);
     mbar_init_a(out_free(1), 8);
-    *begun = 0;
+    begun[0] = begun[1] = 0;
     mbar_init_a(done, 2);
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) dirty[i] = 0;
@@ -564,9 +571,9 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_t = tmem + lanes + i * 128, o_t = tmem + lanes + 256 + i * D, o_other = tmem + lanes + 256 + (1 - i) * D;
     bool ok = true;
-    // Of this query tile; loads of the ring before this item, of which only the
-    // slot and the phase are used (modulo two laps: a CTA may see more than 2^32).
-    unsigned tiles_done = 0, u0 = 0, count0 = 0;  // (count0: the loads before this item, modulo 2^32)
+    // Tiles of this query tile; all tiles before this item, for their slots and
+    // phases (they may pass 2^32, which is no multiple of the laps) and modulo 2^32.
+    unsigned tiles_done = 0, n0 = 0, count0 = 0;
     int outputs_done = 0, exchanges = 0;
     Work w;
     for (int k = 0; ok && take(k, w); ++k) {
@@ -603,10 +610,9 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         asm volatile("prefetch.global.L1 [%0];" ::"l"(p.mask + (static_cast<int64_t>(w.it.start) + token) * p.words));
       // The values of a tile of new tokens, looked through
       // for elements that are not finite; a thread takes one token's row.
-      auto clean_values = [&](unsigned u) -> bool {  // the u-th load of the item
-        if (!__all_sync(~0u, wait_load(u0 + u, count0 + u))) return false;
-        const unsigned s = (u0 + u) % S::kSlots;
-        const uint32_t at_row = sbase + S::kRing + s * S::kTile + r * 128;
+      auto clean_values = [&](int t) -> bool {  // of the item's t-th tile
+        if (!__all_sync(~0u, wait_load(1, n0 + t, count0 + t))) return false;
+        const uint32_t at_row = slot_at(1, n0 + t) + r * 128;
         // x * 0 + sum is NaN from the first x that is not finite
         uint32_t sum = 0;
 #pragma unroll
@@ -722,14 +728,14 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         const int t = w.tile(i, j);
         const bool fresh = t >= w.ctx, masked = fresh || w.it.len - t * kRows < kRows;
         ok = __all_sync(~0u, wait_for(s_full(i), (tiles_done + j) & 1, abort_flag, p.status));
-        if (ok && fresh) ok = clean_values(2 * (t - w.it.t0) + 1);
+        if (ok && fresh) ok = clean_values(t - w.it.t0);
         if (!ok) break;
         tc_fence_after();
         step(j, t, masked, fresh);
       }
       tiles_done += mine_n;
-      u0 = (u0 + 2 * (w.it.t1 - w.it.t0)) % (2 * S::kSlots);
-      count0 += 2 * (w.it.t1 - w.it.t0);
+      n0 = (n0 + w.it.t1 - w.it.t0) % S::kLaps;
+      count0 += w.it.t1 - w.it.t0;
       if (mine_n > 0) {
         ok = __all_sync(~0u, ok && wait_for(o_full(i), outputs_done & 1, abort_flag, p.status));
         ++outputs_done;
@@ -854,21 +860,20 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
     }
   } else if (warp < kIssuer) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kLoadRegs));
-    // Each warp brings kWarpRows rows of every tile; a barrier takes an arrival of every
+    // Four warps bring 32 rows each of a tile; a barrier takes an arrival of every
     // thread, which comes by itself when the thread's copies have landed.
-    const int lw = warp - 8;
-    unsigned told = 0;         // loads that were given a slot, but for laps dropped
-    unsigned slots_given = 0;  // all of them (modulo 2^32)
-    unsigned raw_begun = 0, raw_done = 0;
+    const int lw = (warp - 8) & 3, group = (warp - 8) >> 2;  // E4M3: group 0 the keys and the queries, 1 the values
+    unsigned n = 0;      // the next tile, but for laps dropped
+    unsigned count = 0;  // the same of all tiles (modulo 2^32)
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
       return __all_sync(~0u, wait_for(bar, parity, abort_flag, p.status));
     };
     auto passed = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(~0u, mbar_test_wait_a(bar, parity)); };
-    auto next_slot = [&]() -> bool {  // waits for the slot of load `told`
-      if (told >= S::kSlots && !wait(empty(told % S::kSlots), ((told / S::kSlots) & 1) ^ 1)) return false;
-      ++slots_given;
-      if (lw == 0 && lane == 0) *begun = slots_given;
+    auto next_slot = [&](int part) -> bool {  // waits for the slot of tile n's load
+      if (n >= (part == 0 ? S::kKeySlots : S::kValueSlots) && !wait(empty(slot_of(part, n)), phase_of(part, n) ^ 1))
+        return false;
+      if (lw == 0 && lane == 0) begun[part] = count + 1;
       return true;
     };
     // 16-byte chunks of this warp's rows of a tile of bf16 rows (lane x's row at src; null: zeros).
@@ -877,8 +882,8 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       const int ch = lane % kChunks;
       const uint32_t to = tile_at + (ch >> 3) * kPanel;
 #pragma unroll 4
-      for (int q = 0; q < kChunks * kWarpRows / 32; ++q) {
-        const int at = (q * 32 + lane) / kChunks, row = lw * kWarpRows + at;
+      for (int q = 0; q < kChunks; ++q) {
+        const int at = (q * 32 + lane) / kChunks, row = lw * 32 + at;
         const uint8_t* from =
             reinterpret_cast<const uint8_t*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(src), at));
         const bool real = from != nullptr;
@@ -886,36 +891,31 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
                     real ? from + ch * 16 : reinterpret_cast<const uint8_t*>(p.q), real ? 16 : 0);
       }
     };
-    // The same of E4M3 rows, as they are; every thread reads back what it wrote.
-    constexpr int kRawChunks = D / 16, kRawSteps = kRawChunks * kWarpRows / 32;
-    auto raw_at = [&](unsigned u, int q) {
-      return sbase + S::kRawRing + (u % (kFp8 ? S::kRaw : 1)) * S::kRawTile + ((q * kLoadWarps + lw) * 32 + lane) * 16;
+    // The same of E4M3 rows, as they are, to this group's part of the raw ring;
+    // every thread reads back what it wrote.
+    constexpr int kRawChunks = D / 16;
+    auto raw_at = [&](int q) { return sbase + S::kRawRing + group * S::kRawTile + ((q * 4 + lw) * 32 + lane) * 16; };
+    auto copy_raw = [&](int q, const void* src) {
+      const uint8_t* from = reinterpret_cast<const uint8_t*>(
+          __shfl_sync(~0u, reinterpret_cast<unsigned long long>(src), (q * 32 + lane) / kRawChunks));
+      const bool real = from != nullptr;
+      cp_async_16(raw_at(q), real ? from + lane % kRawChunks * 16 : reinterpret_cast<const uint8_t*>(p.q), real ? 16 : 0);
     };
-    auto copy_raw = [&](unsigned u, const void* src) {
-#pragma unroll 4
-      for (int q = 0; q < kRawSteps; ++q) {
-        const int at = (q * 32 + lane) / kRawChunks, ch = lane % kRawChunks;
-        const uint8_t* from =
-            reinterpret_cast<const uint8_t*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(src), at));
-        const bool real = from != nullptr;
-        cp_async_16(raw_at(u, q), real ? from + ch * 16 : reinterpret_cast<const uint8_t*>(p.q), real ? 16 : 0);
-      }
-    };
-    auto widen = [&]() -> bool {  // the oldest raw tile, which has landed, into its slot
-      if (!next_slot()) return false;
+    // The raw tile, which has landed, into its slot, and the next one in its place.
+    auto widen = [&](const void* next, bool more) {
       // A chunk becomes two, of which a lane of the second panel writes the later
       // one first: the eight lanes of a row then fall into eight bank groups.
       const int ch = 2 * (lane % kRawChunks);
       const bool swap = (ch >> 3) != 0;
-      const uint32_t to = sbase + S::kRing + (told % S::kSlots) * S::kTile + (ch >> 3) * kPanel;
+      const uint32_t to = slot_at(group, n) + (ch >> 3) * kPanel;
       constexpr int kTogether = 2;  // chunks at a time, for their latencies; a loop, as its code would not stay in the cache
 #pragma unroll 1
-      for (int q0 = 0; q0 < kRawSteps; q0 += kTogether) {
+      for (int q0 = 0; q0 < kRawChunks; q0 += kTogether) {
         uint32_t x[kTogether][4];
         uint32_t nan = 0;
 #pragma unroll
         for (int q = 0; q < kTogether; ++q) {
-          const uint4 v = lds128(raw_at(raw_done, q0 + q));
+          const uint4 v = lds128(raw_at(q0 + q));
           x[q][0] = swap ? v.z : v.x;
           x[q][1] = swap ? v.w : v.y;
           x[q][2] = swap ? v.x : v.z;
@@ -928,7 +928,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         const bool some = (nan & 0x80808080u) != 0;
 #pragma unroll
         for (int q = 0; q < kTogether; ++q) {
-          const int row = lw * kWarpRows + ((q0 + q) * 32 + lane) / kRawChunks;
+          const int row = lw * 32 + ((q0 + q) * 32 + lane) / kRawChunks;
           uint32_t y[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) e4m3x4_to_bf16(x[q][e], y[2 * e], y[2 * e + 1]);
@@ -940,36 +940,35 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           sts128(first, make_uint4(y[0], y[1], y[2], y[3]));
           sts128(first ^ 16, make_uint4(y[4], y[5], y[6], y[7]));
         }
+        if (more) {
+#pragma unroll
+          for (int q = 0; q < kTogether; ++q) copy_raw(q0 + q, next);
+        }
       }
-      mbar_arrive_a(full(told % S::kSlots));
-      ++told;
-      ++raw_done;
-      return true;
+      mbar_arrive_a(full(slot_of(group, n)));
     };
-    // Only slots, phases and whether the first lap is over are used: two to four laps stay.
+    // Only slots, phases and whether the first lap is over are used of n.
     auto drop_laps = [&]() {
-      if (told >= 4 * S::kSlots) told -= (told / (2 * S::kSlots) - 1) * (2 * S::kSlots);
+      if (n >= 2 * S::kLaps) n -= (n / S::kLaps - 1) * S::kLaps;
     };
-    // The loads of an item that may begin before its queries are there: nothing gives their slots back without them.
-    constexpr int kFirst = S::kSlots >= 4 ? 4 : 2;
     bool shared_before = false, more = true;
     Work w;
     for (int k = 0; ok && more; ++k) {
       more = take(k, w);
       const Item& it = w.it;
-      // Lane x's rows of keys and values of key tile t: key kWarpRows lw + x.  Its
+      // Lane x's rows of keys and values of key tile t: key 32 lw + x.  Its
       // page's number is fetched a tile ahead and looked at when its rows are due.
       int page_next = 0;
       auto page_index = [&](int key) { return p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size; };
       auto fetch_page = [&](int t) {
-        const int key = t * kRows + lw * kWarpRows + lane % kWarpRows;
+        const int key = t * kRows + lw * 32 + lane % 32;
         if (t < it.t1 && t < w.ctx && key < it.len) page_next = p.table[it.seq * p.ld_table + page_index(key)];
       };
       const void *src_k = nullptr, *src_v = nullptr;
       auto find_rows = [&](int t) {
         src_k = src_v = nullptr;
         if (t < w.ctx) {
-          const int key = t * kRows + lw * kWarpRows + lane % kWarpRows;
+          const int key = t * kRows + lw * 32 + lane % 32;
           if (key >= it.len) return;
           const int64_t page = page_next;
           if (page < 0 || page >= p.num_pages) {
@@ -981,7 +980,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           src_k = p.kp + at;
           src_v = p.vp + at;
         } else {
-          const int node = (t - w.ctx) * kRows + lw * kWarpRows + lane % kWarpRows;
+          const int node = (t - w.ctx) * kRows + lw * 32 + lane % 32;
           if (node >= it.n) return;
           src_k = p.k + (static_cast<int64_t>(it.start) + node) * p.ldk + it.kv_head * D;
           src_v = p.v + (static_cast<int64_t>(it.start) + node) * p.ldv + it.kv_head * D;
@@ -1005,60 +1004,87 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         return block ? wait(bar, parity) : passed(bar, parity);
       };
       drop_laps();
-      const int loads = more ? 2 * (it.t1 - it.t0) : 0;
-      if (more) fetch_page(it.t0);
-      bool asked = !more;  // for the queries
+      if (!more) break;
+      fetch_page(it.t0);
+      auto load_queries = [&]() {
 #pragma unroll 1
-      for (int u = 0; u <= loads; ++u) {
-        const bool tail = u == loads;
-        const int t = it.t0 + (u >> 1);
-        const bool direct = !kFp8 || t >= w.ctx;  // bf16 rows
-        const bool due = !asked && (u == kFirst || tail);
-        bool ask = !asked && u >= 1 && queries_free(false);
-        // Raw tiles stay in flight but before a wait for the others, who may need them to go on, and a load past them.
-        if (kFp8) {
-          const bool all = !more || (due && !ask) || (!tail && direct);
-          if (all) {
-            cp_async_wait_group<0>();
-          } else {
-            cp_async_wait_group<(kFp8 ? static_cast<int>(S::kRaw) - 1 : 0)>();
+        for (int i = 0; i < (w.shared ? 1 : 2); ++i) {
+          const int row = it.row0 + i * kRows + lw * 32 + lane;
+          const void* src = nullptr;
+          if (row < it.n * p.group) {
+            int head;
+            const int token = token_of(p, it, row - it.row0, head);
+            src = p.q + (static_cast<int64_t>(it.start) + token) * p.ldq +
+                  static_cast<int64_t>(it.kv_head * p.group + head) * D;
           }
-#pragma unroll 1
-          while (ok && raw_begun - raw_done > (all ? 0 : S::kRaw - 1)) ok = widen();
+          copy_rows(sbase + i * S::kTile, src);
         }
-        if (ok && due && !ask) ask = ok = queries_free(true);
-        if (!ok) break;
-        if (ask) {
-          asked = true;
-#pragma unroll 1
-          for (int i = 0; i < (w.shared ? 1 : 2); ++i) {
-            const int row = it.row0 + i * kRows + lw * kWarpRows + lane % kWarpRows;
-            const void* src = nullptr;
-            if (row < it.n * p.group) {
-              int head;
-              const int token = token_of(p, it, row - it.row0, head);
-              src = p.q + (static_cast<int64_t>(it.start) + token) * p.ldq +
-                    static_cast<int64_t>(it.kv_head * p.group + head) * D;
-            }
-            copy_rows(sbase + i * S::kTile, src);
-          }
-          cp_async_arrive(q_full);
+        cp_async_arrive(q_full);
+      };
+      if (kFp8) {
+        // The first raw tile on its way, the queries, then tile after tile, each
+        // making room for the next.  Nothing is kept back from the others here.
+        bool raw = it.t0 < w.ctx;
+        find_rows(it.t0);
+        const void* src = group == 0 ? src_k : src_v;
+        if (raw) {
+#pragma unroll 2
+          for (int q = 0; q < kRawChunks; ++q) copy_raw(q, src);
         }
-        if (tail) break;
-        if ((u & 1) == 0) {
-          find_rows(t);
-          fetch_page(t + 1);
-        }
-        const void* src = u & 1 ? src_v : src_k;
-        if (direct) {
-          ok = next_slot();
+        fetch_page(it.t0 + 1);
+        if (group == 0) {
+          ok = queries_free(true);
           if (!ok) break;
-          copy_rows(sbase + S::kRing + (told % S::kSlots) * S::kTile, src);
-          cp_async_arrive(full(told % S::kSlots));
-          ++told;
-        } else {
-          copy_raw(raw_begun++, src);
-          cp_async_commit();
+          load_queries();
+        }
+#pragma unroll 1
+        for (int t = it.t0; t < it.t1; ++t) {
+          const void* next = nullptr;
+          if (t + 1 < it.t1) {
+            find_rows(t + 1);
+            next = group == 0 ? src_k : src_v;
+            fetch_page(t + 2);
+          }
+          const bool raw_next = t + 1 < it.t1 && t + 1 < w.ctx;
+          ok = next_slot(group);
+          if (!ok) break;
+          if (raw) {
+            cp_async_wait_all();
+            widen(next, raw_next);
+          } else {
+            copy_rows(slot_at(group, n), src);
+            cp_async_arrive(full(slot_of(group, n)));
+          }
+          ++n;
+          ++count;
+          src = next;
+          raw = raw_next;
+        }
+      } else {
+        // The queries as soon as their buffers are free, but no later than the
+        // third tile: nothing gives the slots of an item back without them.
+        static_assert(S::kKeySlots >= 2 && S::kValueSlots >= 2, "two tiles may come before the queries");
+        bool asked = false;
+#pragma unroll 1
+        for (int u = 0; u <= 2 * (it.t1 - it.t0); ++u) {
+          const int t = it.t0 + (u >> 1), part = u & 1;
+          const bool tail = t == it.t1, due = u == 4 || tail;
+          if (!asked && u > 0 && queries_free(due)) {
+            asked = true;
+            load_queries();
+          }
+          ok = asked || !due;
+          if (!ok || tail) break;
+          if (part == 0) {
+            find_rows(t);
+            fetch_page(t + 1);
+          }
+          ok = next_slot(part);
+          if (!ok) break;
+          copy_rows(slot_at(part, n), part == 0 ? src_k : src_v);
+          cp_async_arrive(full(slot_of(part, n)));
+          n += part;
+          count += part;
         }
       }
     }
@@ -1071,14 +1097,13 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       const int i = warp - kIssuer;
       const uint32_t id_s = idesc_bf16_f32(128, 128);
       const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // v: rows along the contraction
-      auto slot = [&](unsigned u) { return sbase + S::kRing + (u % S::kSlots) * S::kTile; };
       // A slot is free after two arrivals: one of each issuer where both use it,
       // or both of the one that does.
-      auto release = [&](unsigned u, bool alone) {
-        commit(leader, empty(u % S::kSlots));
-        if (alone && leader) mbar_arrive_a(empty(u % S::kSlots));
+      auto release = [&](int part, unsigned n, bool alone) {
+        commit(leader, empty(slot_of(part, n)));
+        if (alone && leader) mbar_arrive_a(empty(slot_of(part, n)));
       };
-      unsigned u0 = 0, count0 = 0, tiles_done = 0, turns = 0;
+      unsigned n0 = 0, count0 = 0, tiles_done = 0, turns = 0;
       bool ok = true, first_turn = i == 0;  // of tile 0: nobody hands it over
       Work w;
       for (int k = 0; ok && take(k, w); ++k) {
@@ -1090,11 +1115,10 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           if (leader) mbar_arrive_a(q_free);
         } else {
           const float ks = kFp8 && p.k_scale != nullptr ? p.k_scale[w.it.kv_head] : 1.0f;
-          auto load_of = [&](int j) { return static_cast<unsigned>(2 * (w.tile(i, j) - w.it.t0)); };
-          auto wait_slot = [&](unsigned u) { return wait_load(u0 + u, count0 + u); };
+          auto tile_of = [&](int j) { return static_cast<unsigned>(w.tile(i, j) - w.it.t0); };
+          auto wait_part = [&](int part, int j) { return wait_load(part, n0 + tile_of(j), count0 + tile_of(j)); };
           auto scores = [&](int j) {
-            const unsigned u = u0 + load_of(j);
-            const uint32_t qa = sbase + (w.shared ? 0 : i * S::kTile), ka = slot(u);
+            const uint32_t qa = sbase + (w.shared ? 0 : i * S::kTile), ka = slot_at(0, n0 + tile_of(j));
             // a negative factor of the scores: the product is negated
             const bool negative = p.scale_log2 < 0.0f != (w.tile(i, j) < w.ctx && ks < 0.0f);
             const uint32_t id = id_s | (negative ? 1u << 13 : 0u);
@@ -1105,28 +1129,27 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
                 mma_ss(leader, tmem + i * 128, sw128_kmajor_desc(qa + d * kPanel + kk * 32),
                        sw128_kmajor_desc(ka + d * kPanel + kk * 32), id, d + kk > 0 ? 1u : 0u);
             commit(leader, s_full(i));
-            release(u, w.shared);
+            release(0, n0 + tile_of(j), w.shared);
             if (j + 1 == n) commit(leader, q_free);
           };
-          auto values = [&](unsigned u, int part, bool more) {
-            const uint32_t va = slot(u);
+          auto values = [&](int j, int half) {
+            const uint32_t va = slot_at(1, n0 + tile_of(j));
 #pragma unroll
-            for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
               mma_ts(leader, tmem + 256 + i * D, tmem + i * 128 + kk * 8, sw128_mnmajor_desc(va + kk * 2048), id_o,
-                     more || kk > 0 ? 1u : 0u);
+                     j > 0 || kk > 0 ? 1u : 0u);
           };
-          ok = __all_sync(~0u, wait_slot(load_of(0)));
+          ok = __all_sync(~0u, wait_part(0, 0));
           if (!ok) break;
           // (the loads are ordinary writes of other threads, seen here through the barrier)
           fence_proxy_async_smem();
           tc_fence_after();
           scores(0);
           for (int j = 0; j < n; ++j) {
-            const unsigned u = u0 + load_of(j) + 1;
-            ok = wait_slot(load_of(j) + 1);
+            ok = wait_part(1, j);
             if (!w.shared) {
               // Turns, as the two tiles would fall into step: both in the softmax, then both at the tensor core.
-              ok = ok && (j + 1 >= n || wait_slot(load_of(j + 1)));
+              ok = ok && (j + 1 >= n || wait_part(0, j + 1));
               if (ok && !first_turn) ok = wait_for(turn(i), (turns - (i == 0 ? 1 : 0)) & 1, abort_flag, p.status);
               first_turn = false;
               ++turns;
@@ -1135,15 +1158,15 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
             if (!ok) break;
             fence_proxy_async_smem();
             tc_fence_after();
-            values(u, 0, j > 0);
+            values(j, 0);
             ok = __all_sync(~0u, wait_for(p_full(i, 1), (tiles_done + j) & 1, abort_flag, p.status));
             if (!ok) break;
             tc_fence_after();
-            values(u, 1, true);
-            release(u, w.shared);
+            values(j, 1);
+            release(1, n0 + tile_of(j), w.shared);
             if (j + 1 < n) {
               if (w.shared) {
-                ok = __all_sync(~0u, wait_slot(load_of(j + 1)));
+                ok = __all_sync(~0u, wait_part(0, j + 1));
                 if (!ok) break;
                 fence_proxy_async_smem();
                 tc_fence_after();
@@ -1156,8 +1179,8 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           }
         }
         tiles_done += n;
-        u0 = (u0 + 2 * (w.it.t1 - w.it.t0)) % (2 * S::kSlots);
-        count0 += 2 * (w.it.t1 - w.it.t0);
+        n0 = (n0 + w.it.t1 - w.it.t0) % S::kLaps;
+        count0 += w.it.t1 - w.it.t0;
       }
       commit(leader, done);  // also after an expired wait: arrives once the issued MMAs are done
     } else if (warp == kFinder) {
