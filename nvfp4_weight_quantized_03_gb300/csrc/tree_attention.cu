@@ -584,11 +584,12 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       const int row_token = token_of(p, w.it, row - w.it.row0, row_head);
       const int token = row < rows ? row_token : 0;
       float mc = -kInf, l = 0.0f;  // the reference in base-2 units and the sum of 2^(s - m)
-      float v_scale = 1.0f, v_inverse = 1.0f, c_ctx = fabsf(p.scale_log2);
+      float v_scale = 1.0f, v_inverse = 1.0f, v_log2 = 0.0f, c_ctx = fabsf(p.scale_log2);
       if (kFp8) {
         if (p.k_scale != nullptr) c_ctx = fabsf(p.scale_log2 * p.k_scale[w.it.kv_head]);
         if (p.v_scale != nullptr) v_scale = p.v_scale[w.it.kv_head];
         v_inverse = 1.0f / v_scale;
+        v_log2 = log2f(v_scale);
       }
       // Not 0: a masked score of -inf times 0 would be NaN (1e-37 times any score below 1e29 is as good as 0).
       c_ctx = fmaxf(c_ctx, 1e-37f);
@@ -693,10 +694,10 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           mc = up;
         }
         uint64_t part[2] = {0, 0};  // two chains of two fp32 sums
-        const float sub = mc == -kInf ? 0.0f : mc;
+        // (weights of new tokens over an E4M3 cache: divided by the value scale, in the exponent)
+        const float sub = (mc == -kInf ? 0.0f : mc) + (kFp8 && fresh ? v_log2 : 0.0f);
         const uint64_t sub2 = pair(-sub, -sub);
-        const float by = kFp8 && fresh ? v_inverse : 1.0f;
-#pragma unroll 1
+#pragma unroll 2
         for (int q = 0; q < 4; ++q) {
           float x[32];
           load(q, x);
@@ -708,7 +709,6 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
             a = ex2(a);
             b = ex2(b);
             part[e & 1] = add2(part[e & 1], pair(a, b));
-            if (kFp8) unpair(fma2(pair(a, b), pair(by, by), 0), a, b);
             y[e] = pack_bf16(a, b);
           }
           tmem_st_x16(s_t + q * 16, y);
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         }
         float s0, s1;
         unpair(add2(part[0], part[1]), s0, s1);
-        l += s0 + s1;
+        l += kFp8 && fresh ? (s0 + s1) * v_scale : s0 + s1;
       };
 
       for (int j = 0; j < mine_n; ++j) {
