@@ -6,7 +6,9 @@
 // Compaction: of the pages in use, the i-th (ascending) with a number at or past
 // their count L moves into the i-th unused number below L.
 //
-// Bound: bytes, each copied row once in and once out.
+// Bound: bytes, each copied row once in and once out.  Measured: 384 children of 48
+// parents (53 MB) 11.9 us = 0.66 of the copy rate; 1336 pages of 256 KB moved
+// (700 MB) 125 us = 0.82, of which the marks and numbers take some 15 us.
 #include "qerl_internal.h"
 #include "qerl_ptx.cuh"
 
@@ -44,9 +46,11 @@ struct ForkParams {
   const int *parents, *children, *lengths, *new_pages;
 };
 
+constexpr int kForkCtas = 4;  // per SM
+
 // Block (x, y): child x's piece y of the (k or v, head, part of its rows) to copy;
 // the blocks of y == 0 also write the child's table row.
-__global__ void __launch_bounds__(kThreads) fork_kernel(const ForkParams p) {
+__global__ void __launch_bounds__(kThreads, kForkCtas) fork_kernel(const ForkParams p) {
   griddep_wait();
   const PoolParams& c = p.pool;
   const int64_t i = blockIdx.x;
@@ -145,12 +149,32 @@ __device__ __forceinline__ int block_before(int mine, int* warps, int& all) {
   return incl - mine + (warp > 0 ? before : 0);
 }
 
+// The block that numbers the pages of a small table also marks them: 114 entries
+// 9.1 us, with the launches for it 14.5 us; 12288 entries 130.5 us, with them 125.4.
+constexpr int64_t kMarkEntries = 4096, kMarkPages = 131072;
+
 // New numbers and the list of moves, by one block: thread t takes the t-th part
 // of the pool, in words of 16 pages.
+template <bool kMark>
 __global__ void __launch_bounds__(kScanThreads) number_kernel(const CompactParams p) {
   __shared__ int warps[kScanThreads / 32];
   griddep_wait();
   const int64_t n = p.pool.num_pages, words = (n + 15) / 16;  // the array is padded with zeros to whole words
+  if (kMark) {
+    const PoolParams& c = p.pool;
+    for (int64_t w = threadIdx.x; w < words; w += kScanThreads)
+      reinterpret_cast<uint4*>(p.used)[w] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    const int width = static_cast<int>(c.max_pages), entries = static_cast<int>(c.num_seqs * c.max_pages);
+    for (int e = threadIdx.x; e < entries; e += kScanThreads) {
+      const int s = e / width, j = e - s * width;
+      const int page = c.table[s * c.ld_table + j];
+      if (j >= held(p, s, j == 0)) continue;
+      if (page >= c.num_pages) record_error(c.status, QERL_ERR_RANGE);
+      if (page >= 0 && page < c.num_pages) p.used[page] = 1;
+    }
+    __syncthreads();
+  }
   const int64_t each = (words + kScanThreads - 1) / kScanThreads;
   const int64_t w0 = min(threadIdx.x * each, words), w1 = min(w0 + each, words);
   const uint4* used = reinterpret_cast<const uint4*>(p.used);
@@ -278,10 +302,18 @@ qerl_status launch_kv_fork(const KvForkArgs& a, cudaStream_t s) {
   p.children = a.children;
   p.lengths = a.lengths;
   p.new_pages = a.new_pages;
-  // Blocks per child: enough for a whole page, up to 64 (a block takes 8 pieces at a time).
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return QERL_ERR_CUDA;
+  // Blocks per child: for a whole page 8 pieces at a time, but no more than twice
+  // what is resident together, as each looks its child up first (384 children of
+  // up to 64 rows, 8 heads of 128: 11.9 us, as many as are resident 16.5 us,
+  // without a limit 12.9 us).
   const int64_t pieces = 2ll * p.pool.kv_heads *
                          ((static_cast<int64_t>(p.pool.page_size) * p.pool.row_bytes + kWarpPiece - 1) / kWarpPiece);
-  const int64_t y = std::min<int64_t>((pieces + kThreads / 32 - 1) / (kThreads / 32), 64);
+  const int64_t whole = (pieces + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t y = std::max<int64_t>(1, std::min({whole, int64_t{64}, 2 * kForkCtas * static_cast<int64_t>(sms) / a.count}));
   return cuda_status(launch_dependent(fork_kernel, dim3(static_cast<unsigned>(a.count), static_cast<unsigned>(y)),
                                       kThreads, 0, s, p));
 }
@@ -307,14 +339,17 @@ qerl_status launch_kv_compact(const KvCompactArgs& a, cudaStream_t s) {
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return QERL_ERR_CUDA;
-  cudaError_t e = cudaMemsetAsync(p.used, 0, l.number - l.used, s);
-  if (e != cudaSuccess) return QERL_ERR_CUDA;
   const int64_t chunks = (c.max_pages + kEntries - 1) / kEntries;
-  if (c.num_seqs > 0 && chunks > 0 && c.num_pages > 0) {
-    const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(std::min<int64_t>(c.num_seqs, 65535)));
-    if (launch_dependent(mark_kernel, grid, kThreads, 0, s, p) != cudaSuccess) return QERL_ERR_CUDA;
+  if (c.num_seqs * c.max_pages <= kMarkEntries && c.num_pages <= kMarkPages) {
+    if (launch_dependent(number_kernel<true>, dim3(1), kScanThreads, 0, s, p) != cudaSuccess) return QERL_ERR_CUDA;
+  } else {
+    if (cudaMemsetAsync(p.used, 0, l.number - l.used, s) != cudaSuccess) return QERL_ERR_CUDA;
+    if (c.num_seqs > 0 && chunks > 0 && c.num_pages > 0) {
+      const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(std::min<int64_t>(c.num_seqs, 65535)));
+      if (launch_dependent(mark_kernel, grid, kThreads, 0, s, p) != cudaSuccess) return QERL_ERR_CUDA;
+    }
+    if (launch_dependent(number_kernel<false>, dim3(1), kScanThreads, 0, s, p) != cudaSuccess) return QERL_ERR_CUDA;
   }
-  if (launch_dependent(number_kernel, dim3(1), kScanThreads, 0, s, p) != cudaSuccess) return QERL_ERR_CUDA;
   return cuda_status(launch_dependent(move_kernel, dim3(static_cast<unsigned>(4 * sms)), kThreads, 0, s, p));
 }
 

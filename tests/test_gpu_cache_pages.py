@@ -224,6 +224,16 @@ def test_compact_pages_of_every_size(q_, hk, page, dim, dtype, in_place):
         assert torch.equal(before, pool.table)
 
 
+@pytest.mark.parametrize("n,most", [(64, 64), (65, 64), (4097, 1), (1, 5000), (300, 40)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compact_tables_of_every_size(q_, n, most, in_place):
+    """Around the size from which the marks have a launch of their own, and past it."""
+    r = random.Random(n)
+    pool, lengths = _random_pool(q_, r, 3001, n, most, 1, 2, 64, BF)
+    _, status = _compact(q_, pool, lengths, in_place)
+    assert status == "QERL_OK"
+
+
 def test_compact_long_rows(q_):
     """More entries in a row than a block takes at a time, and more rows."""
     r = random.Random(8)
