@@ -49,6 +49,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cuda_bf16.h>
+#include <type_traits>
 
 namespace qerl {
 namespace {
@@ -550,6 +551,11 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       return shared ? (n + 1 - i) >> 1 : n;
     }
     __device__ __forceinline__ int tile(int i, int j) const { return it.t0 + (shared ? 2 * j + i : j); }
+    // 32-key parts of key tile t that hold keys: the products and the softmax leave out the rest.
+    __device__ __forceinline__ int parts(int t) const {
+      const int keys = t < ctx ? it.len - t * kRows : it.n - (t - ctx) * kRows;
+      return keys >= kRows ? 4 : (keys + 31) >> 5;
+    }
   };
   auto take = [&](int k, Work& w) -> bool {
     const int e = k & 1;
@@ -645,21 +651,28 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       // One key tile: scores in, weights out, l and (rarely) the reference moved.
       // Both passes are loops over 32 keys, which read the scores twice: code
       // that runs through once a tile is fetched as slowly as it runs.
-      auto step = [&](int j, int t, bool masked, bool fresh) {
+      // Whole tiles in code of their own (kind kWhole, the others kPartial) take two parts at a time in the second pass, which hides their latencies
+      // beside the widening (64 x 6000 rows E4M3 396 us, in common code 426 us);
+      // without it the smaller code is faster (heads of 64, 96 sequences: 82 us, in
+      // common code 74 us).
+      constexpr int kAny = 0, kPartial = 1, kWhole = 2;
+      auto step = [&](auto kind, int j, int parts, bool hides, bool fresh, const uint32_t (&keep)[4]) {
+        constexpr int kKind = decltype(kind)::value;
+        const bool masked = kKind == kPartial || (kKind == kAny && hides);
         auto load = [&](int q, float (&x)[32]) {
           tmem_ld32(s_t + q * 32, x);
           tmem_ld_wait();
           pin<32>(x);
           if (masked) {
-            const uint32_t keep = sees(t, q);
+            const uint32_t bits = q < 2 ? (q == 0 ? keep[0] : keep[1]) : (q == 2 ? keep[2] : keep[3]);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if ((keep & (1u << e)) == 0) x[e] = -kInf;
+              if ((bits & (1u << e)) == 0) x[e] = -kInf;
           }
         };
         float top = -kInf;
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < (kKind == kWhole ? 4 : parts); ++q) {
           float x[32];
           load(q, x);
           float t2[2] = {top, x[0]};
@@ -697,8 +710,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         // (weights of new tokens over an E4M3 cache: divided by the value scale, in the exponent)
         const float sub = (mc == -kInf ? 0.0f : mc) + (kFp8 && fresh ? v_log2 : 0.0f);
         const uint64_t sub2 = pair(-sub, -sub);
-#pragma unroll 2
-        for (int q = 0; q < 4; ++q) {
+        auto weigh = [&](int q, bool half, bool all) {
           float x[32];
           load(q, x);
           uint32_t y[16];
@@ -712,12 +724,20 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
             y[e] = pack_bf16(a, b);
           }
           tmem_st_x16(s_t + q * 16, y);
-          if (q & 1) {  // half of the keys: the product with v may begin
+          if (half || all) {  // half of the keys, or all: the product with v may begin
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_a(p_full(i, q >> 1));
+            if (lane == 0 && half) mbar_arrive_a(p_full(i, 0));
+            if (lane == 0 && all) mbar_arrive_a(p_full(i, 1));
           }
+        };
+#pragma unroll(kKind == kWhole ? 2 : 1)
+        for (int q = 0; q < (kKind == kWhole ? 4 : parts); ++q) {
+          if (kKind == kWhole)
+            weigh(q, q == 1, q == 3);
+          else
+            weigh(q, q == 1 || (q == 0 && parts == 1), q + 1 == parts);
         }
         float s0, s1;
         unpair(add2(part[0], part[1]), s0, s1);
@@ -727,11 +747,21 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       for (int j = 0; j < mine_n; ++j) {
         const int t = w.tile(i, j);
         const bool fresh = t >= w.ctx, masked = fresh || w.it.len - t * kRows < kRows;
+        uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+        if (masked) {  // (while the scores are computed)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) keep[q] = sees(t, q);
+        }
         ok = __all_sync(~0u, wait_for(s_full(i), (tiles_done + j) & 1, abort_flag, p.status));
         if (ok && fresh) ok = clean_values(t - w.it.t0);
         if (!ok) break;
         tc_fence_after();
-        step(j, t, masked, fresh);
+        if (!kFp8)
+          step(std::integral_constant<int, kAny>{}, j, w.parts(t), masked, fresh, keep);
+        else if (masked)
+          step(std::integral_constant<int, kPartial>{}, j, w.parts(t), true, fresh, keep);
+        else
+          step(std::integral_constant<int, kWhole>{}, j, 4, false, fresh, keep);
       }
       tiles_done += mine_n;
       n0 = (n0 + w.it.t1 - w.it.t0) % S::kLaps;
@@ -1095,7 +1125,6 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       const uint32_t leader = elect_lane();
       // Each issues the products of one query tile.
       const int i = warp - kIssuer;
-      const uint32_t id_s = idesc_bf16_f32(128, 128);
       const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // v: rows along the contraction
       // A slot is free after two arrivals: one of each issuer where both use it,
       // or both of the one that does.
@@ -1121,7 +1150,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
             const uint32_t qa = sbase + (w.shared ? 0 : i * S::kTile), ka = slot_at(0, n0 + tile_of(j));
             // a negative factor of the scores: the product is negated
             const bool negative = p.scale_log2 < 0.0f != (w.tile(i, j) < w.ctx && ks < 0.0f);
-            const uint32_t id = id_s | (negative ? 1u << 13 : 0u);
+            const uint32_t id = idesc_bf16_f32(128, 32 * w.parts(w.tile(i, j))) | (negative ? 1u << 13 : 0u);
 #pragma unroll
             for (int d = 0; d < S::kPanels; ++d)
 #pragma unroll
@@ -1134,9 +1163,10 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           };
           auto values = [&](int j, int half) {
             const uint32_t va = slot_at(1, n0 + tile_of(j));
+            const int steps = 2 * w.parts(w.tile(i, j));
 #pragma unroll
             for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-              mma_ts(leader, tmem + 256 + i * D, tmem + i * 128 + kk * 8, sw128_mnmajor_desc(va + kk * 2048), id_o,
+              if (kk < steps) mma_ts(leader, tmem + 256 + i * D, tmem + i * 128 + kk * 8, sw128_mnmajor_desc(va + kk * 2048), id_o,
                      j > 0 || kk > 0 ? 1u : 0u);
           };
           ok = __all_sync(~0u, wait_part(0, 0));
