@@ -501,6 +501,9 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       const unsigned hit = __ballot_sync(~0u, incl - mine <= begin && begin < incl);
       seq = hit != 0 ? __ffs(hit) - 1 : 0;
       inside = begin - __shfl_sync(~0u, incl - mine, seq);
+      int* const fields = reinterpret_cast<int*>(&sq);  // that lane's, to all
+#pragma unroll
+      for (int f = 0; f < static_cast<int>(sizeof(Sequence) / sizeof(int)); ++f) fields[f] = __shfl_sync(~0u, fields[f], seq);
     }
   } else {
     bool bad = false;
@@ -539,7 +542,10 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
     __syncthreads();
     seq = place[0];
     inside = *inside_seq;
+    if (warp == kFinder && busy) sequence(p, seq, sq);
   }
+  // The kernel that joins partials may be set up; it begins when this one has ended.
+  griddep_launch_dependents();
 
   struct Work {
     Item it;
@@ -1099,7 +1105,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         for (int u = 0; u <= 2 * (it.t1 - it.t0); ++u) {
           const int t = it.t0 + (u >> 1), part = u & 1;
           const bool tail = t == it.t1, due = u == 4 || tail;
-          if (!asked && u > 0 && queries_free(due)) {
+          if (!asked && queries_free(due)) {
             asked = true;
             load_queries();
           }
@@ -1239,7 +1245,6 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       bool go = busy;
       if (go) {
         int b = seq;
-        sequence(p, b, sq);
         const int wide = sq.tiles + kSegmentCost;
         long long seg = quotient(inside, wide);
         int t = static_cast<int>(inside - seg * wide);
@@ -1255,10 +1260,10 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           const int t1 = static_cast<int>(min(static_cast<long long>(needed), t + (end - pos)));
           if (t < t1) {
             const bool whole = t == 0 && t1 == needed;
-            if (t == 0 && !whole)
-              job = make_int4(b, kv_head, block * kBlock, owner(base + needed - 1) - static_cast<int>(blockIdx.x) + 1);
             go = put({sq.start, sq.n, sq.len, b, kv_head, block * kBlock, t, t1, whole ? -1 : t == 0 ? 1 : 0,
                       block * kBlock / p.group, block * kBlock % p.group});
+            if (t == 0 && !whole)
+              job = make_int4(b, kv_head, block * kBlock, owner(base + needed - 1) - static_cast<int>(blockIdx.x) + 1);
           }
           pos = base + sq.tiles + kSegmentCost;
           t = 0;
@@ -1280,8 +1285,8 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           }
         }
       }
-      if (lane == 0) p.jobs[blockIdx.x] = job;
       if (!busy || go) put({});
+      if (lane == 0) p.jobs[blockIdx.x] = job;
     }
   }
   __syncwarp();
