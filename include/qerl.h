@@ -592,7 +592,8 @@ QERL_API qerl_status qerl_prompt_attention(const void* q, int64_t ldq, const voi
  *   qerl_window_prompt_attention: row i attends to rows j <= i with
  *     i - j < window or j < sinks.
  * window >= 1, sinks >= 0.  Everything else as for the call of all rows, its
- * workspace included; a window that no sequence outgrows gives its result. */
+ * workspace included; a window that no sequence outgrows gives its result but for
+ * roundings. */
 QERL_API qerl_status qerl_window_decode_attention(const qerl_kv_cache* cache, const void* q, int64_t ldq,
                                                   int num_heads, const int32_t* lengths, int32_t window,
                                                   int32_t sinks, float scale, void* out, int64_t ldo, float* lse,

@@ -487,6 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       // One key tile: scores in, weights out, l and (rarely) the reference moved.
+      // (With a window mc is a score, not in base-2 units, and is taken from the
+      // scores before their product with c: the fused product leaves the rounding of
+      // a large reference in the exponent, which overflows from scores of 2^31 on.)
       auto step = [&](int j) {
         float x[128];
 #pragma unroll
@@ -524,7 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             float a, b;
-            unpair(fma2(pair(x[half * 64 + 2 * e], x[half * 64 + 2 * e + 1]), c2, sub2), a, b);
+            const uint64_t x2 = pair(x[half * 64 + 2 * e], x[half * 64 + 2 * e + 1]);
+            unpair(kWindow ? fma2(add2(x2, sub2), c2, 0) : fma2(x2, c2, sub2), a, b);
             a = ex2(a);
             b = ex2(b);
             sums[e & 1] = add2(sums[e & 1], pair(a, b));
@@ -554,11 +558,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           t4[q] = fmaxf(t4[q], x[q * 32 + 31]);
         }
         const float top = max3(fmaxf(t4[0], t4[1]), t4[2], t4[3]);
-        const float tc = top == -kInf ? -kInf : top * p.c;
-        if (__any_sync(~0u, tc > mc + kSlack)) {
+        const float tc = kWindow ? top : top == -kInf ? -kInf : top * p.c;
+        if (__any_sync(~0u, kWindow ? (tc - mc) * p.c > kSlack : tc > mc + kSlack)) {
           const float up = fmaxf(mc, tc);
           if (j > 0) {
-            const float f = mc == up ? 1.0f : ex2(mc - up);
+            const float f = mc == up ? 1.0f : ex2(kWindow ? (mc - up) * p.c : mc - up);
             l *= f;
 #pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
@@ -662,7 +666,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         if (live && p.lse != nullptr)
-          p.lse[row * p.heads + w.head] = l == 0.0f ? -kInf : (mc + log2f(l)) * 0.69314718055994530942f;
+          p.lse[row * p.heads + w.head] =
+              l == 0.0f ? -kInf : ((kWindow ? mc * p.c : mc) + log2f(l)) * 0.69314718055994530942f;
         __syncwarp();
       }
     }

@@ -595,7 +595,13 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       int row_head;
       const int row_token = token_of(p, w.it, row - w.it.row0, row_head);
       const int token = row < rows ? row_token : 0;
-      float mc = -kInf, l = 0.0f;  // the reference in base-2 units and the sum of 2^(s - m)
+      // The reference in base-2 units and as a score (of the cache's tiles or of the
+      // new tokens', whose units may differ), and the sum of 2^(s - m).  The
+      // reference is taken from the scores before their product with c: a fused
+      // product would leave the rounding of a large m in the exponent, which
+      // overflows from scores of 2^31 on.
+      float mc = -kInf, ref = -kInf, l = 0.0f;
+      bool ref_fresh = false;
       float v_scale = 1.0f, v_inverse = 1.0f, v_log2 = 0.0f, c_ctx = fabsf(p.scale_log2);
       if (kFp8) {
         if (p.k_scale != nullptr) c_ctx = fabsf(p.scale_log2 * p.k_scale[w.it.kv_head]);
@@ -691,12 +697,14 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           top = max3(t2[0], t2[1], x[31]);
         }
         const float c = kFp8 && !fresh ? c_ctx : c_new;
-        const uint64_t c2 = pair(c, c);
-        const float tc = top == -kInf ? -kInf : top * c;
-        if (__any_sync(~0u, tc > mc + kSlack)) {
-          const float up = fmaxf(mc, tc);
+        if (kFp8 && fresh != ref_fresh) {
+          ref = mc == -kInf ? -kInf : mc / c;
+          ref_fresh = fresh;
+        }
+        if (__any_sync(~0u, (top - ref) * c > kSlack)) {
+          const float up = fmaxf(ref, top);
           if (j > 0) {
-            const float f = mc == up ? 1.0f : ex2(mc - up);
+            const float f = ref == up ? 1.0f : ex2((ref - up) * c);
             l *= f;
 #pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
@@ -710,12 +718,15 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
               tmem_st_x16(o_t + q * 16, y);
             }
           }
-          mc = up;
+          ref = up;
+          mc = up == -kInf ? -kInf : up * c;
         }
         uint64_t part[2] = {0, 0};  // two chains of two fp32 sums
-        // (weights of new tokens over an E4M3 cache: divided by the value scale, in the exponent)
-        const float sub = (mc == -kInf ? 0.0f : mc) + (kFp8 && fresh ? v_log2 : 0.0f);
-        const uint64_t sub2 = pair(-sub, -sub);
+        const float sub = ref == -kInf ? 0.0f : ref;
+        const uint64_t c2 = pair(c, c), sub2 = pair(-sub, -sub);
+        // weights of new tokens over an E4M3 cache: divided by the value scale, in the exponent
+        const float lower = kFp8 && fresh ? -v_log2 : 0.0f;
+        const uint64_t lower2 = pair(lower, lower);
         auto weigh = [&](int q, bool half, bool all) {
           float x[32];
           load(q, x);
@@ -723,7 +734,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float a, b;
-            unpair(fma2(pair(x[2 * e], x[2 * e + 1]), c2, sub2), a, b);
+            unpair(fma2(add2(pair(x[2 * e], x[2 * e + 1]), sub2), c2, lower2), a, b);
             a = ex2(a);
             b = ex2(b);
             part[e & 1] = add2(part[e & 1], pair(a, b));

@@ -288,3 +288,43 @@ def test_compact_captured(q_):
         pool.table = want  # the next replay starts from the new table
         pool.dev_table.copy_(new)
         pool.same()
+
+
+def test_pages_past_32_bits(q_):
+    """Byte and element offsets past 2^32: a copy to a far page, and the far pages moved to the front."""
+    num, hk, page, dim = 2 ** 20 + 9, 2, 16, 128
+    pages = [torch.zeros((num, hk, page, dim), dtype=BF, device="cuda") for _ in range(2)]
+    a, b = num - 1, num - 3
+    for x in pages:
+        x[a] = torch.randn((hk, page, dim), device="cuda").to(BF)
+    want = [x[a].clone() for x in pages]
+    table = _i32([[a], [0]])
+    cache = q_.kv_cache(*pages, table)
+    ws = q_.workspace(q_.qerl_kv_fork_workspace_size())
+    q_.kv_fork(cache, _i32([0]), _i32([1]), _i32([11]), _i32([b]), ws)
+    assert _status(q_, ws) == "QERL_OK" and table.tolist() == [[a], [b]]
+    for x, w in zip(pages, want):
+        assert torch.equal(x[b, :, :11], w[:, :11]) and (x[b, :, 11:] == 0).all()
+    ws = q_.workspace(q_.qerl_kv_compact_workspace_size(num))
+    new, live = q_.kv_compact(cache, _i32([16, 11]), ws)
+    assert _status(q_, ws) == "QERL_OK" and new.tolist() == [[1], [0]] and live.item() == 2
+    for x, w in zip(pages, want):
+        assert torch.equal(x[1], w) and torch.equal(x[0, :, :11], w[:, :11])
+
+
+def test_two_forks_and_compactions_at_once(q_):
+    """On two streams, each with pools and workspaces of its own."""
+    r = random.Random(7)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    pools = [_random_pool(q_, r, 4000, 50, 200, 2, 8, 128, BF) for _ in streams]
+    made = [(_i32(lengths), torch.empty_like(pool.dev_table).contiguous(), _i32([0]),
+             q_.workspace(q_.qerl_kv_compact_workspace_size(4000))) for pool, lengths in pools]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for (pool, _), (lengths, new, live, ws), s in zip(pools, made, streams):
+            q_.check(q_.qerl_kv_compact(pool.cache, lengths, new, live, ws, stream=s))
+    torch.cuda.synchronize()
+    for (pool, lengths), (_, new, live, ws) in zip(pools, made):
+        count, want = _compact_plain(pool, lengths)
+        assert live.item() == count and torch.equal(new.cpu(), want) and _status(q_, ws) == "QERL_OK"
+        pool.same()

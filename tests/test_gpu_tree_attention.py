@@ -401,3 +401,74 @@ def test_a_verified_draft_is_appended(q_):
             o, l, to, tl = masked64(case.q[last[s], h][None], k, v, 0.1, keep, "split")
             assert_within(one[s, h][None], o, to)
             assert_within(lse1[s, h][None], l, tl)
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_pages_past_32_bits(q_, dtype):
+    """Byte offsets (and for bf16 element offsets) in the cache past 2^32."""
+    case = Case(q_, [500], [7], 8, 2, 128, 16, dtype, "tree", seed=31)
+    first = 2 ** 20 + 5
+    far = [torch.empty((first + x.shape[0], *x.shape[1:]), dtype=x.dtype, device="cuda") for x in case.pages]
+    for a, b in zip(far, case.pages):
+        a[first:] = b
+    assert far[0].nbytes > 2 ** 32
+    table = case.cache.tensors[2]
+    table += first
+    case.cache = q_.kv_cache(far[0].view(dtype), far[1].view(dtype), table, case.ks, case.vs)
+    out, lse = case.run(0.1)
+    case.check(0.1, out, lse)
+
+
+def test_two_calls_at_once(q_):
+    """On two streams, each with a workspace of its own."""
+    cases = [Case(q_, [3000, 20, 700], [30, 9, 61], 14, 2, 128, 16, BF, "tree", seed=41),
+             Case(q_, [5000], [12], 8, 2, 64, 16, F8, "chain", seed=42)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    made = []
+    for c in cases:
+        shape = (c.tokens, c.heads, c.dim)
+        made.append((torch.empty(shape, dtype=BF, device="cuda"), torch.empty(shape[:2], device="cuda"), _i32(c.cu),
+                     _i32(c.lens), c.workspace()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, (out, lse, cu, lengths, ws), s in zip(cases, made, streams):
+            q_.check(q_.qerl_tree_attention(c.cache, c.q, c.k, c.v, cu, lengths, c.mask, 0.1, out, lse, ws, stream=s))
+    torch.cuda.synchronize()
+    for c, (out, lse, _, _, ws) in zip(cases, made):
+        assert q_.qerl_read_status(ws) == 0
+        c.check(0.1, out, lse)
+
+
+def test_extreme_scores_and_values(q_):
+    """Queries near bf16's largest give infinite scores or weights of one key alone; nothing else is touched."""
+    case = Case(q_, [200, 130], [6, 6], 4, 2, 64, 16, BF, "tree", seed=43)
+    case.q[:6] *= 1e30
+    out, lse = case.run(1.0)
+    for s in (1,):
+        rows = slice(6, 12)
+        keep = torch.cat([torch.ones((6, 130), dtype=torch.bool, device="cuda"), case.keep[s]], 1)
+        for h in range(4):
+            k, v = (torch.cat([x[h // 2].double(), y[rows, h // 2].double()]) for x, y in zip(case.rows[s], (case.k, case.v)))
+            o, l, to, tl = masked64(case.q[rows, h], k, v, 1.0, keep, "bf16")
+            assert_within(out[rows, h], o, to)
+            assert_within(lse[rows, h], l, tl)
+    # scores up to 1e32: the largest key has all of the weight
+    for h in range(4):
+        keep = torch.cat([torch.ones((6, 200), dtype=torch.bool, device="cuda"), case.keep[0]], 1)
+        k, v = (torch.cat([x[h // 2].double(), y[:6, h // 2].double()]) for x, y in zip(case.rows[0], (case.k, case.v)))
+        score = torch.where(keep, case.q[:6, h].double() @ k.T, -math.inf)
+        top2 = score.topk(2, 1).values
+        clear = top2[:, 0] - top2[:, 1] > 2.0 ** -20 * (case.q[:6, h].double().abs() @ k.abs().T).amax(1) + 100
+        best = v[score.argmax(1)]
+        assert clear.any()
+        assert torch.equal(out[:6, h][clear].double(), best[clear])
+
+
+@pytest.mark.parametrize("scale_log2", [-64, -20, 0, 30, 64])
+def test_value_scales_of_a_wide_range(q_, scale_log2):
+    """New tokens of the size of the cache's values, whatever the scale."""
+    case = Case(q_, [150], [10], 4, 2, 64, 16, F8, "tree", seed=44)
+    case.vs.fill_(2.0 ** scale_log2)
+    case.v.mul_(2.0 ** scale_log2)
+    out, lse = case.run(0.1)
+    case.check(0.1, out, lse)

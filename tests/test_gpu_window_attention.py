@@ -160,10 +160,35 @@ def test_prompt_window_without_effect_is_the_plain_call(q_):
     q, k, v = _rows(700, 4, 128, g), _rows(700, 2, 128, g), _rows(700, 2, 128, g)
     cu = torch.tensor([0, 300, 700], dtype=torch.int32, device="cuda")
     want = q_.prompt_attention(q, k, v, cu, 0.1)
-    for window, sinks in ((700, 0), (400, 3), (1, 700)):
+    got = q_.window_prompt_attention(q, k, v, cu, 700, 0, 0.1)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    for window, sinks in ((400, 3), (1, 700)):  # of the rows, not of a sequence: the weights round otherwise
         got = q_.window_prompt_attention(q, k, v, cu, window, sinks, 0.1)
-        for a, b in zip(got, want):
-            assert torch.equal(a, b)
+        _check_prompt(q, k, v, [0, 300, 700], window, sinks, 0.1, *got)
+        _check_prompt(q, k, v, [0, 300, 700], 700, 0, 0.1, *got)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_scores_of_any_size(q_, dim):
+    """Scores up to 1e32: the largest visible key has all of the weight, and nothing is lost to the reference."""
+    g = torch.Generator(device="cuda").manual_seed(15)
+    n, window, sinks = 400, 100, 3
+    q, k, v = _rows(n, 2, dim, g), _rows(n, 1, dim, g), _rows(n, 1, dim, g)
+    for size in (1e9, 1e12, 1e30):
+        big = q * size
+        out, lse = _prompt(q_, big, k, v, [0, n], window, sinks, 1.0)
+        at = torch.arange(n, device="cuda")
+        keep = window_keep(at, at, window, sinks)
+        for h in range(2):
+            score = torch.where(keep, big[:, h].double() @ k[:, 0].double().T, -math.inf)
+            top2 = score.topk(2, 1).values
+            # fp32 products and sums: 2^-20 of the magnitudes (attention_reference), and 2^100 between the weights
+            near = 2.0 ** -20 * (big[:, h].double().abs() @ k[:, 0].double().abs().T).amax(1)
+            clear = top2[:, 0] - top2[:, 1] > 2 * near + 100
+            assert clear[1:].float().mean() > 0.9
+            assert torch.equal(out[clear, h].double(), v[score.argmax(1)][clear, 0].double())
+            assert ((lse[:, h].double() - top2[:, 0]).abs() <= near + 2.0 ** -22 * top2[:, 0].abs() + math.log(n))[clear].all()
 
 
 def test_prompt_rows_masked_by_infinite_scores(q_):
