@@ -638,7 +638,8 @@ QERL_API qerl_status qerl_window_prompt_attention(const void* q, int64_t ldq, co
  * type.  A page number outside the cache records QERL_ERR_RANGE and its rows read
  * as zeros.  The result does not depend on timing.
  * workspace >= qerl_tree_attention_workspace_size(), 256-byte aligned, its header
- * (256 bytes) zero-filled before its first use; ordered calls may share it. */
+ * (256 bytes) zero-filled before its first use; ordered calls of any shapes may
+ * share it, but not with qerl_decode_attention, whose counters it would spoil. */
 QERL_API size_t qerl_tree_attention_workspace_size(int64_t tokens, int num_heads, int num_kv_heads, int head_dim,
                                                    int64_t num_seqs);
 QERL_API qerl_status qerl_tree_attention(const qerl_kv_cache* cache, const void* q, int64_t ldq, const void* k,
@@ -687,7 +688,8 @@ QERL_API qerl_status qerl_kv_fork(const qerl_kv_cache* cache, const int32_t* par
  *   live_pages device int32: L.
  * Pages past L keep their contents.  workspace >=
  * qerl_kv_compact_workspace_size(num_pages), 256-byte aligned, its header (256
- * bytes) zero-filled before its first use; ordered calls may share it. */
+ * bytes) zero-filled before its first use; ordered calls for pools of any size
+ * may share it, but not with qerl_decode_attention. */
 QERL_API size_t qerl_kv_compact_workspace_size(int64_t num_pages);
 QERL_API qerl_status qerl_kv_compact(const qerl_kv_cache* cache, const int32_t* lengths, int32_t* new_table,
                                      int64_t ld_new, int32_t* live_pages, void* workspace, size_t ws_bytes,

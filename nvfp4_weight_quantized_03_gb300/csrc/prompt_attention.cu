@@ -1,7 +1,8 @@
 // prompt_attention.cu -- causal attention of packed whole prompts on the
-// tensor cores.
+// tensor cores, of all rows or within a window.
 //
-//   s_ij = scale * q_i . k_j,  j <= i within the sequence;
+//   s_ij = scale * q_i . k_j,  j <= i within the sequence (with a window of w rows
+//   and n sinks: and i - j < w or j < n);
 //   out_i = sum_j exp(s_ij - lse_i) v_j,   lse_i = log sum_j exp(s_ij)
 //
 // Bound: the two products, 4 * head_dim operations per (i, j <= i, head).
@@ -46,6 +47,17 @@
 // products take 2048).  Heads of 64 have half the products per exponential and
 // are held by the softmax: 2400 cycles a pair, of which the exponentials of
 // both tiles take 1024 and their issue 1320 on each scheduler.
+//
+// With a window (16384 rows x 40 heads, window 2048, 16 sinks: 517 us, 0.67 of the
+// rate of the visible pairs' products; 10 to 3001 rows x 28 heads, window 500, 4
+// sinks: 127 us, 0.30) an item has the same steps at the same pace, but more of
+// what it computes is masked: a row of 500 visible keys takes part in 7 key tiles
+// of 128, one of them for 4 sinks.  Tried and left: the second query tile leaving
+// out the first tile of the window, which it never sees (its turn stays idle, or,
+// with its steps moved up, four slots are too few: 3% slower); a tile of 32 keys
+// for the sinks (5% slower: its code is fetched cold once an item); the softmax as
+// loops over 32 keys (10% slower: the scores are read twice, and here no other
+// warps contend for instruction fetches).
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -43,6 +43,21 @@
 // the values of the new tokens are looked through before the product; elements
 // that are not finite are replaced by 0 there and added back in the end to the
 // rows that do see them.
+//
+// Measured: 48 sequences to 8192 rows, 25 nodes, 40/8 heads of 128: 98 us = 0.77 of
+// the copy rate (a segment's start and end cost two to three tiles); 64 x 6000
+// rows E4M3, 61 nodes, 28/4 heads: 417 us where the products take 179 (215 with the
+// rows that fill 512): widening and softmax share the schedulers (issue 54%,
+// tensor pipe 35%); 96 sequences to 2500 rows, 30 nodes, 32/8 heads of 64: 79 us
+// where the bytes take 28 (five to nine segments a CTA, each 11000 cycles for
+// three tiles: a chain of latencies); a chain of 5 over 777 rows 12.2 us.  What
+// made it so: instruction fetches bound the first forms (1.9 warps of a scheduler
+// waited for one), so that code is small and in loops: E4M3 829 us with every
+// kind of load inlined where it is used, 753 us in one place each, 713 us without
+// a polling wait, 507 us with the widening as a loop; bf16 108 to 101 us with the
+// softmax as loops.  Loads that announce themselves (130 to 109 us), four warps
+// each for keys and values of an E4M3 cache (510 to 428 us) and products of the
+// parts of a tile that hold keys (79 to 77 us) came on top.
 #include "qerl_internal.h"
 #include "qerl_ptx.cuh"
 
@@ -99,7 +114,12 @@ struct Shape {
   static constexpr int kThreads = 384 + 32 * kLoadWarps;
   // At launch 512 threads have 128 registers each, 640 have 96:
   // 256 * 184 + 128 * 88 + 128 * 56 = 512 * 128, 256 * 136 + 256 * 72 + 128 * 64 = 640 * 96.
+  // (A share above the launch's goes by setmaxnreg.inc, one below by .dec, and their
+  // sum stays within the launch's: anything else faults or waits forever.)
   static constexpr int kSoftmaxRegs = kFp8 ? 136 : 184, kLoadRegs = kFp8 ? 72 : 88, kOtherRegs = kFp8 ? 64 : 56;
+  static_assert(kSoftmaxRegs * 256 + kLoadRegs * 32 * kLoadWarps + kOtherRegs * 128 <= kThreads * (kFp8 ? 96 : 128) &&
+                    kSoftmaxRegs >= (kFp8 ? 96 : 128) && kLoadRegs <= (kFp8 ? 96 : 128) && kOtherRegs <= (kFp8 ? 96 : 128),
+                "shares of the launch's registers");
   static constexpr int kPanels = D / 64;
   static constexpr uint32_t kTile = kPanels * kPanel;
   // Slots of the keys' and of the values' ring.
