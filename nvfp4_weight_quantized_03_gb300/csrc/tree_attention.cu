@@ -294,8 +294,8 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
   return true;
 }
 
-// The scheduler is up to two items ahead, and an item may last as long as the
-// cache is long: it waits until another role gives up (or some 2000 s).
+// The warp that finds the items is up to two ahead, and an item may last as long
+// as the cache is long: it waits until another role gives up (or some 2000 s).
 __device__ __forceinline__ bool wait_patiently(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
   for (int i = 0; i < (1 << 27); ++i) {
     if (mbar_try_wait_hint_a(bar, parity, QERL_WAIT_HINT_NS)) return true;
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         mc = top;
       }
       const bool live = row < rows;
-      const bool fix = dirty[k & 3] == k + 1;
+      const bool fix = __any_sync(~0u, dirty[k & 3] == k + 1);
       const float f = l == 0.0f ? 0.0f : v_scale / l;
       const bool whole = w.it.slot < 0;
       float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (whole ? 0 : w.it.slot)) * slot_floats(p.slot_rows, D);
@@ -859,18 +859,33 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           tmem_ld_wait();
           pin<32>(v);
         }
-        if (fix && live) {
+        if (fix) {
+          // A lane looks through one of 32 tokens, then the warp goes through those with something to add back.
           for (int t = max(w.it.t0, w.ctx); t < w.it.t1; ++t)
-            for (int q = 0; q < 4; ++q) {
-              uint32_t keep = sees(t, q);
-              while (keep != 0) {
-                const int node = (t - w.ctx) * kRows + q * 32 + __ffs(keep) - 1;
-                keep &= keep - 1;
-                const __nv_bfloat16* src = p.v + (static_cast<int64_t>(w.it.start) + node) * p.ldv + w.it.kv_head * D + col;
+            for (int q = 0; q < 4 && (t - w.ctx) * kRows + q * 32 < w.it.n; ++q) {
+              const uint32_t keep = sees(t, q);
+              const int node = (t - w.ctx) * kRows + q * 32;
+              const __nv_bfloat16* src = p.v + (static_cast<int64_t>(w.it.start) + node) * p.ldv + w.it.kv_head * D + col;
+              uint32_t sum = 0;
+              if (node + lane < w.it.n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint4 a = *reinterpret_cast<const uint4*>(src + lane * p.ldv + e * 8);
+                  sum = times0_plus(a.x, sum);
+                  sum = times0_plus(a.y, sum);
+                  sum = times0_plus(a.z, sum);
+                  sum = times0_plus(a.w, sum);
+                }
+              }
+              uint32_t found = __ballot_sync(~0u, (sum & 0x7FFF7FFFu) != 0) & __reduce_or_sync(~0u, keep);
+              while (found != 0) {
+                const int x = __ffs(found) - 1;
+                found &= found - 1;
+                const float mine = __bfloat162float(src[x * p.ldv + lane]);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                  const float y = __bfloat162float(src[e]);
-                  if (!(fabsf(y) < kInf)) v[e] += y * v_inverse;
+                  const float y = __shfl_sync(~0u, mine, e);
+                  if ((keep >> x & 1) != 0 && !(fabsf(y) < kInf)) v[e] += y * v_inverse;
                 }
               }
             }
@@ -1323,7 +1338,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
   __syncwarp();
   {  // every MMA is done before the tensor memory goes back (bounded)
     volatile int no_abort = 0;
-    wait_for(done, 0, &no_abort, p.status);
+    if (!wait_patiently(done, 0, abort_flag, p.status)) wait_for(done, 0, &no_abort, p.status);
   }
   tc_fence_before();
   __syncthreads();

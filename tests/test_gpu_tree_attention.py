@@ -472,3 +472,37 @@ def test_value_scales_of_a_wide_range(q_, scale_log2):
     case.v.mul_(2.0 ** scale_log2)
     out, lse = case.run(0.1)
     case.check(0.1, out, lse)
+
+
+@pytest.mark.parametrize("heads,dim", [(1, 128), (3, 64)])
+def test_long_chain_with_values_that_are_not_finite(q_, heads, dim):
+    """What is added back to the rows that see it is found in a time that no wait of the kernel takes for a fault."""
+    n, at = 150000, [3, 70001, 149990]
+    g = torch.Generator(device="cuda").manual_seed(21)
+    q, k, v = _rows(n, heads, dim, g), _rows(n, 1, dim, g), _rows(n, 1, dim, g)
+    cache = q_.kv_cache(*(torch.zeros((1, 1, 16, dim), dtype=BF, device="cuda") for _ in range(2)), _i32([[0]]))
+    ws = q_.workspace(q_.qerl_tree_attention_workspace_size(n, heads, 1, dim, 1))
+
+    def run():
+        out, lse = torch.empty((n, heads, dim), dtype=BF, device="cuda"), torch.empty((n, heads), device="cuda")
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        q_.check(q_.qerl_tree_attention(cache, q, k, v, _i32([0, n]), _i32([5]), None, dim ** -0.5, out, lse, ws))
+        end.record()
+        assert q_.qerl_read_status(ws) == q_.QERL_OK
+        return out, lse, start.elapsed_time(end)
+
+    for x, a in enumerate(at):
+        v[a, 0, 7 * x + 1] = (math.inf, math.nan, -math.inf)[x]
+    out, lse, slow = run()
+    for x, a in enumerate(at):
+        v[a, 0, 7 * x + 1] = 0
+    clean, lse2, fast = run()
+    assert torch.equal(lse, lse2) and torch.isfinite(clean.float()).all()
+    for x, a in enumerate(at):
+        column = out[:, :, 7 * x + 1].float()
+        assert (column[a:] == math.inf).all() if x == 0 else not torch.isfinite(column[a:]).any()
+        assert torch.equal(out[:a, :, 7 * x + 1], clean[:a, :, 7 * x + 1])
+        out[:, :, 7 * x + 1] = clean[:, :, 7 * x + 1]
+    assert torch.equal(out, clean)
+    assert slow < 20 * fast  # (one token after the other in every thread: 80 times)
