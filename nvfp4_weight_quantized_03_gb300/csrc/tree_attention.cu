@@ -40,9 +40,9 @@
 // are bf16, are divided by it first.
 //
 // A masked weight is 0, but 0 * NaN is NaN: rows past a length read as zeros, and
-// the values of the new tokens are looked through before the product; elements
-// that are not finite are replaced by 0 there and added back in the end to the
-// rows that do see them.
+// the values of new tokens that some row of the item does not see are looked
+// through before the product; elements that are not finite are replaced by 0 there
+// and added back in the end to the rows that do see them.
 //
 // Measured: 48 sequences to 8192 rows, 25 nodes, 40/8 heads of 128: 98 us = 0.77 of
 // the copy rate (a segment's start and end cost two to three tiles); 64 x 6000
@@ -314,9 +314,25 @@ __device__ __forceinline__ float weight_of(float m, float top) {
 // A sequence's place on the line.
 struct Sequence {
   int start, n, len;  // its first new token, their count, its rows in the cache
-  int blocks, ctx, tiles;  // segments per key-value head; key tiles of the cache, of a segment
+  int blocks, ctx, tiles;  // segments per key-value head; key tiles of the cache, of all keys
+  // Key tiles of a segment.  In order, a block sees the new tokens up to its last row's.
+  __device__ __forceinline__ int needed(const TreeParams& p, int block) const {
+    if (p.mask != nullptr || block + 1 >= blocks) return tiles;
+    return ctx + (block * kBlock + kBlock - 1) / p.group / kRows + 1;
+  }
+  // Cost of the segments of a key-value head's first `count` blocks.  In order,
+  // block i sees floor((2 i + 1) / group) + 1 tiles of new tokens; with i = a * group + b
+  // the quotient is 2 a, one more from b = group / 2 on.
+  __device__ __forceinline__ long long before(const TreeParams& p, int count) const {
+    if (p.mask != nullptr || count == 0) return static_cast<long long>(count) * (tiles + kSegmentCost);
+    const long long inner = min(count, blocks - 1);
+    const int a = static_cast<int>(inner) / p.group, b = static_cast<int>(inner) - a * p.group, z = p.group >> 1;
+    const long long quotients =
+        static_cast<long long>(a) * (a - 1) * p.group + static_cast<long long>(a) * (p.group - z + 2 * b) + max(b - z, 0);
+    return inner * (ctx + 1 + kSegmentCost) + quotients + (count == blocks ? tiles + kSegmentCost : 0);
+  }
   __device__ __forceinline__ long long cost(const TreeParams& p) const {
-    return n > 0 ? static_cast<long long>(p.kv_heads) * blocks * (tiles + kSegmentCost) : 0;
+    return n > 0 ? p.kv_heads * before(p, blocks) : 0;
   }
 };
 // false: its offsets break the rules.
@@ -644,6 +660,8 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         const unsigned long long m = p.mask[static_cast<int64_t>(w.it.start + token) * p.words + word];
         return static_cast<uint32_t>(m >> (at & 32)) & below(w.it.n - at);
       };
+      // The first tile of new tokens of which this item's rows may not see all.
+      const int first_hidden = w.ctx + (p.mask == nullptr ? (w.it.token0 + 1) / kRows : 0);
       // The mask's words are on their way to the L1 cache during the tiles before.
       if (p.mask != nullptr && row < rows)
         asm volatile("prefetch.global.L1 [%0];" ::"l"(p.mask + (static_cast<int64_t>(w.it.start) + token) * p.words));
@@ -783,14 +801,14 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
 
       for (int j = 0; j < mine_n; ++j) {
         const int t = w.tile(i, j);
-        const bool fresh = t >= w.ctx, masked = fresh || w.it.len - t * kRows < kRows;
+        const bool fresh = t >= w.ctx, masked = fresh ? t >= first_hidden : w.it.len - t * kRows < kRows;
         uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
         if (masked) {  // (while the scores are computed)
 #pragma unroll
           for (int q = 0; q < 4; ++q) keep[q] = sees(t, q);
         }
         ok = __all_sync(~0u, wait_for(s_full(i), (tiles_done + j) & 1, abort_flag, p.status));
-        if (ok && fresh) ok = clean_values(t - w.it.t0);
+        if (ok && fresh && masked) ok = clean_values(t - w.it.t0);
         if (!ok) break;
         tc_fence_after();
         if (!kFp8)
@@ -861,7 +879,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         }
         if (fix) {
           // A lane looks through one of 32 tokens, then the warp goes through those with something to add back.
-          for (int t = max(w.it.t0, w.ctx); t < w.it.t1; ++t)
+          for (int t = max(w.it.t0, first_hidden); t < w.it.t1; ++t)
             for (int q = 0; q < 4 && (t - w.ctx) * kRows + q * 32 < w.it.n; ++q) {
               const uint32_t keep = sees(t, q);
               const int node = (t - w.ctx) * kRows + q * 32;
@@ -1291,18 +1309,17 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       bool go = busy;
       if (go) {
         int b = seq;
-        const int wide = sq.tiles + kSegmentCost;
-        long long seg = quotient(inside, wide);
-        int t = static_cast<int>(inside - seg * wide);
-        int kv_head = static_cast<int>(quotient(seg, sq.blocks)), block = static_cast<int>(seg - static_cast<long long>(kv_head) * sq.blocks);
+        const long long wide = sq.before(p, sq.blocks);  // of a key-value head
+        int kv_head = static_cast<int>(quotient(inside, wide)), block = 0;
+        inside -= kv_head * wide;
+        for (int beyond = sq.blocks; beyond - block > 1;) {  // the block in which the place lies
+          const int middle = block + (beyond - block) / 2;
+          (sq.before(p, middle) <= inside ? block : beyond) = middle;
+        }
+        int t = static_cast<int>(inside - sq.before(p, block));
         for (long long pos = begin; go && pos < end;) {
           const long long base = pos - t;
-          // In order, a block sees the new tokens up to its last row's.
-          int needed = sq.tiles;
-          if (p.mask == nullptr) {
-            const int last_row = min((block + 1) * kBlock, sq.n * p.group) - 1;
-            needed = sq.ctx + last_row / p.group / kRows + 1;
-          }
+          const int needed = sq.needed(p, block);
           const int t1 = static_cast<int>(min(static_cast<long long>(needed), t + (end - pos)));
           if (t < t1) {
             const bool whole = t == 0 && t1 == needed;
@@ -1311,7 +1328,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
             if (t == 0 && !whole)
               job = make_int4(b, kv_head, block * kBlock, owner(base + needed - 1) - static_cast<int>(blockIdx.x) + 1);
           }
-          pos = base + sq.tiles + kSegmentCost;
+          pos = base + needed + kSegmentCost;
           t = 0;
           if (++block == sq.blocks) {
             block = 0;

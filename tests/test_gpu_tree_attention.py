@@ -506,3 +506,12 @@ def test_long_chain_with_values_that_are_not_finite(q_, heads, dim):
         out[:, :, 7 * x + 1] = clean[:, :, 7 * x + 1]
     assert torch.equal(out, clean)
     assert slow < 20 * fast  # (one token after the other in every thread: 80 times)
+
+
+@pytest.mark.parametrize("heads,hk", [(1, 1), (2, 2), (3, 1), (14, 2), (12, 1), (80, 1)])
+@pytest.mark.parametrize("counts", [[700], [513, 1, 0, 400, 128]])
+def test_chains_of_many_blocks(q_, heads, hk, counts):
+    """In order, the segments of a sequence have different lengths on the line."""
+    case = Case(q_, [150, 0, 20, 129, 1][:len(counts)], counts, heads, hk, 64, 16, BF, "chain", seed=heads)
+    out, lse = case.run(0.125)
+    case.check(0.125, out, lse)
