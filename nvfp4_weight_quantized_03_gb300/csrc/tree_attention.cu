@@ -24,8 +24,9 @@
 //                   over the scores; then the tile's outputs
 //   4 or 8 more     loads: q and k, v tiles through a ring.  Pages may be of any
 //                   size, so rows are gathered with cp.async; bytes of an E4M3
-//                   cache pass through a ring of their own and are widened to
-//                   bf16 on the way (exact)
+//                   cache pass through a ring of their own and are widened on
+//                   the way (exact), keys to bf16 as the queries are, values to
+//                   fp16, which takes a fifth of the instructions
 //   two more        issue S_i = Q_i K^T and O_i += P_i V of tile 0, tile 1
 //   one more        finds the CTA's next items
 // Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each).
@@ -35,9 +36,11 @@
 // while the other's softmax is computed.
 //
 // Roundings: scores, m, l, O are fp32; the weights 2^(s - m) are rounded to bf16
-// for the product with v, l sums the unrounded ones.  With an E4M3 cache O is in
-// units of the head's value scale, so the weights of the new tokens, whose values
-// are bf16, are divided by it first.
+// for the product with v, l sums the unrounded ones.  With an E4M3 cache the
+// weights of its rows are rounded to fp16 instead (m lies at most 2^8 below the
+// maximum, so they reach 2^8 of 2^16; below 2^-14 the step stays 2^-24, and l is at
+// least 1).  O is then in units of the head's value scale, so the weights of the new
+// tokens, whose values are bf16, are divided by it first.
 //
 // A masked weight is 0, but 0 * NaN is NaN: rows past a length read as zeros, and
 // the values of new tokens that some row of the item does not see are looked
@@ -64,6 +67,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <type_traits>
 
 namespace qerl {
@@ -145,6 +149,10 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -264,6 +272,12 @@ __device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& lo, uint32_
   const uint32_t x = (a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), y = (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u);
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(0x7B807B80u));
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(0x7B807B80u));
+}
+// Four E4M3 bytes -> four fp16 (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 // The barrier takes this thread's arrival when its copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
@@ -701,10 +715,13 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       // One key tile: scores in, weights out, l and (rarely) the reference moved.
       // Both passes are loops over 32 keys, which read the scores twice: code
       // that runs through once a tile is fetched as slowly as it runs.
-      // Whole tiles in code of their own (kind kWhole, the others kPartial) take two parts at a time in the second pass, which hides their latencies
-      // beside the widening (64 x 6000 rows E4M3 396 us, in common code 426 us);
-      // without it the smaller code is faster (heads of 64, 96 sequences: 82 us, in
-      // common code 74 us).
+      // Whole tiles have code of their own (kWhole) where they go on for long, of an
+      // E4M3 cache, or of a bf16 cache where the products hold the kernel (more than
+      // 128 rows): 64 keys at a time, the last 64 of the first pass still in
+      // registers for the second (4 x 512 tokens over 8192 rows, 28/4 heads: 250 us,
+      // in common code 257; for 128 rows and few tiles a segment the second code
+      // costs more fetches than it saves: 96 sequences with heads of 64 90 against 76).
+      // All 128 scores in registers: 2% faster there, 8% slower in the others.
       constexpr int kAny = 0, kPartial = 1, kWhole = 2;
       auto step = [&](auto kind, int j, int parts, bool hides, bool fresh, const uint32_t (&keep)[4]) {
         constexpr int kKind = decltype(kind)::value;
@@ -721,10 +738,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           }
         };
         float top = -kInf;
-#pragma unroll 1
-        for (int q = 0; q < (kKind == kWhole ? 4 : parts); ++q) {
-          float x[32];
-          load(q, x);
+        auto largest = [&](const float* x) {
           float t2[2] = {top, x[0]};
 #pragma unroll
           for (int e = 1; e < 29; e += 4) {
@@ -733,6 +747,25 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           }
           t2[0] = max3(t2[0], x[29], x[30]);
           top = max3(t2[0], t2[1], x[31]);
+        };
+        float x64[64];  // of a whole tile, a half
+        if (kKind == kWhole) {
+#pragma unroll 1
+          for (int half = 1; half >= 0; --half) {
+            tmem_ld32(s_t + half * 64, x64);
+            tmem_ld32(s_t + half * 64 + 32, x64 + 32);
+            tmem_ld_wait();
+            pin<64>(x64);
+            largest(x64);
+            largest(x64 + 32);
+          }
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < parts; ++q) {
+            float x[32];
+            load(q, x);
+            largest(x);
+          }
         }
         const float c = kFp8 && !fresh ? c_ctx : c_new;
         if (kFp8 && fresh != ref_fresh) {
@@ -765,9 +798,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         // weights of new tokens over an E4M3 cache: divided by the value scale, in the exponent
         const float lower = kFp8 && fresh ? -v_log2 : 0.0f;
         const uint64_t lower2 = pair(lower, lower);
-        auto weigh = [&](int q, bool half, bool all) {
-          float x[32];
-          load(q, x);
+        auto weigh = [&](const float* x, int q) {
           uint32_t y[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -776,10 +807,13 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
             a = ex2(a);
             b = ex2(b);
             part[e & 1] = add2(part[e & 1], pair(a, b));
-            y[e] = pack_bf16(a, b);
+            // weights of an E4M3 cache's rows: fp16, as those rows are
+            y[e] = kFp8 && (kKind == kWhole || !fresh) ? pack_f16(a, b) : pack_bf16(a, b);
           }
           tmem_st_x16(s_t + q * 16, y);
-          if (half || all) {  // half of the keys, or all: the product with v may begin
+        };
+        auto announce = [&](bool half, bool all) {  // half of the keys, or all: the product with v may begin
+          if (half || all) {
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -787,12 +821,27 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
             if (lane == 0 && all) mbar_arrive_a(p_full(i, 1));
           }
         };
-#pragma unroll(kKind == kWhole ? 2 : 1)
-        for (int q = 0; q < (kKind == kWhole ? 4 : parts); ++q) {
-          if (kKind == kWhole)
-            weigh(q, q == 1, q == 3);
-          else
-            weigh(q, q == 1 || (q == 0 && parts == 1), q + 1 == parts);
+        if (kKind == kWhole) {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            if (half == 1) {
+              tmem_ld32(s_t + 64, x64);
+              tmem_ld32(s_t + 96, x64 + 32);
+              tmem_ld_wait();
+              pin<64>(x64);
+            }
+            weigh(x64, 2 * half);
+            weigh(x64 + 32, 2 * half + 1);
+            announce(half == 0, half == 1);
+          }
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < parts; ++q) {
+            float x[32];
+            load(q, x);
+            weigh(x, q);
+            announce(q == 1 || (q == 0 && parts == 1), q + 1 == parts);
+          }
         }
         float s0, s1;
         unpair(add2(part[0], part[1]), s0, s1);
@@ -811,12 +860,10 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         if (ok && fresh && masked) ok = clean_values(t - w.it.t0);
         if (!ok) break;
         tc_fence_after();
-        if (!kFp8)
-          step(std::integral_constant<int, kAny>{}, j, w.parts(t), masked, fresh, keep);
-        else if (masked)
-          step(std::integral_constant<int, kPartial>{}, j, w.parts(t), true, fresh, keep);
+        if (masked || (kFp8 ? fresh : w.shared))
+          step(std::integral_constant<int, kFp8 ? kPartial : kAny>{}, j, w.parts(t), kFp8 || masked, fresh, keep);
         else
-          step(std::integral_constant<int, kWhole>{}, j, 4, false, fresh, keep);
+          step(std::integral_constant<int, kWhole>{}, j, 4, false, !kFp8 && fresh, keep);
       }
       tiles_done += mine_n;
       n0 = (n0 + w.it.t1 - w.it.t0) % S::kLaps;
@@ -1012,7 +1059,6 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
 #pragma unroll 1
       for (int q0 = 0; q0 < kRawChunks; q0 += kTogether) {
         uint32_t x[kTogether][4];
-        uint32_t nan = 0;
 #pragma unroll
         for (int q = 0; q < kTogether; ++q) {
           const uint4 v = lds128(raw_at(q0 + q));
@@ -1021,24 +1067,35 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           x[q][2] = swap ? v.x : v.z;
           x[q][3] = swap ? v.y : v.w;
         }
+        uint32_t y[kTogether][8];
+        if (group == 1) {
 #pragma unroll
-        for (int q = 0; q < kTogether; ++q)
+          for (int q = 0; q < kTogether; ++q)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) nan |= (x[q][e] & 0x7F7F7F7Fu) + 0x01010101u;
-        const bool some = (nan & 0x80808080u) != 0;
+            for (int e = 0; e < 4; ++e) e4m3x4_to_f16(x[q][e], y[q][2 * e], y[q][2 * e + 1]);
+        } else {
+          uint32_t nan = 0;
+#pragma unroll
+          for (int q = 0; q < kTogether; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) nan |= (x[q][e] & 0x7F7F7F7Fu) + 0x01010101u;
+          const bool some = (nan & 0x80808080u) != 0;
+#pragma unroll
+          for (int q = 0; q < kTogether; ++q) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) e4m3x4_to_bf16(x[q][e], y[q][2 * e], y[q][2 * e + 1]);
+            if (some) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) nan_bytes_to_bf16(x[q][e], y[q][2 * e], y[q][2 * e + 1]);
+            }
+          }
+        }
 #pragma unroll
         for (int q = 0; q < kTogether; ++q) {
           const int row = lw * 32 + ((q0 + q) * 32 + lane) / kRawChunks;
-          uint32_t y[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) e4m3x4_to_bf16(x[q][e], y[2 * e], y[2 * e + 1]);
-          if (some) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) nan_bytes_to_bf16(x[q][e], y[2 * e], y[2 * e + 1]);
-          }
           const uint32_t first = to + row * 128 + ((((ch & 7) + (swap ? 1 : 0)) ^ (row & 7)) << 4);
-          sts128(first, make_uint4(y[0], y[1], y[2], y[3]));
-          sts128(first ^ 16, make_uint4(y[4], y[5], y[6], y[7]));
+          sts128(first, make_uint4(y[q][0], y[q][1], y[q][2], y[q][3]));
+          sts128(first ^ 16, make_uint4(y[q][4], y[q][5], y[q][6], y[q][7]));
         }
         if (more) {
 #pragma unroll
@@ -1216,66 +1273,71 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           const float ks = kFp8 && p.k_scale != nullptr ? p.k_scale[w.it.kv_head] : 1.0f;
           auto tile_of = [&](int j) { return static_cast<unsigned>(w.tile(i, j) - w.it.t0); };
           auto wait_part = [&](int part, int j) { return wait_load(part, n0 + tile_of(j), count0 + tile_of(j)); };
-          auto scores = [&](int j) {
-            const uint32_t qa = sbase + (w.shared ? 0 : i * S::kTile), ka = slot_at(0, n0 + tile_of(j));
+          // One place each for the two products, as code is fetched cold at every item,
+          // and in a turn nothing but waits and products until the next scores are
+          // on their way: the softmax of this tile waits for them.
+          const uint32_t qa = sbase + (w.shared ? 0 : i * S::kTile);
+          for (int j = -1; j < n; ++j) {
+            const bool more = j + 1 < n;
+            const int t = j < 0 ? 0 : w.tile(i, j), t_next = more ? w.tile(i, j + 1) : 0;
+            const uint32_t va = j < 0 ? 0 : slot_at(1, n0 + tile_of(j)), ka = more ? slot_at(0, n0 + tile_of(j + 1)) : 0;
+            const int steps = j < 0 ? 0 : 2 * w.parts(t);
+            // rows of an E4M3 cache and their weights are fp16
+            const uint32_t id_v = kFp8 && t < w.ctx ? id_o & ~(9u << 7) : id_o;
             // a negative factor of the scores: the product is negated
-            const bool negative = p.scale_log2 < 0.0f != (w.tile(i, j) < w.ctx && ks < 0.0f);
-            const uint32_t id = idesc_bf16_f32(128, 32 * w.parts(w.tile(i, j))) | (negative ? 1u << 13 : 0u);
+            const bool negative = p.scale_log2 < 0.0f != (t_next < w.ctx && ks < 0.0f);
+            const uint32_t id_k = idesc_bf16_f32(128, more ? 32 * w.parts(t_next) : 32) | (negative ? 1u << 13 : 0u);
+            if (j >= 0) {
+              ok = wait_part(1, j);
+              if (!w.shared) {
+                // Turns, as the two tiles would fall into step: both in the softmax, then both at the tensor
+                // core (without turns 4 x 512 tokens over 8192 rows 269 us, handed on before the scores 247,
+                // behind them 226, in their midst, so that the other's products follow at once, 223).
+                ok = ok && (!more || wait_part(0, j + 1));
+                if (ok && !first_turn) ok = wait_for(turn(i), (turns - (i == 0 ? 1 : 0)) & 1, abort_flag, p.status);
+                first_turn = false;
+                ++turns;
+              }
+#pragma unroll 1
+              for (int half = 0; half < 2; ++half) {
+                ok = __all_sync(~0u, ok && wait_for(p_full(i, half), (tiles_done + j) & 1, abort_flag, p.status));
+                if (!ok) break;
+                if (half == 0) fence_proxy_async_smem();
+                tc_fence_after();
 #pragma unroll
-            for (int d = 0; d < S::kPanels; ++d)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ss(leader, tmem + i * 128, sw128_kmajor_desc(qa + d * kPanel + kk * 32),
-                       sw128_kmajor_desc(ka + d * kPanel + kk * 32), id, d + kk > 0 ? 1u : 0u);
-            commit(leader, s_full(i));
-            release(0, n0 + tile_of(j), w.shared);
-            if (j + 1 == n) commit(leader, q_free);
-          };
-          auto values = [&](int j, int half) {
-            const uint32_t va = slot_at(1, n0 + tile_of(j));
-            const int steps = 2 * w.parts(w.tile(i, j));
-#pragma unroll
-            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-              if (kk < steps) mma_ts(leader, tmem + 256 + i * D, tmem + i * 128 + kk * 8, sw128_mnmajor_desc(va + kk * 2048), id_o,
-                     j > 0 || kk > 0 ? 1u : 0u);
-          };
-          ok = __all_sync(~0u, wait_part(0, 0));
-          if (!ok) break;
-          // (the loads are ordinary writes of other threads, seen here through the barrier)
-          fence_proxy_async_smem();
-          tc_fence_after();
-          scores(0);
-          for (int j = 0; j < n; ++j) {
-            ok = wait_part(1, j);
-            if (!w.shared) {
-              // Turns, as the two tiles would fall into step: both in the softmax, then both at the tensor core.
-              ok = ok && (j + 1 >= n || wait_part(0, j + 1));
-              if (ok && !first_turn) ok = wait_for(turn(i), (turns - (i == 0 ? 1 : 0)) & 1, abort_flag, p.status);
-              first_turn = false;
-              ++turns;
+                for (int kk = 0; kk < 4; ++kk)
+                  if (4 * half + kk < steps)
+                    mma_ts(leader, tmem + 256 + i * D, tmem + i * 128 + half * 32 + kk * 8,
+                           sw128_mnmajor_desc(va + half * 8192 + kk * 2048), id_v, j > 0 || half > 0 || kk > 0 ? 1u : 0u);
+              }
+              if (!ok) break;
             }
-            ok = __all_sync(~0u, ok && wait_for(p_full(i, 0), (tiles_done + j) & 1, abort_flag, p.status));
-            if (!ok) break;
-            fence_proxy_async_smem();
-            tc_fence_after();
-            values(j, 0);
-            ok = __all_sync(~0u, wait_for(p_full(i, 1), (tiles_done + j) & 1, abort_flag, p.status));
-            if (!ok) break;
-            tc_fence_after();
-            values(j, 1);
-            release(1, n0 + tile_of(j), w.shared);
-            if (j + 1 < n) {
-              if (w.shared) {
+            if (more) {
+              if (w.shared || j < 0) {
+                if (j >= 0) release(1, n0 + tile_of(j), true);
                 ok = __all_sync(~0u, wait_part(0, j + 1));
                 if (!ok) break;
+                // (the loads are ordinary writes of other threads, seen here through the barrier)
                 fence_proxy_async_smem();
                 tc_fence_after();
               }
-              scores(j + 1);
+#pragma unroll
+              for (int d = 0; d < S::kPanels; ++d)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  mma_ss(leader, tmem + i * 128, sw128_kmajor_desc(qa + d * kPanel + kk * 32),
+                         sw128_kmajor_desc(ka + d * kPanel + kk * 32), id_k, d + kk > 0 ? 1u : 0u);
+                  if (d * 4 + kk + 1 == 2 * S::kPanels && !w.shared && j >= 0 && leader)
+                    mbar_arrive_a(turn(1 - i));
+                }
+              commit(leader, s_full(i));
             } else {
               commit(leader, o_full(i));
             }
-            if (!w.shared && leader) mbar_arrive_a(turn(1 - i));
+            if (!w.shared && !more && leader) mbar_arrive_a(turn(1 - i));
+            if (j >= 0 && !(w.shared && more)) release(1, n0 + tile_of(j), w.shared);
+            if (more) release(0, n0 + tile_of(j + 1), w.shared);
+            if (j + 2 == n) commit(leader, q_free);
           }
         }
         tiles_done += n;
