@@ -47,20 +47,25 @@
 // through before the product; elements that are not finite are replaced by 0 there
 // and added back in the end to the rows that do see them.
 //
-// Measured: 48 sequences to 8192 rows, 25 nodes, 40/8 heads of 128: 98 us = 0.77 of
+// Measured: 48 sequences to 8192 rows, 25 nodes, 40/8 heads of 128: 99 us = 0.76 of
 // the copy rate (a segment's start and end cost two to three tiles); 64 x 6000
-// rows E4M3, 61 nodes, 28/4 heads: 417 us where the products take 179 (215 with the
-// rows that fill 512): widening and softmax share the schedulers (issue 54%,
-// tensor pipe 35%); 96 sequences to 2500 rows, 30 nodes, 32/8 heads of 64: 79 us
-// where the bytes take 28 (five to nine segments a CTA, each 11000 cycles for
-// three tiles: a chain of latencies); a chain of 5 over 777 rows 12.2 us.  What
-// made it so: instruction fetches bound the first forms (1.9 warps of a scheduler
-// waited for one), so that code is small and in loops: E4M3 829 us with every
-// kind of load inlined where it is used, 753 us in one place each, 713 us without
-// a polling wait, 507 us with the widening as a loop; bf16 108 to 101 us with the
-// softmax as loops.  Loads that announce themselves (130 to 109 us), four warps
-// each for keys and values of an E4M3 cache (510 to 428 us) and products of the
-// parts of a tile that hold keys (79 to 77 us) came on top.
+// rows E4M3, 61 nodes, 28/4 heads: 398 us where the products take 179 (215 with the
+// rows that fill 512): a tile's chain, 2700 cycles of softmax, then the second
+// half of its values' product and the next scores, 1700, beside the widening
+// (issue 53%, tensor pipe 38%); 96 sequences to 2500 rows, 30 nodes, 32/8 heads of
+// 64: 76 us where the bytes take 28 (five to nine segments a CTA, each 11000 cycles
+// for three tiles: a chain of latencies); a chain of 5 over 777 rows 12.8 us, of
+// which a call without work takes 10.2.  Long chains: 512 new tokens over 8192
+// rows, 4 sequences, 28/4 heads 223 us = 0.59 of the bf16 rate, 131072 tokens of one
+// head 3.29 ms = 0.71.  What made it so: instruction fetches bound the first forms
+// (1.9 warps of a scheduler waited for one), so that code is small and in loops:
+// E4M3 829 us with every kind of load inlined where it is used, 753 us in one
+// place each, 713 us without a polling wait, 507 us with the widening as a loop;
+// bf16 108 to 101 us with the softmax as loops.  Loads that announce themselves
+// (130 to 109 us), four warps each for keys and values of an E4M3 cache (510 to
+// 428 us) and products of the parts of a tile that hold keys (79 to 77 us) came on
+// top; then values as fp16, whole tiles 64 keys at a time and one place for each
+// product in the issuers (422 to 398 us; long chains 257 to 223 us).
 #include "qerl_internal.h"
 #include "qerl_ptx.cuh"
 
