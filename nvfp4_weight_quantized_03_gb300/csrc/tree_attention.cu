@@ -858,8 +858,19 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         const bool fresh = t >= w.ctx, masked = fresh ? t >= first_hidden : w.it.len - t * kRows < kRows;
         uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
         if (masked) {  // (while the scores are computed)
+          unsigned long long word[2] = {~0ull, ~0ull};
+          int limit = fresh ? w.it.n - (t - w.ctx) * kRows : w.it.len - t * kRows;  // keys of the tile
+          if (fresh && p.mask != nullptr) {
+            const int at = 2 * (t - w.ctx);
+            const unsigned long long* src = p.mask + (static_cast<int64_t>(w.it.start) + token) * p.words + at;
+            word[0] = at < p.words ? src[0] : 0;
+            word[1] = at + 1 < p.words ? src[1] : 0;
+          } else if (fresh) {
+            limit = min(limit, token + 1 - (t - w.ctx) * kRows);
+          }
+          if (fresh && row >= rows) limit = 0;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) keep[q] = sees(t, q);
+          for (int q = 0; q < 4; ++q) keep[q] = static_cast<uint32_t>(word[q >> 1] >> (32 * (q & 1))) & below(limit - q * 32);
         }
         ok = __all_sync(~0u, wait_for(s_full(i), (tiles_done + j) & 1, abort_flag, p.status));
         if (ok && fresh && masked) ok = clean_values(t - w.it.t0);
