@@ -53,7 +53,7 @@
 // rows that fill 512): a tile's chain, 2700 cycles of softmax, then the second
 // half of its values' product and the next scores, 1700, beside the widening
 // (issue 53%, tensor pipe 38%); 96 sequences to 2500 rows, 30 nodes, 32/8 heads of
-// 64: 76 us where the bytes take 28 (five to nine segments a CTA, each 11000 cycles
+// 64: 73 us where the bytes take 28 (five to nine segments a CTA, each 11000 cycles
 // for three tiles: a chain of latencies); a chain of 5 over 777 rows 12.8 us, of
 // which a call without work takes 10.2.  Long chains: 512 new tokens over 8192
 // rows, 4 sequences, 28/4 heads 223 us = 0.59 of the bf16 rate, 131072 tokens of one
