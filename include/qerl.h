@@ -606,7 +606,8 @@ QERL_API qerl_status qerl_window_prompt_attention(const void* q, int64_t ldq, co
                                                   size_t ws_bytes, void* stream);
 
 /* Attention of several new tokens per sequence over the cache and over one
- * another, to verify drafted tokens (a tree or a chain) in one pass.  Sequence s
+ * another, to verify drafted tokens (a tree or a chain) in one pass, or for the
+ * next part of a prompt whose first rows are in the cache.  Sequence s
  * has the rows cu_tokens[s] .. cu_tokens[s + 1] - 1 of q, k, v (rotated, not yet
  * in the cache) and lengths[s] rows in the cache; its new token t attends to all
  * of those rows and to the new tokens j of its sequence that it sees:

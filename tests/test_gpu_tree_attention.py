@@ -515,3 +515,29 @@ def test_chains_of_many_blocks(q_, heads, hk, counts):
     case = Case(q_, [150, 0, 20, 129, 1][:len(counts)], counts, heads, hk, 64, 16, BF, "chain", seed=heads)
     out, lse = case.run(0.125)
     case.check(0.125, out, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("heads,hk", [(6, 2), (9, 1)])
+def test_parts_of_prompts_over_the_cache(q_, dtype, heads, hk):
+    """Long chains behind rows in the cache: whole tiles of both, with and without a mask of their own."""
+    case = Case(q_, [700, 129, 0], [520, 77, 260], heads, hk, 128, 32, dtype, "chain", seed=heads, pad=1)
+    out, lse = case.run(0.09)
+    case.check(0.09, out, lse)
+    t = torch.arange(520, device="cuda")
+    bits = torch.zeros((case.tokens, 9), dtype=torch.int64, device="cuda")  # the same as a mask
+    for s in range(3):
+        for w in range(9):
+            n = case.counts[s]
+            seen = (t[:n] + 1 - 64 * w).clamp(0, 64)
+            bits[case.cu[s]:case.cu[s] + n, w] = torch.where(seen == 64, -1, (torch.ones_like(seen) << seen.clamp(max=63)) - 1)
+    case.mask = bits
+    out2, lse2 = case.run(0.09)
+    case.check(0.09, out2, lse2)
+
+
+@pytest.mark.parametrize("heads,hk,count", [(1024, 1, 2), (1024, 2, 1), (1023, 3, 3)])
+def test_the_largest_groups(q_, heads, hk, count):
+    case = Case(q_, [140], [count], heads, hk, 64, 16, BF, "tree", seed=heads)
+    out, lse = case.run(0.125)
+    case.check(0.125, out, lse)
