@@ -56,8 +56,8 @@
 // 64: 73 us where the bytes take 28 (five to nine segments a CTA, each 11000 cycles
 // for three tiles: a chain of latencies); a chain of 5 over 777 rows 12.8 us, of
 // which a call without work takes 10.2.  Long chains: 512 new tokens over 8192
-// rows, 4 sequences, 28/4 heads 223 us = 0.59 of the bf16 rate, 131072 tokens of one
-// head 3.29 ms = 0.71.  What made it so: instruction fetches bound the first forms
+// rows, 4 sequences, 28/4 heads 219 us = 0.60 of the bf16 rate, 131072 tokens of one
+// head 3.23 ms = 0.73.  What made it so: instruction fetches bound the first forms
 // (1.9 warps of a scheduler waited for one), so that code is small and in loops:
 // E4M3 829 us with every kind of load inlined where it is used, 753 us in one
 // place each, 713 us without a polling wait, 507 us with the widening as a loop;
@@ -65,7 +65,7 @@
 // (130 to 109 us), four warps each for keys and values of an E4M3 cache (510 to
 // 428 us) and products of the parts of a tile that hold keys (79 to 77 us) came on
 // top; then values as fp16, whole tiles 64 keys at a time and one place for each
-// product in the issuers (422 to 398 us; long chains 257 to 223 us).
+// product in the issuers (422 to 398 us; long chains 257 to 219 us).
 #include "qerl_internal.h"
 #include "qerl_ptx.cuh"
 
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
   // ---- this CTA's stretch of the line ---------------------------------------
   constexpr int kWarps = kThreads / 32;
   auto scan = [&](long long v) -> long long {  // inclusive over the block
-#pragma unroll
+#pragma unroll 1
     for (int i = 1; i < 32; i <<= 1) {
       const long long up = __shfl_up_sync(~0u, v, i);
       if (lane >= i) v += up;
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
     if (lane == 31) sums[warp] = v;
     __syncthreads();
     long long w = lane < kWarps ? sums[lane] : 0;
-#pragma unroll
+#pragma unroll 1
     for (int i = 1; i < kWarps; i <<= 1) {
       const long long up = __shfl_up_sync(~0u, w, i);
       if (lane >= i) w += up;
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
   };
   auto total_of = [&]() -> long long {  // of the last scan
     long long w = lane < kWarps ? sums[lane] : 0;
-#pragma unroll
+#pragma unroll 1
     for (int i = 16; i > 0; i >>= 1) w += __shfl_xor_sync(~0u, w, i);
     return w;
   };
@@ -563,6 +563,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
   } else {
     bool bad = false;
     long long mine = 0, first_cost = 0;
+#pragma unroll 1
     for (int b = threadIdx.x; b < p.num_seqs; b += kThreads) {
       const long long c = cost_of(b, bad);
       if (b == threadIdx.x) first_cost = c;
@@ -701,6 +702,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         }
         if ((sum & 0x7FFF7FFFu) != 0) {
           dirty[k & 3] = k + 1;
+#pragma unroll 1
           for (int q = 0; q < S::kPanels * 8; ++q) {
             const uint32_t at = at_row + (q >> 3) * kPanel + (((q & 7) ^ (r & 7)) << 4);
             const uint4 x = lds128(at);
@@ -942,7 +944,9 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         }
         if (fix) {
           // A lane looks through one of 32 tokens, then the warp goes through those with something to add back.
+#pragma unroll 1
           for (int t = max(w.it.t0, first_hidden); t < w.it.t1; ++t)
+#pragma unroll 1
             for (int q = 0; q < 4 && (t - w.ctx) * kRows + q * 32 < w.it.n; ++q) {
               const uint32_t keep = sees(t, q);
               const int node = (t - w.ctx) * kRows + q * 32;
