@@ -37,10 +37,12 @@
 //
 // Roundings: scores, m, l, O are fp32; the weights 2^(s - m) are rounded to bf16
 // for the product with v, l sums the unrounded ones.  With an E4M3 cache the
-// weights of its rows are rounded to fp16 instead (m lies at most 2^8 below the
-// maximum, so they reach 2^8 of 2^16; below 2^-14 the step stays 2^-24, and l is at
-// least 1).  O is then in units of the head's value scale, so the weights of the new
-// tokens, whose values are bf16, are divided by it first.
+// weights of its rows are rounded to fp16 instead.  They are taken 2^7 times as
+// large there: m lies at most 2^8 below the maximum, so they reach 2^15 of fp16's
+// 2^16, and one is lost to the product only below 2^-32 of the largest (without the
+// factor below 2^-25, and 130000 of those are a third of a percent of the sum, which
+// keeps them).  O is then in units of the head's value scale, so the weights of the
+// new tokens, whose values are bf16, are divided by it first.
 //
 // A masked weight is 0, but 0 * NaN is NaN: rows past a length read as zeros, and
 // the values of new tokens that some row of the item does not see are looked
@@ -82,6 +84,9 @@ constexpr int kRows = 128;   // rows of a query tile, keys of a key tile
 constexpr int kBlock = 256;  // rows of a segment
 constexpr uint32_t kPanel = kRows * 128;  // 128 rows of 64 bf16, 128-byte swizzle
 constexpr float kSlack = 8.0f;
+// Base-2 factor of all weights, and so of l and O: of the partials too.
+template <bool kFp8>
+constexpr float kAbove = kFp8 ? 7.0f : 0.0f;
 constexpr int kMaxCtas = 160;
 constexpr int kSegmentCost = 2;  // of a segment's start and end, in key tiles
 constexpr int kMaxTokens = 1 << 20;  // of a sequence
@@ -803,14 +808,14 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         const float sub = ref == -kInf ? 0.0f : ref;
         const uint64_t c2 = pair(c, c), sub2 = pair(-sub, -sub);
         // weights of new tokens over an E4M3 cache: divided by the value scale, in the exponent
-        const float lower = kFp8 && fresh ? -v_log2 : 0.0f;
-        const uint64_t lower2 = pair(lower, lower);
+        const float raise = kAbove<kFp8> - (kFp8 && fresh ? v_log2 : 0.0f);
+        const uint64_t raise2 = pair(raise, raise);
         auto weigh = [&](const float* x, int q) {
           uint32_t y[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float a, b;
-            unpair(fma2(add2(pair(x[2 * e], x[2 * e + 1]), sub2), c2, lower2), a, b);
+            unpair(fma2(add2(pair(x[2 * e], x[2 * e + 1]), sub2), c2, raise2), a, b);
             a = ex2(a);
             b = ex2(b);
             part[e & 1] = add2(part[e & 1], pair(a, b));
@@ -1009,7 +1014,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           __stcg(slot + static_cast<int64_t>(D + 1) * p.slot_rows + slot_row, l);
         } else if (p.lse != nullptr) {
           p.lse[(static_cast<int64_t>(w.it.start) + token) * p.heads + head0 + row_head] =
-              l == 0.0f ? -kInf : (mc + log2f(l)) * 0.69314718055994530942f;
+              l == 0.0f ? -kInf : (mc + (log2f(l) - kAbove<kFp8>)) * 0.69314718055994530942f;
         }
       }
       if (both) {  // the other tile's warps still read this tile's outputs and (m, l)
@@ -1445,8 +1450,8 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
 }
 
 // Block (c, y): 16 columns of the segment that CTA c began and others went on with.
-template <int D>
-__global__ void __launch_bounds__(kBlock) join_kernel(const __grid_constant__ TreeParams p, const int has_scale) {
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(kBlock) join_kernel(const __grid_constant__ TreeParams p) {
   griddep_wait();
   const int4 job = p.jobs[blockIdx.x];
   if (job.w == 0) return;
@@ -1502,7 +1507,7 @@ __global__ void __launch_bounds__(kBlock) join_kernel(const __grid_constant__ Tr
     }
   }
   const int token = row / p.group, head = job.y * p.group + row - token * p.group;
-  const float f = sum == 0.0f ? 0.0f : (has_scale ? p.v_scale[job.y] : 1.0f) / sum;
+  const float f = sum == 0.0f ? 0.0f : (kFp8 && p.v_scale != nullptr ? p.v_scale[job.y] : 1.0f) / sum;
   uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(start) + token) * p.ldo +
                                         static_cast<int64_t>(head) * D + blockIdx.y * 16);
 #pragma unroll
@@ -1512,7 +1517,7 @@ __global__ void __launch_bounds__(kBlock) join_kernel(const __grid_constant__ Tr
                         pack_bf16(acc[8 * e + 6] * f, acc[8 * e + 7] * f));
   if (blockIdx.y == 0 && p.lse != nullptr)
     p.lse[(static_cast<int64_t>(start) + token) * p.heads + head] =
-        sum == 0.0f ? -kInf : (top + log2f(sum)) * 0.69314718055994530942f;
+        sum == 0.0f ? -kInf : (top + (log2f(sum) - kAbove<kFp8>)) * 0.69314718055994530942f;
 }
 
 template <int D, bool kFp8>
@@ -1529,8 +1534,8 @@ qerl_status launch(const TreeParams& p, int grid, int dev, cudaStream_t s) {
   if (launch_dependent(tree_kernel<D, kFp8>, dim3(static_cast<unsigned>(grid)), S::kThreads, S::kSmem, s, p) !=
       cudaSuccess)
     return QERL_ERR_CUDA;
-  return cuda_status(launch_dependent(join_kernel<D>, dim3(static_cast<unsigned>(grid), D / 16), kBlock, 0, s, p,
-                                      static_cast<int>(kFp8 && p.v_scale != nullptr)));
+  return cuda_status(
+      launch_dependent(join_kernel<D, kFp8>, dim3(static_cast<unsigned>(grid), D / 16), kBlock, 0, s, p));
 }
 
 // Rows of a partial: no segment has more.
