@@ -32,6 +32,24 @@ def mixed64(q, k, v, scale, keep, rows):
     return out, lse, tol + 1e-30, tol_lse
 
 
+def check_mixed(case, scale, out, lse):
+    group = case.heads // case.hk
+    for s, (m, c) in enumerate(zip(case.lens, case.counts)):
+        rows = slice(case.cu[s], case.cu[s] + c)
+        if c == 0:
+            continue
+        keep = torch.cat([torch.ones((c, m), dtype=torch.bool, device="cuda"), case.keep[s]], 1)
+        for h in range(case.heads):
+            j = h // group
+            k, v = (torch.cat([x[j].double() * f[j].double(), y[rows, j].double()])
+                    for x, f, y in zip(case.rows[s], (case.ks, case.vs), (case.k, case.v)))
+            o, l, to, tl = mixed64(case.q[rows, h], k, v, scale, keep, m)
+            assert_within(out[rows, h], o, to, f"sequence {s} head {h}")
+            none = torch.isinf(l)
+            assert (lse[rows, h][none] == -math.inf).all() and (out[rows, h][none] == 0).all()
+            assert_within(lse[rows, h][~none], l[~none], tl[~none], f"lse of sequence {s} head {h}")
+
+
 # ---- weights over an E4M3 cache ----------------------------------------------
 
 
@@ -60,3 +78,54 @@ def test_many_tiny_weights_are_not_lost(q_, dim, count, bits):
     assert (o > 2 * to).all()
     assert_within(out, o.expand_as(out), to.expand_as(out), "output")
     assert_within(lse, l.expand_as(lse), tl.expand_as(lse), "lse")
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("count", [1, 9])
+def test_weights_of_a_cache_row_keep_the_bits_of_fp16(q_, dim, count):
+    """Two rows with values 1 and -1: the output is the difference of two weights near 1/2.  The larger is exact;
+    a rounding of the smaller to bf16 puts it off by up to 2^-10, twice what fp16 may."""
+    n, hk = 300, 16
+    case = Case(q_, [2] * n, [count] * n, hk, hk, dim, 2, F8, "any", seed=dim)
+    case.mask.zero_()
+    for keep in case.keep:
+        keep.zero_()
+    case.pages[1][:, :, 0], case.pages[1][:, :, 1] = 0x38, 0xB8  # 1 and -1
+    case.vs.fill_(1.0)
+    scale = 0.005
+    out, lse = case.run(scale)
+    # all sequences at once: [n, hk, 2, dim] keys
+    k = torch.stack([x[0].double() for x in case.rows]) * case.ks.double()[:, None, None]
+    q = case.q.view(n, count, hk, dim).double()
+    s = torch.einsum("nchd,nhjd->nchj", q, k) * scale
+    p = torch.softmax(s, -1)
+    want = (p[..., 0] - p[..., 1])[..., None].expand(n, count, hk, dim)
+    d = 2.0 ** -20 * (1.0 + scale * torch.einsum("nchd,nhjd->nchj", q.abs(), k.abs()).amax(-1))[..., None]
+    assert want.abs().median() < 0.05
+    assert_within(out.view(n, count, hk, dim), want, 2.0 ** -8 * want.abs() + 4 * d + 2.0 ** -11 + 2.0 ** -31)
+
+
+@pytest.mark.parametrize("heads,hk,dim,page", [(40, 8, 128, 24), (45, 3, 64, 100), (28, 4, 128, 32)])
+@pytest.mark.parametrize("kind", ["chain", "tree", "any"])
+def test_e4m3_batches_at_the_bound_of_fp16(q_, heads, hk, dim, page, kind):
+    case = Case(q_, [5, 0, 700, 128, 129, 3000, 0, 383, 64], [3, 7, 0, 33, 16, 50, 61, 1, 150], heads, hk, dim, page, F8,
+                kind, seed=heads)
+    out, lse = case.run(1 / math.sqrt(dim))
+    check_mixed(case, 1 / math.sqrt(dim), out, lse)
+
+
+def test_every_e4m3_key(q_):
+    """One row per sequence and a query of one element per head: lse is the score, the key's value."""
+    codes = [c for c in range(256) if c & 0x7F != 0x7F]
+    case = Case(q_, [1] * 4, [1] * 4, 64, 1, 64, 4, F8, "any", seed=1)
+    case.mask.zero_()
+    case.ks.fill_(1.0)
+    values = torch.tensor((codes + [0, 0])[:256], dtype=torch.uint8, device="cuda").view(4, 64)
+    for s in range(4):
+        case.pages[0][int(case.cache.tensors[2][s, 0]), 0, 0] = values[s]
+    case.q.copy_(torch.eye(64, device="cuda").to(BF).expand(4, 64, 64))
+    for scale in (1.0, 256.0):
+        _, lse = case.run(scale)
+        want = values.view(F8).double() * scale
+        # one product of two exact factors: the factor of the score and lse's own steps
+        assert_within(lse, want, 2.0 ** -20 * want.abs(), f"scale {scale}")
