@@ -784,10 +784,11 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           ref = mc == -kInf ? -kInf : mc / c;
           ref_fresh = fresh;
         }
-        if (__any_sync(~0u, (top - ref) * c > kSlack)) {
-          const float up = fmaxf(ref, top);
+        // A row moves its own reference only: what its neighbours in the warp see rounds none of its weights.
+        const bool moves = (top - ref) * c > kSlack;
+        if (__any_sync(~0u, moves)) {
           if (j > 0) {
-            const float f = ref == up ? 1.0f : ex2((ref - up) * c);
+            const float f = moves ? ex2((ref - top) * c) : 1.0f;
             l *= f;
 #pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
@@ -801,8 +802,10 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
               tmem_st_x16(o_t + q * 16, y);
             }
           }
-          ref = up;
-          mc = up == -kInf ? -kInf : up * c;
+          if (moves) {
+            ref = top;
+            mc = top * c;
+          }
         }
         uint64_t part[2] = {0, 0};  // two chains of two fp32 sums
         const float sub = ref == -kInf ? 0.0f : ref;

@@ -129,3 +129,36 @@ def test_every_e4m3_key(q_):
         want = values.view(F8).double() * scale
         # one product of two exact factors: the factor of the score and lse's own steps
         assert_within(lse, want, 2.0 ** -20 * want.abs(), f"scale {scale}")
+
+
+# ---- rows do not see what they do not attend to -----------------------------------
+
+
+# Many sequences, so that a CTA's stretch holds several key tiles: groups of new tokens of up to 128 rows (whose
+# two query tiles share them) and of more.
+LONG = [(24, 1500, 20, 16, 4), (12, 2100, 70, 8, 4), (20, 1300, 300, 4, 2)]
+
+
+def _long(q_, seqs, rows, count, heads, hk, dtype, dim, seed):
+    r = random.Random(seed)
+    return Case(q_, [rows + r.randint(-300, 300) for _ in range(seqs)], [count - r.randint(0, 3) for _ in range(seqs)],
+                heads, hk, dim, 32, dtype, "any", seed=seed)
+
+
+@pytest.mark.parametrize("seqs,rows,count,heads,hk", LONG)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_a_large_key_changes_no_bit_of_rows_that_do_not_see_it(q_, seqs, rows, count, heads, hk, dim, dtype):
+    """Its score moves the reference of the rows that do, far above the cache's scores before it."""
+    case = _long(q_, seqs, rows, count, heads, hk, dtype, dim, seed=61)
+    clean, lse = case.run(0.1)
+    hit = torch.zeros(case.tokens, dtype=torch.bool, device="cuda")
+    for s in range(seqs):
+        for at in (1, case.counts[s] - 2):
+            case.k[case.cu[s] + at] *= 64
+            hit[case.cu[s]:case.cu[s + 1]] |= case.keep[s][:, at]
+    assert hit.any() and not hit.all()
+    out, lse2 = case.run(0.1)
+    assert (out[hit] != clean[hit]).any()
+    assert torch.equal(lse[~hit], lse2[~hit])
+    assert torch.equal(out[~hit], clean[~hit])
