@@ -162,3 +162,70 @@ def test_a_large_key_changes_no_bit_of_rows_that_do_not_see_it(q_, seqs, rows, c
     assert (out[hit] != clean[hit]).any()
     assert torch.equal(lse[~hit], lse2[~hit])
     assert torch.equal(out[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("seqs,rows,count,heads,hk", LONG)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_masked_drafts_hold_anything_in_items_of_many_tiles(q_, seqs, rows, count, heads, hk, dim, dtype):
+    """A value or key that is not finite reaches the tokens that see it and no others, where a tile with masks is
+    not the first of its item, the reference has moved, and the two query tiles exchange their outputs."""
+    case = _long(q_, seqs, rows, count, heads, hk, dtype, dim, seed=62)
+    clean, lse = case.run(0.1)
+    check = check_mixed if dtype == F8 else lambda c, *a: c.check(*a)
+    check(case, 0.1, clean, lse)
+    kinds = [math.nan, math.inf, -math.inf]
+    places = [[0, 3, case.counts[s] - 1] for s in range(seqs)]
+    for s in range(seqs):  # values: columns 7, 8, 9 of the tokens that see them
+        for x, at in enumerate(places[s]):
+            case.v[case.cu[s] + at, :, 7 + x] = kinds[(s + x) % 3]
+    out, lse2 = case.run(0.1)
+    assert torch.equal(lse, lse2)
+    for s in range(seqs):
+        mine = slice(case.cu[s], case.cu[s + 1])
+        for x, at in enumerate(places[s]):
+            reached = case.keep[s][:, at]
+            column = out[mine, :, 7 + x]
+            assert not torch.isfinite(column[reached].float()).any()
+            assert torch.equal(column[~reached], clean[mine, :, 7 + x][~reached])
+    rest = [c for c in range(dim) if c not in (7, 8, 9)]
+    assert torch.equal(out[:, :, rest], clean[:, :, rest])
+    hit = torch.zeros(case.tokens, dtype=torch.bool, device="cuda")
+    for s in range(seqs):
+        for x, at in enumerate(places[s]):
+            case.k[case.cu[s] + at, :, 5] = kinds[(s + x) % 3]
+            hit[case.cu[s]:case.cu[s + 1]] |= case.keep[s][:, at]
+    out, lse2 = case.run(0.1)
+    assert hit.any() and not hit.all()
+    assert torch.equal(lse[~hit], lse2[~hit]) and torch.equal(out[~hit], clean[~hit])
+
+
+# ---- numbers of sequences -----------------------------------------------------
+
+
+# Up to 32 are looked through by one warp, up to the threads (512; E4M3 640) in one round, more in several.
+@pytest.mark.parametrize("n", [32, 33, 96, 512, 513, 640, 641, 1300])
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_numbers_of_sequences_and_offsets_that_break_the_rules(q_, n, dtype):
+    r = random.Random(n)
+    lens = [r.choice([0, 3, 40, 129]) for _ in range(n)]
+    counts = [r.choice([0, 1, 2, 5]) for _ in range(n)]
+    for i in (0, 1, -1):
+        counts[i] = 0
+    counts[2] = counts[n // 2] = counts[-2] = 3
+    lens[n // 3], counts[n // 3] = 5000, 7
+    case = Case(q_, lens, counts, 4, 2, 64, 16, dtype, "tree", seed=n, lead=2, tail=3)
+    out, lse = case.run(0.125)
+    (check_mixed if dtype == F8 else lambda c, *a: c.check(*a))(case, 0.125, out, lse)
+    for x in (out, lse):
+        assert (x[:2] == 5).all() and (x[-3:] == 5).all()
+    good = case.cu
+    for at, to in ((0, -1), (2, good[3] + 1), (n // 2, good[n // 2 + 1] + 1), (n - 2, good[n - 1] + 2),
+                   (n - 1, good[n - 2] - 1), (n, case.tokens + 1)):
+        case.cu = list(good)
+        case.cu[at] = to
+        broken, lse2 = case.run(0.125, status="QERL_ERR_RANGE")
+        assert (broken == 5).all() and (lse2 == 5).all(), f"offset {at}"
+    case.cu = good
+    again, lse2 = case.run(0.125)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
