@@ -635,9 +635,8 @@ QERL_API qerl_status qerl_window_prompt_attention(const void* q, int64_t ldq, co
  * that sees nothing (or only s_tj = -inf) gives out = 0, lse = -inf.  Scores,
  * softmax and sums are fp32; the softmax weights are rounded to bf16 for the
  * product with v (those of a QERL_E4M3 cache's rows to fp16: by half a step, 2^-11,
- * or by 2^-32 of the largest).  For a QERL_E4M3 cache, whose value scales are to
- * lie within 2^-64 .. 2^64, the new tokens' k and v are used as they are, not
- * rounded to its type.  A page number outside the cache
+ * or by 2^-32 of the largest).  For a QERL_E4M3 cache the new tokens' k and v are
+ * used as they are, not rounded to its type.  A page number outside the cache
  * records QERL_ERR_RANGE and its rows read as zeros.  The result does not depend
  * on timing.
  * workspace >= qerl_tree_attention_workspace_size(), 256-byte aligned, its header

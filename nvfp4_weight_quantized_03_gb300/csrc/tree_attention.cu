@@ -41,8 +41,9 @@
 // large there: m lies at most 2^8 below the maximum, so they reach 2^15 of fp16's
 // 2^16, and one is lost to the product only below 2^-32 of the largest (without the
 // factor below 2^-25, and 130000 of those are a third of a percent of the sum, which
-// keeps them).  O is then in units of the head's value scale, so the weights of the
-// new tokens, whose values are bf16, are divided by it first.
+// keeps them).  O is in units of the head's value scale while its tiles are of the
+// cache, and takes the scale before the first tile of new tokens, whose values are
+// bf16 (or at the end): a scale may be of any size and sign, or 0.
 //
 // A masked weight is 0, but 0 * NaN is NaN: rows past a length read as zeros, and
 // the values of new tokens that some row of the item does not see are looked
@@ -334,6 +335,10 @@ __device__ __forceinline__ bool wait_patiently(uint32_t bar, uint32_t parity, vo
 __device__ __forceinline__ float weight_of(float m, float top) {
   return m == -__int_as_float(0x7f800000) ? 1.0f : ex2(m - top);
 }
+
+// Units of the outputs over an E4M3 cache once they have the value scale: large beside
+// a large one, whose product with sums of some 2^41 would overflow.
+__device__ __forceinline__ float value_unit(float scale) { return fabsf(scale) > 0x1p40f ? 0x1p64f : 1.0f; }
 
 // A sequence's place on the line.
 struct Sequence {
@@ -663,12 +668,12 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       // overflows from scores of 2^31 on.
       float mc = -kInf, ref = -kInf, l = 0.0f;
       bool ref_fresh = false;
-      float v_scale = 1.0f, v_inverse = 1.0f, v_log2 = 0.0f, c_ctx = fabsf(p.scale_log2);
+      float unit = 1.0f, v_scale = 1.0f, c_ctx = fabsf(p.scale_log2);  // v_scale in units of `unit`
       if (kFp8) {
         if (p.k_scale != nullptr) c_ctx = fabsf(p.scale_log2 * p.k_scale[w.it.kv_head]);
         if (p.v_scale != nullptr) v_scale = p.v_scale[w.it.kv_head];
-        v_inverse = 1.0f / v_scale;
-        v_log2 = log2f(v_scale);
+        unit = value_unit(v_scale);
+        v_scale /= unit;
       }
       // Not 0: a masked score of -inf times 0 would be NaN (1e-37 times any score below 1e29 is as good as 0).
       c_ctx = fmaxf(c_ctx, 1e-37f);
@@ -780,16 +785,19 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
           }
         }
         const float c = kFp8 && !fresh ? c_ctx : c_new;
+        bool scales = false;
         if (kFp8 && fresh != ref_fresh) {
           ref = mc == -kInf ? -kInf : mc / c;
           ref_fresh = fresh;
+          scales = v_scale != 1.0f;
         }
         // A row moves its own reference only: what its neighbours in the warp see rounds none of its weights.
         const bool moves = (top - ref) * c > kSlack;
-        if (__any_sync(~0u, moves)) {
+        if (__any_sync(~0u, moves) || scales) {
           if (j > 0) {
-            const float f = moves ? ex2((ref - top) * c) : 1.0f;
+            float f = moves ? ex2((ref - top) * c) : 1.0f;
             l *= f;
+            if (kFp8 && scales) f *= v_scale;
 #pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
               float v[16];
@@ -810,8 +818,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         uint64_t part[2] = {0, 0};  // two chains of two fp32 sums
         const float sub = ref == -kInf ? 0.0f : ref;
         const uint64_t c2 = pair(c, c), sub2 = pair(-sub, -sub);
-        // weights of new tokens over an E4M3 cache: divided by the value scale, in the exponent
-        const float raise = kAbove<kFp8> - (kFp8 && fresh ? v_log2 : 0.0f);
+        const float raise = kAbove<kFp8> - (kFp8 && fresh && unit != 1.0f ? 64.0f : 0.0f);
         const uint64_t raise2 = pair(raise, raise);
         auto weigh = [&](const float* x, int q) {
           uint32_t y[16];
@@ -860,7 +867,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         }
         float s0, s1;
         unpair(add2(part[0], part[1]), s0, s1);
-        l += kFp8 && fresh ? (s0 + s1) * v_scale : s0 + s1;
+        l += kFp8 && fresh ? (s0 + s1) * unit : s0 + s1;
       };
 
       for (int j = 0; j < mine_n; ++j) {
@@ -900,7 +907,8 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       }
       if (!ok) break;
       tc_fence_after();
-      float f_own = 1.0f, f_other = 0.0f;
+      // (a tile's last keys tell whether its outputs have the value scale)
+      float f_own = kFp8 && !ref_fresh ? v_scale : 1.0f, f_other = 0.0f;
       const bool both = w.shared && w.count(1) > 0;
       if (both) {
         asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sbase + S::kMl + i * 1024 + r * 8), "f"(mc), "f"(l) : "memory");
@@ -916,15 +924,17 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
                      : "r"(sbase + S::kMl + (1 - i) * 1024 + r * 8)
                      : "memory");
         const float top = fmaxf(mc, m2);
-        f_own = weight_of(mc, top);
+        const float w_own = weight_of(mc, top);
         f_other = weight_of(m2, top);
         // the same sum in the same order on both sides
-        l = i == 0 ? f_own * l + f_other * l2 : f_other * l2 + f_own * l;
+        l = i == 0 ? w_own * l + f_other * l2 : f_other * l2 + w_own * l;
         mc = top;
+        f_own *= w_own;
+        if (kFp8 && w.tile(1 - i, w.count(1 - i) - 1) < w.ctx) f_other *= v_scale;
       }
       const bool live = row < rows;
       const bool fix = __any_sync(~0u, dirty[k & 3] == k + 1);
-      const float f = l == 0.0f ? 0.0f : v_scale / l;
+      const float f = l == 0.0f ? 0.0f : unit / l;
       const bool whole = w.it.slot < 0;
       float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (whole ? 0 : w.it.slot)) * slot_floats(p.slot_rows, D);
       const int slot_row = row - w.it.row0;
@@ -949,6 +959,10 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         } else {
           tmem_ld_wait();
           pin<32>(v);
+          if (kFp8) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= f_own;
+          }
         }
         if (fix) {
           // A lane looks through one of 32 tokens, then the warp goes through those with something to add back.
@@ -978,7 +992,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                   const float y = __shfl_sync(~0u, mine, e);
-                  if ((keep >> x & 1) != 0 && !(fabsf(y) < kInf)) v[e] += y * v_inverse;
+                  if ((keep >> x & 1) != 0 && !(fabsf(y) < kInf)) v[e] += y;
                 }
               }
             }
@@ -1510,7 +1524,7 @@ __global__ void __launch_bounds__(kBlock) join_kernel(const __grid_constant__ Tr
     }
   }
   const int token = row / p.group, head = job.y * p.group + row - token * p.group;
-  const float f = sum == 0.0f ? 0.0f : (kFp8 && p.v_scale != nullptr ? p.v_scale[job.y] : 1.0f) / sum;
+  const float f = sum == 0.0f ? 0.0f : (kFp8 && p.v_scale != nullptr ? value_unit(p.v_scale[job.y]) : 1.0f) / sum;
   uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(start) + token) * p.ldo +
                                         static_cast<int64_t>(head) * D + blockIdx.y * 16);
 #pragma unroll

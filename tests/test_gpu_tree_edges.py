@@ -131,6 +131,54 @@ def test_every_e4m3_key(q_):
         assert_within(lse, want, 2.0 ** -20 * want.abs(), f"scale {scale}")
 
 
+# ---- value scales ---------------------------------------------------------------
+
+
+@pytest.mark.parametrize("scale", [-0.01, 0.0, -0.0, 2.0 ** -80, -2.0 ** -100, 2.0 ** 39, 2.0 ** 41, -2.0 ** 100])
+@pytest.mark.parametrize("same_size", [False, True])
+@pytest.mark.parametrize("count", [10, 70])
+def test_value_scales_of_any_size_and_sign(q_, scale, same_size, count):
+    """New tokens' values near 1, or as large as the cache's.  Some tokens see no new ones: theirs are the cache's
+    values alone, however small those are beside the new tokens'."""
+    case = Case(q_, [150, 700], [count, 12], 8, 2, 64, 16, F8, "any", seed=44)
+    case.vs.fill_(scale)
+    if same_size:
+        case.v.mul_(abs(scale))
+    case.mask[::5] = 0
+    for s, keep in enumerate(case.keep):
+        rows = torch.arange(case.cu[s], case.cu[s + 1], device="cuda")
+        keep[rows % 5 == 0] = False
+    out, lse = case.run(0.1)
+    group = case.heads // case.hk
+    for s, (m, c) in enumerate(zip(case.lens, case.counts)):
+        rows = slice(case.cu[s], case.cu[s] + c)
+        keep = torch.cat([torch.ones((c, m), dtype=torch.bool, device="cuda"), case.keep[s]], 1)
+        for h in range(case.heads):
+            j = h // group
+            k = torch.cat([case.rows[s][0][j].double() * case.ks[j].double(), case.k[rows, j].double()])
+            # in units of 2^-100 of the values, so that the bound's 1e-30 is small
+            v = torch.cat([case.rows[s][1][j].double() * scale, case.v[rows, j].double()]) * 2.0 ** 100
+            o, l, to, tl = mixed64(case.q[rows, h], k, v, 0.1, keep, m)
+            assert_within(out[rows, h].double() * 2.0 ** 100, o, to, f"sequence {s} head {h}")
+            assert_within(lse[rows, h], l, tl)
+
+
+def test_value_scales_differ_by_head_and_over_many_ctas(q_):
+    """A long sequence whose segments are joined, with a scale of either side of 1 for its heads."""
+    case = Case(q_, [20011], [30], 8, 4, 128, 32, F8, "tree", seed=45)
+    case.vs.copy_(torch.tensor([-3.0, 2.0 ** -70, 2.0 ** 70, 0.02]))
+    out, lse = case.run(0.09)
+    group = 2
+    keep = torch.cat([torch.ones((30, 20011), dtype=torch.bool, device="cuda"), case.keep[0]], 1)
+    for h in range(8):
+        j = h // group
+        k = torch.cat([case.rows[0][0][j].double() * case.ks[j].double(), case.k[:, j].double()])
+        v = torch.cat([case.rows[0][1][j].double() * case.vs[j].double(), case.v[:, j].double()])
+        o, l, to, tl = mixed64(case.q[:, h], k, v, 0.09, keep, 20011)
+        assert_within(out[:, h], o, to, f"head {h}")
+        assert_within(lse[:, h], l, tl)
+
+
 # ---- rows do not see what they do not attend to -----------------------------------
 
 
