@@ -571,10 +571,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float top = max3(fmaxf(t4[0], t4[1]), t4[2], t4[3]);
         const float tc = kWindow ? top : top == -kInf ? -kInf : top * p.c;
-        if (__any_sync(~0u, kWindow ? (tc - mc) * p.c > kSlack : tc > mc + kSlack)) {
-          const float up = fmaxf(mc, tc);
+        // A row moves its own reference only: keys that its neighbours in the warp
+        // see round none of its weights.
+        const bool moves = kWindow ? (tc - mc) * p.c > kSlack : tc > mc + kSlack;
+        if (__any_sync(~0u, moves)) {
           if (j > 0) {
-            const float f = mc == up ? 1.0f : ex2(kWindow ? (mc - up) * p.c : mc - up);
+            const float f = moves ? ex2(kWindow ? (mc - tc) * p.c : mc - tc) : 1.0f;
             l *= f;
 #pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
@@ -588,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_x16(o_t + q * 16, y);
             }
           }
-          mc = up;
+          if (moves) mc = tc;
           if (kEarly) {
             sums[0] = sums[1] = 0;
             weights(0);
