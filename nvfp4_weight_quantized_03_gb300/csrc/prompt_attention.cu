@@ -81,6 +81,10 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 constexpr uint32_t kPanel = kRows * 128;  // 128 rows of 64 bf16, 128-byte swizzle
 constexpr float kSlack = 8.0f;
+// How far (base 2) a reference may lie from 0 before its rounding is kept out of
+// the weights: up to 2^15 it is 2^-10 at most, and the weight of a key at the
+// reference 1 in bf16, as in the sum to well below half a step of the output.
+constexpr float kFar = 32768.0f;
 // The longest sequence.  A wait may last two items (the loads and the finder are
 // done that much before the last outputs), and an item takes 1430 cycles per key
 // tile: 2^24 rows stay 5 times below the wait limit of 4e9 cycles, which would
@@ -462,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Work w;
     for (int k = 0; ok && take(k, w); ++k) {
       const int mine = i == 0 ? w.n0 : w.n1;
-      float mc = -kInf, l = 0.0f;  // the reference in base-2 units and the sum of 2^(s - m)
+      float mc = -kInf, ref = -kInf, l = 0.0f;  // the reference in base-2 units and as a score, the sum of 2^(s - m)
       // The values of a tile with masked keys (load u of the ring), looked through for
       // elements that are not finite; a thread takes one key's row.
       auto clean_values = [&](unsigned u) -> bool {
@@ -499,9 +503,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       // One key tile: scores in, weights out, l and (rarely) the reference moved.
-      // (With a window mc is a score, not in base-2 units, and is taken from the
-      // scores before their product with c: the fused product leaves the rounding of
-      // a large reference in the exponent, which overflows from scores of 2^31 on.)
+      // The fused product x c - mc leaves the rounding of mc in the exponent, the same
+      // for all keys of a row.  Of a far reference that is too much (2^7 and more from
+      // scores of 2^31 on), so it is taken from such a row's scores first.  (Taken
+      // from every score, which needs no such case, 2 to 4% slower; the rows looked at
+      // in every step instead of the flag 0.5 to 6%.)
+      auto is_far = [&](float m) { return fabsf(m) > kFar && m != -kInf; };
+      bool some_far = false;  // of the warp's rows; they change with a reference only
       auto step = [&](int j) {
         float x[128];
 #pragma unroll
@@ -533,14 +541,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t c2 = pair(p.c, p.c);
         uint64_t sums[2];  // two chains of two fp32 sums
         uint32_t w[32];
+        float sub = mc == -kInf ? 0.0f : mc;
         auto weights = [&](int half) {
-          const float sub = mc == -kInf ? 0.0f : mc;
           const uint64_t sub2 = pair(-sub, -sub);
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             float a, b;
-            const uint64_t x2 = pair(x[half * 64 + 2 * e], x[half * 64 + 2 * e + 1]);
-            unpair(kWindow ? fma2(add2(x2, sub2), c2, 0) : fma2(x2, c2, sub2), a, b);
+            unpair(fma2(pair(x[half * 64 + 2 * e], x[half * 64 + 2 * e + 1]), c2, sub2), a, b);
             a = ex2(a);
             b = ex2(b);
             sums[e & 1] = add2(sums[e & 1], pair(a, b));
@@ -570,13 +577,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           t4[q] = fmaxf(t4[q], x[q * 32 + 31]);
         }
         const float top = max3(fmaxf(t4[0], t4[1]), t4[2], t4[3]);
-        const float tc = kWindow ? top : top == -kInf ? -kInf : top * p.c;
-        // A row moves its own reference only: keys that its neighbours in the warp
-        // see round none of its weights.
-        const bool moves = kWindow ? (tc - mc) * p.c > kSlack : tc > mc + kSlack;
-        if (__any_sync(~0u, moves)) {
+        const float tc = top == -kInf ? -kInf : top * p.c;
+        if (__any_sync(~0u, tc > mc + kSlack || some_far)) {
+          // A row moves its own reference only: keys that its neighbours in the warp
+          // see round none of its weights.
+          const bool far = is_far(mc), moves = far ? (top - ref) * p.c > kSlack : tc > mc + kSlack;
           if (j > 0) {
-            const float f = moves ? ex2(kWindow ? (mc - tc) * p.c : mc - tc) : 1.0f;
+            const float f = moves ? ex2(far || is_far(tc) ? (ref - top) * p.c : mc - tc) : 1.0f;
             l *= f;
 #pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
@@ -590,7 +597,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_x16(o_t + q * 16, y);
             }
           }
-          if (moves) mc = tc;
+          if (moves) {
+            ref = top;
+            mc = sub = tc;
+          }
+          some_far = __any_sync(~0u, is_far(mc));
+          if (some_far) {
+            const float from = is_far(mc) ? -ref : 0.0f;
+            const uint64_t from2 = pair(from, from);
+#pragma unroll
+            for (int e = 0; e < 64; ++e) unpair(add2(pair(x[2 * e], x[2 * e + 1]), from2), x[2 * e], x[2 * e + 1]);
+            if (is_far(mc)) sub = 0.0f;
+          }
           if (kEarly) {
             sums[0] = sums[1] = 0;
             weights(0);
@@ -681,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (live && p.lse != nullptr)
           p.lse[row * p.heads + w.head] =
-              l == 0.0f ? -kInf : ((kWindow ? mc * p.c : mc) + log2f(l)) * 0.69314718055994530942f;
+              l == 0.0f ? -kInf : (mc + log2f(l)) * 0.69314718055994530942f;
         __syncwarp();
       }
     }
