@@ -620,7 +620,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kFp8, NT>::kCtas)) decode_
           x[nt][mt][i] = v;
           top[i & 1] = fmaxf(top[i & 1], v);
         }
-      grow |= top[0] > m[nt][0] + (kBelow<kFp8> + kSlack) || top[1] > m[nt][1] + (kBelow<kFp8> + kSlack);
+      // (the difference is exact where it matters; the sum would be rounded up to let
+      // weights of an E4M3 cache reach 2^16, infinity in fp16, at scores of 2^27)
+      grow |= top[0] - m[nt][0] > kBelow<kFp8> + kSlack || top[1] - m[nt][1] > kBelow<kFp8> + kSlack;
     }
     if (__any_sync(~0u, grow)) {
 #pragma unroll
