@@ -740,6 +740,8 @@ def qerl_tree_attention(cache, q, k, v, cu_tokens, lengths, mask, scale, out, ls
         if mask.dim() != 2 or mask.shape[0] != t or not mask.is_contiguous():
             raise ValueError(f"mask: expected contiguous [{t}, words], got {tuple(mask.shape)}")
         words, mask_p = mask.shape[1], mask.data_ptr()
+        if words < 1 and t > 0:  # (an empty tensor's address is none, which means tokens in order)
+            raise ValueError("mask: a token has at least one word")
     lse_p = None if lse is None else _lse(lse, t, h, dev)
     if workspace.get_device() != dev or not workspace.is_contiguous() or cache.device != dev:
         _memory(workspace, cache, dev)
