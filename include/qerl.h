@@ -665,7 +665,8 @@ QERL_API qerl_status qerl_tree_attention(const qerl_kv_cache* cache, const void*
  * call copies from: what such items leave in the child's table row and in these
  * pages is not specified.  A sequence number, length or page number outside the
  * cache, or a child that is its own parent, records QERL_ERR_RANGE; nothing of
- * that item is written.
+ * that item is written.  (A negative entry of a full page is one given up, e.g.
+ * behind a window, and is passed on.)
  * workspace >= qerl_kv_fork_workspace_size(), 256-byte aligned, zero-filled before
  * its first use (status word only). */
 QERL_API size_t qerl_kv_fork_workspace_size(void);

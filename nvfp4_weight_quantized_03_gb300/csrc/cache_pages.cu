@@ -58,17 +58,20 @@ __global__ void __launch_bounds__(kThreads, kForkCtas) fork_kernel(const ForkPar
   bool bad = parent < 0 || parent >= c.num_seqs || child < 0 || child >= c.num_seqs || parent == child || length < 0 ||
              length > c.max_pages * c.page_size;
   const int full = bad ? 0 : length / c.page_size, rest = bad ? 0 : length - full * c.page_size;
+  const int* from = c.table + parent * c.ld_table;
   int last = 0;
   if (rest > 0) {
-    last = c.table[parent * c.ld_table + full];
+    last = from[full];
     bad = last < 0 || last >= c.num_pages || fresh < 0 || fresh >= c.num_pages;
   }
-  if (bad) {
+  // Every block looks through the full pages' entries, as nothing of a bad item is
+  // written (a negative one is a page given up, and passed on).
+  for (int j = threadIdx.x; j < full; j += kThreads) bad |= from[j] >= c.num_pages;
+  if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0 && blockIdx.y == 0) record_error(c.status, QERL_ERR_RANGE);
     return;
   }
   if (blockIdx.y == 0) {
-    const int* from = c.table + parent * c.ld_table;
     int* to = c.table + child * c.ld_table;
     for (int j = threadIdx.x; j < full; j += kThreads) to[j] = from[j];
     if (rest > 0 && threadIdx.x == 0) to[full] = fresh;

@@ -1,0 +1,34 @@
+"""Fork and compaction: page numbers and lengths outside the cache are recorded wherever they stand."""
+import pytest
+import torch
+
+from test_gpu_cache_pages import BF, F8, Pool, _compact, _fork_plain, _i32, _status, q_  # noqa: F401 (q_ is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("page", [16, 100])
+@pytest.mark.parametrize("at", [0, 1, 299])
+@pytest.mark.parametrize("number", [2000, 2 ** 31 - 1])
+@pytest.mark.parametrize("rest", [0, 1, 15])
+def test_fork_of_a_sequence_with_a_full_page_outside(q_, page, at, number, rest):
+    """Nothing of that child is written, whether or not it has rows to copy; the child beside it is done."""
+    table = torch.zeros((5, 310), dtype=torch.int32)
+    table[0] = torch.arange(310) + 100
+    table[1] = torch.arange(310) + 500
+    table[0, at] = number
+    table[0, 40] = -3  # a page given up is none outside
+    pool = Pool(q_, 2000, 2, page, 64, BF, table)
+    ws = q_.workspace(q_.qerl_kv_fork_workspace_size())
+    good = [1, 4, 7 * page + 5, 7]
+    args = [_i32([a, b]) for a, b in zip([0, 3, 300 * page + rest, 6], good)]
+    q_.check(q_.qerl_kv_fork(pool.cache, *args, ws))
+    assert _status(q_, ws) == "QERL_ERR_RANGE"
+    _fork_plain(pool, *[[x] for x in good])
+    pool.same()
+    # a child of the rows in front of that page is done
+    short = [[0], [3], [at * page], [6]]
+    q_.check(q_.qerl_kv_fork(pool.cache, *map(_i32, short), ws))
+    assert _status(q_, ws) == "QERL_OK"
+    _fork_plain(pool, *short)
+    pool.same()
