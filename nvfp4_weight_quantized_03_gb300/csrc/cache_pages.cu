@@ -169,6 +169,8 @@ __global__ void __launch_bounds__(kScanThreads) number_kernel(const CompactParam
       reinterpret_cast<uint4*>(p.used)[w] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     const int width = static_cast<int>(c.max_pages), entries = static_cast<int>(c.num_seqs * c.max_pages);
+    if (width == 0)  // no entry's thread looks at the lengths
+      for (int s = threadIdx.x; s < c.num_seqs; s += kScanThreads) held(p, s, true);
     for (int e = threadIdx.x; e < entries; e += kScanThreads) {
       const int s = e / width, j = e - s * width;
       const int page = c.table[s * c.ld_table + j];
@@ -347,8 +349,9 @@ qerl_status launch_kv_compact(const KvCompactArgs& a, cudaStream_t s) {
     if (launch_dependent(number_kernel<true>, dim3(1), kScanThreads, 0, s, p) != cudaSuccess) return QERL_ERR_CUDA;
   } else {
     if (cudaMemsetAsync(p.used, 0, l.number - l.used, s) != cudaSuccess) return QERL_ERR_CUDA;
-    if (c.num_seqs > 0 && chunks > 0 && c.num_pages > 0) {
-      const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(std::min<int64_t>(c.num_seqs, 65535)));
+    if (c.num_seqs > 0) {  // without entries or pages too: lengths and numbers outside are recorded there
+      const dim3 grid(static_cast<unsigned>(std::max<int64_t>(chunks, 1)),
+                      static_cast<unsigned>(std::min<int64_t>(c.num_seqs, 65535)));
       if (launch_dependent(mark_kernel, grid, kThreads, 0, s, p) != cudaSuccess) return QERL_ERR_CUDA;
     }
     if (launch_dependent(number_kernel<false>, dim3(1), kScanThreads, 0, s, p) != cudaSuccess) return QERL_ERR_CUDA;

@@ -32,3 +32,23 @@ def test_fork_of_a_sequence_with_a_full_page_outside(q_, page, at, number, rest)
     assert _status(q_, ws) == "QERL_OK"
     _fork_plain(pool, *short)
     pool.same()
+
+
+@pytest.mark.parametrize("lengths", [[0, 5, 0], [-1, 0, 0], [0, 0, 2 ** 31 - 1]])
+def test_compact_records_lengths_of_a_cache_without_entries(q_, lengths):
+    for pages in (0, 7, 200000):
+        pool = Pool(q_, pages, 1, 4, 64, F8, torch.zeros((3, 0), dtype=torch.int32))
+        assert _compact(q_, pool, lengths) == (0, "QERL_ERR_RANGE")
+        assert _compact(q_, pool, [0, 0, 0]) == (0, "QERL_OK")
+
+
+@pytest.mark.parametrize("n,most", [(3, 5), (300, 40)])
+def test_compact_records_entries_and_lengths_of_a_cache_without_pages(q_, n, most):
+    table = torch.full((n, most), -2, dtype=torch.int32)
+    pool = Pool(q_, 0, 1, 4, 64, F8, table.clone())
+    assert _compact(q_, pool, [4] * n) == (0, "QERL_OK")  # pages given up
+    assert _compact(q_, pool, [4] * (n - 1) + [4 * most + 1]) == (0, "QERL_ERR_RANGE")
+    table[n - 1, 0] = 0
+    pool = Pool(q_, 0, 1, 4, 64, F8, table)
+    assert _compact(q_, pool, [4] * n) == (0, "QERL_ERR_RANGE")
+    assert _compact(q_, pool, [4] * (n - 1) + [0]) == (0, "QERL_OK")
