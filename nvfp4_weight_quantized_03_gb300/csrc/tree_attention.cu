@@ -678,17 +678,25 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
       // Not 0: a masked score of -inf times 0 would be NaN (1e-37 times any score below 1e29 is as good as 0).
       c_ctx = fmaxf(c_ctx, 1e-37f);
       const float c_new = fmaxf(fabsf(p.scale_log2), 1e-37f);
-      // Bits of the keys 32 q .. 32 q + 31 of key tile t that this row attends to.
-      auto below = [](int n) -> uint32_t { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; };
-      auto sees = [&](int t, int q) -> uint32_t {
-        if (t < w.ctx) return below(w.it.len - t * kRows - q * 32);
-        const int at = (t - w.ctx) * kRows + q * 32;
-        if (row >= rows) return 0;
-        if (p.mask == nullptr) return below(token + 1 - at);
-        const int word = at >> 6;
-        if (word >= p.words) return 0;
-        const unsigned long long m = p.mask[static_cast<int64_t>(w.it.start + token) * p.words + word];
-        return static_cast<uint32_t>(m >> (at & 32)) & below(w.it.n - at);
+      // Bits of the keys 32 q .. 32 q + 31 of key tile t that this row attends to, for
+      // its weights and for what is added back in the end; a mask's words are looked up
+      // together, for their latencies.
+      auto sees = [&](int t, uint32_t (&keep)[4]) {
+        auto below = [](int n) -> uint32_t { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; };
+        const bool fresh = t >= w.ctx;
+        unsigned long long word[2] = {~0ull, ~0ull};
+        int limit = fresh ? w.it.n - (t - w.ctx) * kRows : w.it.len - t * kRows;  // keys of the tile
+        if (fresh && p.mask != nullptr) {
+          const int at = 2 * (t - w.ctx);
+          const unsigned long long* src = p.mask + (static_cast<int64_t>(w.it.start) + token) * p.words + at;
+          word[0] = at < p.words ? src[0] : 0;
+          word[1] = at + 1 < p.words ? src[1] : 0;
+        } else if (fresh) {
+          limit = min(limit, token + 1 - (t - w.ctx) * kRows);
+        }
+        if (fresh && row >= rows) limit = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) keep[q] = static_cast<uint32_t>(word[q >> 1] >> (32 * (q & 1))) & below(limit - q * 32);
       };
       // The first tile of new tokens of which this item's rows may not see all.
       const int first_hidden = w.ctx + (p.mask == nullptr ? (w.it.token0 + 1) / kRows : 0);
@@ -874,21 +882,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         const int t = w.tile(i, j);
         const bool fresh = t >= w.ctx, masked = fresh ? t >= first_hidden : w.it.len - t * kRows < kRows;
         uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-        if (masked) {  // (while the scores are computed)
-          unsigned long long word[2] = {~0ull, ~0ull};
-          int limit = fresh ? w.it.n - (t - w.ctx) * kRows : w.it.len - t * kRows;  // keys of the tile
-          if (fresh && p.mask != nullptr) {
-            const int at = 2 * (t - w.ctx);
-            const unsigned long long* src = p.mask + (static_cast<int64_t>(w.it.start) + token) * p.words + at;
-            word[0] = at < p.words ? src[0] : 0;
-            word[1] = at + 1 < p.words ? src[1] : 0;
-          } else if (fresh) {
-            limit = min(limit, token + 1 - (t - w.ctx) * kRows);
-          }
-          if (fresh && row >= rows) limit = 0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) keep[q] = static_cast<uint32_t>(word[q >> 1] >> (32 * (q & 1))) & below(limit - q * 32);
-        }
+        if (masked) sees(t, keep);  // (while the scores are computed)
         ok = __all_sync(~0u, wait_for(s_full(i), (tiles_done + j) & 1, abort_flag, p.status));
         if (ok && fresh && masked) ok = clean_values(t - w.it.t0);
         if (!ok) break;
@@ -967,10 +961,12 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         if (fix) {
           // A lane looks through one of 32 tokens, then the warp goes through those with something to add back.
 #pragma unroll 1
-          for (int t = max(w.it.t0, first_hidden); t < w.it.t1; ++t)
+          for (int t = max(w.it.t0, first_hidden); t < w.it.t1; ++t) {
+            uint32_t bits[4];
+            sees(t, bits);
 #pragma unroll 1
             for (int q = 0; q < 4 && (t - w.ctx) * kRows + q * 32 < w.it.n; ++q) {
-              const uint32_t keep = sees(t, q);
+              const uint32_t keep = q < 2 ? (q == 0 ? bits[0] : bits[1]) : (q == 2 ? bits[2] : bits[3]);
               const int node = (t - w.ctx) * kRows + q * 32;
               const __nv_bfloat16* src = p.v + (static_cast<int64_t>(w.it.start) + node) * p.ldv + w.it.kv_head * D + col;
               uint32_t sum = 0;
@@ -996,6 +992,7 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
                 }
               }
             }
+          }
         }
         if (whole) {
           // Through shared memory, so that a store covers 64 bytes of a row.
