@@ -16,7 +16,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqerl.so")
 SOURCES = ["api.cu", "quantize.cu", "aqn.cu", "linear.cu", "backward.cu", "noalloc.cu", "kv_cache.cu",
            "decode_attention.cu", "prompt_attention.cu", "tree_attention.cu", "cache_pages.cu"]
-HEADERS = ["qerl_ptx.cuh", "qerl_internal.h", os.path.join("..", "..", "include", "qerl.h")]
+HEADERS = ["qerl_ptx.cuh", "attention.cuh", "qerl_internal.h", os.path.join("..", "..", "include", "qerl.h")]
 
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -54,12 +54,11 @@
 // is lost to the product only below 2^-32 of the largest (with m at the maximum
 // below 2^-25, and 100000 of those are a third of a percent of the sum, which
 // keeps them).
+#include "attention.cuh"
 #include "qerl_internal.h"
-#include "qerl_ptx.cuh"
 
 #include <algorithm>
 #include <atomic>
-#include <cuda_bf16.h>
 
 namespace qerl {
 namespace {
@@ -172,27 +171,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Four E4M3 bytes -> two f16x2 words (exact).
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 
 // cp_async_16 with an L2 cache policy.
 __device__ __forceinline__ void cp_async_16_hint(uint32_t smem_dst, const void* gsrc, uint32_t src_bytes, uint64_t pol) {
@@ -216,10 +194,6 @@ __device__ __forceinline__ int join_free(int segment) { return 3 + (segment & 1)
 __device__ __forceinline__ void bar_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory"); }
 __device__ __forceinline__ void bar_arrive(int id) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
-}
-// 2^(m - top); 1 for a part without a finite score, whose sums are 0 (or NaN, which stays).
-__device__ __forceinline__ float weight_of(float m, float top) {
-  return m == -__int_as_float(0x7f800000) ? 1.0f : ex2(m - top);
 }
 
 // A place on the line of work: key tile `tile` of `tiles` of (sequence b, part
@@ -270,12 +244,6 @@ __device__ __forceinline__ void advance(const DecodeParams& p, Cursor& c) {
       return;
     }
   }
-}
-
-// a / b for a >= 0, b > 0; the 64-bit division costs several times the 32-bit one.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
-  return a / b;
 }
 
 template <int D, bool kFp8, int NT, bool kWindow>

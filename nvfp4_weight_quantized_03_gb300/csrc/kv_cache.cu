@@ -21,12 +21,11 @@
 // 37 us (5.5 TB/s).  An E4M3 cache: 9132 tokens of 40 + 2 x 8 heads (262 MB,
 // 38.5 us) 56 us; with fewer threads and the same two stages less is in flight,
 // and warps wait for loads in a third of their cycles.
+#include "attention.cuh"
 #include "qerl_internal.h"
-#include "qerl_ptx.cuh"
 
 #include <algorithm>
 #include <atomic>
-#include <cuda_bf16.h>
 
 namespace qerl {
 namespace {
@@ -58,12 +57,6 @@ struct AppendParams {
   int* status;
 };
 
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 // Two fp32 values times `inverse` -> E4M3 (nearest even, saturating, NaN kept), in the low 16 bits.
 __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi, float inverse) {
   const float a = lo * inverse, b = hi * inverse;
