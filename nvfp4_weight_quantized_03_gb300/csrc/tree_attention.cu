@@ -534,7 +534,8 @@ __global__ void __launch_bounds__((Shape<D, kFp8>::kThreads), 1) tree_kernel(con
         v_scale /= unit;
       }
       // Not 0: a masked score of -inf times 0 would be NaN (1e-37 times any score below 1e29 is as good as 0).
-      c_ctx = fmaxf(c_ctx, 1e-37f);
+      // A key scale of NaN stays.
+      if (c_ctx < 1e-37f) c_ctx = 1e-37f;
       const float c_new = fmaxf(fabsf(p.scale_log2), 1e-37f);
       // Bits of the keys 32 q .. 32 q + 31 of key tile t that this row attends to, for
       // its weights and for what is added back in the end; a mask's words are looked up

@@ -179,6 +179,19 @@ def test_value_scales_differ_by_head_and_over_many_ctas(q_):
         assert_within(lse[:, h], l, tl)
 
 
+def test_key_scales_of_any_size_and_sign(q_):
+    """0 makes the cache's scores 0; one that is not finite reaches the outputs of its heads."""
+    for scale in (0.0, -0.0, -0.01, 2.0 ** -120, math.nan, math.inf):
+        case = Case(q_, [150, 700], [10, 70], 8, 2, 64, 16, F8, "any", seed=46)
+        case.ks[1] = scale
+        out, lse = case.run(0.1)
+        if math.isfinite(scale):
+            check_mixed(case, 0.1, out, lse)
+        else:
+            assert not torch.isfinite(out[:, 4:].float()).any() and not torch.isfinite(lse[:, 4:]).any()
+            assert torch.isfinite(out[:, :4].float()).all() and torch.isfinite(lse[:, :4]).all()
+
+
 # ---- rows do not see what they do not attend to -----------------------------------
 
 
