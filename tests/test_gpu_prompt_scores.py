@@ -89,3 +89,31 @@ def test_a_later_key_changes_no_bit_of_the_rows_before_it(q_, dim, window, size)
         hit = keep[:, a]
         assert (out[hit] != clean[hit]).any()
         assert torch.equal(lse[~hit], lse2[~hit]) and torch.equal(out[~hit], clean[~hit]), f"key {a}"
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_captured_call_within_a_window_follows_the_offsets(q_, dim):
+    """A replay takes the offsets that stand there; two graphs of two windows share a workspace in order."""
+    g = torch.Generator(device="cuda").manual_seed(18)
+    n = 700
+    q, k, v = _rows(n, 2, dim, g), _rows(n, 1, dim, g), _rows(n, 1, dim, g)
+    cu = torch.tensor([0, 100, n], dtype=torch.int32, device="cuda")
+    ws = q_.workspace(q_.qerl_prompt_attention_workspace_size(n, 2, 1, dim, 2))
+    windows, made = ((130, 4), (40, 0)), []
+    for window in windows:
+        out, lse = torch.empty_like(q), torch.empty((n, 2), device="cuda")
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            q_.check(q_.qerl_window_prompt_attention(q, k, v, cu, *window, 0.1, out, lse, ws))
+        made.append((graph, out, lse))
+    for middle in (100, 0, 511, n):
+        cu[1] = middle
+        for graph, _, _ in made:
+            graph.replay()
+        torch.cuda.synchronize()
+        for window, (_, out, lse) in zip(windows, made):
+            want, lse2 = _call(q_, q, k, v, [0, middle, n], 0.1, window)
+            assert torch.equal(out, want) and torch.equal(lse, lse2)
+    assert q_.qerl_read_status(ws) == 0

@@ -290,3 +290,37 @@ def test_numbers_of_sequences_and_offsets_that_break_the_rules(q_, n, dtype):
     case.cu = good
     again, lse2 = case.run(0.125)
     assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+# ---- the largest calls ---------------------------------------------------------
+
+
+def _chain(q_, n, g):
+    q, k, v = (torch.randn((n, 1, 64), generator=g, device="cuda").to(BF) for _ in range(3))
+    cache = q_.kv_cache(*(torch.zeros((1, 1, 16, 64), dtype=BF, device="cuda") for _ in range(2)), _i32([[0]]))
+    out, lse = torch.full((n, 1, 64), 5.0, dtype=BF, device="cuda"), torch.full((n, 1), 5.0, device="cuda")
+    ws = q_.workspace(q_.qerl_tree_attention_workspace_size(n, 1, 1, 64, 1))
+    q_.check(q_.qerl_tree_attention(cache, q, k, v, _i32([0, n]), _i32([0]), None, 0.125, out, lse, ws))
+    return q, k, v, out, lse, q_.STATUS_NAMES[q_.qerl_read_status(ws)]
+
+
+def test_the_longest_chain_and_one_token_more(q_):
+    g = torch.Generator(device="cuda").manual_seed(71)
+    n = 2 ** 20
+    q, k, v, out, lse, status = _chain(q_, n, g)
+    assert status == "QERL_OK"
+    at = torch.tensor([0, 1, 255, 256, 2 ** 19 + 3, n - 129, n - 1], device="cuda")
+    keep = torch.arange(n, device="cuda") <= at[:, None]
+    o, l, to, tl = masked64(q[at, 0], k[:, 0], v[:, 0], 0.125, keep, "bf16")
+    assert_within(out[at, 0], o, to)
+    assert_within(lse[at, 0], l, tl)
+    _, _, _, out, lse, status = _chain(q_, n + 1, g)
+    assert status == "QERL_ERR_RANGE"
+    assert (out == 5).all() and (lse == 5).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_the_widest_masks(q_, dtype):
+    case = Case(q_, [100, 300], [9, 4], 4, 2, 64, 16, dtype, "any", seed=72, words=2 ** 14)
+    out, lse = case.run(0.125)
+    (check_mixed if dtype == F8 else lambda c, *a: c.check(*a))(case, 0.125, out, lse)
