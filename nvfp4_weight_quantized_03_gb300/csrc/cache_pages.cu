@@ -7,8 +7,10 @@
 // their count L moves into the i-th unused number below L.
 //
 // Bound: bytes, each copied row once in and once out.  Measured: 384 children of 48
-// parents (53 MB) 11.9 us = 0.66 of the copy rate; 1336 pages of 256 KB moved
-// (700 MB) 125 us = 0.82, of which the marks and numbers take some 15 us.
+// parents (53 MB) 12.4 us = 0.63 of the copy rate; 1336 pages of 256 KB moved
+// (700 MB) 125 us = 0.82, of which the marks and numbers take some 15 us; a million
+// pages of 1 KB in use of two 1.73 ms, where the bytes take 0.30: one block numbers
+// the pool.
 #include "qerl_internal.h"
 #include "qerl_ptx.cuh"
 
@@ -314,7 +316,8 @@ qerl_status launch_kv_fork(const KvForkArgs& a, cudaStream_t s) {
   // Blocks per child: for a whole page 8 pieces at a time, but no more than twice
   // what is resident together, as each looks its child up first (384 children of
   // up to 64 rows, 8 heads of 128: 11.9 us, as many as are resident 16.5 us,
-  // without a limit 12.9 us).
+  // without a limit 12.9 us; 12.4 us since every block also looks through the
+  // full pages' numbers).
   const int64_t pieces = 2ll * p.pool.kv_heads *
                          ((static_cast<int64_t>(p.pool.page_size) * p.pool.row_bytes + kWarpPiece - 1) / kWarpPiece);
   const int64_t whole = (pieces + kThreads / 32 - 1) / (kThreads / 32);

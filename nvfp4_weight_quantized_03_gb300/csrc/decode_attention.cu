@@ -5,7 +5,7 @@
 //   lse = log sum_j exp(s_j)
 // (a window of w rows and n sinks: of these j those with j >= len - w or j < n,
 // which the tiles take as if they lay side by side; nothing else differs: 192
-// sequences to 12000 rows, window 4096, 64 sinks, 40/8 heads 332 us = 0.98 of the
+// sequences to 12000 rows, window 4096, 64 sinks, 40/8 heads 336 us = 0.96 of the
 // copy rate, one of 50001 rows with a window of 1000 9.2 us, of which the call
 // takes most)
 // for every query head; the G = num_heads / num_kv_heads query heads of a

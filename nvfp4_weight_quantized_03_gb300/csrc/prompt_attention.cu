@@ -48,9 +48,9 @@
 // are held by the softmax: 2400 cycles a pair, of which the exponentials of
 // both tiles take 1024 and their issue 1320 on each scheduler.
 //
-// With a window (16384 rows x 40 heads, window 2048, 16 sinks: 517 us, 0.67 of the
+// With a window (16384 rows x 40 heads, window 2048, 16 sinks: 512 us, 0.68 of the
 // rate of the visible pairs' products; 10 to 3001 rows x 28 heads, window 500, 4
-// sinks: 127 us, 0.30) an item has the same steps at the same pace, but more of
+// sinks: 128 us, 0.30) an item has the same steps at the same pace, but more of
 // what it computes is masked: a row of 500 visible keys takes part in 7 key tiles
 // of 128, one of them for 4 sinks.  Tried and left: the second query tile leaving
 // out the first tile of the window, which it never sees (its turn stays idle, or,

@@ -52,14 +52,15 @@
 //
 // Measured: 48 sequences to 8192 rows, 25 nodes, 40/8 heads of 128: 99 us = 0.76 of
 // the copy rate (a segment's start and end cost two to three tiles); 64 x 6000
-// rows E4M3, 61 nodes, 28/4 heads: 400 us where the products take 179 (215 with the
+// rows E4M3, 61 nodes, 28/4 heads: 394 us where the products take 179 (215 with the
 // rows that fill 512): a tile's chain, 2700 cycles of softmax, then the second
 // half of its values' product and the next scores, 1700, beside the widening
 // (issue 53%, tensor pipe 38%); 96 sequences to 2500 rows, 30 nodes, 32/8 heads of
 // 64: 74 us where the bytes take 28 (five to nine segments a CTA, each 11000 cycles
 // for three tiles: a chain of latencies); a chain of 5 over 777 rows 12.6 us, of
 // which a call without work takes 10.2.  Long chains: 512 new tokens over 8192
-// rows, 4 sequences, 28/4 heads 219 us = 0.60 of the bf16 rate, 131072 tokens of one
+// rows, 4 sequences, 28/4 heads 214 us = 0.62 of the bf16 rate (E4M3 rows 249 us, 32/8
+// heads of 64 over E4M3 rows 242 us = 0.31), 131072 tokens of one
 // head 3.23 ms = 0.73.  What made it so: instruction fetches bound the first forms
 // (1.9 warps of a scheduler waited for one), so that code is small and in loops:
 // E4M3 829 us with every kind of load inlined where it is used, 753 us in one
